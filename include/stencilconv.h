@@ -12,7 +12,7 @@
  *    was enqueued (argument errors) or a launch failed (SC_ERR_CUDA).
  *  - Arguments are validated on the host before any launch; there is no CPU
  *    fallback.
- *  - All data is fp32.  Sizes are ints; element offsets are computed in
+ *  - All data is fp32 unless an entry point takes a dtype.  Sizes are ints; element offsets are computed in
  *    64-bit, so tensors may exceed 2^31 elements as long as each size fits.
  */
 #ifndef STENCILCONV_H
@@ -36,11 +36,12 @@ typedef enum {
     SC_OK = 0,
     SC_ERR_NULL = -1,            /* a required pointer is NULL */
     SC_ERR_SHAPE = -2,           /* a size is < 1, or the sizes overflow */
-    SC_ERR_UNSUPPORTED = -3,     /* valid convolution the library does not run */
-    SC_ERR_ALIGN = -4,           /* a pointer is not 16-byte aligned */
+    SC_ERR_UNSUPPORTED = -3,     /* valid parameters the library does not run */
+    SC_ERR_ALIGN = -4,           /* a pointer or stride is not 16-byte aligned */
     SC_ERR_ALIAS = -5,           /* output overlaps an input */
     SC_ERR_CUDA = -6,            /* a CUDA call failed; see sc_last_cuda_error */
-    SC_ERR_DEVICE_TIMEOUT = -7   /* a device-side bounded wait gave up */
+    SC_ERR_DEVICE_TIMEOUT = -7,  /* a device-side bounded wait gave up */
+    SC_ERR_RANGE = -8            /* a device-side index was outside its table */
 } sc_status;
 
 typedef enum { SC_NCHW = 0, SC_NHWC = 1 } sc_layout;
@@ -215,6 +216,134 @@ int conv2d_fwd_tc_fused2(const float *x, const float *w1, const float *b1,
                          int act1, int act2, sc_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------
+ * Attention over a feature map.  An NHWC feature map [N][H][W][C] is, as it
+ * lies in memory, a batch of N sequences of H*W states of C = heads * D
+ * channels: 1x1 convolutions of it (conv2d_fwd, conv2d_fwd_tc_bf16) are the
+ * keys and values of the attention below, a pixel (y, x) being state y*W + x
+ * with the two positions y and x.
+ * ---------------------------------------------------------------------
+ */
+
+/* Strides, in elements, of a [batch][token][head][D] tensor whose D elements
+ * are contiguous.  Non-negative multiples of 16 bytes (0 on an axis that all
+ * share); an axis of size 1 may have any. */
+typedef struct {
+    long long batch, token, head;
+} sc_head_strides;
+
+typedef struct {
+    sc_head_strides q, k, v, out;
+} sc_attn_strides;
+
+/*
+ * cross_attention_fwd: attention of Tq query tokens to Tk states of another
+ * length ("Attention Is All You Need", Sections 3.2.1 and 3.2.3; key heads
+ * shared by groups of query heads as in "GQA: Training Generalized
+ * Multi-Query Transformer Models from Multi-Head Checkpoints"):
+ *   s_j = scale * sum_d q[n][t][h][d] k[n][j][h * Hkv / Hq][d]   for the valid states j of sequence n
+ *   out[n][t][h] = sum_j exp(s_j) v[n][j][h * Hkv / Hq] / sum_j exp(s_j)
+ *   lse[n][h][t] = log(sum_j exp(s_j))
+ * State j of sequence n is valid if j < k_len[n] and key_mask[n][j] != 0.
+ * Without a valid state, out is 0 and lse is -infinity.  What the keys and
+ * values of states that are not valid hold (NaN included) has no effect.
+ * q, out : [N][Tq][Hq][D], k, v : [N][Tk][Hkv][D], all of `dtype` (SC_F32 or
+ *   SC_BF16), 16-byte aligned, packed in that order if strides is NULL.  out
+ *   overlaps no input.
+ * lse : N*Hq*Tq floats, or NULL.
+ * k_len : N ints in device memory (a value below 0 counts as 0, one above Tk
+ *   as Tk), or NULL for Tk.  key_mask : N*Tk bytes, or NULL.
+ * Supported: Hq % Hkv == 0; D % 8 == 0, D <= 128; scale > 0; Tq, Tk and
+ *   N*Tq*Hq up to 2^30.
+ * Scores, softmax and sums are fp32; bf16 outputs are rounded once (to
+ * nearest even).
+ * A call may take a stream-ordered temporary buffer (see
+ * sc_release_workspace).  Returns SC_OK or a negative sc_status.
+ */
+int cross_attention_fwd(const void *q, const void *k, const void *v, void *out, float *lse, const int *k_len,
+                        const unsigned char *key_mask, int N, int Tq, int Tk, int Hq, int Hkv, int D, float scale,
+                        int dtype, const sc_attn_strides *strides, sc_stream_t stream);
+
+/* Which elements of a head are a pair: i and i + rot_dim / 2, or 2 i and 2 i + 1. */
+typedef enum { SC_ROT_HALF = 0, SC_ROT_INTERLEAVED = 1 } sc_rot_mode;
+
+/* Scaling of a rotation's frequencies for contexts longer than the original one. */
+typedef enum {
+    SC_ROT_SCALE_NONE = 0,
+    SC_ROT_SCALE_LINEAR = 1,   /* f / factor ("Extending Context Window of Large Language Models via Positional
+                                  Interpolation") */
+    SC_ROT_SCALE_NTK = 2,      /* base * factor^(pairs / (pairs - 1)) */
+    SC_ROT_SCALE_BANDS = 3     /* by the turns of a pair over `original` positions: more than 32 keep f, fewer than
+                                  one get f / factor, a linear blend between; cos and sin times
+                                  0.1 log(factor) + 1 ("YaRN: Efficient Context Window Extension of Large Language
+                                  Models", Section 3) */
+} sc_rot_scale;
+
+/*
+ * rotary_table_fwd: cosines and sines of a rotation ("RoFormer: Enhanced
+ * Transformer with Rotary Position Embedding", Section 3.2.2), made once and
+ * kept by the caller: table[p][i] = (cos, sin)(p f_i), 0 <= p < positions,
+ * 0 <= i < pairs, f_i = base^(-i / pairs) changed by `rule` (sc_rot_scale).
+ * Computed in 64 bits, rounded once.
+ * table : positions * pairs * 2 floats, 16-byte aligned.  base > 1.
+ * factor >= 1 (not used by SC_ROT_SCALE_NONE).  original > 0: the context
+ *   that SC_ROT_SCALE_BANDS counts turns over (not used by the others).
+ *   SC_ROT_SCALE_NTK needs pairs >= 2.
+ * Returns SC_OK or a negative sc_status.
+ */
+int rotary_table_fwd(float *table, int positions, int pairs, double base, int rule, double factor, double original,
+                     sc_stream_t stream);
+
+/*
+ * rotary_fwd: rotates each head's first rot_dim elements by its token's
+ * position: pair i of (a, b) becomes (a cos - b sin, b cos + a sin) with
+ * (cos, sin) = table[p][i]; the others are copied.  With inverse != 0 by the
+ * opposite angle (the transposed map).
+ * axes 1: pairs = rot_dim / 2, p = pos[t].  axes 2 (a feature map's row and
+ *   column): pairs = rot_dim / 4, the first half of the rot_dim / 2 pairs is
+ *   turned by p = pos[t], the second by p = pos[tokens + t], each with the
+ *   table's pairs from the first.
+ * x, y : [tokens][heads][D] of `dtype`, 16-byte aligned, packed unless
+ *   strides are given (their batch stride is not used).  y may be x (with
+ *   the same strides), else it overlaps no input.
+ * table : positions * pairs * 2 floats of rotary_table_fwd.  pos : axes *
+ *   tokens ints in device memory; for a position outside [0, positions) the
+ *   head's turned elements become NaN and sc_last_device_status returns
+ *   SC_ERR_RANGE.
+ * Supported: D % 8 == 0, D <= 256; rot_dim <= D, rot_dim % (8 * axes) == 0
+ *   (with rot_dim 0, table and pos may be NULL).
+ * Returns SC_OK or a negative sc_status.
+ */
+int rotary_fwd(const void *x, void *y, const float *table, const int *pos, int tokens, int heads, int D, int rot_dim,
+               int positions, int mode, int axes, int inverse, int dtype, const sc_head_strides *x_strides,
+               const sc_head_strides *y_strides, sc_stream_t stream);
+
+/* One tensor of qk_norm_rotary_fwd: x and y as in rotary_fwd (token and head
+ * strides in elements; both 0: packed), weight D floats (16-byte aligned) or
+ * NULL for ones. */
+typedef struct {
+    const void *x;
+    void *y;
+    const float *weight;
+    const int *pos;
+    int tokens, heads;
+    long long x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+} sc_norm_heads;
+
+/*
+ * qk_norm_rotary_fwd: RMS norm of each head of the queries and the keys
+ * ("Root Mean Square Layer Normalization"; per head as in "Scaling Vision
+ * Transformers to 22 Billion Parameters", Section 2) and their rotation, in
+ * one pass and one launch:
+ *   y = rotate(x * (mean_d(x^2) + eps)^(-1/2) * weight)
+ * The rotation as rotary_fwd's.  q and k may have different numbers of
+ * tokens and heads; either may be NULL (a step's queries whose keys are kept).
+ * Returns SC_OK or a negative sc_status.
+ */
+int qk_norm_rotary_fwd(const sc_norm_heads *q, const sc_norm_heads *k, const float *table, int D, int rot_dim,
+                       int positions, float eps, int mode, int axes, int dtype, sc_stream_t stream);
+
+/*
  * stencil_pipeline_fwd: three stencil stages fused in one pass over a
  * single-channel image ("Model-Based Warp Overlapped Tiling for Image
  * Processing Programs on GPUs", Abstract: stages fused into overlapped
@@ -242,8 +371,9 @@ int sc_repack(const float *src, float *dst, int N, int C, int H, int W,
 
 /*
  * sc_last_device_status: synchronize `stream`, then return and clear the
- * device-side status word of the current device (SC_OK, or
- * SC_ERR_DEVICE_TIMEOUT when a kernel's bounded wait expired).  Returns
+ * device-side status word of the current device (SC_OK,
+ * SC_ERR_DEVICE_TIMEOUT when a kernel's bounded wait expired, or
+ * SC_ERR_RANGE when a position lay outside a rotation table).  Returns
  * SC_ERR_CUDA if the synchronization itself failed.
  */
 int sc_last_device_status(sc_stream_t stream);

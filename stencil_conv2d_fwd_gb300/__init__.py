@@ -26,16 +26,25 @@ SC_ERR_ALIGN = -4
 SC_ERR_ALIAS = -5
 SC_ERR_CUDA = -6
 SC_ERR_DEVICE_TIMEOUT = -7
+SC_ERR_RANGE = -8
 SC_NCHW = 0
 SC_NHWC = 1
 SC_ACT_NONE = 0
 SC_ACT_RELU = 1
 SC_F32 = 0
 SC_BF16 = 1
+SC_ROT_HALF = 0
+SC_ROT_INTERLEAVED = 1
+SC_ROT_SCALE_NONE = 0
+SC_ROT_SCALE_LINEAR = 1
+SC_ROT_SCALE_NTK = 2
+SC_ROT_SCALE_BANDS = 3
 
 # Every symbol include/stencilconv.h declares, with (restype, argtypes).
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
+_D = ctypes.c_double
 SIGNATURES = {
     "conv2d_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "conv2d_fwd_tc": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
@@ -61,6 +70,10 @@ SIGNATURES = {
     "sc_test_conv_wait_expiry": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "sc_test_workspace_allocs": (ctypes.c_longlong, []),
     "conv2d_chain_fwd_host": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "cross_attention_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P]),
+    "rotary_table_fwd": (_I, [_P, _I, _I, _D, _I, _D, _D, _P]),
+    "rotary_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "qk_norm_rotary_fwd": (_I, [_P, _P, _P, _I, _I, _I, _F, _I, _I, _I, _P]),
 }
 SC_CHAIN_MAX_LAYERS = 64
 
@@ -69,6 +82,26 @@ class ScConvLayer(ctypes.Structure):
     """sc_conv_layer: one layer of conv2d_chain_fwd_host (device filters and bias)."""
     _fields_ = [("w", ctypes.c_void_p), ("b", ctypes.c_void_p), ("Cout", ctypes.c_int), ("R", ctypes.c_int),
                 ("S", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+class ScHeadStrides(ctypes.Structure):
+    """sc_head_strides: element strides of a [batch][token][head][D] tensor."""
+    _fields_ = [("batch", ctypes.c_longlong), ("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
+class ScAttnStrides(ctypes.Structure):
+    """sc_attn_strides: the strides of cross_attention_fwd's tensors."""
+    _fields_ = [("q", ScHeadStrides), ("k", ScHeadStrides), ("v", ScHeadStrides), ("out", ScHeadStrides)]
+
+
+class ScNormHeads(ctypes.Structure):
+    """sc_norm_heads: one tensor of qk_norm_rotary_fwd."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("tokens", ctypes.c_int), ("heads", ctypes.c_int),
+                ("x_token_stride", ctypes.c_longlong), ("x_head_stride", ctypes.c_longlong),
+                ("y_token_stride", ctypes.c_longlong), ("y_head_stride", ctypes.c_longlong)]
+
+
 SC_NOALLOC_SCRATCH_FLOATS = 8 * 1024 * 1024
 
 _lib = None
@@ -231,6 +264,52 @@ def conv2d_chain_fwd_host(x_host, y_host, N, H, W, Cin, layers, stream=None) -> 
         arr[i] = ScConvLayer(_ptr(w), _ptr(b), cout, r, s_, act)
     return load().conv2d_chain_fwd_host(_ptr(x_host), _ptr(y_host), N, H, W, Cin, len(layers),
                                         ctypes.cast(arr, ctypes.c_void_p), _stream(stream))
+
+
+def cross_attention_fwd(q, k, v, out, N, Tq, Tk, Hq, Hkv, D, scale, dtype=SC_F32, k_len=None, key_mask=None, lse=None,
+                        strides=None, stream=None) -> int:
+    """Attention of Tq query tokens to Tk states (see the header).
+
+    q, out: [N][Tq][Hq][D]; k, v: [N][Tk][Hkv][D]; k_len: N int32; key_mask: N*Tk bytes;
+    strides: four (batch, token, head) triples in elements, for q, k, v and out, or None (packed)."""
+    if strides is not None:
+        strides = ctypes.byref(ScAttnStrides(*(ScHeadStrides(*s) for s in strides)))
+    return load().cross_attention_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(k_len), _ptr(key_mask),
+                                      N, Tq, Tk, Hq, Hkv, D, scale, dtype, strides, _stream(stream))
+
+
+def rotary_table_fwd(table, positions, pairs, base=10000.0, rule=SC_ROT_SCALE_NONE, factor=1.0, original=0.0,
+                     stream=None) -> int:
+    """Cosines and sines of a rotation: table[positions][pairs][2] fp32 (see the header)."""
+    return load().rotary_table_fwd(_ptr(table), positions, pairs, base, rule, factor, original, _stream(stream))
+
+
+def rotary_fwd(x, y, table, pos, tokens, heads, D, rot_dim, positions, mode=SC_ROT_HALF, axes=1, inverse=False,
+               dtype=SC_F32, x_strides=None, y_strides=None, stream=None) -> int:
+    """Rotate each head's first rot_dim elements by its token's position (see the header).
+
+    x_strides, y_strides: (token, head) in elements, or None (packed)."""
+    xs = None if x_strides is None else ctypes.byref(ScHeadStrides(0, *x_strides))
+    ys = None if y_strides is None else ctypes.byref(ScHeadStrides(0, *y_strides))
+    return load().rotary_fwd(_ptr(x), _ptr(y), _ptr(table), _ptr(pos), tokens, heads, D, rot_dim, positions, mode,
+                             axes, 1 if inverse else 0, dtype, xs, ys, _stream(stream))
+
+
+def _norm_heads(t):
+    if t is None:
+        return None
+    x, y, weight, pos, tokens, heads, *strides = t
+    return ctypes.byref(ScNormHeads(_ptr(x), _ptr(y), _ptr(weight), _ptr(pos), tokens, heads, *strides))
+
+
+def qk_norm_rotary_fwd(q, k, table, D, rot_dim, positions, eps=1e-6, mode=SC_ROT_HALF, axes=1, dtype=SC_F32,
+                       stream=None) -> int:
+    """RMS norm of each head of q and k and their rotation, in one launch (see the header).
+
+    q, k: (x, y, weight, pos, tokens, heads[, x_token_stride, x_head_stride, y_token_stride,
+    y_head_stride]) or None."""
+    return load().qk_norm_rotary_fwd(_norm_heads(q), _norm_heads(k), _ptr(table), D, rot_dim, positions, eps, mode,
+                                     axes, dtype, _stream(stream))
 
 
 def sc_empty_kernel(blocks, threads, stream=None) -> int:

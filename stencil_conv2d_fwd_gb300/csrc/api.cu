@@ -444,11 +444,12 @@ const char *sc_status_string(int status)
     case SC_OK: return "ok";
     case SC_ERR_NULL: return "a required pointer is NULL";
     case SC_ERR_SHAPE: return "a size is < 1 or the sizes overflow";
-    case SC_ERR_UNSUPPORTED: return "unsupported convolution parameters";
-    case SC_ERR_ALIGN: return "a pointer is not 16-byte aligned";
+    case SC_ERR_UNSUPPORTED: return "unsupported parameters";
+    case SC_ERR_ALIGN: return "a pointer or stride is not 16-byte aligned";
     case SC_ERR_ALIAS: return "output overlaps an input";
     case SC_ERR_CUDA: return "a CUDA call failed";
     case SC_ERR_DEVICE_TIMEOUT: return "a device-side bounded wait expired";
+    case SC_ERR_RANGE: return "a device-side index was outside its table";
     default: return "unknown status";
     }
 }

@@ -1,0 +1,301 @@
+"""cross_attention_fwd against the plain 64-bit form, and its refusals.
+
+The bounds are those of attention_ref.py: fp32 scores and sums, one rounding
+of the weights and of the output to bf16 for bf16 tensors."""
+import math
+
+import numpy as np
+import pytest
+
+import attention_ref as ref
+import stencil_conv2d_fwd_gb300 as scl
+
+BF16, F32 = scl.SC_BF16, scl.SC_F32
+
+
+def make(torch, dtype, *shape, seed=0, gain=1.0):
+    g = torch.Generator().manual_seed(seed)
+    t = torch.randn(*shape, generator=g) * gain
+    return (t.bfloat16() if dtype == BF16 else t).cuda()
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def valid_of(N, Tk, k_len=None, key_mask=None):
+    valid = np.ones((N, Tk), bool)
+    if k_len is not None:
+        valid &= np.arange(Tk)[None, :] < np.asarray(k_len)[:, None]
+    if key_mask is not None:
+        valid &= np.asarray(key_mask) != 0
+    return valid
+
+
+def run_and_check(torch, sc, q, k, v, dtype, k_len=None, key_mask=None, scale=None, strides=None, out=None, stream=None,
+                  ref_kv=None):
+    N, Tq, Hq, D = q.shape
+    Tk, Hkv = k.shape[1], k.shape[2]
+    scale = D ** -0.5 if scale is None else scale
+    if out is None:
+        out = torch.full((N, Tq, Hq, D), float("nan"), dtype=q.dtype, device="cuda")
+    lse = torch.full((N, Hq, Tq), float("nan"), device="cuda")
+    kl = None if k_len is None else torch.tensor(k_len, dtype=torch.int32, device="cuda")
+    km = None if key_mask is None else torch.as_tensor(np.asarray(key_mask, np.uint8)).cuda()
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    sc.check(sc.cross_attention_fwd(q, k, v, out, N, Tq, Tk, Hq, Hkv, D, scale, dtype, k_len=kl, key_mask=km, lse=lse,
+                                    strides=strides, stream=stream), "cross_attention_fwd")
+    sc.check(sc.sc_last_device_status(stream), "device status")
+    kk, vv = ref_kv if ref_kv is not None else (k, v)
+    valid = None if k_len is None and key_mask is None else valid_of(N, Tk, k_len, key_mask)
+    o, z, wabs, mag = ref.attention(f64(q), f64(kk), f64(vv), scale, valid)
+    got, gz = f64(out), f64(lse)
+    err = np.abs(got - o)
+    bound = ref.out_bound(o, wabs, mag, D, Tk, dtype == BF16)
+    assert np.isfinite(got).all()
+    assert (err <= bound).all(), f"out: worst {np.max(err / bound):.2f} of its bound at {np.unravel_index(np.argmax(err / bound), err.shape)}"
+    assert np.array_equal(np.isneginf(gz), np.isneginf(z))
+    ok = np.isfinite(z)
+    zerr = np.abs(np.where(ok, gz, 0) - np.where(ok, z, 0))
+    assert (zerr <= ref.lse_bound(z, mag, D, Tk)).all(), f"lse: worst {np.max(zerr / ref.lse_bound(z, mag, D, Tk)):.2f}"
+    return out, lse
+
+
+# (N, Tq, Tk, Hq, Hkv, D): one token to many; lengths around tiles; odd widths; shared heads
+SHAPES = [
+    (1, 1, 1, 1, 1, 8),
+    (1, 1, 960, 4, 4, 64),
+    (2, 1, 257, 4, 2, 24),
+    (3, 1, 1000, 5, 1, 64),
+    (1, 1, 20000, 4, 1, 64),
+    (2, 1, 333, 16, 2, 96),
+    (2, 2, 129, 3, 3, 40),
+    (2, 3, 700, 4, 4, 32),
+    (1, 5, 128, 6, 2, 128),
+    (1, 9, 130, 2, 1, 80),
+    (2, 16, 640, 8, 2, 64),
+    (1, 16, 9000, 2, 1, 128),
+    (3, 77, 391, 4, 4, 64),
+    (1, 100, 1, 2, 2, 48),
+    (1, 127, 127, 3, 1, 128),
+    (1, 128, 128, 1, 1, 64),
+    (1, 129, 129, 2, 2, 16),
+    (2, 255, 513, 2, 1, 72),
+    (1, 257, 385, 5, 1, 104),
+    (1, 300, 1300, 4, 4, 128),
+    (1, 1000, 300, 2, 2, 56),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_shapes(sc, shape, dtype):
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, dtype, N, Tq, Hq, D, seed=1, gain=2.0)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=2), make(torch, dtype, N, Tk, Hkv, D, seed=3)
+    run_and_check(torch, sc, q, k, v, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tq,G", [(1, 1), (1, 4), (3, 1), (77, 1), (70, 4), (300, 2)])
+@pytest.mark.parametrize("Tk", [100, 128, 700, 4500])
+def test_lengths(sc, dtype, Tq, G, Tk):
+    """Lengths of zero, one, around a tile's end, all of Tk, above it and below zero; garbage beyond them."""
+    import torch
+    lens = [0, 1, 63, 64, min(Tk, 127), Tk - 1, Tk, Tk + 9, -3]
+    N, Hkv, D = len(lens), 2, 64
+    q = make(torch, dtype, N, Tq, Hkv * G, D, seed=4, gain=2.0)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=5), make(torch, dtype, N, Tk, Hkv, D, seed=6)
+    for n, L in enumerate(lens):
+        k[n, max(0, L):] = float("nan")
+        v[n, max(0, L):] = float("inf")
+    out, lse = run_and_check(torch, sc, q, k, v, dtype, k_len=lens)
+    assert (out[0] == 0).all() and (out[-1] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tq,G,D", [(1, 1, 64), (1, 4, 128), (2, 2, 32), (77, 1, 64), (40, 3, 128), (290, 1, 80)])
+def test_masks(sc, dtype, Tq, G, D):
+    """Masks that leave nothing, one state, every other one, a padded map, and whole tiles empty;
+    NaN and infinities in the masked places; a length on top."""
+    import torch
+    h, w = 25, 31
+    Tk, N, Hkv = h * w, 6, 2
+    rng = np.random.default_rng(7)
+    mask = np.zeros((N, Tk), np.uint8)
+    mask[1, 700] = 1
+    mask[2, ::2] = 255
+    m = np.zeros((h, w), np.uint8)
+    m[:19, :17] = 1
+    mask[3] = m.reshape(-1)
+    mask[4] = rng.random(Tk) < 0.5
+    mask[5, 300:520] = 2
+    lens = [Tk, Tk, Tk, Tk, 333, 400]
+    q = make(torch, dtype, N, Tq, Hkv * G, D, seed=8, gain=2.0)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=9), make(torch, dtype, N, Tk, Hkv, D, seed=10)
+    bad = torch.as_tensor(~valid_of(N, Tk, lens, mask)).cuda()
+    k[bad] = float("nan")
+    v[bad] = float("-inf")
+    v[bad & (torch.arange(Tk, device="cuda") % 2 == 0)] = float("nan")
+    out, lse = run_and_check(torch, sc, q, k, v, dtype, k_len=lens, key_mask=mask)
+    assert (out[0] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tq", [1, 2, 40, 140])
+@pytest.mark.parametrize("order", ["rising", "falling", "one"])
+def test_running_maximum(sc, dtype, Tq, order):
+    """Scores that rise over the keys by far more than a rounding's range, that fall, and one key that outweighs all."""
+    import torch
+    N, Tk, H, D = 1, 1500, 2, 64
+    q = make(torch, dtype, N, Tq, H, D, seed=11)
+    k, v = make(torch, dtype, N, Tk, H, D, seed=12), make(torch, dtype, N, Tk, H, D, seed=13)
+    q[..., 0] = 8.0
+    if order == "one":
+        k[:, 777, :, 0] = 60.0
+    else:
+        ramp = torch.linspace(-100, 100, Tk, device="cuda").view(1, Tk, 1)
+        k[..., 0] = (ramp if order == "rising" else -ramp).to(k.dtype)
+    run_and_check(torch, sc, q, k, v, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tq", [1, 50, 200])
+def test_strides(sc, dtype, Tq):
+    """Keys and values of one fused projection, heads before tokens, a batch that shares its keys, and an
+    output inside a wider row."""
+    import torch
+    N, Tk, Hq, Hkv, D = 2, 300, 6, 2, 40
+    wide = make(torch, dtype, N, Tk, 2 * Hkv, D, seed=14)
+    k, v = wide[:, :, :Hkv], wide[:, :, Hkv:]
+    qh = make(torch, dtype, N, Hq, Tq, D, seed=15)
+    q = qh.permute(0, 2, 1, 3)
+    row = torch.zeros(N, Tq, Hq * D + 64, dtype=q.dtype, device="cuda")
+    out = row[:, :, 32:32 + Hq * D].unflatten(2, (Hq, D))
+    st = [t.stride()[:3] for t in (q, k, v, out)]
+    run_and_check(torch, sc, q, k, v, dtype, strides=st, out=out)
+    assert (row[:, :, :32] == 0).all() and (row[:, :, 32 + Hq * D:] == 0).all()
+    one = k[:1].expand(N, -1, -1, -1)
+    out2 = torch.empty(N, Tq, Hq, D, dtype=q.dtype, device="cuda")
+    st = [q.stride()[:3], one.stride()[:3], v.stride()[:3], out2.stride()[:3]]
+    assert st[1][0] == 0
+    run_and_check(torch, sc, q, one, v, dtype, strides=st, out=out2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tq,Hq,Hkv", [(1, 4, 1), (33, 3, 3)])
+def test_offsets_beyond_32_bits(sc, dtype, Tq, Hq, Hkv):
+    """Keys and values of more than 2^31 elements; the valid states are the last ones."""
+    import torch
+    D = 128
+    Tk = (2 ** 31) // (Hkv * D) + 4099
+    k = torch.empty(1, Tk, Hkv, D, dtype=torch.bfloat16 if dtype == BF16 else torch.float32, device="cuda")
+    v = torch.empty_like(k)
+    q = make(torch, dtype, 1, Tq, Hq, D, seed=16)
+    tail = 4000
+    k[:, -tail:] = make(torch, dtype, 1, tail, Hkv, D, seed=17)
+    v[:, -tail:] = make(torch, dtype, 1, tail, Hkv, D, seed=18)
+    mask = torch.zeros(1, Tk, dtype=torch.uint8, device="cuda")
+    mask[:, -tail:] = 1
+    out = torch.empty_like(q)
+    sc.check(sc.cross_attention_fwd(q, k, v, out, 1, Tq, Tk, Hq, Hkv, D, D ** -0.5, dtype, key_mask=mask))
+    sc.check(sc.sc_last_device_status())
+    o, z, wabs, mag = ref.attention(f64(q), f64(k[:, -tail:]), f64(v[:, -tail:]), D ** -0.5)
+    assert (np.abs(f64(out) - o) <= ref.out_bound(o, wabs, mag, D, Tk, dtype == BF16)).all()
+    del k, v
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tq", [1, 16, 150])
+def test_other_stream_and_repeatable(sc, dtype, Tq):
+    """A stream of the caller's; the same bits each time, on any stream and from a CUDA graph."""
+    import torch
+    N, Tk, Hq, Hkv, D = 1, 30000, 4, 2, 64
+    q = make(torch, dtype, N, Tq, Hq, D, seed=19, gain=2.0)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=20), make(torch, dtype, N, Tk, Hkv, D, seed=21)
+    s = torch.cuda.Stream()
+    first, lse1 = run_and_check(torch, sc, q, k, v, dtype, stream=s)
+    second, lse2 = run_and_check(torch, sc, q, k, v, dtype)
+    assert torch.equal(first, second) and torch.equal(lse1, lse2)
+    out = torch.zeros_like(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sc.check(sc.cross_attention_fwd(q, k, v, out, N, Tq, Tk, Hq, Hkv, D, D ** -0.5, dtype))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)
+    q.copy_(q * 0.5)
+    g.replay()
+    torch.cuda.synchronize()
+    assert not torch.equal(out, first)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Tq", [1, 140])
+def test_nan_in_a_valid_state_is_not_hidden(sc, Tq):
+    import torch
+    q, k, v = (make(torch, BF16, 1, t, 1, 64, seed=22 + i) for i, t in enumerate((Tq, 500, 500)))
+    k[0, 300] = float("nan")
+    out = torch.zeros_like(q)
+    sc.check(sc.cross_attention_fwd(q, k, v, out, 1, Tq, 500, 1, 1, 64, 0.125, BF16))
+    assert torch.isnan(out).all()
+
+
+A, B, C, O = 1 << 30, 1 << 32, 1 << 34, 1 << 36   # fake, aligned, far apart: never dereferenced
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(q=None), scl.SC_ERR_NULL),
+    (dict(k=None), scl.SC_ERR_NULL),
+    (dict(v=None), scl.SC_ERR_NULL),
+    (dict(out=None), scl.SC_ERR_NULL),
+    (dict(N=0), scl.SC_ERR_SHAPE),
+    (dict(Tq=0), scl.SC_ERR_SHAPE),
+    (dict(Tk=-1), scl.SC_ERR_SHAPE),
+    (dict(Hkv=0), scl.SC_ERR_SHAPE),
+    (dict(D=0), scl.SC_ERR_SHAPE),
+    (dict(N=1 << 30, Tq=1 << 30), scl.SC_ERR_SHAPE),
+    (dict(Tk=(1 << 30) + 1), scl.SC_ERR_SHAPE),
+    (dict(Hkv=3), scl.SC_ERR_UNSUPPORTED),
+    (dict(D=12), scl.SC_ERR_UNSUPPORTED),
+    (dict(D=136), scl.SC_ERR_UNSUPPORTED),
+    (dict(dtype=2), scl.SC_ERR_UNSUPPORTED),
+    (dict(scale=0.0), scl.SC_ERR_UNSUPPORTED),
+    (dict(scale=-1.0), scl.SC_ERR_UNSUPPORTED),
+    (dict(scale=math.inf), scl.SC_ERR_UNSUPPORTED),
+    (dict(scale=math.nan), scl.SC_ERR_UNSUPPORTED),
+    (dict(q=A + 8), scl.SC_ERR_ALIGN),
+    (dict(out=O + 2), scl.SC_ERR_ALIGN),
+    (dict(lse=(1 << 38) + 2), scl.SC_ERR_ALIGN),
+    (dict(k_len=(1 << 38) + 2), scl.SC_ERR_ALIGN),
+    (dict(strides=[(2048, 256, 64), (2560, 130, 64), (2560, 128, 64), (2048, 256, 64)]), scl.SC_ERR_ALIGN),
+    (dict(strides=[(2048, 256, 64), (2560, 128, 64), (2560, 128, 64), (-2048, 256, 64)]), scl.SC_ERR_SHAPE),
+    (dict(strides=[(1 << 60, 256, 64), (2560, 128, 64), (2560, 128, 64), (2048, 256, 64)]), scl.SC_ERR_SHAPE),
+    (dict(strides=[(2048, 256, 64), (2560, 128, 64), (2560, 128, 64), (2048, 256, 32)]), scl.SC_ERR_ALIAS),
+    (dict(strides=[(2048, 256, 64), (2560, 128, 64), (2560, 128, 64), (0, 256, 64)]), scl.SC_ERR_ALIAS),
+    (dict(out=A), scl.SC_ERR_ALIAS),
+    (dict(out=B + 64), scl.SC_ERR_ALIAS),
+    (dict(out=C + 128), scl.SC_ERR_ALIAS),
+    (dict(lse=O + 64), scl.SC_ERR_ALIAS),
+    (dict(lse=A + 64), scl.SC_ERR_ALIAS),
+    (dict(k_len=O + 64), scl.SC_ERR_ALIAS),
+    (dict(key_mask=O + 64), scl.SC_ERR_ALIAS),
+    (dict(lse=1 << 38, key_mask=(1 << 38) + 3), scl.SC_ERR_ALIAS),
+])
+def test_refusals(change, expect):
+    a = dict(q=A, k=B, v=C, out=O, N=2, Tq=8, Tk=20, Hq=4, Hkv=2, D=64, scale=0.125, dtype=BF16, k_len=None,
+             key_mask=None, lse=None, strides=None)
+    a.update(change)
+    rc = scl.cross_attention_fwd(a["q"], a["k"], a["v"], a["out"], a["N"], a["Tq"], a["Tk"], a["Hq"], a["Hkv"], a["D"],
+                                 a["scale"], a["dtype"], k_len=a["k_len"], key_mask=a["key_mask"], lse=a["lse"],
+                                 strides=a["strides"], stream=0)
+    assert rc == expect, scl.sc_status_string(rc)
