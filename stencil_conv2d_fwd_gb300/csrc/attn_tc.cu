@@ -1,0 +1,668 @@
+// Attention of many query rows on the tensor cores (tcgen05, accumulators in
+// tensor memory).
+//
+//   S = Q K^T,  P = 2^(c S - m),  O = P V,  out = O / sum_j P_j,   c = scale log2 e
+//
+// over tiles of 128 rows and 128 keys, in one pass over the keys: m and the
+// sum are running values of a row.  A row is a (token, head of the group)
+// pair, so the query heads that share a key head share its tiles.
+//
+// A CTA works on two streams, each with its S tile and its O accumulator in
+// tensor memory; while one stream's softmax runs, the tensor cores work on
+// the other.
+//   * Two row tiles (PAIR): stream i is row tile i, and every key tile is used
+//     by both.
+//   * One row tile: stream i takes every other key tile; the two (m, sum, O)
+//     are joined at the end.  For calls with at most 128 rows per key head.
+// Warps 0-3 and 4-7 are the streams' softmax, one thread per row (a warp
+// reads the quadrant of tensor memory that it may address): scores from
+// tensor memory, masked, 2^x, and P back to tensor memory as the second
+// product's A operand, over the scores' columns.  O is rescaled only when a
+// row's maximum has grown by more than 2^8 since the last rescaling (P then
+// stays below 256, exact in every type here); the division at the end cancels
+// the common factor.  Warp 8 issues the TMA copies, warp 9 the MMAs, warps
+// 10-11 clear the value rows of states that a length or a mask leaves out
+// (their weight is 0, but 0 times an infinity would not be).
+//
+// Accumulators, softmax and sums are fp32; P is rounded to bf16 for the
+// second product (a relative error of 2^-8 of single terms, the size of the
+// output's own rounding).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <cstring>
+#include <mutex>
+
+#include "attn.h"
+#include "launch.h"
+#include "tc_common.cuh"
+
+namespace sc {
+
+namespace at {
+
+constexpr int TILE = 128;              // rows of a row tile, keys of a key tile
+constexpr int BLK = TILE * 128;        // bytes of 128 rows of 64 bf16 (one 128-byte swizzled row each)
+constexpr int THREADS = 384;
+constexpr int MAX_SLOTS = 12;
+constexpr int VC = 8;                  // barriers of cleared value tiles: more than the ring holds
+constexpr float GROW = 8.f;            // log2 growth of a row's maximum that rescales O
+constexpr size_t SMEM_CAP = 227 * 1024;
+
+struct Geom {
+    int row_tiles;        // row tiles of a (sequence, key head)
+    int units;            // CTAs' row units of it: pairs of row tiles, or row tiles
+    int tb, gb, gblocks;  // tokens and group heads of a row tile; blocks of gb heads
+    int splits;           // CTAs that share a row unit's keys
+    int slots;
+    uint32_t smem;
+};
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::
+            "r"(dst),
+        "l"(reinterpret_cast<unsigned long long>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] B[smem], bf16 operands
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        ".reg .b64 db;\n"
+        "setp.ne.b32 p, %5, 0;\n"
+        "mov.b64 db, {%2, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+template <int ID, int N>
+__device__ __forceinline__ void named_sync()
+{
+    asm volatile("bar.sync %0, %1;\n" ::"n"(ID), "n"(N) : "memory");
+}
+
+// Matrix descriptors' high words: 128-byte swizzle, 8-row groups 1024 bytes
+// apart.  Low words: the start address; the second operand V is N-major, its
+// 64-column blocks BLK bytes apart.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t DESC_LO_K = 1u << 16;
+constexpr uint32_t DESC_LO_V = (uint32_t)(BLK >> 4) << 16;
+
+struct Shared {
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], vclean[VC], q_full, s_full[2], p_full[2], o_full[2];
+    uint32_t words[2][2][4];   // valid bits of a key tile, per stream, two tiles deep
+    float m[TILE], l[TILE];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+};
+
+// Shared memory: row tiles (of one row tile at least the room of its 128 x DP
+// fp32 sums, which the streams' join uses), the ring, then Shared.
+template <int DP, int PL, bool PAIR>
+constexpr int q_region()
+{
+    return (PAIR ? 2 * PL : (PL > 2 ? PL : 2)) * (DP / 64) * BLK;
+}
+
+// PL operand planes: 1 (bf16 tensors), or 3 (fp32 tensors split into three
+// bf16 planes, see attn_split.cu).
+template <int DP, int PL, bool PAIR>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, const AttnArgs a, const Geom g, const AttnPartials part,
+                   int *status, unsigned long long timeout_ns)
+{
+    constexpr int DB = DP / 64;                 // 64-column blocks of a head
+    constexpr int QT = PAIR ? 2 : 1;            // row tiles
+    constexpr int SLOT = DB * BLK;
+    constexpr int PP = PL == 1 ? 1 : 2;         // planes of P
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    Shared &sh = *reinterpret_cast<Shared *>(dyn + q_region<DP, PL, PAIR>() + g.slots * SLOT);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t q_smem = smem_u32(dyn), ring = q_smem + q_region<DP, PL, PAIR>();
+    if (q_smem & 1023u) {   // the swizzled tiles need it; there is no static shared memory before them
+        if (tid == 0) atomicExch(status, kDeviceTimeout);
+        return;
+    }
+
+    // what this CTA does
+    const int split = blockIdx.x % g.splits;
+    const int unit = (blockIdx.x / g.splits) % g.units;
+    const int nh = blockIdx.x / g.splits / g.units;
+    const int n = nh / a.Hkv, h = nh - n * a.Hkv;
+    int len = a.Tk;
+    if (a.k_len) len = max(0, min(len, a.k_len[n]));
+    const bool ragged = a.key_mask != nullptr || len < a.Tk;   // value rows to clear
+    const int tiles_all = (len + TILE - 1) / TILE;
+    const int t_begin = (int)((long long)tiles_all * split / g.splits);
+    const int nt = (int)((long long)tiles_all * (split + 1) / g.splits) - t_begin;
+
+    if (tid == 0) {
+        for (int i = 0; i < MAX_SLOTS; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < VC; ++i) mbar_init(smem_u32(&sh.vclean[i]), 2);
+        mbar_init(smem_u32(&sh.q_full), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.s_full[i]), 1);
+            mbar_init(smem_u32(&sh.p_full[i]), 4);
+            mbar_init(smem_u32(&sh.o_full[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) tc::tmem_alloc(smem_u32(&sh.tmem), 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const uint32_t t_s = tmem, t_o = tmem + 2 * TILE;   // S (and P) of stream i at t_s + 128 i, O at t_o + DP i
+
+    // A wait that runs out marks the CTA: every later wait returns at once and
+    // all loops, which are finite, run to their end.
+    volatile int *abort_flag = &sh.abort;
+    auto wait = [&](uint64_t &bar, uint32_t parity) {
+        const uint32_t b = smem_u32(&bar);
+        if (mbar_try_wait(b, parity)) return;
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait(b, parity)) {
+            if (*abort_flag) return;
+            if (global_ns() - t0 > timeout_ns) {
+                *abort_flag = 1;
+                return;
+            }
+        }
+    };
+
+    // Order of the ring's tiles, the order in which the MMAs use them: the
+    // first LAG key tiles, then value tile j and key tile j + LAG in turn.
+    constexpr int LAG = PAIR ? 1 : 2;
+    uint32_t issued = 0;   // ring entries whose copies have been issued (the copying thread's count)
+
+    if (warp == 8) {
+        if (lane == 0 && nt > 0) {
+            // row tiles: tokens and heads past the end read as zero
+            mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(QT * PL * DB * g.gb * g.tb * 128));
+            for (int i = 0; i < QT; ++i) {
+                const int rt = unit * QT + i;
+                const int tok = rt / g.gblocks * g.tb, gh = rt % g.gblocks * g.gb;
+                for (int p = 0; p < PL; ++p)
+                    for (int d = 0; d < DB; ++d)
+                        tma_load_5d(q_smem + ((i * PL + p) * DB + d) * BLK, &mq, d * 64, gh, tok, PL == 1 ? h : nh,
+                                    PL == 1 ? n : p, smem_u32(&sh.q_full));
+            }
+            // (h, n) of the tensor; 0 on an axis that all share
+            const int kh = a.ks.h ? h : 0, kn = a.ks.n ? n : 0, vh = a.vs.h ? h : 0, vn = a.vs.n ? n : 0;
+            auto load = [&](const CUtensorMap *map, int tile, int ch, int cn) {
+                for (int p = 0; p < PL; ++p, ++issued) {
+                    const uint32_t slot = issued % g.slots, round = issued / g.slots;
+                    if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
+                    if (*abort_flag) return;
+                    mbar_arrive_expect_tx(smem_u32(&sh.full[slot]), SLOT);
+                    for (int d = 0; d < DB; ++d)
+                        tma_load_5d(ring + slot * SLOT + d * BLK, map, d * 64, (t_begin + tile) * TILE, ch, cn, p,
+                                    smem_u32(&sh.full[slot]));
+                }
+            };
+            for (int j = 0; j < LAG && j < nt; ++j) load(&mk, j, kh, kn);
+            for (int j = 0; j < nt; ++j) {
+                load(&mv, j, vh, vn);
+                if (j + LAG < nt) load(&mk, j + LAG, kh, kn);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        if (lane == 0 && nt > 0) {
+            const int ksteps = (a.D + 15) / 16, nv = ksteps * 16;
+            const uint32_t idesc_s = tc::idesc_mma(1, TILE), idesc_v = tc::idesc_mma(1, nv) | (1u << 16);
+            wait(sh.q_full, 0);
+            // S of stream i from the key tile whose first plane is ring entry c
+            auto mma_s = [&](int i, uint32_t c, bool release) {
+                uint32_t acc = 0;
+                for (int pk = 0; pk < PL; ++pk) {
+                    const uint32_t slot = (c + pk) % g.slots;
+                    wait(sh.full[slot], ((c + pk) / g.slots) & 1);
+                    tc::fence_after_sync();
+                    const uint32_t kb = ring + slot * SLOT;
+                    for (int pq = 0; pq < PL - pk; ++pq) {
+                        const uint32_t qb = q_smem + ((PAIR ? i : 0) * PL + pq) * SLOT;
+                        for (int k = 0; k < ksteps; ++k) {
+                            const uint32_t off = (k >> 2) * BLK + (k & 3) * 32;
+                            tc::mma_w<tc::OpBF16>(t_s + i * TILE, ((qb + off) >> 4) | DESC_LO_K, DESC_HI,
+                                                  ((kb + off) >> 4) | DESC_LO_K, DESC_HI, idesc_s, acc);
+                            acc = 1;
+                        }
+                    }
+                    if (release) tc::mma_commit(smem_u32(&sh.empty[slot]));
+                }
+                tc::mma_commit(smem_u32(&sh.s_full[i]));
+            };
+            // O of stream i += P V; use = the stream's count of P tiles so far
+            auto mma_v = [&](int i, uint32_t c, int j, uint32_t use, bool release, bool last) {
+                wait(sh.p_full[i], use & 1);
+                if (ragged) wait(sh.vclean[j % VC], (j / VC) & 1);
+                uint32_t acc = use > 0;
+                for (int pv = 0; pv < PL; ++pv) {
+                    const uint32_t slot = (c + pv) % g.slots;
+                    wait(sh.full[slot], ((c + pv) / g.slots) & 1);
+                    tc::fence_after_sync();
+                    const uint32_t vb = ring + slot * SLOT;
+                    for (int pp = 0; pp < PP && pp < PL - pv; ++pp) {
+                        for (int k = 0; k < TILE / 16; ++k) {
+                            mma_ts(t_o + i * DP, t_s + i * TILE + pp * 64 + k * 8, ((vb + k * 2048) >> 4) | DESC_LO_V,
+                                   DESC_HI, idesc_v, acc);
+                            acc = 1;
+                        }
+                    }
+                    if (release) tc::mma_commit(smem_u32(&sh.empty[slot]));
+                }
+                if (last) tc::mma_commit(smem_u32(&sh.o_full[i]));
+            };
+            if constexpr (PAIR) {
+                mma_s(0, 0, false);
+                mma_s(1, 0, true);
+                uint32_t c = PL;
+                for (int j = 0; j < nt; ++j) {
+                    const bool more = j + 1 < nt;
+                    mma_v(0, c, j, j, false, !more);
+                    if (more) mma_s(0, c + PL, false);
+                    mma_v(1, c, j, j, true, !more);
+                    if (more) mma_s(1, c + PL, true);
+                    c += more ? 2 * PL : PL;
+                }
+            } else {
+                mma_s(0, 0, true);
+                if (nt > 1) mma_s(1, PL, true);
+                uint32_t c = nt > 1 ? 2 * PL : PL;
+                for (int j = 0; j < nt; ++j) {
+                    const bool more = j + 2 < nt;
+                    mma_v(j & 1, c, j, j >> 1, true, !more);
+                    c += PL;
+                    if (more) {
+                        mma_s(j & 1, c, true);
+                        c += PL;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 10) {
+        // value rows that are not valid: zero, in every plane and block
+        if (ragged) {
+            uint32_t c = (uint32_t)(LAG < nt ? LAG : nt) * PL;
+            const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
+            for (int j = 0; j < nt; ++j) {
+                bool bad[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int key = (t_begin + j) * TILE + (warp - 10) * 64 + i * 32 + lane;
+                    // states past Tk are not in the tensor and read as zero
+                    bad[i] = key < a.Tk && (key >= len || (mb && mb[key] == 0));
+                }
+                for (int p = 0; p < PL; ++p, ++c) {
+                    const uint32_t slot = c % g.slots;
+                    wait(sh.full[slot], (c / g.slots) & 1);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!bad[i]) continue;
+                        const uint32_t row = ring + slot * SLOT + ((warp - 10) * 64 + i * 32 + lane) * 128;
+                        for (int d = 0; d < DB; ++d)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) tc::st_shared_v4(row + d * BLK + e * 16, 0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.vclean[j % VC]));
+                if (j + LAG < nt) c += PL;
+            }
+        }
+    } else {
+        const int i = warp >> 2;                   // stream
+        const int row = (warp & 3) * 32 + lane;    // row of the tile
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = t_s + i * TILE + lanes, to = t_o + i * DP + lanes;
+        const int step = PAIR ? 1 : 2;
+        const float c = a.scale * kLog2e;
+        float m = -INFINITY, l = 0.f;   // m: maximum that P is relative to, in units of log2
+        const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
+        int use = 0;
+        for (int j = PAIR ? 0 : i; j < nt; j += step, ++use) {
+            const int key0 = (t_begin + j) * TILE;
+            uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+            bool masked = key0 + TILE > len;
+            if (mb) {
+                // one key per thread, a word per warp
+                const int key = key0 + row;
+                const uint32_t word = __ballot_sync(0xffffffffu, key < len && mb[key] != 0);
+                if (lane == 0) sh.words[i][use & 1][warp & 3] = word;
+                if (i == 0)
+                    named_sync<1, 128>();
+                else
+                    named_sync<2, 128>();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = sh.words[i][use & 1][e];
+                masked = (w[0] & w[1] & w[2] & w[3]) != ~0u;
+            } else if (masked) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int left = len - key0 - 32 * e;
+                    w[e] = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
+                }
+            }
+            wait(sh.s_full[i], use & 1);
+            tc::fence_after_sync();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tc::tmem_ld<32>(ts + e * 32, s[e]);
+            tc::tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!((w[e] >> k) & 1u)) s[e][k] = 0xff800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mx[e] = __uint_as_float(s[e][0]);
+#pragma unroll
+                for (int k = 1; k < 32; ++k) mx[e] = fmaxf(mx[e], __uint_as_float(s[e][k]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            const bool grow = top - m > GROW;   // false where both are -infinity
+            float f = 1.f;
+            if (grow) {
+                f = ex2(m - top);
+                m = top;
+                l *= f;
+            }
+            if (use > 0 && __any_sync(0xffffffffu, grow)) {
+                // the stream's last product is complete: it was issued before this S
+                for (int d = 0; d < DP; d += 32) {
+                    if (d >= a.D) break;
+                    uint32_t o[32];
+                    tc::tmem_ld<32>(to + d, o);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st32(to + d, o);
+                }
+            }
+            const float mc = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                uint32_t p0[32], p1[32];
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    const float x = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32]), c, -mc));
+                    const float y = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32 + 1]), c, -mc));
+                    sum[e + k / 32] += x;
+                    sum[(e + k / 32) ^ 1] += y;
+                    p0[k / 2] = tc::pack_bf16(x, y);
+                    if constexpr (PP == 2)
+                        p1[k / 2] = tc::pack_bf16(x - __uint_as_float(p0[k / 2] << 16),
+                                                  y - __uint_as_float(p0[k / 2] & 0xffff0000u));
+                }
+                tmem_st32(ts + e * 16, p0);
+                if constexpr (PP == 2) tmem_st32(ts + 64 + e * 16, p1);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[i]));
+        }
+        if (use > 0) {
+            wait(sh.o_full[i], 0);
+            tc::fence_after_sync();
+        }
+        // this thread's row
+        const int rt = PAIR ? unit * 2 + i : unit;
+        const int tok = rt / g.gblocks * g.tb + row / g.gb, gh = rt % g.gblocks * g.gb + row % g.gb;
+        const bool live = rt < g.row_tiles && row < g.gb * g.tb && tok < a.Tq && gh < a.G;
+        const int hq = h * a.G + gh;
+        // the joined (m, l) and the factors of the streams' O
+        float f0 = 1.f, f1 = 0.f;
+        float *stage = reinterpret_cast<float *>(dyn);
+        if constexpr (!PAIR) {
+            // stream 1 hands its sums over in the row tile's shared memory (the
+            // scores' products are complete once either stream's O is), one
+            // column of 128 rows after the other
+            if (i == 1) {
+                sh.m[row] = m;
+                sh.l[row] = l;
+                if (use > 0) {
+                    for (int d = 0; d < DP; d += 32) {
+                        if (d >= a.D) break;
+                        uint32_t o[32];
+                        tc::tmem_ld<32>(to + d, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) stage[(d + k) * TILE + row] = __uint_as_float(o[k]);
+                    }
+                }
+                named_sync<3, 256>();
+            } else {
+                named_sync<3, 256>();
+                const float m1 = sh.m[row], l1 = sh.l[row];
+                const float mm = fmaxf(m, m1), ms = mm == -INFINITY ? 0.f : mm;
+                f0 = ex2(m - ms);
+                f1 = ex2(m1 - ms);
+                l = l * f0 + l1 * f1;
+                m = mm;
+            }
+        }
+        if (PAIR || i == 0) {
+            const bool any = nt > 0, two = !PAIR && nt > 1;
+            const bool final_out = part.parts == 0;
+            const float inv = final_out ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            const long long prow = ((long long)split * a.N * a.Hkv + nh) * ((long long)a.Tq * a.G) + (long long)tok * a.G + gh;
+            for (int d = 0; d < DP; d += 32) {
+                if (d >= a.D) break;
+                uint32_t o[32];
+                if (any) {
+                    tc::tmem_ld<32>(to + d, o);
+                    tc::tmem_wait_ld();
+                }
+                float y[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    float v = any ? __uint_as_float(o[k]) * f0 : 0.f;
+                    if (two) v = fmaf(stage[(d + k) * TILE + row], f1, v);
+                    y[k] = l == 0.f ? 0.f : v * inv;
+                }
+                if (!live) continue;
+                if (final_out && PL == 1) {
+                    __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.out) + n * a.os.n + tok * a.os.t + hq * a.os.h + d;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        if (d + k < a.D)
+                            *reinterpret_cast<uint4 *>(op + k) =
+                                make_uint4(tc::pack_bf16(y[k], y[k + 1]), tc::pack_bf16(y[k + 2], y[k + 3]),
+                                           tc::pack_bf16(y[k + 4], y[k + 5]), tc::pack_bf16(y[k + 6], y[k + 7]));
+                } else {
+                    float *op = final_out ? static_cast<float *>(a.out) + n * a.os.n + tok * a.os.t + hq * a.os.h + d
+                                          : part.o + prow * a.D + d;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        if (d + k < a.D)
+                            *reinterpret_cast<float4 *>(op + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                }
+            }
+            if (live) {
+                if (!final_out)
+                    part.ml[prow] = make_float2(m, l);
+                else if (a.lse)
+                    a.lse[((long long)n * a.Hq + hq) * a.Tq + tok] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+            }
+        }
+        tc::fence_before_sync();
+    }
+    __syncthreads();
+    if (sh.abort) {
+        // give the copies and products in flight their time to end before the
+        // shared and tensor memory are given back
+        if (tid == 0) atomicExch(status, kDeviceTimeout);
+        if (warp == 8 && lane == 0 && nt > 0) {
+            (void)mbar_wait_bounded(smem_u32(&sh.q_full), 0, timeout_ns);
+            for (uint32_t e = issued > (uint32_t)g.slots ? issued - g.slots : 0; e < issued; ++e)
+                (void)mbar_wait_bounded(smem_u32(&sh.full[e % g.slots]), (e / g.slots) & 1, timeout_ns);
+        }
+        if (warp == 9 && lane == 0) {
+            tc::mma_commit(smem_u32(&sh.drain));
+            (void)mbar_wait_bounded(smem_u32(&sh.drain), 0, timeout_ns);
+        }
+        __syncthreads();
+    }
+    if (warp == 9) tc::tmem_dealloc(tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// A map of bf16 rows of D elements with four outer axes (strides in bytes).
+bool encode_map(CUtensorMap *m, const void *base, int D, const long long (&size)[4], const long long (&stride)[4],
+                int box1, int box2)
+{
+    cuuint64_t dims[5] = {(cuuint64_t)D}, strides[4];
+    for (int i = 0; i < 4; ++i) {
+        dims[i + 1] = (cuuint64_t)size[i];
+        // an axis of one element may come with any stride: the map wants a
+        // multiple of 16 above zero
+        strides[i] = size[i] == 1 ? 16 : (cuuint64_t)stride[i];
+    }
+    const cuuint32_t box[5] = {64, (cuuint32_t)box1, (cuuint32_t)box2, 1, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP, int PL, bool PAIR>
+cudaError_t launch(const AttnArgs &a, Geom g, const CUtensorMap (&maps)[3], const AttnPartials &part, cudaStream_t st)
+{
+    constexpr int SLOT = DP / 64 * BLK;
+    const size_t fixed = q_region<DP, PL, PAIR>() + sizeof(Shared);
+    g.slots = (int)((SMEM_CAP - fixed) / SLOT);
+    if (g.slots > MAX_SLOTS) g.slots = MAX_SLOTS;
+    g.smem = (uint32_t)(fixed + (size_t)g.slots * SLOT);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    static KernelCache cache;
+    e = ensure_dynamic_smem(cache, dev, attn_tc_kernel<DP, PL, PAIR>, (int)g.smem);
+    if (e != cudaSuccess) return e;
+    int *status = device_status_ptr();
+    if (!status) return cudaErrorInvalidDevice;
+    const long long grid = (long long)a.N * a.Hkv * g.units * g.splits;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    attn_tc_kernel<DP, PL, PAIR><<<(unsigned)grid, THREADS, g.smem, st>>>(maps[0], maps[1], maps[2], a, g, part, status,
+                                                                       1000000000ull);
+    return cudaGetLastError();
+}
+
+}  // namespace at
+
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st)
+{
+    if (!at::encoder()) return cudaErrorNotSupported;
+    at::Geom g = {};
+    g.gb = a.G < at::TILE ? a.G : at::TILE;
+    g.tb = at::TILE / g.gb;
+    g.gblocks = (a.G + g.gb - 1) / g.gb;
+    const long long rt = (long long)((a.Tq + g.tb - 1) / g.tb) * g.gblocks;
+    if (rt > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+    g.row_tiles = (int)rt;
+    const bool pair = g.row_tiles > 1;
+    g.units = pair ? (g.row_tiles + 1) / 2 : 1;
+    // CTAs per row unit: fill the GPU, at least four key tiles each
+    const long long blocks = (long long)a.N * a.Hkv * g.units;
+    const long long tiles = (a.Tk + at::TILE - 1) / at::TILE;
+    long long splits = device_sm_count() / blocks;
+    if (splits > tiles / 4) splits = tiles / 4;
+    if (splits < 1) splits = 1;
+    g.splits = (int)splits;
+
+    // a shared axis (stride 0) of the keys or values is one coordinate of the
+    // map; the row tiles, and key tiles, need their own axes
+    if ((a.G > 1 && a.qs.h == 0) || (a.Tq > 1 && a.qs.t == 0) || (a.Hkv > 1 && a.qs.h == 0) || (a.N > 1 && a.qs.n == 0) ||
+        (a.Tk > 1 && (a.ks.t == 0 || a.vs.t == 0)))
+        return cudaErrorNotSupported;
+    CUtensorMap maps[3];
+    {
+        const long long size[4] = {a.G, a.Tq, a.Hkv, a.N};
+        const long long stride[4] = {a.qs.h * 2, a.qs.t * 2, a.qs.h * a.G * 2, a.qs.n * 2};
+        if (!at::encode_map(&maps[0], a.q, a.D, size, stride, g.gb, g.tb)) return cudaErrorNotSupported;
+    }
+    for (int i = 0; i < 2; ++i) {
+        const HeadStrides &s = i ? a.vs : a.ks;
+        const long long size[4] = {a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1};
+        const long long stride[4] = {s.t * 2, s.h * 2, s.n * 2, 16};
+        if (!at::encode_map(&maps[1 + i], i ? a.v : a.k, a.D, size, stride, at::TILE, 1)) return cudaErrorNotSupported;
+    }
+    AttnPartials part{nullptr, nullptr, 0};
+    void *ws = nullptr;
+    if (g.splits > 1) {
+        part.parts = g.splits;
+        const size_t nrow = (size_t)g.splits * a.N * a.Hq * a.Tq;
+        const cudaError_t e = workspace_alloc(&ws, nrow * ((size_t)a.D * 4 + sizeof(float2)), st);
+        if (e != cudaSuccess) return e;
+        part.o = static_cast<float *>(ws);
+        part.ml = reinterpret_cast<float2 *>(part.o + nrow * a.D);
+    }
+    cudaError_t e;
+    if (a.D <= 64)
+        e = pair ? at::launch<64, 1, true>(a, g, maps, part, st) : at::launch<64, 1, false>(a, g, maps, part, st);
+    else
+        e = pair ? at::launch<128, 1, true>(a, g, maps, part, st) : at::launch<128, 1, false>(a, g, maps, part, st);
+    if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, true, part, st);
+    if (ws) {
+        const cudaError_t ef = workspace_free(ws, st);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e;
+}
+
+}  // namespace sc
