@@ -39,9 +39,12 @@ struct AttnPartials {
 
 // Few rows per key head: keys streamed through registers (attn_rows.cu).
 cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t st);
-// Many rows per key head, bf16: tensor cores (attn_tc.cu).
-// cudaErrorNotSupported where its copies cannot address the tensors.
-cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st);
+// Many rows per key head: tensor cores (attn_tc.cu).  cudaErrorNotSupported
+// where its copies cannot address the tensors.
+cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st);
+// The three bf16 planes of fp32 q ([plane][N][Hkv][Tq][G][D]), k and v
+// ([plane][N][Hkv][Tk][D]) (attn_split.cu).
+cudaError_t launch_attn_split(const AttnArgs &a, void *const (&planes)[3], cudaStream_t st);
 // Joins partial results into out and lse (attn_join.cu).
 cudaError_t launch_attn_join(const AttnArgs &a, bool bf16, const AttnPartials &p, cudaStream_t st);
 

@@ -278,8 +278,8 @@ int cross_attention_fwd(const void *q, const void *k, const void *v, void *out, 
     a.G = Hq / Hkv;
     a.scale = scale;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == SC_BF16 && (long long)Tq * a.G > 4) {
-        const cudaError_t e = sc::launch_attn_tc(a, st);
+    if ((long long)Tq * a.G > (dtype == SC_BF16 ? 4 : 16)) {
+        const cudaError_t e = sc::launch_attn_tc(a, dtype == SC_BF16, st);
         if (e != cudaErrorNotSupported) return from_cuda(e);
     }
     return from_cuda(sc::launch_attn_rows(a, dtype == SC_BF16, st));

@@ -1,0 +1,90 @@
+// Splits fp32 queries, keys and values into three bf16 planes for the tensor
+// cores:  x0 = bf16(x), x1 = bf16(x - x0), x2 = bf16(x - x0 - x1), so that
+// x = x0 + x1 + x2 to 24 bits (the differences are exact).  A product x y is
+// then x0 y0 + x0 y1 + x1 y0 + (x0 y2 + x1 y1 + x2 y0), the terms left out
+// below 2^-24 |x y| (bf16 has fp32's range, so nothing over- or underflows
+// that fp32 holds).  Bound by memory: 4 bytes read and 6 written an element.
+#include <cuda_bf16.h>
+
+#include "attn.h"
+#include "launch.h"
+
+namespace sc {
+
+namespace {
+
+constexpr int kSplitThreads = 256;
+
+struct SplitPart {
+    const float *x;
+    uint32_t *y;                 // bf16 planes, plane_words words apart
+    long long plane_words;
+    HeadStrides s;
+    int T, H, G;                 // rows [n][T][H] of x; written as [n][H / G][T][G]
+    long long chunks;            // rows * D / 8
+};
+
+struct SplitArgs {
+    SplitPart p[3];
+    int D8;                      // D / 8
+};
+
+__global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitArgs a)
+{
+    const SplitPart &p = a.p[blockIdx.y];
+    const long long stride = (long long)gridDim.x * kSplitThreads;
+    for (long long e = (long long)blockIdx.x * kSplitThreads + threadIdx.x; e < p.chunks; e += stride) {
+        const long long row = e / a.D8;
+        const int c = (int)(e - row * a.D8);
+        const long long nt = row / p.H;
+        const int h = (int)(row - nt * p.H), n = (int)(nt / p.T), t = (int)(nt - (long long)n * p.T);
+        const float4 *src = reinterpret_cast<const float4 *>(p.x + n * p.s.n + t * p.s.t + h * p.s.h + c * 8);
+        const float4 v0 = src[0], v1 = src[1];
+        float f[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        const long long orow = (((long long)n * (p.H / p.G) + h / p.G) * p.T + t) * p.G + h % p.G;
+        uint32_t *dst = p.y + (orow * a.D8 + c) * 4;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                f[2 * i] -= __uint_as_float(w[i] << 16);
+                f[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+            }
+            *reinterpret_cast<uint4 *>(dst + k * p.plane_words) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_split(const AttnArgs &a, void *const (&planes)[3], cudaStream_t st)
+{
+    SplitArgs s;
+    s.D8 = a.D / 8;
+    const void *x[3] = {a.q, a.k, a.v};
+    const HeadStrides hs[3] = {a.qs, a.ks, a.vs};
+    long long most = 0;
+    for (int i = 0; i < 3; ++i) {
+        SplitPart &p = s.p[i];
+        p.x = static_cast<const float *>(x[i]);
+        p.y = static_cast<uint32_t *>(planes[i]);
+        p.s = hs[i];
+        p.T = i ? a.Tk : a.Tq;
+        p.H = i ? a.Hkv : a.Hq;
+        p.G = i ? 1 : a.G;
+        const long long rows = (long long)a.N * p.T * p.H;
+        p.chunks = rows * s.D8;
+        p.plane_words = rows * a.D / 2;
+        if (p.chunks > most) most = p.chunks;
+    }
+    long long blocks = (most + kSplitThreads - 1) / kSplitThreads;
+    const long long cap = 16LL * device_sm_count();
+    if (blocks > cap) blocks = cap;
+    attn_split_kernel<<<dim3((unsigned)blocks, 3), kSplitThreads, 0, st>>>(s);
+    return cudaGetLastError();
+}
+
+}  // namespace sc

@@ -24,9 +24,15 @@
 // 10-11 clear the value rows of states that a length or a mask leaves out
 // (their weight is 0, but 0 times an infinity would not be).
 //
-// Accumulators, softmax and sums are fp32; P is rounded to bf16 for the
-// second product (a relative error of 2^-8 of single terms, the size of the
-// output's own rounding).
+// Accumulators, softmax and sums are fp32.  bf16 tensors: P is rounded to bf16
+// for the second product (a relative error of 2^-8 of single terms, the size
+// of the output's own rounding), and O stays in tensor memory.  fp32 tensors:
+// Q, K, V (attn_split.cu) and P are three bf16 planes each, a product the six
+// of planes i + j <= 2, the small ones first.  The tensor cores cut each sum
+// short instead of rounding it, and over hundreds of products into one
+// accumulator that adds up (1e-5 of the result at 3136 keys); so there O holds
+// one key tile's product at a time, which the softmax threads add to sums of
+// their own in registers.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -42,8 +48,17 @@ namespace sc {
 
 namespace at {
 
-constexpr int TILE = 128;              // rows of a row tile, keys of a key tile
+constexpr int TILE = 128;              // rows of a row tile
 constexpr int BLK = TILE * 128;        // bytes of 128 rows of 64 bf16 (one 128-byte swizzled row each)
+// Keys of a key tile.  Tensor memory of a stream (256 columns): the scores from
+// 0, the first plane of P over them, the second from keys on; the third over
+// the scores' second half (64 columns of O: read before it is written) or
+// from 3/2 keys on; O the last DP.
+template <int DP, int PL>
+constexpr int key_tile() { return PL == 3 && DP == 128 ? 64 : 128; }
+// Registers of the softmax warps and of the others, out of the 168 a thread
+// that the block is launched with (launch() checks): 8 x 216 + 4 x 72 = 12 x 168.
+constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 216, REGS_OTHER = 72;
 constexpr int THREADS = 384;
 constexpr int MAX_SLOTS = 12;
 constexpr int VC = 8;                  // barriers of cleared value tiles: more than the ring holds
@@ -95,6 +110,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 template <int ID, int N>
@@ -105,10 +126,10 @@ __device__ __forceinline__ void named_sync()
 
 // Matrix descriptors' high words: 128-byte swizzle, 8-row groups 1024 bytes
 // apart.  Low words: the start address; the second operand V is N-major, its
-// 64-column blocks BLK bytes apart.
+// 64-column blocks one block of key rows apart (desc_lo_v).
 constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t DESC_LO_K = 1u << 16;
-constexpr uint32_t DESC_LO_V = (uint32_t)(BLK >> 4) << 16;
+constexpr uint32_t desc_lo_v(int key_tile) { return (uint32_t)(key_tile * 128 >> 4) << 16; }
 
 struct Shared {
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], vclean[VC], q_full, s_full[2], p_full[2], o_full[2];
@@ -124,7 +145,7 @@ struct Shared {
 template <int DP, int PL, bool PAIR>
 constexpr int q_region()
 {
-    return (PAIR ? 2 * PL : (PL > 2 ? PL : 2)) * (DP / 64) * BLK;
+    return (PAIR ? 2 * PL : (PL > 2 ? PL : 2)) * (DP / 64) * BLK;   // a multiple of 1024
 }
 
 // PL operand planes: 1 (bf16 tensors), or 3 (fp32 tensors split into three
@@ -137,8 +158,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 {
     constexpr int DB = DP / 64;                 // 64-column blocks of a head
     constexpr int QT = PAIR ? 2 : 1;            // row tiles
-    constexpr int SLOT = DB * BLK;
-    constexpr int PP = PL == 1 ? 1 : 2;         // planes of P
+    constexpr int KT = key_tile<DP, PL>();
+    constexpr int KBLK = KT * 128;              // bytes of a key tile's rows of 64 bf16
+    constexpr int SLOT = DB * KBLK;
     extern __shared__ __align__(1024) unsigned char dyn[];
     Shared &sh = *reinterpret_cast<Shared *>(dyn + q_region<DP, PL, PAIR>() + g.slots * SLOT);
 
@@ -157,7 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int len = a.Tk;
     if (a.k_len) len = max(0, min(len, a.k_len[n]));
     const bool ragged = a.key_mask != nullptr || len < a.Tk;   // value rows to clear
-    const int tiles_all = (len + TILE - 1) / TILE;
+    const int tiles_all = (len + KT - 1) / KT;
     const int t_begin = (int)((long long)tiles_all * split / g.splits);
     const int nt = (int)((long long)tiles_all * (split + 1) / g.splits) - t_begin;
 
@@ -182,7 +204,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
-    const uint32_t t_s = tmem, t_o = tmem + 2 * TILE;   // S (and P) of stream i at t_s + 128 i, O at t_o + DP i
+    constexpr int P1 = KT, P2 = DP == 64 ? KT / 2 : KT + KT / 2, TO = 256 - DP;   // columns of a stream
+    auto p_plane = [](int p) { return p == 0 ? 0 : (p == 1 ? P1 : P2); };
 
     // A wait that runs out marks the CTA: every later wait returns at once and
     // all loops, which are finite, run to their end.
@@ -205,237 +228,334 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int LAG = PAIR ? 1 : 2;
     uint32_t issued = 0;   // ring entries whose copies have been issued (the copying thread's count)
 
-    if (warp == 8) {
-        if (lane == 0 && nt > 0) {
-            // row tiles: tokens and heads past the end read as zero
-            mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(QT * PL * DB * g.gb * g.tb * 128));
-            for (int i = 0; i < QT; ++i) {
-                const int rt = unit * QT + i;
-                const int tok = rt / g.gblocks * g.tb, gh = rt % g.gblocks * g.gb;
-                for (int p = 0; p < PL; ++p)
-                    for (int d = 0; d < DB; ++d)
-                        tma_load_5d(q_smem + ((i * PL + p) * DB + d) * BLK, &mq, d * 64, gh, tok, PL == 1 ? h : nh,
-                                    PL == 1 ? n : p, smem_u32(&sh.q_full));
-            }
-            // (h, n) of the tensor; 0 on an axis that all share
-            const int kh = a.ks.h ? h : 0, kn = a.ks.n ? n : 0, vh = a.vs.h ? h : 0, vn = a.vs.n ? n : 0;
-            auto load = [&](const CUtensorMap *map, int tile, int ch, int cn) {
-                for (int p = 0; p < PL; ++p, ++issued) {
-                    const uint32_t slot = issued % g.slots, round = issued / g.slots;
-                    if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
-                    if (*abort_flag) return;
-                    mbar_arrive_expect_tx(smem_u32(&sh.full[slot]), SLOT);
-                    for (int d = 0; d < DB; ++d)
-                        tma_load_5d(ring + slot * SLOT + d * BLK, map, d * 64, (t_begin + tile) * TILE, ch, cn, p,
-                                    smem_u32(&sh.full[slot]));
-                }
-            };
-            for (int j = 0; j < LAG && j < nt; ++j) load(&mk, j, kh, kn);
-            for (int j = 0; j < nt; ++j) {
-                load(&mv, j, vh, vn);
-                if (j + LAG < nt) load(&mk, j + LAG, kh, kn);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 9) {
-        if (lane == 0 && nt > 0) {
-            const int ksteps = (a.D + 15) / 16, nv = ksteps * 16;
-            const uint32_t idesc_s = tc::idesc_mma(1, TILE), idesc_v = tc::idesc_mma(1, nv) | (1u << 16);
-            wait(sh.q_full, 0);
-            // S of stream i from the key tile whose first plane is ring entry c
-            auto mma_s = [&](int i, uint32_t c, bool release) {
-                uint32_t acc = 0;
-                for (int pk = 0; pk < PL; ++pk) {
-                    const uint32_t slot = (c + pk) % g.slots;
-                    wait(sh.full[slot], ((c + pk) / g.slots) & 1);
-                    tc::fence_after_sync();
-                    const uint32_t kb = ring + slot * SLOT;
-                    for (int pq = 0; pq < PL - pk; ++pq) {
-                        const uint32_t qb = q_smem + ((PAIR ? i : 0) * PL + pq) * SLOT;
-                        for (int k = 0; k < ksteps; ++k) {
-                            const uint32_t off = (k >> 2) * BLK + (k & 3) * 32;
-                            tc::mma_w<tc::OpBF16>(t_s + i * TILE, ((qb + off) >> 4) | DESC_LO_K, DESC_HI,
-                                                  ((kb + off) >> 4) | DESC_LO_K, DESC_HI, idesc_s, acc);
-                            acc = 1;
-                        }
-                    }
-                    if (release) tc::mma_commit(smem_u32(&sh.empty[slot]));
-                }
-                tc::mma_commit(smem_u32(&sh.s_full[i]));
-            };
-            // O of stream i += P V; use = the stream's count of P tiles so far
-            auto mma_v = [&](int i, uint32_t c, int j, uint32_t use, bool release, bool last) {
-                wait(sh.p_full[i], use & 1);
-                if (ragged) wait(sh.vclean[j % VC], (j / VC) & 1);
-                uint32_t acc = use > 0;
-                for (int pv = 0; pv < PL; ++pv) {
-                    const uint32_t slot = (c + pv) % g.slots;
-                    wait(sh.full[slot], ((c + pv) / g.slots) & 1);
-                    tc::fence_after_sync();
-                    const uint32_t vb = ring + slot * SLOT;
-                    for (int pp = 0; pp < PP && pp < PL - pv; ++pp) {
-                        for (int k = 0; k < TILE / 16; ++k) {
-                            mma_ts(t_o + i * DP, t_s + i * TILE + pp * 64 + k * 8, ((vb + k * 2048) >> 4) | DESC_LO_V,
-                                   DESC_HI, idesc_v, acc);
-                            acc = 1;
-                        }
-                    }
-                    if (release) tc::mma_commit(smem_u32(&sh.empty[slot]));
-                }
-                if (last) tc::mma_commit(smem_u32(&sh.o_full[i]));
-            };
-            if constexpr (PAIR) {
-                mma_s(0, 0, false);
-                mma_s(1, 0, true);
-                uint32_t c = PL;
-                for (int j = 0; j < nt; ++j) {
-                    const bool more = j + 1 < nt;
-                    mma_v(0, c, j, j, false, !more);
-                    if (more) mma_s(0, c + PL, false);
-                    mma_v(1, c, j, j, true, !more);
-                    if (more) mma_s(1, c + PL, true);
-                    c += more ? 2 * PL : PL;
-                }
-            } else {
-                mma_s(0, 0, true);
-                if (nt > 1) mma_s(1, PL, true);
-                uint32_t c = nt > 1 ? 2 * PL : PL;
-                for (int j = 0; j < nt; ++j) {
-                    const bool more = j + 2 < nt;
-                    mma_v(j & 1, c, j, j >> 1, true, !more);
-                    c += PL;
-                    if (more) {
-                        mma_s(j & 1, c, true);
-                        c += PL;
-                    }
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp >= 10) {
-        // value rows that are not valid: zero, in every plane and block
-        if (ragged) {
-            uint32_t c = (uint32_t)(LAG < nt ? LAG : nt) * PL;
-            const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
-            for (int j = 0; j < nt; ++j) {
-                bool bad[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int key = (t_begin + j) * TILE + (warp - 10) * 64 + i * 32 + lane;
-                    // states past Tk are not in the tensor and read as zero
-                    bad[i] = key < a.Tk && (key >= len || (mb && mb[key] == 0));
-                }
-                for (int p = 0; p < PL; ++p, ++c) {
-                    const uint32_t slot = c % g.slots;
-                    wait(sh.full[slot], (c / g.slots) & 1);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!bad[i]) continue;
-                        const uint32_t row = ring + slot * SLOT + ((warp - 10) * 64 + i * 32 + lane) * 128;
+    if (warp >= 8) {
+        // one instruction for the four warps, as its form asks
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_OTHER));
+        if (warp == 8) {
+            if (lane == 0 && nt > 0) {
+                // row tiles: tokens and heads past the end read as zero
+                mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(QT * PL * DB * g.gb * g.tb * 128));
+                for (int i = 0; i < QT; ++i) {
+                    const int rt = unit * QT + i;
+                    const int tok = rt / g.gblocks * g.tb, gh = rt % g.gblocks * g.gb;
+                    for (int p = 0; p < PL; ++p)
                         for (int d = 0; d < DB; ++d)
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) tc::st_shared_v4(row + d * BLK + e * 16, 0u, 0u, 0u, 0u);
+                            tma_load_5d(q_smem + ((i * PL + p) * DB + d) * BLK, &mq, d * 64, gh, tok, PL == 1 ? h : nh,
+                                        PL == 1 ? n : p, smem_u32(&sh.q_full));
+                }
+                // (h, n) of the tensor; 0 on an axis that all share (the planes share none)
+                const int kh = PL > 1 || a.ks.h ? h : 0, kn = PL > 1 || a.ks.n ? n : 0;
+                const int vh = PL > 1 || a.vs.h ? h : 0, vn = PL > 1 || a.vs.n ? n : 0;
+                auto load = [&](const CUtensorMap *map, int tile, int ch, int cn) {
+                    for (int p = PL - 1; p >= 0; --p, ++issued) {   // the smallest plane first
+                        const uint32_t slot = issued % g.slots, round = issued / g.slots;
+                        if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
+                        if (*abort_flag) return;
+                        mbar_arrive_expect_tx(smem_u32(&sh.full[slot]), SLOT);
+                        for (int d = 0; d < DB; ++d)
+                            tma_load_5d(ring + slot * SLOT + d * KBLK, map, d * 64, (t_begin + tile) * KT, ch, cn, p,
+                                        smem_u32(&sh.full[slot]));
+                    }
+                };
+                for (int j = 0; j < LAG && j < nt; ++j) load(&mk, j, kh, kn);
+                for (int j = 0; j < nt; ++j) {
+                    load(&mv, j, vh, vn);
+                    if (j + LAG < nt) load(&mk, j + LAG, kh, kn);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            if (lane == 0 && nt > 0) {
+                const int ksteps = (a.D + 15) / 16, nv = ksteps * 16;
+                const uint32_t idesc_s = tc::idesc_mma(1, KT), idesc_v = tc::idesc_mma(1, nv) | (1u << 16);
+                wait(sh.q_full, 0);
+                // S of stream i from the key tile whose first plane is ring entry c
+                auto mma_s = [&](int i, uint32_t c, bool release) {
+                    uint32_t acc = 0;
+                    for (int pk = PL - 1; pk >= 0; --pk, ++c) {
+                        const uint32_t slot = c % g.slots;
+                        wait(sh.full[slot], (c / g.slots) & 1);
+                        tc::fence_after_sync();
+                        const uint32_t kb = ring + slot * SLOT;
+                        for (int pq = PL - 1 - pk; pq >= 0; --pq) {
+                            const uint32_t qb = q_smem + ((PAIR ? i : 0) * PL + pq) * DB * BLK;
+                            for (int k = 0; k < ksteps; ++k) {
+                                const uint32_t off = (k & 3) * 32;
+                                tc::mma_w<tc::OpBF16>(tmem + i * 256, ((qb + (k >> 2) * BLK + off) >> 4) | DESC_LO_K, DESC_HI,
+                                                      ((kb + (k >> 2) * KBLK + off) >> 4) | DESC_LO_K, DESC_HI, idesc_s, acc);
+                                acc = 1;
+                            }
+                        }
+                        if (release) tc::mma_commit(smem_u32(&sh.empty[slot]));
+                    }
+                    tc::mma_commit(smem_u32(&sh.s_full[i]));
+                };
+                // O of stream i = P V (fp32 tensors), or += P V; use = the stream's count of P tiles so far
+                auto mma_v = [&](int i, uint32_t c, int j, uint32_t use, bool release, bool last) {
+                    wait(sh.p_full[i], use & 1);
+                    if (ragged) wait(sh.vclean[j % VC], (j / VC) & 1);
+                    uint32_t acc = PL == 1 && use > 0;
+                    for (int pv = PL - 1; pv >= 0; --pv, ++c) {
+                        const uint32_t slot = c % g.slots;
+                        wait(sh.full[slot], (c / g.slots) & 1);
+                        tc::fence_after_sync();
+                        const uint32_t vb = ring + slot * SLOT;
+                        for (int pp = PL - 1 - pv; pp >= 0; --pp) {
+                            for (int k = 0; k < KT / 16; ++k) {
+                                mma_ts(tmem + i * 256 + TO, tmem + i * 256 + p_plane(pp) + k * 8,
+                                       ((vb + k * 2048) >> 4) | desc_lo_v(KT), DESC_HI, idesc_v, acc);
+                                acc = 1;
+                            }
+                        }
+                        if (release) tc::mma_commit(smem_u32(&sh.empty[slot]));
+                    }
+                    if (last) tc::mma_commit(smem_u32(&sh.o_full[i]));
+                };
+                if constexpr (PAIR) {
+                    mma_s(0, 0, false);
+                    mma_s(1, 0, true);
+                    uint32_t c = PL;
+                    for (int j = 0; j < nt; ++j) {
+                        const bool more = j + 1 < nt;
+                        mma_v(0, c, j, j, false, !more);
+                        if (more) mma_s(0, c + PL, false);
+                        mma_v(1, c, j, j, true, !more);
+                        if (more) mma_s(1, c + PL, true);
+                        c += more ? 2 * PL : PL;
+                    }
+                } else {
+                    mma_s(0, 0, true);
+                    if (nt > 1) mma_s(1, PL, true);
+                    uint32_t c = nt > 1 ? 2 * PL : PL;
+                    for (int j = 0; j < nt; ++j) {
+                        const bool more = j + 2 < nt;
+                        mma_v(j & 1, c, j, j >> 1, true, !more);
+                        c += PL;
+                        if (more) {
+                            mma_s(j & 1, c, true);
+                            c += PL;
+                        }
                     }
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.vclean[j % VC]));
-                if (j + LAG < nt) c += PL;
+            }
+            __syncwarp();
+        } else {
+            // value rows that are not valid: zero, in every plane and block
+            if (ragged) {
+                // every entry of the ring is waited for in turn, the key tiles' too: a
+                // barrier's parity tells a round only from its neighbours
+                uint32_t c = 0;
+                auto pass = [&]() {
+                    for (int p = 0; p < PL; ++p, ++c) wait(sh.full[c % g.slots], (c / g.slots) & 1);
+                };
+                for (int j = 0; j < LAG && j < nt; ++j) pass();
+                const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
+                constexpr int KW = KT / 64;   // keys of a lane: two warps share the tile
+                for (int j = 0; j < nt; ++j) {
+                    const int row0 = (warp - 10) * 32 * KW + lane;
+                    bool bad[KW];
+    #pragma unroll
+                    for (int i = 0; i < KW; ++i) {
+                        const int key = (t_begin + j) * KT + row0 + i * 32;
+                        // states past Tk are not in the tensor and read as zero
+                        bad[i] = key < a.Tk && (key >= len || (mb && mb[key] == 0));
+                    }
+                    for (int p = 0; p < PL; ++p, ++c) {
+                        const uint32_t slot = c % g.slots;
+                        wait(sh.full[slot], (c / g.slots) & 1);
+    #pragma unroll
+                        for (int i = 0; i < KW; ++i) {
+                            if (!bad[i]) continue;
+                            const uint32_t at = ring + slot * SLOT + (row0 + i * 32) * 128;
+                            for (int d = 0; d < DB; ++d)
+    #pragma unroll
+                                for (int e = 0; e < 8; ++e) tc::st_shared_v4(at + d * KBLK + e * 16, 0u, 0u, 0u, 0u);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.vclean[j % VC]));
+                    if (j + LAG < nt) pass();
+                }
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS_SOFTMAX));
         const int i = warp >> 2;                   // stream
         const int row = (warp & 3) * 32 + lane;    // row of the tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = t_s + i * TILE + lanes, to = t_o + i * DP + lanes;
+        const uint32_t ts = tmem + i * 256 + lanes, to = ts + TO;
         const int step = PAIR ? 1 : 2;
         const float c = a.scale * kLog2e;
         float m = -INFINITY, l = 0.f;   // m: maximum that P is relative to, in units of log2
+        float acc[PL == 3 ? DP : 1];    // fp32 tensors: the row's sums, relative to m
+#pragma unroll
+        for (int d = 0; d < (PL == 3 ? DP : 1); ++d) acc[d] = 0.f;
         const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
+        constexpr int KW = KT / 32;     // words of a tile's valid bits
         int use = 0;
+        // 32 scores from column 32 e; those that are not valid become -infinity
+        auto load_scores = [&](int e, uint32_t (&s)[32], uint32_t w, bool masked) {
+            tc::tmem_ld<32>(ts + e * 32, s);
+            tc::tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    if (!((w >> k) & 1u)) s[k] = 0xff800000u;
+            }
+        };
         for (int j = PAIR ? 0 : i; j < nt; j += step, ++use) {
-            const int key0 = (t_begin + j) * TILE;
-            uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
-            bool masked = key0 + TILE > len;
+            const int key0 = (t_begin + j) * KT;
+            uint32_t w[KW];
+#pragma unroll
+            for (int e = 0; e < KW; ++e) w[e] = ~0u;
+            bool masked = key0 + KT > len;
             if (mb) {
                 // one key per thread, a word per warp
                 const int key = key0 + row;
-                const uint32_t word = __ballot_sync(0xffffffffu, key < len && mb[key] != 0);
+                const uint32_t word = __ballot_sync(0xffffffffu, row < KT && key < len && mb[key] != 0);
                 if (lane == 0) sh.words[i][use & 1][warp & 3] = word;
                 if (i == 0)
                     named_sync<1, 128>();
                 else
                     named_sync<2, 128>();
+                uint32_t all = ~0u;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = sh.words[i][use & 1][e];
-                masked = (w[0] & w[1] & w[2] & w[3]) != ~0u;
+                for (int e = 0; e < KW; ++e) {
+                    w[e] = sh.words[i][use & 1][e];
+                    all &= w[e];
+                }
+                masked = all != ~0u;
             } else if (masked) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < KW; ++e) {
                     const int left = len - key0 - 32 * e;
                     w[e] = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
                 }
             }
             wait(sh.s_full[i], use & 1);
             tc::fence_after_sync();
-            uint32_t s[4][32];
+            if constexpr (PL == 1) {
+                uint32_t s[4][32];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) tc::tmem_ld<32>(ts + e * 32, s[e]);
-            tc::tmem_wait_ld();
-            if (masked) {
+                for (int e = 0; e < 4; ++e) tc::tmem_ld<32>(ts + e * 32, s[e]);
+                tc::tmem_wait_ld();
+                if (masked) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!((w[e] >> k) & 1u)) s[e][k] = 0xff800000u;
-            }
-            float mx[4];
+                        for (int k = 0; k < 32; ++k)
+                            if (!((w[e] >> k) & 1u)) s[e][k] = 0xff800000u;
+                }
+                float mx[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                mx[e] = __uint_as_float(s[e][0]);
+                for (int e = 0; e < 4; ++e) {
+                    mx[e] = __uint_as_float(s[e][0]);
 #pragma unroll
-                for (int k = 1; k < 32; ++k) mx[e] = fmaxf(mx[e], __uint_as_float(s[e][k]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            const bool grow = top - m > GROW;   // false where both are -infinity
-            float f = 1.f;
-            if (grow) {
-                f = ex2(m - top);
+                    for (int k = 1; k < 32; ++k) mx[e] = fmaxf(mx[e], __uint_as_float(s[e][k]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const bool grow = top - m > GROW;   // false where both are -infinity
+                float f = 1.f;
+                if (grow) {
+                    f = ex2(m - top);
+                    m = top;
+                    l *= f;
+                }
+                if (use > 0 && __any_sync(0xffffffffu, grow)) {
+                    // the stream's last product is complete: it was issued before this S
+                    for (int d = 0; d < DP; d += 32) {
+                        if (d >= a.D) break;
+                        uint32_t o[32];
+                        tc::tmem_ld<32>(to + d, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st32(to + d, o);
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int k = 0; k < 64; k += 2) {
+                        const float x = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32]), c, -mc));
+                        const float y = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32 + 1]), c, -mc));
+                        sum[e + k / 32] += x;
+                        sum[(e + k / 32) ^ 1] += y;
+                        p[k / 2] = tc::pack_bf16(x, y);
+                    }
+                    tmem_st32(ts + e * 16, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            } else {
+                // the scores' second half stays in registers where P's third
+                // plane is written over it
+                constexpr int HOLD = DP == 64 ? KW / 2 : 0;
+                uint32_t hold[HOLD > 0 ? HOLD : 1][32];
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < KW; ++e) {
+                    uint32_t s[32];
+                    load_scores(e, s, w[e], masked);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        top = fmaxf(top, __uint_as_float(s[k]));
+                        if (e >= KW - HOLD) hold[e - (KW - HOLD)][k] = s[k];
+                    }
+                }
+                top = fmaxf(top * c, m);
+                const float mc = top == -INFINITY ? 0.f : top, f = ex2(m - mc);   // 1 or less; 0 at the first scores
                 m = top;
-                l *= f;
-            }
-            if (use > 0 && __any_sync(0xffffffffu, grow)) {
-                // the stream's last product is complete: it was issued before this S
-                for (int d = 0; d < DP; d += 32) {
-                    if (d >= a.D) break;
-                    uint32_t o[32];
-                    tc::tmem_ld<32>(to + d, o);
-                    tc::tmem_wait_ld();
+                // the last tile's product, relative to the last maximum; it is
+                // complete: it was issued before this S
+                if (use > 0) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                    tmem_st32(to + d, o);
+                    for (int d = 0; d < DP; d += 16) {
+                        if (d < a.D) {
+                            uint32_t o[16];
+                            tc::tmem_ld<16>(to + d, o);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) acc[d + k] = (acc[d + k] + __uint_as_float(o[k])) * f;
+                        }
+                    }
                 }
-            }
-            const float mc = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                uint32_t p0[32], p1[32];
+                for (int e = 0; e < KW; ++e) {
+                    uint32_t s[32];
+                    if (e < KW - HOLD) {
+                        load_scores(e, s, w[e], masked);
+                    } else {
 #pragma unroll
-                for (int k = 0; k < 64; k += 2) {
-                    const float x = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32]), c, -mc));
-                    const float y = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32 + 1]), c, -mc));
-                    sum[e + k / 32] += x;
-                    sum[(e + k / 32) ^ 1] += y;
-                    p0[k / 2] = tc::pack_bf16(x, y);
-                    if constexpr (PP == 2)
-                        p1[k / 2] = tc::pack_bf16(x - __uint_as_float(p0[k / 2] << 16),
-                                                  y - __uint_as_float(p0[k / 2] & 0xffff0000u));
+                        for (int k = 0; k < 32; ++k) s[k] = hold[HOLD > 0 ? e - (KW - HOLD) : 0][k];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 32; q += 16) {
+                        uint32_t p0[8], p1[8], p2[8];
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            float x = ex2(fmaf(__uint_as_float(s[q + k]), c, -mc));
+                            float y = ex2(fmaf(__uint_as_float(s[q + k + 1]), c, -mc));
+                            sum[0] += x;
+                            sum[1] += y;
+                            p0[k / 2] = tc::pack_bf16(x, y);
+                            x -= __uint_as_float(p0[k / 2] << 16);
+                            y -= __uint_as_float(p0[k / 2] & 0xffff0000u);
+                            p1[k / 2] = tc::pack_bf16(x, y);
+                            p2[k / 2] = tc::pack_bf16(x - __uint_as_float(p1[k / 2] << 16),
+                                                      y - __uint_as_float(p1[k / 2] & 0xffff0000u));
+                        }
+                        tmem_st8(ts + (32 * e + q) / 2, p0);
+                        tmem_st8(ts + P1 + (32 * e + q) / 2, p1);
+                        tmem_st8(ts + P2 + (32 * e + q) / 2, p2);
+                    }
                 }
-                tmem_st32(ts + e * 16, p0);
-                if constexpr (PP == 2) tmem_st32(ts + 64 + e * 16, p1);
+                l = l * f + (sum[0] + sum[1]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_wait_st();
             tc::fence_before_sync();
             __syncwarp();
@@ -445,6 +565,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             wait(sh.o_full[i], 0);
             tc::fence_after_sync();
         }
+        // 32 of the row's sums, from column d
+        auto row_sums = [&](int d, float (&y)[32]) {
+            uint32_t o[32];
+            tc::tmem_ld<32>(to + d, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) + (PL == 3 ? acc[PL == 3 ? d + k : 0] : 0.f);
+        };
         // this thread's row
         const int rt = PAIR ? unit * 2 + i : unit;
         const int tok = rt / g.gblocks * g.tb + row / g.gb, gh = rt % g.gblocks * g.gb + row % g.gb;
@@ -461,13 +589,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 sh.m[row] = m;
                 sh.l[row] = l;
                 if (use > 0) {
-                    for (int d = 0; d < DP; d += 32) {
-                        if (d >= a.D) break;
-                        uint32_t o[32];
-                        tc::tmem_ld<32>(to + d, o);
-                        tc::tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) stage[(d + k) * TILE + row] = __uint_as_float(o[k]);
+                    for (int d = 0; d < DP; d += 32) {
+                        if (d < a.D) {
+                            float y[32];
+                            row_sums(d, y);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) stage[(d + k) * TILE + row] = y[k];
+                        }
                     }
                 }
                 named_sync<3, 256>();
@@ -486,17 +615,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool final_out = part.parts == 0;
             const float inv = final_out ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
             const long long prow = ((long long)split * a.N * a.Hkv + nh) * ((long long)a.Tq * a.G) + (long long)tok * a.G + gh;
+#pragma unroll
             for (int d = 0; d < DP; d += 32) {
-                if (d >= a.D) break;
-                uint32_t o[32];
-                if (any) {
-                    tc::tmem_ld<32>(to + d, o);
-                    tc::tmem_wait_ld();
-                }
+                if (d >= a.D) continue;
                 float y[32];
+                if (any) {
+                    row_sums(d, y);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) y[k] = 0.f;
+                }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    float v = any ? __uint_as_float(o[k]) * f0 : 0.f;
+                    float v = y[k] * f0;
                     if (two) v = fmaf(stage[(d + k) * TILE + row], f1, v);
                     y[k] = l == 0.f ? 0.f : v * inv;
                 }
@@ -582,7 +713,7 @@ bool encode_map(CUtensorMap *m, const void *base, int D, const long long (&size)
 template <int DP, int PL, bool PAIR>
 cudaError_t launch(const AttnArgs &a, Geom g, const CUtensorMap (&maps)[3], const AttnPartials &part, cudaStream_t st)
 {
-    constexpr int SLOT = DP / 64 * BLK;
+    constexpr int SLOT = DP / 64 * key_tile<DP, PL>() * 128;
     const size_t fixed = q_region<DP, PL, PAIR>() + sizeof(Shared);
     g.slots = (int)((SMEM_CAP - fixed) / SLOT);
     if (g.slots > MAX_SLOTS) g.slots = MAX_SLOTS;
@@ -594,6 +725,12 @@ cudaError_t launch(const AttnArgs &a, Geom g, const CUtensorMap (&maps)[3], cons
     static KernelCache cache;
     e = ensure_dynamic_smem(cache, dev, attn_tc_kernel<DP, PL, PAIR>, (int)g.smem);
     if (e != cudaSuccess) return e;
+    // the register split is of REGS_LAUNCH a thread: with fewer, a warp would wait for registers that never come
+    static const int regs = [] {
+        cudaFuncAttributes fa = {};
+        return cudaFuncGetAttributes(&fa, attn_tc_kernel<DP, PL, PAIR>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs != REGS_LAUNCH) return cudaErrorNotSupported;
     int *status = device_status_ptr();
     if (!status) return cudaErrorInvalidDevice;
     const long long grid = (long long)a.N * a.Hkv * g.units * g.splits;
@@ -605,9 +742,14 @@ cudaError_t launch(const AttnArgs &a, Geom g, const CUtensorMap (&maps)[3], cons
 
 }  // namespace at
 
-cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st)
+cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
 {
     if (!at::encoder()) return cudaErrorNotSupported;
+    // a shared axis (stride 0) of bf16 keys or values is one coordinate of the
+    // map; the row tiles, and key tiles, need their own axes
+    if (bf16 && ((a.G > 1 && a.qs.h == 0) || (a.Tq > 1 && a.qs.t == 0) || (a.Hkv > 1 && a.qs.h == 0) ||
+                 (a.N > 1 && a.qs.n == 0) || (a.Tk > 1 && (a.ks.t == 0 || a.vs.t == 0))))
+        return cudaErrorNotSupported;
     at::Geom g = {};
     g.gb = a.G < at::TILE ? a.G : at::TILE;
     g.tb = at::TILE / g.gb;
@@ -615,49 +757,70 @@ cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st)
     const long long rt = (long long)((a.Tq + g.tb - 1) / g.tb) * g.gblocks;
     if (rt > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
     g.row_tiles = (int)rt;
-    const bool pair = g.row_tiles > 1;
-    g.units = pair ? (g.row_tiles + 1) / 2 : 1;
+    // two row tiles of three planes of 128 columns do not fit in shared memory
+    const bool pair = g.row_tiles > 1 && (bf16 || a.D <= 64);
+    g.units = pair ? (g.row_tiles + 1) / 2 : g.row_tiles;
     // CTAs per row unit: fill the GPU, at least four key tiles each
     const long long blocks = (long long)a.N * a.Hkv * g.units;
-    const long long tiles = (a.Tk + at::TILE - 1) / at::TILE;
+    const int kt = bf16 ? at::key_tile<64, 1>() : (a.D <= 64 ? at::key_tile<64, 3>() : at::key_tile<128, 3>());
+    const long long tiles = (a.Tk + kt - 1) / kt;
     long long splits = device_sm_count() / blocks;
     if (splits > tiles / 4) splits = tiles / 4;
     if (splits < 1) splits = 1;
     g.splits = (int)splits;
 
-    // a shared axis (stride 0) of the keys or values is one coordinate of the
-    // map; the row tiles, and key tiles, need their own axes
-    if ((a.G > 1 && a.qs.h == 0) || (a.Tq > 1 && a.qs.t == 0) || (a.Hkv > 1 && a.qs.h == 0) || (a.N > 1 && a.qs.n == 0) ||
-        (a.Tk > 1 && (a.ks.t == 0 || a.vs.t == 0)))
-        return cudaErrorNotSupported;
-    CUtensorMap maps[3];
-    {
-        const long long size[4] = {a.G, a.Tq, a.Hkv, a.N};
-        const long long stride[4] = {a.qs.h * 2, a.qs.t * 2, a.qs.h * a.G * 2, a.qs.n * 2};
-        if (!at::encode_map(&maps[0], a.q, a.D, size, stride, g.gb, g.tb)) return cudaErrorNotSupported;
-    }
-    for (int i = 0; i < 2; ++i) {
-        const HeadStrides &s = i ? a.vs : a.ks;
-        const long long size[4] = {a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1};
-        const long long stride[4] = {s.t * 2, s.h * 2, s.n * 2, 16};
-        if (!at::encode_map(&maps[1 + i], i ? a.v : a.k, a.D, size, stride, at::TILE, 1)) return cudaErrorNotSupported;
+    // workspace: partial results, and the planes of fp32 tensors
+    const int planes = bf16 ? 1 : 3;
+    const long long rows = (long long)a.N * a.Hq * a.Tq, keys = (long long)a.N * a.Hkv * a.Tk;
+    auto pad = [](size_t b) { return (b + 255) & ~(size_t)255; };
+    const size_t po = g.splits > 1 ? pad((size_t)g.splits * rows * a.D * 4) : 0;
+    const size_t pml = g.splits > 1 ? pad((size_t)g.splits * rows * sizeof(float2)) : 0;
+    const size_t pq = bf16 ? 0 : pad((size_t)rows * a.D * 6), pk = bf16 ? 0 : pad((size_t)keys * a.D * 6);
+    char *ws = nullptr;
+    if (po + pml + pq + pk > 0) {
+        const cudaError_t e = workspace_alloc(reinterpret_cast<void **>(&ws), po + pml + pq + 2 * pk, st);
+        if (e != cudaSuccess) return e;
     }
     AttnPartials part{nullptr, nullptr, 0};
-    void *ws = nullptr;
-    if (g.splits > 1) {
-        part.parts = g.splits;
-        const size_t nrow = (size_t)g.splits * a.N * a.Hq * a.Tq;
-        const cudaError_t e = workspace_alloc(&ws, nrow * ((size_t)a.D * 4 + sizeof(float2)), st);
-        if (e != cudaSuccess) return e;
-        part.o = static_cast<float *>(ws);
-        part.ml = reinterpret_cast<float2 *>(part.o + nrow * a.D);
+    if (g.splits > 1) part = AttnPartials{reinterpret_cast<float *>(ws), reinterpret_cast<float2 *>(ws + po), g.splits};
+    void *const plane[3] = {ws + po + pml, ws + po + pml + pq, ws + po + pml + pq + pk};
+
+    CUtensorMap maps[3];
+    bool ok;
+    if (bf16) {
+        const long long size[4] = {a.G, a.Tq, a.Hkv, a.N};
+        const long long stride[4] = {a.qs.h * 2, a.qs.t * 2, a.qs.h * a.G * 2, a.qs.n * 2};
+        ok = at::encode_map(&maps[0], a.q, a.D, size, stride, g.gb, g.tb);
+    } else {
+        const long long size[4] = {a.G, a.Tq, (long long)a.N * a.Hkv, planes}, d = a.D * 2LL;
+        const long long stride[4] = {d, d * a.G, d * a.G * a.Tq, d * rows};
+        ok = at::encode_map(&maps[0], plane[0], a.D, size, stride, g.gb, g.tb);
     }
-    cudaError_t e;
-    if (a.D <= 64)
-        e = pair ? at::launch<64, 1, true>(a, g, maps, part, st) : at::launch<64, 1, false>(a, g, maps, part, st);
-    else
-        e = pair ? at::launch<128, 1, true>(a, g, maps, part, st) : at::launch<128, 1, false>(a, g, maps, part, st);
-    if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, true, part, st);
+    for (int i = 0; i < 2 && ok; ++i) {
+        if (bf16) {
+            const HeadStrides &s = i ? a.vs : a.ks;
+            const long long size[4] = {a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1};
+            const long long stride[4] = {s.t * 2, s.h * 2, s.n * 2, 16};
+            ok = at::encode_map(&maps[1 + i], i ? a.v : a.k, a.D, size, stride, kt, 1);
+        } else {
+            const long long size[4] = {a.Tk, a.Hkv, a.N, planes}, d = a.D * 2LL;
+            const long long stride[4] = {d, d * a.Tk, d * a.Tk * a.Hkv, d * keys};
+            ok = at::encode_map(&maps[1 + i], plane[1 + i], a.D, size, stride, kt, 1);
+        }
+    }
+    cudaError_t e = ok ? cudaSuccess : cudaErrorNotSupported;
+    if (e == cudaSuccess && !bf16) e = launch_attn_split(a, plane, st);
+    if (e == cudaSuccess) {
+        if (bf16 && a.D <= 64)
+            e = pair ? at::launch<64, 1, true>(a, g, maps, part, st) : at::launch<64, 1, false>(a, g, maps, part, st);
+        else if (bf16)
+            e = pair ? at::launch<128, 1, true>(a, g, maps, part, st) : at::launch<128, 1, false>(a, g, maps, part, st);
+        else if (a.D <= 64)
+            e = pair ? at::launch<64, 3, true>(a, g, maps, part, st) : at::launch<64, 3, false>(a, g, maps, part, st);
+        else
+            e = at::launch<128, 3, false>(a, g, maps, part, st);
+    }
+    if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st);
     if (ws) {
         const cudaError_t ef = workspace_free(ws, st);
         if (e == cudaSuccess) e = ef;

@@ -236,25 +236,34 @@ cudaError_t launch_rot_v(const RotaryArgs &a, cudaStream_t st)
 
 // Pair i of a position p is turned by p f_i, f_i = base^(-i / pairs) changed by
 // the scaling rule.  All in 64 bits, rounded once: at positions of 10^5 and
-// more a 32-bit product p f_i would be off by 10^-3 radians.
-__global__ void rotary_table_kernel(const RotaryTableArgs a)
+// more a 32-bit product p f_i would be off by 10^-3 radians.  The angle is
+// counted in turns, whose whole part is dropped before the sine; a thread has
+// one pair and kTablePos positions, so that a power is taken once for them.
+constexpr int kTablePos = 16;
+
+__global__ void __launch_bounds__(256) rotary_table_kernel(const RotaryTableArgs a)
 {
     const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const long long total = (long long)a.positions * a.pairs;
-    if (e >= total) return;
-    const int pos = (int)(e / a.pairs), i = (int)(e - (long long)pos * a.pairs);
-    double f = pow(a.base, -(double)i / (double)a.pairs), magnitude = 1.0;
+    const long long p0 = e / a.pairs * kTablePos;
+    const int i = (int)(e % a.pairs);
+    if (p0 >= a.positions) return;
+    const double two_pi = 6.283185307179586476925;
+    double f = pow(a.base, -(double)i / (double)a.pairs) / two_pi, magnitude = 1.0;
     if (a.rule == 1) {
         f /= a.factor;
     } else if (a.rule == 3) {
-        const double turns = a.original * f / 6.283185307179586476925;
-        const double keep = fmin(fmax((turns - 1.0) / 31.0, 0.0), 1.0);
+        const double keep = fmin(fmax((a.original * f - 1.0) / 31.0, 0.0), 1.0);
         f = f * keep + f / a.factor * (1.0 - keep);
         magnitude = 0.1 * log(a.factor) + 1.0;
     }
-    double s, c;
-    sincos((double)pos * f, &s, &c);
-    reinterpret_cast<float2 *>(a.table)[e] = make_float2((float)(c * magnitude), (float)(s * magnitude));
+    const int n = (int)min((long long)kTablePos, a.positions - p0);
+    for (int k = 0; k < n; ++k) {
+        const double turns = (double)(p0 + k) * f;
+        double s, c;
+        sincospi(2.0 * (turns - rint(turns)), &s, &c);
+        reinterpret_cast<float2 *>(a.table)[(p0 + k) * a.pairs + i] =
+            make_float2((float)(c * magnitude), (float)(s * magnitude));
+    }
 }
 
 }  // namespace
@@ -270,7 +279,7 @@ cudaError_t launch_rotary(const RotaryArgs &a, bool bf16, cudaStream_t st)
 
 cudaError_t launch_rotary_table(const RotaryTableArgs &a, cudaStream_t st)
 {
-    const long long total = (long long)a.positions * a.pairs;
+    const long long total = ((long long)a.positions + kTablePos - 1) / kTablePos * a.pairs;
     const long long blocks = (total + 255) / 256;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     rotary_table_kernel<<<(unsigned)blocks, 256, 0, st>>>(a);
