@@ -84,18 +84,64 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
-// D[tmem] (+)= A[tmem] B[smem], bf16 operands
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc)
+// One thread of the warp (elect.sync).  The MMA warp runs its loops whole and
+// predicates each instruction on this, so that the descriptors stay in uniform
+// registers: issued from a branch of one lane, each product took some 130
+// clocks to issue, twice what it takes to run.
+__device__ __forceinline__ uint32_t elect_one()
 {
+    uint32_t one;
     asm volatile(
         "{\n"
         ".reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(one));
+    return one;
+}
+
+// D[tmem] (+)= A[smem] B[smem] and D[tmem] (+)= A[tmem] B[smem], bf16 operands
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        ".reg .b64 da, db;\n"
+        "setp.ne.b32 p, %6, 0;\n"
+        "setp.ne.b32 q, %7, 0;\n"
+        "mov.b64 da, {%1, %2};\n"
+        "mov.b64 db, {%3, %4};\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n"
+        "}\n" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t acc)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
         ".reg .b64 db;\n"
         "setp.ne.b32 p, %5, 0;\n"
+        "setp.ne.b32 q, %6, 0;\n"
         "mov.b64 db, {%2, %3};\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n"
         "}\n" ::"r"(d),
-        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t one, uint32_t bar)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred q;\n"
+        "setp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+        "}\n" ::"r"(bar),
+        "r"(one)
         : "memory");
 }
 
@@ -164,7 +210,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ __align__(1024) unsigned char dyn[];
     Shared &sh = *reinterpret_cast<Shared *>(dyn + q_region<DP, PL, PAIR>() + g.slots * SLOT);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (the shuffle makes the warp's number, and all that follows from it, uniform)
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t q_smem = smem_u32(dyn), ring = q_smem + q_region<DP, PL, PAIR>();
     if (q_smem & 1023u) {   // the swizzled tiles need it; there is no static shared memory before them
         if (tid == 0) atomicExch(status, kDeviceTimeout);
@@ -203,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
     constexpr int P1 = KT, P2 = DP == 64 ? KT / 2 : KT + KT / 2, TO = 256 - DP;   // columns of a stream
     auto p_plane = [](int p) { return p == 0 ? 0 : (p == 1 ? P1 : P2); };
 
@@ -265,53 +312,53 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
         } else if (warp == 9) {
-            if (lane == 0 && nt > 0) {
-                const int ksteps = (a.D + 15) / 16, nv = ksteps * 16;
-                const uint32_t idesc_s = tc::idesc_mma(1, KT), idesc_v = tc::idesc_mma(1, nv) | (1u << 16);
+            if (nt > 0) {
+                const uint32_t one = elect_one();
+                const uint32_t idesc_s = tc::idesc_mma(1, KT), idesc_v = tc::idesc_mma(1, (a.D + 15) / 16 * 16) | (1u << 16);
                 wait(sh.q_full, 0);
                 // S of stream i from the key tile whose first plane is ring entry c
                 auto mma_s = [&](int i, uint32_t c, bool release) {
-                    uint32_t acc = 0;
+#pragma unroll
                     for (int pk = PL - 1; pk >= 0; --pk, ++c) {
                         const uint32_t slot = c % g.slots;
                         wait(sh.full[slot], (c / g.slots) & 1);
                         tc::fence_after_sync();
-                        const uint32_t kb = ring + slot * SLOT;
+                        const uint32_t kb = ((ring + slot * SLOT) >> 4) | DESC_LO_K;
+#pragma unroll
                         for (int pq = PL - 1 - pk; pq >= 0; --pq) {
-                            const uint32_t qb = q_smem + ((PAIR ? i : 0) * PL + pq) * DB * BLK;
-                            for (int k = 0; k < ksteps; ++k) {
-                                const uint32_t off = (k & 3) * 32;
-                                tc::mma_w<tc::OpBF16>(tmem + i * 256, ((qb + (k >> 2) * BLK + off) >> 4) | DESC_LO_K, DESC_HI,
-                                                      ((kb + (k >> 2) * KBLK + off) >> 4) | DESC_LO_K, DESC_HI, idesc_s, acc);
-                                acc = 1;
-                            }
+                            const uint32_t qb = ((q_smem + ((PAIR ? i : 0) * PL + pq) * DB * BLK) >> 4) | DESC_LO_K;
+#pragma unroll
+                            for (int k = 0; k < DP / 16; ++k)
+                                if (k * 16 < a.D)
+                                    mma_ss(one, tmem + i * 256, qb + ((k >> 2) * BLK + (k & 3) * 32) / 16, DESC_HI,
+                                           kb + ((k >> 2) * KBLK + (k & 3) * 32) / 16, DESC_HI, idesc_s,
+                                           pk != PL - 1 || pq != PL - 1 - pk || k > 0);
                         }
-                        if (release) tc::mma_commit(smem_u32(&sh.empty[slot]));
+                        if (release) mma_commit(one, smem_u32(&sh.empty[slot]));
                     }
-                    tc::mma_commit(smem_u32(&sh.s_full[i]));
+                    mma_commit(one, smem_u32(&sh.s_full[i]));
                 };
                 // O of stream i = P V (fp32 tensors), or += P V; use = the stream's count of P tiles so far
                 auto mma_v = [&](int i, uint32_t c, int j, uint32_t use, bool release, bool last) {
                     wait(sh.p_full[i], use & 1);
                     if (ragged) wait(sh.vclean[j % VC], (j / VC) & 1);
-                    uint32_t acc = PL == 1 && use > 0;
+#pragma unroll
                     for (int pv = PL - 1; pv >= 0; --pv, ++c) {
                         const uint32_t slot = c % g.slots;
                         wait(sh.full[slot], (c / g.slots) & 1);
                         tc::fence_after_sync();
-                        const uint32_t vb = ring + slot * SLOT;
-                        for (int pp = PL - 1 - pv; pp >= 0; --pp) {
-                            for (int k = 0; k < KT / 16; ++k) {
-                                mma_ts(tmem + i * 256 + TO, tmem + i * 256 + p_plane(pp) + k * 8,
-                                       ((vb + k * 2048) >> 4) | desc_lo_v(KT), DESC_HI, idesc_v, acc);
-                                acc = 1;
-                            }
-                        }
-                        if (release) tc::mma_commit(smem_u32(&sh.empty[slot]));
+                        const uint32_t vb = ((ring + slot * SLOT) >> 4) | desc_lo_v(KT);
+#pragma unroll
+                        for (int pp = PL - 1 - pv; pp >= 0; --pp)
+#pragma unroll
+                            for (int k = 0; k < KT / 16; ++k)
+                                mma_ts(one, tmem + i * 256 + TO, tmem + i * 256 + p_plane(pp) + k * 8, vb + k * 128, DESC_HI,
+                                       idesc_v, pv != PL - 1 || pp != PL - 1 - pv || k > 0 || (PL == 1 && use > 0));
+                        if (release) mma_commit(one, smem_u32(&sh.empty[slot]));
                     }
-                    if (last) tc::mma_commit(smem_u32(&sh.o_full[i]));
+                    if (last) mma_commit(one, smem_u32(&sh.o_full[i]));
                 };
-                if constexpr (PAIR) {
+            if constexpr (PAIR) {
                     mma_s(0, 0, false);
                     mma_s(1, 0, true);
                     uint32_t c = PL;
