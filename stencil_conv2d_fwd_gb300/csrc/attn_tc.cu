@@ -164,6 +164,14 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+// The largest of three, one instruction at the rate of a maximum of two.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 template <int ID, int N>
 __device__ __forceinline__ void named_sync()
 {
@@ -178,7 +186,7 @@ constexpr uint32_t DESC_LO_K = 1u << 16;
 constexpr uint32_t desc_lo_v(int key_tile) { return (uint32_t)(key_tile * 128 >> 4) << 16; }
 
 struct Shared {
-    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], vclean[VC], q_full, s_full[2], p_full[2], o_full[2];
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], vclean[VC], q_full, s_full[2], p_full[2][2], o_full[2];
     uint32_t words[2][2][4];   // valid bits of a key tile, per stream, two tiles deep
     float m[TILE], l[TILE];
     uint64_t drain;
@@ -239,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(smem_u32(&sh.q_full), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.s_full[i]), 1);
-            mbar_init(smem_u32(&sh.p_full[i]), 4);
+            for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&sh.p_full[i][k]), 4);
             mbar_init(smem_u32(&sh.o_full[i]), 1);
         }
         mbar_init(smem_u32(&sh.drain), 1);
@@ -339,26 +347,34 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mma_commit(one, smem_u32(&sh.s_full[i]));
                 };
                 // O of stream i = P V (fp32 tensors), or += P V; use = the stream's count of P tiles so far
+                // P comes in two halves of the key tile: the first half's products run while the second is made
                 auto mma_v = [&](int i, uint32_t c, int j, uint32_t use, bool release, bool last) {
-                    wait(sh.p_full[i], use & 1);
-                    if (ragged) wait(sh.vclean[j % VC], (j / VC) & 1);
 #pragma unroll
-                    for (int pv = PL - 1; pv >= 0; --pv, ++c) {
-                        const uint32_t slot = c % g.slots;
-                        wait(sh.full[slot], (c / g.slots) & 1);
+                    for (int part = 0; part < 2; ++part) {
+                        wait(sh.p_full[i][part], use & 1);
+                        if (part == 0 && ragged) wait(sh.vclean[j % VC], (j / VC) & 1);
                         tc::fence_after_sync();
-                        const uint32_t vb = ((ring + slot * SLOT) >> 4) | desc_lo_v(KT);
 #pragma unroll
-                        for (int pp = PL - 1 - pv; pp >= 0; --pp)
+                        for (int pv = PL - 1; pv >= 0; --pv) {
+                            const uint32_t e = c + (PL - 1 - pv), slot = e % g.slots;
+                            if (part == 0) {
+                                wait(sh.full[slot], (e / g.slots) & 1);
+                                tc::fence_after_sync();
+                            }
+                            const uint32_t vb = ((ring + slot * SLOT) >> 4) | desc_lo_v(KT);
 #pragma unroll
-                            for (int k = 0; k < KT / 16; ++k)
-                                mma_ts(one, tmem + i * 256 + TO, tmem + i * 256 + p_plane(pp) + k * 8, vb + k * 128, DESC_HI,
-                                       idesc_v, pv != PL - 1 || pp != PL - 1 - pv || k > 0 || (PL == 1 && use > 0));
-                        if (release) mma_commit(one, smem_u32(&sh.empty[slot]));
+                            for (int pp = PL - 1 - pv; pp >= 0; --pp)
+#pragma unroll
+                                for (int k = part * KT / 32; k < (part + 1) * KT / 32; ++k)
+                                    mma_ts(one, tmem + i * 256 + TO, tmem + i * 256 + p_plane(pp) + k * 8, vb + k * 128,
+                                           DESC_HI, idesc_v,
+                                           pv != PL - 1 || pp != PL - 1 - pv || k > 0 || (PL == 1 && use > 0));
+                            if (part == 1 && release) mma_commit(one, smem_u32(&sh.empty[slot]));
+                        }
                     }
                     if (last) mma_commit(one, smem_u32(&sh.o_full[i]));
                 };
-            if constexpr (PAIR) {
+                if constexpr (PAIR) {
                     mma_s(0, 0, false);
                     mma_s(1, 0, true);
                     uint32_t c = PL;
@@ -401,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < nt; ++j) {
                     const int row0 = (warp - 10) * 32 * KW + lane;
                     bool bad[KW];
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < KW; ++i) {
                         const int key = (t_begin + j) * KT + row0 + i * 32;
                         // states past Tk are not in the tensor and read as zero
@@ -410,12 +426,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int p = 0; p < PL; ++p, ++c) {
                         const uint32_t slot = c % g.slots;
                         wait(sh.full[slot], (c / g.slots) & 1);
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < KW; ++i) {
                             if (!bad[i]) continue;
                             const uint32_t at = ring + slot * SLOT + (row0 + i * 32) * 128;
                             for (int d = 0; d < DB; ++d)
-    #pragma unroll
+#pragma unroll
                                 for (int e = 0; e < 8; ++e) tc::st_shared_v4(at + d * KBLK + e * 16, 0u, 0u, 0u, 0u);
                         }
                     }
@@ -441,6 +457,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
         constexpr int KW = KT / 32;     // words of a tile's valid bits
         int use = 0;
+        // half of a key tile's P is in tensor memory
+        auto hand_over = [&](int part) {
+            tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[i][part]));
+        };
         // 32 scores from column 32 e; those that are not valid become -infinity
         auto load_scores = [&](int e, uint32_t (&s)[32], uint32_t w, bool masked) {
             tc::tmem_ld<32>(ts + e * 32, s);
@@ -499,7 +522,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int e = 0; e < 4; ++e) {
                     mx[e] = __uint_as_float(s[e][0]);
 #pragma unroll
-                    for (int k = 1; k < 32; ++k) mx[e] = fmaxf(mx[e], __uint_as_float(s[e][k]));
+                    for (int k = 1; k < 31; k += 2)
+                        mx[e] = max3(mx[e], __uint_as_float(s[e][k]), __uint_as_float(s[e][k + 1]));
+                    mx[e] = fmaxf(mx[e], __uint_as_float(s[e][31]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 const bool grow = top - m > GROW;   // false where both are -infinity
@@ -535,6 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         p[k / 2] = tc::pack_bf16(x, y);
                     }
                     tmem_st32(ts + e * 16, p);
+                    hand_over(e / 2);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             } else {
@@ -542,18 +568,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // plane is written over it
                 constexpr int HOLD = DP == 64 ? KW / 2 : 0;
                 uint32_t hold[HOLD > 0 ? HOLD : 1][32];
-                float top = -INFINITY;
+                float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < KW; ++e) {
                     uint32_t s[32];
                     load_scores(e, s, w[e], masked);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        top = fmaxf(top, __uint_as_float(s[k]));
-                        if (e >= KW - HOLD) hold[e - (KW - HOLD)][k] = s[k];
+                    for (int k = 0; k < 32; k += 2) {
+                        mx[k / 2 & 1] = max3(mx[k / 2 & 1], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                        if (e >= KW - HOLD) {
+                            hold[e - (KW - HOLD)][k] = s[k];
+                            hold[e - (KW - HOLD)][k + 1] = s[k + 1];
+                        }
                     }
                 }
-                top = fmaxf(top * c, m);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]) * c, m);
                 const float mc = top == -INFINITY ? 0.f : top, f = ex2(m - mc);   // 1 or less; 0 at the first scores
                 m = top;
                 // the last tile's product, relative to the last maximum; it is
@@ -600,13 +629,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_st8(ts + P1 + (32 * e + q) / 2, p1);
                         tmem_st8(ts + P2 + (32 * e + q) / 2, p2);
                     }
+                    if (e == KW / 2 - 1) hand_over(0);
+                    if (e == KW - 1) hand_over(1);
                 }
                 l = l * f + (sum[0] + sum[1]);
             }
-            tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[i]));
         }
         if (use > 0) {
             wait(sh.o_full[i], 0);
