@@ -1,7 +1,9 @@
 // Joins partial attention results of disjoint parts of the keys:
 //   m = max_i m_i,  l = sum_i l_i 2^(m_i - m),  out = sum_i o_i 2^(m_i - m) / l
-// in the order of i, so the result does not depend on which part finished
-// first.  One CTA per row; its threads are (part group, element) pairs.
+// in an order that the sizes alone give, so the result does not depend on
+// which part finished first.  Bound by reading the partials: a thread has four
+// elements of a row; with many parts, `groups` threads share them, each every
+// groups-th part, and are joined in order.
 #include <cuda_bf16.h>
 
 #include "attn.h"
@@ -13,59 +15,88 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 
-template <bool BF16>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, const AttnPartials p)
+// m, l, o <- joined with (m2, l2, o2)
+__device__ __forceinline__ void join4(float &m, float &l, float4 &o, float m2, float l2, const float4 &o2)
 {
-    __shared__ float so[kJoinThreads], sl[kJoinThreads], sm[kJoinThreads];
+    const float mm = fmaxf(m, m2), ms = mm == -INFINITY ? 0.f : mm;
+    const float f1 = ex2(m - ms), f2 = ex2(m2 - ms);
+    m = mm;
+    l = l * f1 + l2 * f2;
+    o.x = o.x * f1 + o2.x * f2;
+    o.y = o.y * f1 + o2.y * f2;
+    o.z = o.z * f1 + o2.z * f2;
+    o.w = o.w * f1 + o2.w * f2;
+}
+
+struct JoinGeom {
+    int quads;    // D / 4: threads of a row and group
+    int groups;   // threads that share a row's parts
+    int rows;     // rows of a CTA: quads * groups * rows <= kJoinThreads
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, const AttnPartials p, const JoinGeom g)
+{
+    __shared__ float4 so[kJoinThreads];
+    __shared__ float2 sml[kJoinThreads];
     pdl_wait();
     const int rows = a.Tq * a.G;
-    const int row = blockIdx.x % rows, nh = blockIdx.x / rows;
-    const int n = nh / a.Hkv, h = nh % a.Hkv;
-    const int groups = kJoinThreads / a.D;
-    const int d = threadIdx.x % a.D, grp = threadIdx.x / a.D;
-    const long long nrow = (long long)a.N * a.Hkv * rows, at0 = (long long)nh * rows + row;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    if (grp < groups) {
-        for (int i = grp; i < p.parts; i += groups) {
+    const long long nrow = (long long)a.N * a.Hkv * rows;
+    const int c = threadIdx.x % g.quads, grp = threadIdx.x / g.quads % g.groups, r = threadIdx.x / (g.quads * g.groups);
+    const long long at0 = (long long)blockIdx.x * g.rows + r;
+    const bool act = r < g.rows && at0 < nrow;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (act) {
+#pragma unroll 4
+        for (int i = grp; i < p.parts; i += g.groups) {
             const long long at = i * nrow + at0;
             const float2 ml = p.ml[at];
-            const float oi = p.o[at * a.D + d];
-            const float mm = fmaxf(m, ml.x), ms = mm == -INFINITY ? 0.f : mm;
-            const float f1 = ex2(m - ms), f2 = ex2(ml.x - ms);
-            l = l * f1 + ml.y * f2;
-            o = o * f1 + oi * f2;
-            m = mm;
+            join4(m, l, o, ml.x, ml.y, *reinterpret_cast<const float4 *>(p.o + at * a.D + 4 * c));
         }
     }
-    so[threadIdx.x] = o;
-    sl[threadIdx.x] = l;
-    sm[threadIdx.x] = m;
-    __syncthreads();
-    if (grp != 0) return;
-    for (int j = 1; j < groups; ++j) {
-        const int e = j * a.D + d;
-        const float mm = fmaxf(m, sm[e]), ms = mm == -INFINITY ? 0.f : mm;
-        const float f1 = ex2(m - ms), f2 = ex2(sm[e] - ms);
-        l = l * f1 + sl[e] * f2;
-        o = o * f1 + so[e] * f2;
-        m = mm;
+    if (g.groups > 1) {
+        so[threadIdx.x] = o;
+        sml[threadIdx.x] = make_float2(m, l);
+        __syncthreads();
+        if (!act || grp != 0) return;
+        for (int j = 1; j < g.groups; ++j) {
+            const int e = threadIdx.x + j * g.quads;
+            join4(m, l, o, sml[e].x, sml[e].y, so[e]);
+        }
     }
+    if (!act) return;
+    const int nh = (int)(at0 / rows), row = (int)(at0 - (long long)nh * rows);
+    const int n = nh / a.Hkv, h = nh % a.Hkv;
     const int t = row / a.G, hq = h * a.G + row % a.G;
-    const long long oat = n * a.os.n + t * a.os.t + hq * a.os.h + d;
-    const float y = l == 0.f ? 0.f : o / l;
-    if constexpr (BF16)
-        static_cast<__nv_bfloat16 *>(a.out)[oat] = __float2bfloat16_rn(y);
-    else
-        static_cast<float *>(a.out)[oat] = y;
-    if (d == 0 && a.lse) a.lse[((long long)n * a.Hq + hq) * a.Tq + t] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+    const long long oat = n * a.os.n + t * a.os.t + hq * a.os.h + 4 * c;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float y[4] = {l == 0.f ? 0.f : o.x * inv, l == 0.f ? 0.f : o.y * inv, l == 0.f ? 0.f : o.z * inv,
+                        l == 0.f ? 0.f : o.w * inv};
+    if constexpr (BF16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(y[0], y[1]), hi = __floats2bfloat162_rn(y[2], y[3]);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + oat) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + oat) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    if (c == 0 && a.lse) a.lse[((long long)n * a.Hq + hq) * a.Tq + t] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_join(const AttnArgs &a, bool bf16, const AttnPartials &p, cudaStream_t st)
 {
+    JoinGeom g;
+    g.quads = a.D / 4;
+    // a group has at least four parts; more than one only as far as threads go
+    g.groups = p.parts / 4;
+    if (g.groups > kJoinThreads / g.quads) g.groups = kJoinThreads / g.quads;
+    if (g.groups < 1) g.groups = 1;
+    g.rows = kJoinThreads / (g.quads * g.groups);
+    const long long nrow = (long long)a.N * a.Hkv * a.Tq * a.G;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.N * a.Hkv * a.Tq * a.G));
+    cfg.gridDim = dim3((unsigned)((nrow + g.rows - 1) / g.rows));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -73,8 +104,8 @@ cudaError_t launch_attn_join(const AttnArgs &a, bool bf16, const AttnPartials &p
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true>, a, p)
-                : cudaLaunchKernelEx(&cfg, attn_join_kernel<false>, a, p);
+    return bf16 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true>, a, p, g)
+                : cudaLaunchKernelEx(&cfg, attn_join_kernel<false>, a, p, g);
 }
 
 }  // namespace sc

@@ -342,8 +342,8 @@ cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
         const size_t nrow = (size_t)part.parts * a.N * a.Hkv * rows;
         const cudaError_t e = workspace_alloc(&ws, nrow * ((size_t)a.D * 4 + sizeof(float2)), st);
         if (e != cudaSuccess) return e;
-        part.ml = static_cast<float2 *>(ws);
-        part.o = reinterpret_cast<float *>(part.ml + nrow);
+        part.o = static_cast<float *>(ws);   // rows of D floats: 16-byte aligned
+        part.ml = reinterpret_cast<float2 *>(part.o + nrow * a.D);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks * g.splits));

@@ -432,7 +432,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const uint32_t at = ring + slot * SLOT + (row0 + i * 32) * 128;
                             for (int d = 0; d < DB; ++d)
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) tc::st_shared_v4(at + d * KBLK + e * 16, 0u, 0u, 0u, 0u);
+                                for (int e = 0; e < 8; ++e)   // from chunk `lane` on: no two lanes in one bank
+                                    tc::st_shared_v4(at + d * KBLK + ((e + lane) & 7) * 16, 0u, 0u, 0u, 0u);
                         }
                     }
                     fence_proxy_async_smem();
@@ -457,6 +458,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
         constexpr int KW = KT / 32;     // words of a tile's valid bits
         int use = 0;
+        // this thread's byte of key tile j: 0 where the state is not valid
+        auto mask_byte = [&](int j) {
+            const int key = (t_begin + j) * KT + row;
+            return row < KT && j < nt && key < len ? (int)mb[key] : 0;
+        };
+        int next = mb ? mask_byte(PAIR ? 0 : i) : 0;
         // half of a key tile's P is in tensor memory
         auto hand_over = [&](int part) {
             tmem_wait_st();
@@ -481,9 +488,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int e = 0; e < KW; ++e) w[e] = ~0u;
             bool masked = key0 + KT > len;
             if (mb) {
-                // one key per thread, a word per warp
-                const int key = key0 + row;
-                const uint32_t word = __ballot_sync(0xffffffffu, row < KT && key < len && mb[key] != 0);
+                // one key per thread, a word per warp; the next tile's byte is
+                // read a tile ahead (its latency was a third of a masked tile's time)
+                const uint32_t word = __ballot_sync(0xffffffffu, next != 0);
+                next = mask_byte(j + step);
                 if (lane == 0) sh.words[i][use & 1][warp & 3] = word;
                 if (i == 0)
                     named_sync<1, 128>();
