@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 from . import _build
@@ -94,14 +95,6 @@ class ScAttnStrides(ctypes.Structure):
     _fields_ = [("q", ScHeadStrides), ("k", ScHeadStrides), ("v", ScHeadStrides), ("out", ScHeadStrides)]
 
 
-class ScNormHeads(ctypes.Structure):
-    """sc_norm_heads: one tensor of qk_norm_rotary_fwd."""
-    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("weight", ctypes.c_void_p),
-                ("pos", ctypes.c_void_p), ("tokens", ctypes.c_int), ("heads", ctypes.c_int),
-                ("x_token_stride", ctypes.c_longlong), ("x_head_stride", ctypes.c_longlong),
-                ("y_token_stride", ctypes.c_longlong), ("y_head_stride", ctypes.c_longlong)]
-
-
 SC_NOALLOC_SCRATCH_FLOATS = 8 * 1024 * 1024
 
 _lib = None
@@ -144,10 +137,26 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """torch's current stream of the current device as a raw handle.
+
+    torch.cuda.current_stream() builds a Stream object (3 us of a call that takes 8); the raw
+    handle is taken directly where this torch offers it."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.init()
+        _raw_stream = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
+
+
 def _stream(s) -> Optional[int]:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -295,11 +304,16 @@ def rotary_fwd(x, y, table, pos, tokens, heads, D, rot_dim, positions, mode=SC_R
                              axes, 1 if inverse else 0, dtype, xs, ys, _stream(stream))
 
 
+# sc_norm_heads as bytes (a ctypes.Structure takes three times as long to fill)
+_NORM_HEADS = struct.Struct("@PPPPiiqqqq")
+
+
 def _norm_heads(t):
     if t is None:
         return None
     x, y, weight, pos, tokens, heads, *strides = t
-    return ctypes.byref(ScNormHeads(_ptr(x), _ptr(y), _ptr(weight), _ptr(pos), tokens, heads, *strides))
+    return _NORM_HEADS.pack(_ptr(x) or 0, _ptr(y) or 0, _ptr(weight) or 0, _ptr(pos) or 0, tokens, heads,
+                            *(strides or (0, 0, 0, 0)))
 
 
 def qk_norm_rotary_fwd(q, k, table, D, rot_dim, positions, eps=1e-6, mode=SC_ROT_HALF, axes=1, dtype=SC_F32,

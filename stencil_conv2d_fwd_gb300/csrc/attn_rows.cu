@@ -1,91 +1,71 @@
-// Attention of a few query rows over many keys (a decoder's next token, a
-// short draft): every key and value is used by R <= 8 rows, so the kernel is
-// bound by reading K and V once.
+// Attention of a few fp32 query rows over many keys (a decoder's next token, a
+// short draft): every key and value is used by R <= 4 rows, so the kernel is
+// bound by reading K and V once.  Also the path of tensors that the tensor
+// cores' copies cannot address (shared query axes, shared states).
 //
 //   s_j = scale * q . k_j,  m = max_j s_j,  l = sum_j 2^((s_j - m) log2 e),
 //   o = sum_j 2^((s_j - m) log2 e) v_j,     out = o / l
 //
 // One pass: m, l and o are running values, o and l rescaled when m grows.  A
-// key's D elements are held by LPK lanes, 16 bytes each, straight from global
+// key's D elements are held by LPK lanes, eight each, straight from global
 // memory in registers; the dot product is summed over those lanes by
-// shuffles, after which all of them have the key's weight for their own slice
-// of its value.  Nothing is shared between warps until the end, when (m, l,
-// o) of the lane groups, the warps and the CTAs of a cluster (distributed
-// shared memory) are joined, in that fixed order.  With more CTAs per row
-// than a cluster holds, each cluster writes one partial result and
-// attn_join.cu joins them.
-#include <cooperative_groups.h>
-#include <cuda_bf16.h>
-
-#include "attn.h"
+// shuffles (eight elements a lane, not four, to shuffle half as often), after
+// which all of them have the key's weight for their own slice of its value.
+// Nothing is shared between warps until the end (attn_rows.cuh).
+#include "attn_rows.cuh"
 #include "launch.h"
-
-namespace cg = cooperative_groups;
 
 namespace sc {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCluster = 8;
+constexpr int E = 8;   // elements of a key per lane
 
+// Eight elements at p, as stored.
 template <class T>
-struct Elem;
-template <>
-struct Elem<float> {
-    static constexpr int E = 4;   // elements of 16 bytes
-    static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[4])
+struct Chunk {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void zero()
     {
-        f[0] = __uint_as_float(u.x);
-        f[1] = __uint_as_float(u.y);
-        f[2] = __uint_as_float(u.z);
-        f[3] = __uint_as_float(u.w);
-    }
-    static __device__ __forceinline__ float from(float v) { return v; }
-};
-template <>
-struct Elem<__nv_bfloat16> {
-    static constexpr int E = 8;
-    static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[8])
-    {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (auto &x : w) x = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = ldg16(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ void unpack(float (&f)[E]) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[4 * i] = __uint_as_float(w[i].x);
+                f[4 * i + 1] = __uint_as_float(w[i].y);
+                f[4 * i + 2] = __uint_as_float(w[i].z);
+                f[4 * i + 3] = __uint_as_float(w[i].w);
+            }
+        } else {
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(u[i] << 16);
+                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
         }
     }
-    static __device__ __forceinline__ __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
 };
-
-struct RowsGeom {
-    int splits;      // CTAs per row block (a multiple of the cluster size)
-    int cluster;
-    int row_blocks;
-};
-
-__device__ __forceinline__ uint4 ldg16(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 
 // LPK lanes per key, R rows per CTA, U keys of a lane group in flight.
 template <class T, int LPK, int R, int U>
-__global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const AttnArgs a, const RowsGeom g, const AttnPartials part)
+__global__ void __launch_bounds__(kRowThreads, 2) attn_rows_kernel(const AttnArgs a, const RowsGeom g, const AttnPartials part)
 {
-    constexpr int E = Elem<T>::E;
     constexpr int KPW = 32 / LPK;   // keys per warp-wide load
     constexpr int DP = LPK * E;
-    __shared__ float sm_o[kWarps][R][DP];
-    __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
-    __shared__ float cta_o[R][DP], cta_m[R], cta_l[R];
+    __shared__ RowSums<R, DP> sm;
 
     pdl_trigger();   // the join kernel may be set up; it waits for this grid's end
+    if (g.cluster > 1) cluster_arrive();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int split = blockIdx.x % g.splits;
     const int blk = blockIdx.x / g.splits;
@@ -107,7 +87,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const AttnArgs a
         for (int i = 0; i < E; ++i) f[i] = 0.f;
         if (row < rows && dact) {
             const int t = row / a.G, hq = h * a.G + row % a.G;
-            Elem<T>::unpack(ldg16(static_cast<const T *>(a.q) + n * a.qs.n + t * a.qs.t + hq * a.qs.h + dl * E), f);
+            Chunk<T> x;
+            x.load(static_cast<const T *>(a.q) + n * a.qs.n + t * a.qs.t + hq * a.qs.h + dl * E);
+            x.unpack(f);
         }
 #pragma unroll
         for (int i = 0; i < E; ++i) q[r][i] = f[i] * (a.scale * kLog2e);
@@ -132,8 +114,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const AttnArgs a
         for (int i = 0; i < E; ++i) o[r][i] = 0.f;
     }
 
-    constexpr int STEP = kWarps * KPW * U;
-    uint4 kr[U], vr[U];
+    constexpr int STEP = kRowWarps * KPW * U;
+    Chunk<T> kr[U], vr[U];
     bool ok[U];
     // keys and values of this lane group's next U keys; invalid ones are not
     // read (whatever is stored there does not reach a sum)
@@ -142,18 +124,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const AttnArgs a
         for (int u = 0; u < U; ++u) {
             const int key = base + u * KPW + grp;
             ok[u] = key < k1 && (!mb || mb[key] != 0);
-            kr[u] = make_uint4(0u, 0u, 0u, 0u);
-            vr[u] = make_uint4(0u, 0u, 0u, 0u);
+            kr[u].zero();
+            vr[u].zero();
             if (ok[u] && dact) {
-                kr[u] = ldg16(kb + key * a.ks.t);
-                vr[u] = ldg16(vb + key * a.vs.t);
+                kr[u].load(kb + key * a.ks.t);
+                vr[u].load(vb + key * a.vs.t);
             }
         }
     };
     int base = k0 + warp * KPW * U;
     fetch(base);
     for (; base < k1; base += STEP) {
-        uint4 kc[U], vc[U];
+        Chunk<T> kc[U], vc[U];
         bool okc[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -166,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const AttnArgs a
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float kf[E];
-            Elem<T>::unpack(kc[u], kf);
+            kc[u].unpack(kf);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 float acc = q[r][0] * kf[0];
@@ -206,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const AttnArgs a
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float vf[E];
-            Elem<T>::unpack(vc[u], vf);
+            vc[u].unpack(vf);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float p = ex2(s[u][r] - (m[r] == -INFINITY ? 0.f : m[r]));
@@ -238,149 +220,34 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(const AttnArgs a
 #pragma unroll
         for (int r = 0; r < R; ++r) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) sm_o[warp][r][dl * E + i] = o[r][i];
+            for (int i = 0; i < E; ++i) sm.o[warp][r][dl * E + i] = o[r][i];
             if (dl == 0) {
-                sm_m[warp][r] = m[r];
-                sm_l[warp][r] = l[r];
+                sm.m[warp][r] = m[r];
+                sm.l[warp][r] = l[r];
             }
         }
     }
-    __syncthreads();
-    // ... the warps of the CTA ...
-    for (int e = tid; e < R * DP; e += kThreads) {
-        const int r = e / DP, d = e % DP;
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w][r]);
-        const float ms = mm == -INFINITY ? 0.f : mm;
-        float ls = 0.f, os = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(sm_m[w][r] - ms);
-            ls = fmaf(sm_l[w][r], f, ls);
-            os = fmaf(sm_o[w][r][d], f, os);
-        }
-        cta_o[r][d] = os;
-        if (d == 0) {
-            cta_m[r] = mm;
-            cta_l[r] = ls;
-        }
-    }
-    // ... and the CTAs of the cluster, each finishing a share of the elements
-    cg::cluster_group cl = cg::this_cluster();
-    const int C = g.cluster, rank = split % C;
-    if (C > 1)
-        cl.sync();
-    else
-        __syncthreads();
-    for (int e = rank * kThreads + tid; e < R * DP; e += C * kThreads) {
-        const int r = e / DP, d = e % DP, row = row0 + r;
-        float mm = -INFINITY;
-        float mc[kMaxCluster], lc[kMaxCluster], oc[kMaxCluster];
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            if (c < C) {
-                mc[c] = C > 1 ? *cl.map_shared_rank(&cta_m[r], c) : cta_m[r];
-                lc[c] = C > 1 ? *cl.map_shared_rank(&cta_l[r], c) : cta_l[r];
-                oc[c] = C > 1 ? *cl.map_shared_rank(&cta_o[r][d], c) : cta_o[r][d];
-                mm = fmaxf(mm, mc[c]);
-            }
-        }
-        const float ms = mm == -INFINITY ? 0.f : mm;
-        float ls = 0.f, os = 0.f;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            if (c < C) {
-                const float f = ex2(mc[c] - ms);
-                ls = fmaf(lc[c], f, ls);
-                os = fmaf(oc[c], f, os);
-            }
-        }
-        if (row < rows && d < a.D) {
-            const int t = row / a.G, hq = h * a.G + row % a.G;
-            if (part.parts > 0) {
-                const long long at = ((long long)(split / C) * a.N * a.Hkv + nh) * rows + row;
-                part.o[at * a.D + d] = os;
-                if (d == 0) part.ml[at] = make_float2(mm, ls);
-            } else {
-                static_cast<T *>(a.out)[n * a.os.n + t * a.os.t + hq * a.os.h + d] =
-                    Elem<T>::from(ls == 0.f ? 0.f : os / ls);
-                if (d == 0 && a.lse)
-                    a.lse[((long long)n * a.Hq + hq) * a.Tq + t] = ls == 0.f ? -INFINITY : mm * kLn2 + logf(ls);
-            }
-        }
-    }
-    if (C > 1) cl.sync();   // no CTA leaves while another reads its shared memory
+    finish_rows<T, R, DP>(sm, a, g, part, nh, row0, split);
 }
 
-template <class T, int LPK, int R, int U>
-cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
-{
-    const long long rows = (long long)a.Tq * a.G;
-    RowsGeom g;
-    g.row_blocks = (int)((rows + R - 1) / R);
-    const long long blocks = (long long)a.N * a.Hkv * g.row_blocks;
-    // CTAs per row block: enough to fill the GPU twice over, none with less
-    // than one step of keys
-    constexpr int STEP = kWarps * (32 / LPK) * U;
-    const long long want = (4LL * device_sm_count() + blocks - 1) / blocks;
-    const long long most = ((long long)a.Tk + STEP - 1) / STEP;
-    long long s = want < most ? want : most;
-    if (s <= kMaxCluster) {
-        int c = 1;
-        while (c < s) c *= 2;
-        g.splits = g.cluster = c;
-    } else {
-        g.cluster = kMaxCluster;
-        g.splits = (int)((s + kMaxCluster - 1) / kMaxCluster * kMaxCluster);
-    }
-    if (blocks * g.splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    AttnPartials part{nullptr, nullptr, 0};
-    void *ws = nullptr;
-    if (g.splits > g.cluster) {
-        part.parts = g.splits / g.cluster;
-        const size_t nrow = (size_t)part.parts * a.N * a.Hkv * rows;
-        const cudaError_t e = workspace_alloc(&ws, nrow * ((size_t)a.D * 4 + sizeof(float2)), st);
-        if (e != cudaSuccess) return e;
-        part.o = static_cast<float *>(ws);   // rows of D floats: 16-byte aligned
-        part.ml = reinterpret_cast<float2 *>(part.o + nrow * a.D);
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks * g.splits));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = g.cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, LPK, R, U>, a, g, part);
-    if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, sizeof(T) == 2, part, st);
-    if (ws) {
-        const cudaError_t ef = workspace_free(ws, st);
-        if (e == cudaSuccess) e = ef;
-    }
-    return e;
-}
-
-template <class T, int LPK>
+template <class T, int LPK, int U>
 cudaError_t launch_rows_r(const AttnArgs &a, cudaStream_t st)
 {
     const long long rows = (long long)a.Tq * a.G;
-    if (rows == 1) return launch_rows<T, LPK, 1, 4>(a, st);
-    if (rows == 2) return launch_rows<T, LPK, 2, 4>(a, st);
-    return launch_rows<T, LPK, 4, 2>(a, st);
+    constexpr int STEP = kRowWarps * (32 / LPK) * U;
+    const bool bf16 = sizeof(T) == 2;
+    if (rows == 1) return launch_rows_kernel(attn_rows_kernel<T, LPK, 1, U>, a, bf16, 1, STEP, 0, st);
+    if (rows == 2) return launch_rows_kernel(attn_rows_kernel<T, LPK, 2, U>, a, bf16, 2, STEP, 0, st);
+    if (rows == 3) return launch_rows_kernel(attn_rows_kernel<T, LPK, 3, U>, a, bf16, 3, STEP, 0, st);
+    return launch_rows_kernel(attn_rows_kernel<T, LPK, 4, U>, a, bf16, 4, STEP, 0, st);
 }
 
 template <class T>
 cudaError_t launch_rows_t(const AttnArgs &a, cudaStream_t st)
 {
-    const int lanes = a.D / Elem<T>::E;
-    if (lanes <= 4) return launch_rows_r<T, 4>(a, st);
-    if (lanes <= 8) return launch_rows_r<T, 8>(a, st);
-    if (lanes <= 16) return launch_rows_r<T, 16>(a, st);
-    return launch_rows_r<T, 32>(a, st);
+    if (a.D <= 32) return launch_rows_r<T, 4, 2>(a, st);
+    if (a.D <= 64) return launch_rows_r<T, 8, 2>(a, st);
+    return launch_rows_r<T, 16, 2>(a, st);
 }
 
 }  // namespace
