@@ -11,7 +11,12 @@
 // exchange; elements beyond `rot` are handled as chunk pairs that are only
 // copied.  A row's D / (2 V) threads sum their squares by shuffles.  A thread
 // does kHeads heads of one token, with the token's cosines, sines and the
-// norm's weights in registers and all its loads issued first.
+// norm's weights in registers and all its loads issued first, and keeps what
+// it loaded as stored until each head's turn: with floats for all four heads
+// (116 registers, 16 warps an SM) 131072 tokens of 8 x 128 bf16 took 149.6 us,
+// now (32 warps an SM) 97.3 (6.2 TB/s); 65536 + 14400 tokens of 16 x 128 fp32
+// with the norm 210 and 193 us (6.8 TB/s).  Two heads a thread read the table
+// twice as often: 100 and 218 us at the same occupancy.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -24,61 +29,77 @@ namespace sc {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kHeads = 4;   // heads of a token per thread
+constexpr int kHeads = 4;     // heads of a token per thread
+// CTAs an SM: at most 64 registers a thread, 80 where eight weights' and eight
+// angles' floats of each chunk are held (64 spill them: 90 us, not 47, for the
+// keys of 32 maps of 56 x 56, 8 x 64 bf16).
+template <int V, bool NORM>
+constexpr int rot_ctas() { return V == 8 && NORM ? 3 : 4; }
 
-// V elements at p (16 bytes, or 8 for four bf16), to and from floats
+// V elements (16 bytes, or 8 for four bf16) as stored, and as floats.
+template <class T, int V>
+struct Packed {
+    static constexpr int W = V * (int)sizeof(T) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T *p)
+    {
+        if constexpr (W == 4) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            w[0] = u.x;
+            w[1] = u.y;
+            w[2] = u.z;
+            w[3] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0] = u.x;
+            w[1] = u.y;
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const
+    {
+        if constexpr (W == 4)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+    __device__ __forceinline__ void unpack(float (&f)[V]) const
+    {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ void pack(const float (&f)[V])
+    {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[i] = __float_as_uint(f[i]);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+    }
+};
+
+// V floats at p, 16-byte aligned, of a table that every CTA reads.
 template <int V>
-__device__ __forceinline__ void load_v(const float *p, float (&f)[V])
+__device__ __forceinline__ void load_floats(const float *p, float (&f)[V])
 {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-        const float4 u = *reinterpret_cast<const float4 *>(p + i);
+        const float4 u = __ldg(reinterpret_cast<const float4 *>(p + i));
         f[i] = u.x;
         f[i + 1] = u.y;
         f[i + 2] = u.z;
         f[i + 3] = u.w;
     }
-}
-template <int V>
-__device__ __forceinline__ void load_v(const __nv_bfloat16 *p, float (&f)[V])
-{
-    uint32_t w[V / 2];
-    if constexpr (V == 8) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        w[0] = u.x;
-        w[1] = u.y;
-        w[2] = u.z;
-        w[3] = u.w;
-    } else {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        w[0] = u.x;
-        w[1] = u.y;
-    }
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-template <int V>
-__device__ __forceinline__ void store_v(float *p, const float (&f)[V])
-{
-#pragma unroll
-    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-}
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-template <int V>
-__device__ __forceinline__ void store_v(__nv_bfloat16 *p, const float (&f)[V])
-{
-    if constexpr (V == 8)
-        *reinterpret_cast<uint4 *>(p) = make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
-                                                   bf16_pair(f[6], f[7]));
-    else
-        *reinterpret_cast<uint2 *>(p) = make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
 }
 
 struct RotGeom {
@@ -88,7 +109,7 @@ struct RotGeom {
 };
 
 template <class T, int V, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a, const RotGeom g, int *status)
+__global__ void __launch_bounds__(kRotThreads, rot_ctas<V, NORM>()) rotary_kernel(const RotaryArgs a, const RotGeom g, int *status)
 {
     const bool second = blockIdx.x >= g.blocks0;
     const NormHeads &P = a.part[second ? 1 : 0];
@@ -115,25 +136,30 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a,
         cb = ca + a.rot / 2;
     }
 
+    // the position first: the table's row waits for it
+    int pos = 0, axis = 0, p0 = 0;
+    const int pairs = a.rot / (2 * a.axes);
+    if (act && turn) {
+        // V pairs lie on one axis: rot is a multiple of 2 V axes
+        axis = slot * V / pairs;
+        p0 = slot * V - axis * pairs;
+        pos = __ldg(P.pos + (long long)axis * P.tokens + tok);
+    }
     const T *x = static_cast<const T *>(P.x) + tok * P.x_t + h0 * P.x_h;
     T *y = static_cast<T *>(P.y) + tok * P.y_t + h0 * P.y_h;
-    float fa[kHeads][V], fb[kHeads][V];
+    Packed<T, V> ra[kHeads], rb[kHeads];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
         if (i < nh) {
-            load_v<V>(x + i * P.x_h + ca, fa[i]);
-            load_v<V>(x + i * P.x_h + cb, fb[i]);
+            ra[i].load(x + i * P.x_h + ca);
+            rb[i].load(x + i * P.x_h + cb);
         } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) fa[i][j] = fb[i][j] = 0.f;
+            for (int j = 0; j < Packed<T, V>::W; ++j) ra[i].w[j] = rb[i].w[j] = 0u;
         }
     }
     float cs[V], sn[V];
     if (act && turn) {
-        // V pairs lie on one axis: rot is a multiple of 2 V axes
-        const int pairs = a.rot / (2 * a.axes);
-        const int axis = slot * V / pairs, p0 = slot * V - axis * pairs;
-        const int pos = P.pos[(long long)axis * P.tokens + tok];
         if (pos >= 0 && pos < a.positions) {
             const float4 *row = reinterpret_cast<const float4 *>(a.table + ((long long)pos * pairs + p0) * 2);
 #pragma unroll
@@ -161,22 +187,25 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a,
 #pragma unroll
         for (int j = 0; j < V; ++j) wa[j] = wb[j] = 1.f;
         if (act && P.weight) {
-            load_v<V>(P.weight + ca, wa);
-            load_v<V>(P.weight + cb, wb);
+            load_floats<V>(P.weight + ca, wa);
+            load_floats<V>(P.weight + cb, wb);
         }
     }
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
+        float fa[V], fb[V];
+        ra[i].unpack(fa);
+        rb[i].unpack(fb);
         if constexpr (NORM) {
             float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) ss = fmaf(fa[i][j], fa[i][j], fmaf(fb[i][j], fb[i][j], ss));
+            for (int j = 0; j < V; ++j) ss = fmaf(fa[j], fa[j], fmaf(fb[j], fb[j], ss));
             for (int off = g.lanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
             const float rs = rsqrtf(ss / (float)a.D + a.eps);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                fa[i][j] *= rs * wa[j];
-                fb[i][j] *= rs * wb[j];
+                fa[j] *= rs * wa[j];
+                fb[j] *= rs * wb[j];
             }
         }
         if (i >= nh) continue;
@@ -185,24 +214,26 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a,
                 // pairs (0, 1), (2, 3), ... of the 2 V adjacent elements
 #pragma unroll
                 for (int j = 0; j < V; j += 2) {
-                    const float p = fa[i][j], q = fa[i][j + 1];
-                    fa[i][j] = p * cs[j / 2] - q * sn[j / 2];
-                    fa[i][j + 1] = q * cs[j / 2] + p * sn[j / 2];
-                    const float r = fb[i][j], s = fb[i][j + 1];
-                    fb[i][j] = r * cs[V / 2 + j / 2] - s * sn[V / 2 + j / 2];
-                    fb[i][j + 1] = s * cs[V / 2 + j / 2] + r * sn[V / 2 + j / 2];
+                    const float p = fa[j], q = fa[j + 1];
+                    fa[j] = p * cs[j / 2] - q * sn[j / 2];
+                    fa[j + 1] = q * cs[j / 2] + p * sn[j / 2];
+                    const float r = fb[j], u = fb[j + 1];
+                    fb[j] = r * cs[V / 2 + j / 2] - u * sn[V / 2 + j / 2];
+                    fb[j + 1] = u * cs[V / 2 + j / 2] + r * sn[V / 2 + j / 2];
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float p = fa[i][j], q = fb[i][j];
-                    fa[i][j] = p * cs[j] - q * sn[j];
-                    fb[i][j] = q * cs[j] + p * sn[j];
+                    const float p = fa[j], q = fb[j];
+                    fa[j] = p * cs[j] - q * sn[j];
+                    fb[j] = q * cs[j] + p * sn[j];
                 }
             }
         }
-        store_v<V>(y + i * P.y_h + ca, fa[i]);
-        store_v<V>(y + i * P.y_h + cb, fb[i]);
+        ra[i].pack(fa);
+        rb[i].pack(fb);
+        ra[i].store(y + i * P.y_h + ca);
+        rb[i].store(y + i * P.y_h + cb);
     }
 }
 
