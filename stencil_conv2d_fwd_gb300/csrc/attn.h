@@ -40,14 +40,13 @@ struct AttnPartials {
 // Up to 16 bf16 rows per key head: keys streamed through warp-wide MMAs
 // (attn_mma.cu).
 cudaError_t launch_attn_mma(const AttnArgs &a, cudaStream_t st);
-// Few rows per key head: keys streamed through registers (attn_rows.cu).
-cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t st);
-// Many rows per key head: tensor cores (attn_tc.cu).  cudaErrorNotSupported
-// where its copies cannot address the tensors.
+// Few fp32 rows per key head: keys streamed through registers (attn_rows.cu).
+cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t st);
+// Many rows per key head: tensor cores (attn_tc.cu).
 cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st);
-// The three bf16 planes of fp32 q ([plane][N][Hkv][Tq][G][D]), k and v
-// ([plane][N][Hkv][Tk][D]) (attn_split.cu).
-cudaError_t launch_attn_split(const AttnArgs &a, void *const (&planes)[3], cudaStream_t st);
+// Copies of q ([plane][N][Hkv][Tq][G][D]), k and v ([plane][N][Hkv][Tk][D]) for
+// it: fp32 tensors as three bf16 planes, bf16 ones as one (attn_split.cu).
+cudaError_t launch_attn_split(const AttnArgs &a, bool bf16, void *const (&planes)[3], cudaStream_t st);
 // Joins partial results into out and lse (attn_join.cu).
 cudaError_t launch_attn_join(const AttnArgs &a, bool bf16, const AttnPartials &p, cudaStream_t st);
 

@@ -280,12 +280,8 @@ int cross_attention_fwd(const void *q, const void *k, const void *v, void *out, 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SC_BF16;
     const long long rows = (long long)Tq * a.G;
-    if (bf16 && rows <= 16) return from_cuda(sc::launch_attn_mma(a, st));
-    if (rows > 16) {
-        const cudaError_t e = sc::launch_attn_tc(a, bf16, st);
-        if (e != cudaErrorNotSupported) return from_cuda(e);
-    }
-    return from_cuda(sc::launch_attn_rows(a, bf16, st));
+    if (rows > 16) return from_cuda(sc::launch_attn_tc(a, bf16, st));
+    return from_cuda(bf16 ? sc::launch_attn_mma(a, st) : sc::launch_attn_rows(a, st));
 }
 
 }  // extern "C"

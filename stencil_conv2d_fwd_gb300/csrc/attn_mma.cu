@@ -53,12 +53,26 @@ __device__ __forceinline__ int spread(int g) { return (g >> 1) + 4 * (g & 1); }
 // DP: head width rounded up to 64 or 128.  RH: 1 for up to 8 rows, 2 for 16.
 constexpr int STAGES = 3;   // of 16 + 16 rows; a step's valid bits are 16 of a 64-bit word: at most 4
 
+// The rings' memory becomes the sums' at the end.  With 8 rows the cluster's
+// sums have their own: the first CTA's place is then free from the start, and
+// no CTA waits for another's loop.  With 16 there is no room.
 template <int DP, int RH>
 struct MmaShared {
     union {
         uint4 ring[kRowWarps][STAGES][2][KEYS][DP / 8];   // K, V
-        RowSums<8 * RH, DP> sums;
+        struct {
+            WarpSums<8 * RH, DP> warps;
+            CtaSums<RH == 1 ? 1 : 8 * RH, RH == 1 ? 1 : DP> shared_ctas;
+        } sums;
     };
+    CtaSums<RH == 1 ? 8 : 1, RH == 1 ? DP : 1> own_ctas;
+    __device__ __forceinline__ CtaSums<8 * RH, DP> &ctas()
+    {
+        if constexpr (RH == 1)
+            return own_ctas;
+        else
+            return sums.shared_ctas;
+    }
 };
 
 template <int DP, int RH>
@@ -76,7 +90,7 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
     MmaShared<DP, RH> &sm = *reinterpret_cast<MmaShared<DP, RH> *>(dyn);
 
     pdl_trigger();   // the join kernel may be set up; it waits for this grid's end
-    if (g.cluster > 1) cluster_arrive();
+    if (RH == 1 && g.cluster > 1) cluster_arrive();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % g.splits;
     const int blk = blockIdx.x / g.splits;
@@ -265,6 +279,7 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
     }
     cp_async_wait<0>();
     __syncthreads();   // the rings' memory becomes the sums'
+    if (RH == 2 && g.cluster > 1) cluster_arrive();
 
     // the warp's sums: row g (and g + 8); l over the quad
 #pragma unroll
@@ -272,8 +287,8 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         if (t == 0) {
-            sm.sums.m[warp][r * 8 + gq] = m[r];
-            sm.sums.l[warp][r * 8 + gq] = l[r];
+            sm.sums.warps.m[warp][r * 8 + gq] = m[r];
+            sm.sums.warps.l[warp][r * 8 + gq] = l[r];
         }
 #pragma unroll
         for (int c = 0; c < VC; ++c)
@@ -281,9 +296,9 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    sm.sums.o[warp][r * 8 + gq][(c * 8 + spread(2 * t + e)) * 8 + j] = o[c * 8 + j][2 * r + e];
+                    sm.sums.warps.o[warp][r * 8 + gq][(c * 8 + spread(2 * t + e)) * 8 + j] = o[c * 8 + j][2 * r + e];
     }
-    finish_rows<__nv_bfloat16, R, DP>(sm.sums, a, g, part, nh, row0, split);
+    finish_rows<__nv_bfloat16, R, DP>(sm.sums.warps, sm.ctas(), a, g, part, nh, row0, split);
 }
 
 template <int DP, int RH>

@@ -1,7 +1,6 @@
 // Attention of a few fp32 query rows over many keys (a decoder's next token, a
 // short draft): every key and value is used by R <= 4 rows, so the kernel is
-// bound by reading K and V once.  Also the path of tensors that the tensor
-// cores' copies cannot address (shared query axes, shared states).
+// bound by reading K and V once.
 //
 //   s_j = scale * q . k_j,  m = max_j s_j,  l = sum_j 2^((s_j - m) log2 e),
 //   o = sum_j 2^((s_j - m) log2 e) v_j,     out = o / l
@@ -21,48 +20,35 @@ namespace {
 
 constexpr int E = 8;   // elements of a key per lane
 
-// Eight elements at p, as stored.
-template <class T>
+// Eight elements at p.
 struct Chunk {
-    uint4 w[sizeof(T) / 2];
-    __device__ __forceinline__ void zero()
+    uint4 w[2];
+    __device__ __forceinline__ void zero() { w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void load(const float *p)
     {
-#pragma unroll
-        for (auto &x : w) x = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ __forceinline__ void load(const T *p)
-    {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = ldg16(reinterpret_cast<const uint4 *>(p) + i);
+        w[0] = ldg16(p);
+        w[1] = ldg16(p + 4);
     }
     __device__ __forceinline__ void unpack(float (&f)[E]) const
     {
-        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                f[4 * i] = __uint_as_float(w[i].x);
-                f[4 * i + 1] = __uint_as_float(w[i].y);
-                f[4 * i + 2] = __uint_as_float(w[i].z);
-                f[4 * i + 3] = __uint_as_float(w[i].w);
-            }
-        } else {
-            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(u[i] << 16);
-                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-            }
+        for (int i = 0; i < 2; ++i) {
+            f[4 * i] = __uint_as_float(w[i].x);
+            f[4 * i + 1] = __uint_as_float(w[i].y);
+            f[4 * i + 2] = __uint_as_float(w[i].z);
+            f[4 * i + 3] = __uint_as_float(w[i].w);
         }
     }
 };
 
 // LPK lanes per key, R rows per CTA, U keys of a lane group in flight.
-template <class T, int LPK, int R, int U>
+template <int LPK, int R, int U>
 __global__ void __launch_bounds__(kRowThreads, 2) attn_rows_kernel(const AttnArgs a, const RowsGeom g, const AttnPartials part)
 {
     constexpr int KPW = 32 / LPK;   // keys per warp-wide load
     constexpr int DP = LPK * E;
-    __shared__ RowSums<R, DP> sm;
+    __shared__ WarpSums<R, DP> sm;
+    __shared__ CtaSums<R, DP> cs;
 
     pdl_trigger();   // the join kernel may be set up; it waits for this grid's end
     if (g.cluster > 1) cluster_arrive();
@@ -87,8 +73,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) attn_rows_kernel(const AttnArg
         for (int i = 0; i < E; ++i) f[i] = 0.f;
         if (row < rows && dact) {
             const int t = row / a.G, hq = h * a.G + row % a.G;
-            Chunk<T> x;
-            x.load(static_cast<const T *>(a.q) + n * a.qs.n + t * a.qs.t + hq * a.qs.h + dl * E);
+            Chunk x;
+            x.load(static_cast<const float *>(a.q) + n * a.qs.n + t * a.qs.t + hq * a.qs.h + dl * E);
             x.unpack(f);
         }
 #pragma unroll
@@ -101,8 +87,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) attn_rows_kernel(const AttnArg
     const int per = (len + g.splits - 1) / g.splits;   // Tk <= 2^30: no sum here passes 2^31
     const int k0 = (int)min((long long)len, (long long)split * per), k1 = min(len, k0 + per);
 
-    const T *kb = static_cast<const T *>(a.k) + n * a.ks.n + h * a.ks.h + dl * E;
-    const T *vb = static_cast<const T *>(a.v) + n * a.vs.n + h * a.vs.h + dl * E;
+    const float *kb = static_cast<const float *>(a.k) + n * a.ks.n + h * a.ks.h + dl * E;
+    const float *vb = static_cast<const float *>(a.v) + n * a.vs.n + h * a.vs.h + dl * E;
     const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
 
     float m[R], l[R], o[R][E];
@@ -115,7 +101,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) attn_rows_kernel(const AttnArg
     }
 
     constexpr int STEP = kRowWarps * KPW * U;
-    Chunk<T> kr[U], vr[U];
+    Chunk kr[U], vr[U];
     bool ok[U];
     // keys and values of this lane group's next U keys; invalid ones are not
     // read (whatever is stored there does not reach a sum)
@@ -135,7 +121,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) attn_rows_kernel(const AttnArg
     int base = k0 + warp * KPW * U;
     fetch(base);
     for (; base < k1; base += STEP) {
-        Chunk<T> kc[U], vc[U];
+        Chunk kc[U], vc[U];
         bool okc[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -227,34 +213,27 @@ __global__ void __launch_bounds__(kRowThreads, 2) attn_rows_kernel(const AttnArg
             }
         }
     }
-    finish_rows<T, R, DP>(sm, a, g, part, nh, row0, split);
+    finish_rows<float, R, DP>(sm, cs, a, g, part, nh, row0, split);
 }
 
-template <class T, int LPK, int U>
+template <int LPK, int U>
 cudaError_t launch_rows_r(const AttnArgs &a, cudaStream_t st)
 {
     const long long rows = (long long)a.Tq * a.G;
     constexpr int STEP = kRowWarps * (32 / LPK) * U;
-    const bool bf16 = sizeof(T) == 2;
-    if (rows == 1) return launch_rows_kernel(attn_rows_kernel<T, LPK, 1, U>, a, bf16, 1, STEP, 0, st);
-    if (rows == 2) return launch_rows_kernel(attn_rows_kernel<T, LPK, 2, U>, a, bf16, 2, STEP, 0, st);
-    if (rows == 3) return launch_rows_kernel(attn_rows_kernel<T, LPK, 3, U>, a, bf16, 3, STEP, 0, st);
-    return launch_rows_kernel(attn_rows_kernel<T, LPK, 4, U>, a, bf16, 4, STEP, 0, st);
-}
-
-template <class T>
-cudaError_t launch_rows_t(const AttnArgs &a, cudaStream_t st)
-{
-    if (a.D <= 32) return launch_rows_r<T, 4, 2>(a, st);
-    if (a.D <= 64) return launch_rows_r<T, 8, 2>(a, st);
-    return launch_rows_r<T, 16, 2>(a, st);
+    if (rows == 1) return launch_rows_kernel(attn_rows_kernel<LPK, 1, U>, a, false, 1, STEP, 0, st);
+    if (rows == 2) return launch_rows_kernel(attn_rows_kernel<LPK, 2, U>, a, false, 2, STEP, 0, st);
+    if (rows == 3) return launch_rows_kernel(attn_rows_kernel<LPK, 3, U>, a, false, 3, STEP, 0, st);
+    return launch_rows_kernel(attn_rows_kernel<LPK, 4, U>, a, false, 4, STEP, 0, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t st)
+cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t st)
 {
-    return bf16 ? launch_rows_t<__nv_bfloat16>(a, st) : launch_rows_t<float>(a, st);
+    if (a.D <= 32) return launch_rows_r<4, 2>(a, st);
+    if (a.D <= 64) return launch_rows_r<8, 2>(a, st);
+    return launch_rows_r<16, 2>(a, st);
 }
 
 }  // namespace sc

@@ -21,13 +21,18 @@ struct RowsGeom {
     int row_blocks;
 };
 
-// Shared memory of R rows of DP sums.
+// Shared memory of R rows of DP sums: the warps', and, in the cluster's first
+// CTA, those of its CTAs.  The other CTAs may write the latter as soon as the
+// first has arrived at the cluster's barrier (cluster_arrive).
 template <int R, int DP>
-struct RowSums {
+struct WarpSums {
     float o[kRowWarps][R][DP];
     float m[kRowWarps][R], l[kRowWarps][R];
-    // the cluster's CTAs' sums, in its first CTA
-    float cta_o[kMaxCluster][R][DP], cta_m[kMaxCluster][R], cta_l[kMaxCluster][R];
+};
+template <int R, int DP>
+struct CtaSums {
+    float o[kMaxCluster][R][DP];
+    float m[kMaxCluster][R], l[kMaxCluster][R];
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
@@ -60,9 +65,10 @@ __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // Every thread of the CTA calls this, its warps' sums written (m in units of
-// log2).  Row r of the block is row0 + r of (sequence, key head) nh.
+// log2) and cluster_arrive called, by when `cs` is no longer used for anything
+// else.  Row r of the block is row0 + r of (sequence, key head) nh.
 template <class T, int R, int DP>
-__device__ __forceinline__ void finish_rows(RowSums<R, DP> &sm, const AttnArgs &a, const RowsGeom &g,
+__device__ __forceinline__ void finish_rows(const WarpSums<R, DP> &sm, CtaSums<R, DP> &cs, const AttnArgs &a, const RowsGeom &g,
                                             const AttnPartials &part, int nh, int row0, int split)
 {
     const int tid = threadIdx.x, rows = a.Tq * a.G;
@@ -70,8 +76,7 @@ __device__ __forceinline__ void finish_rows(RowSums<R, DP> &sm, const AttnArgs &
     const int live = min(R, rows - row0);
     const int C = g.cluster, rank = split % C;
     __syncthreads();
-    // the CTA's sums, into its place in the shared memory of the cluster's
-    // first CTA (which is running: cluster_arrive at the kernel's start)
+    // the CTA's sums, into its place in the shared memory of the cluster's first CTA
     if (C > 1) cluster_wait();
     for (int e = tid; e < live * DP; e += kRowThreads) {
         const int r = e / DP, d = e % DP;
@@ -86,10 +91,10 @@ __device__ __forceinline__ void finish_rows(RowSums<R, DP> &sm, const AttnArgs &
             ls = fmaf(sm.l[w][r], f, ls);
             os = fmaf(sm.o[w][r][d], f, os);
         }
-        remote_store(&sm.cta_o[rank][r][d], os, C > 1);
+        remote_store(&cs.o[rank][r][d], os, C > 1);
         if (d == 0) {
-            remote_store(&sm.cta_m[rank][r], mm, C > 1);
-            remote_store(&sm.cta_l[rank][r], ls, C > 1);
+            remote_store(&cs.m[rank][r], mm, C > 1);
+            remote_store(&cs.l[rank][r], ls, C > 1);
         }
     }
     if (C > 1) {
@@ -107,9 +112,9 @@ __device__ __forceinline__ void finish_rows(RowSums<R, DP> &sm, const AttnArgs &
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c) {
             if (c < C) {
-                mc[c] = sm.cta_m[c][r];
-                lc[c] = sm.cta_l[c][r];
-                oc[c] = sm.cta_o[c][r][d];
+                mc[c] = cs.m[c][r];
+                lc[c] = cs.l[c][r];
+                oc[c] = cs.o[c][r][d];
                 mm = fmaxf(mm, mc[c]);
             }
         }

@@ -1,8 +1,10 @@
-// Splits fp32 queries, keys and values into three bf16 planes for the tensor
-// cores:  x0 = bf16(x), x1 = bf16(x - x0), x2 = bf16(x - x0 - x1), so that
-// x = x0 + x1 + x2 to 24 bits (the differences are exact).  A product x y is
-// then x0 y0 + x0 y1 + x1 y0 + (x0 y2 + x1 y1 + x2 y0), the terms left out
-// below 2^-24 |x y| (bf16 has fp32's range, so nothing over- or underflows
+// Copies queries, keys and values to the workspace in the order of the tensor
+// cores' tiles: fp32 ones split into three bf16 planes, bf16 ones (whose
+// strides the tiles' copies cannot address) as they are.
+//   x0 = bf16(x), x1 = bf16(x - x0), x2 = bf16(x - x0 - x1)
+// so that x = x0 + x1 + x2 to 24 bits (the differences are exact).  A product
+// x y is then x0 y0 + x0 y1 + x1 y0 + (x0 y2 + x1 y1 + x2 y0), the terms left
+// out below 2^-24 |x y| (bf16 has fp32's range, so nothing over- or underflows
 // that fp32 holds).  Bound by memory: 4 bytes read and 6 written an element.
 #include <cuda_bf16.h>
 
@@ -16,7 +18,7 @@ namespace {
 constexpr int kSplitThreads = 256;
 
 struct SplitPart {
-    const float *x;
+    const void *x;
     uint32_t *y;                 // bf16 planes, plane_words words apart
     long long plane_words;
     HeadStrides s;
@@ -29,6 +31,7 @@ struct SplitArgs {
     int D8;                      // D / 8
 };
 
+template <bool BF16>
 __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitArgs a)
 {
     const SplitPart &p = a.p[blockIdx.y];
@@ -38,11 +41,17 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitAr
         const int c = (int)(e - row * a.D8);
         const long long nt = row / p.H;
         const int h = (int)(row - nt * p.H), n = (int)(nt / p.T), t = (int)(nt - (long long)n * p.T);
-        const float4 *src = reinterpret_cast<const float4 *>(p.x + n * p.s.n + t * p.s.t + h * p.s.h + c * 8);
-        const float4 v0 = src[0], v1 = src[1];
-        float f[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        const long long at = n * p.s.n + t * p.s.t + h * p.s.h + c * 8;
         const long long orow = (((long long)n * (p.H / p.G) + h / p.G) * p.T + t) * p.G + h % p.G;
         uint32_t *dst = p.y + (orow * a.D8 + c) * 4;
+        if constexpr (BF16) {
+            *reinterpret_cast<uint4 *>(dst) =
+                *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) + at);
+            continue;
+        }
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + at);
+        const float4 v0 = src[0], v1 = src[1];
+        float f[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             uint32_t w[4];
@@ -60,7 +69,7 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitAr
 
 }  // namespace
 
-cudaError_t launch_attn_split(const AttnArgs &a, void *const (&planes)[3], cudaStream_t st)
+cudaError_t launch_attn_split(const AttnArgs &a, bool bf16, void *const (&planes)[3], cudaStream_t st)
 {
     SplitArgs s;
     s.D8 = a.D / 8;
@@ -69,7 +78,7 @@ cudaError_t launch_attn_split(const AttnArgs &a, void *const (&planes)[3], cudaS
     long long most = 0;
     for (int i = 0; i < 3; ++i) {
         SplitPart &p = s.p[i];
-        p.x = static_cast<const float *>(x[i]);
+        p.x = x[i];
         p.y = static_cast<uint32_t *>(planes[i]);
         p.s = hs[i];
         p.T = i ? a.Tk : a.Tq;
@@ -83,7 +92,10 @@ cudaError_t launch_attn_split(const AttnArgs &a, void *const (&planes)[3], cudaS
     long long blocks = (most + kSplitThreads - 1) / kSplitThreads;
     const long long cap = 16LL * device_sm_count();
     if (blocks > cap) blocks = cap;
-    attn_split_kernel<<<dim3((unsigned)blocks, 3), kSplitThreads, 0, st>>>(s);
+    if (bf16)
+        attn_split_kernel<true><<<dim3((unsigned)blocks, 3), kSplitThreads, 0, st>>>(s);
+    else
+        attn_split_kernel<false><<<dim3((unsigned)blocks, 3), kSplitThreads, 0, st>>>(s);
     return cudaGetLastError();
 }
 

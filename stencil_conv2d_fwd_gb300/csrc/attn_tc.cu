@@ -17,12 +17,20 @@
 // Warps 0-3 and 4-7 are the streams' softmax, one thread per row (a warp
 // reads the quadrant of tensor memory that it may address): scores from
 // tensor memory, masked, 2^x, and P back to tensor memory as the second
-// product's A operand, over the scores' columns.  O is rescaled only when a
-// row's maximum has grown by more than 2^8 since the last rescaling (P then
-// stays below 256, exact in every type here); the division at the end cancels
-// the common factor.  Warp 8 issues the TMA copies, warp 9 the MMAs, warps
-// 10-11 clear the value rows of states that a length or a mask leaves out
-// (their weight is 0, but 0 times an infinity would not be).
+// product's A operand, over the scores' columns.  With bf16 tensors O is
+// rescaled only when a row's maximum has grown by more than 2^8 since the last
+// rescaling (P then stays below 256); the division at the end cancels the
+// common factor.  Warp 8 issues the TMA copies, warp 9 the MMAs.
+//
+// States that a mask leaves out are not read and not computed with: the CTA
+// counts the valid states of its share, warp 8 lists them tile by tile, and
+// warps 8, 10 and 11 copy their rows, 16 bytes a lane (cp.async, into the
+// places where a TMA copy would put them), so that the key tiles are dense
+// and only the last one has scores to leave out.  The last tile of a length is
+// copied the same way.  Rows past the last valid state are zero: what is
+// stored there does not reach a product.  (TMA gathers of four rows took 118
+// us where these copies take MASKED_US, 32 x 77 queries over masked 56 x 56
+// maps, 8 heads of 64.)
 //
 // Accumulators, softmax and sums are fp32.  bf16 tensors: P is rounded to bf16
 // for the second product (a relative error of 2^-8 of single terms, the size
@@ -61,7 +69,7 @@ constexpr int key_tile() { return PL == 3 && DP == 128 ? 64 : 128; }
 constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 216, REGS_OTHER = 72;
 constexpr int THREADS = 384;
 constexpr int MAX_SLOTS = 12;
-constexpr int VC = 8;                  // barriers of cleared value tiles: more than the ring holds
+constexpr int LIST = 512;              // listed states: a tile in use, two ahead and a piece of 128
 constexpr float GROW = 8.f;            // log2 growth of a row's maximum that rescales O
 constexpr size_t SMEM_CAP = 227 * 1024;
 
@@ -70,8 +78,10 @@ struct Geom {
     int units;            // CTAs' row units of it: pairs of row tiles, or row tiles
     int tb, gb, gblocks;  // tokens and group heads of a row tile; blocks of gb heads
     int splits;           // CTAs that share a row unit's keys
-    int slots;
-    uint32_t smem;
+    bool packed;          // q, k and v are the workspace's copies (attn_split.cu)
+    int k_axes[2], v_axes[2];        // whether the maps' (h, n) are axes (1), or shared by all (0)
+    const void *k, *v;               // bf16 keys and values (of plane 0), for copies by row,
+    long long k_row[4], v_row[4];    // and their strides: token, head, sequence, plane
 };
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int c0, int c1, int c2, int c3, int c4,
@@ -185,14 +195,41 @@ constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t DESC_LO_K = 1u << 16;
 constexpr uint32_t desc_lo_v(int key_tile) { return (uint32_t)(key_tile * 128 >> 4) << 16; }
 
+template <bool PAIR>
 struct Shared {
-    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], vclean[VC], q_full, s_full[2], p_full[2][2], o_full[2];
-    uint32_t words[2][2][4];   // valid bits of a key tile, per stream, two tiles deep
-    float m[TILE], l[TILE];
-    uint64_t drain;
+    // barriers of one arrival (full: with a mask three), then those of the four warps of a stream
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], q_full, s_full[2], o_full[2], drain;
+    uint64_t p_full[2][2];
+    int list[LIST];   // states of the coming tiles
+    float m[PAIR ? 1 : TILE], l[PAIR ? 1 : TILE];   // stream 1's, at the end
+    int counts[THREADS / 32];
     uint32_t tmem;
     int abort;
 };
+constexpr int BARS_ONE = 2 * MAX_SLOTS + 6, BARS = BARS_ONE + 4;
+
+template <int N>
+struct Warps {
+    static constexpr int value = N;
+};
+
+// How many of the n bytes at p are not 0, over the CTA's threads (each one's
+// part).
+__device__ __forceinline__ int count_part(const unsigned char *p, int n, int tid)
+{
+    const int head = min(n, (int)(-reinterpret_cast<uintptr_t>(p) & 15u));
+    const int body = (n - head) / 16, tail = n - head - 16 * body;
+    int c = 0;
+    if (tid < head) c += p[tid] != 0;
+    if (tid < tail) c += p[head + 16 * body + tid] != 0;
+    const uint4 *v = reinterpret_cast<const uint4 *>(p + head);
+#pragma unroll 4
+    for (int i = tid; i < body; i += THREADS) {
+        const uint4 w = v[i];
+        c += __popc(__vsetne4(w.x, 0u)) + __popc(__vsetne4(w.y, 0u)) + __popc(__vsetne4(w.z, 0u)) + __popc(__vsetne4(w.w, 0u));
+    }
+    return c;
+}
 
 // Shared memory: row tiles (of one row tile at least the room of its 128 x DP
 // fp32 sums, which the streams' join uses), the ring, then Shared.
@@ -200,6 +237,13 @@ template <int DP, int PL, bool PAIR>
 constexpr int q_region()
 {
     return (PAIR ? 2 * PL : (PL > 2 ? PL : 2)) * (DP / 64) * BLK;   // a multiple of 1024
+}
+
+template <int DP, int PL, bool PAIR>
+constexpr int ring_slots()
+{
+    const int n = ((int)SMEM_CAP - q_region<DP, PL, PAIR>() - (int)sizeof(Shared<PAIR>)) / (DP / 64 * key_tile<DP, PL>() * 128);
+    return n < MAX_SLOTS ? n : MAX_SLOTS;
 }
 
 // PL operand planes: 1 (bf16 tensors), or 3 (fp32 tensors split into three
@@ -215,8 +259,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int KT = key_tile<DP, PL>();
     constexpr int KBLK = KT * 128;              // bytes of a key tile's rows of 64 bf16
     constexpr int SLOT = DB * KBLK;
+    constexpr int SLOTS = ring_slots<DP, PL, PAIR>();
     extern __shared__ __align__(1024) unsigned char dyn[];
-    Shared &sh = *reinterpret_cast<Shared *>(dyn + q_region<DP, PL, PAIR>() + g.slots * SLOT);
+    Shared<PAIR> &sh = *reinterpret_cast<Shared<PAIR> *>(dyn + q_region<DP, PL, PAIR>() + SLOTS * SLOT);
 
     // (the shuffle makes the warp's number, and all that follows from it, uniform)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -233,34 +278,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int n = nh / a.Hkv, h = nh - n * a.Hkv;
     int len = a.Tk;
     if (a.k_len) len = max(0, min(len, a.k_len[n]));
-    const bool ragged = a.key_mask != nullptr || len < a.Tk;   // value rows to clear
     const int tiles_all = (len + KT - 1) / KT;
     const int t_begin = (int)((long long)tiles_all * split / g.splits);
-    const int nt = (int)((long long)tiles_all * (split + 1) / g.splits) - t_begin;
-
-    if (tid == 0) {
-        for (int i = 0; i < MAX_SLOTS; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 1);
-            mbar_init(smem_u32(&sh.empty[i]), 1);
-        }
-        for (int i = 0; i < VC; ++i) mbar_init(smem_u32(&sh.vclean[i]), 2);
-        mbar_init(smem_u32(&sh.q_full), 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.s_full[i]), 1);
-            for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&sh.p_full[i][k]), 4);
-            mbar_init(smem_u32(&sh.o_full[i]), 1);
-        }
-        mbar_init(smem_u32(&sh.drain), 1);
-        sh.abort = 0;
-        fence_mbar_init();
-    }
-    if (warp == 9) tc::tmem_alloc(smem_u32(&sh.tmem), 512);
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
-    constexpr int P1 = KT, P2 = DP == 64 ? KT / 2 : KT + KT / 2, TO = 256 - DP;   // columns of a stream
-    auto p_plane = [](int p) { return p == 0 ? 0 : (p == 1 ? P1 : P2); };
+    const int t_end = (int)((long long)tiles_all * (split + 1) / g.splits);
+    const int key_begin = t_begin * KT, key_end = min(len, t_end * KT);   // this CTA's share
+    const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
+    int keys = max(0, key_end - key_begin);   // valid states of the share
+    int nt = (keys + KT - 1) / KT;            // and key tiles
 
     // A wait that runs out marks the CTA: every later wait returns at once and
     // all loops, which are finite, run to their end.
@@ -281,43 +305,196 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Order of the ring's tiles, the order in which the MMAs use them: the
     // first LAG key tiles, then value tile j and key tile j + LAG in turn.
     constexpr int LAG = PAIR ? 1 : 2;
-    uint32_t issued = 0;   // ring entries whose copies have been issued (the copying thread's count)
+    uint32_t issued = 0;          // ring entries whose copies have been issued
+    int listed = 0, scan = key_begin;   // states listed, and the next one to look at
+    constexpr int AHEAD = 4;      // pieces of 128 bytes of the mask that are read ahead,
+    int byte[AHEAD][4];           // four bytes a lane
+    auto read_mask = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = scan + 128 * b + 32 * i + lane;
+            byte[b][i] = key < key_end ? (int)mb[key] : 0;
+        }
+    };
+    // The seq-th tile: its kind and number.
+    auto tile_of = [&](int seq, bool &value) -> int {
+        const int l0 = min(LAG, nt), both = 2 * (nt - l0), s = seq - l0;
+        value = seq >= l0 && (s >= both || (s & 1) == 0);
+        return seq < l0 ? seq : (s >= both ? nt - l0 + s - both : (value ? s / 2 : l0 + s / 2));
+    };
+    // Copies by row: a warp's part (w of `warps`) of a tile is every warps-th
+    // group of four rows, eight lanes a row.  The rows' states, -1 past the last:
+    const int r4 = lane >> 3, chunk = lane & 7;
+    auto rows_of = [&](int tile, int w, auto warps, auto &state) {
+        constexpr int W = decltype(warps)::value;
+#pragma unroll
+        for (int i = 0; i < (KT / 4 + W - 1) / W; ++i) {
+            const int at = tile * KT + 4 * (w + W * i) + r4;
+            state[i] = -1;
+            // (in range whatever the list holds, should the mask change under the call)
+            if (w + W * i < KT / 4 && at < keys)
+                state[i] = mb ? (int)min((uint32_t)sh.list[at % LIST], (uint32_t)a.Tk - 1u) : key_begin + at;
+        }
+    };
+    // ... and their copies to ring entry `slot`, plane p.  (The states are in
+    // registers by then: between two copies nothing is read.)
+    auto copy_rows = [&](uint32_t slot, bool value, int p, int w, auto warps, const auto &state) {
+        constexpr int W = decltype(warps)::value;
+        const long long *st = value ? g.v_row : g.k_row;
+        const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(value ? g.v : g.k);
+        const __nv_bfloat16 *src = base + n * st[2] + h * st[1] + p * st[3] + chunk * 8;
+        const long long pitch = st[0];
+        const uint32_t dst = ring + slot * SLOT + r4 * 128;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+            const bool on = d * 64 + chunk * 8 < a.D;
+#pragma unroll
+            for (int i = 0; i < (KT / 4 + W - 1) / W; ++i) {
+                const int rows4 = w + W * i;   // rows 4 rows4 + r4
+                if (rows4 >= KT / 4) break;
+                const bool live = on && state[i] >= 0;
+                cp_async16(dst + d * KBLK + rows4 * 512 + ((chunk ^ ((4 * rows4 + r4) & 7)) << 4),
+                           live ? src + state[i] * pitch + d * 64 : base, live ? 16 : 0);
+            }
+        }
+    };
+    // Lists states until `need` of them are listed.
+    auto list_states = [&](int need) {
+        while (listed < need && scan < key_end) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t ok = __ballot_sync(0xffffffffu, byte[0][i] != 0);
+                if (byte[0][i] != 0) sh.list[(listed + __popc(ok & ((1u << lane) - 1u))) % LIST] = scan + 32 * i + lane;
+                listed += __popc(ok);
+#pragma unroll
+                for (int b = 0; b + 1 < AHEAD; ++b) byte[b][i] = byte[b + 1][i];
+            }
+            scan += 128;
+            read_mask(AHEAD - 1);
+        }
+    };
+    // Without a mask: the TMA copies of the seq-th tile (the last tile of a
+    // length by row); the whole of warp 8 calls it.
+    auto load_tile = [&](int seq) {
+        bool value;
+        const int tile = tile_of(seq, value), key0 = key_begin + tile * KT;
+        const bool whole = key0 + KT <= key_end || key_end == a.Tk;   // rows past the tensor's end read as zero
+        for (int p = PL - 1; p >= 0; --p, ++issued) {   // the smallest plane first
+            const uint32_t slot = issued % SLOTS, round = issued / SLOTS;
+            const uint32_t bar = smem_u32(&sh.full[slot]);
+            if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
+            if (*abort_flag) return;
+            if (whole) {
+                const int *ax = value ? g.v_axes : g.k_axes;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, SLOT);
+                    for (int d = 0; d < DB; ++d)
+                        tma_load_5d(ring + slot * SLOT + d * KBLK, value ? &mv : &mk, d * 64, key0, h * ax[0], n * ax[1], p, bar);
+                }
+            } else {
+                int state[KT / 4];
+                rows_of(tile, 0, Warps<1>{}, state);
+                copy_rows(slot, value, p, 0, Warps<1>{}, state);
+                cp_async_commit();
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+            }
+        }
+    };
+    // With a mask: warp w of three copies its part of every tile, PEND ring
+    // entries behind which it tells the MMA warp of the one that has landed.
+    // (An entry is released once the 2 PL after it have been multiplied.)
+    auto copy_tiles = [&](int w) {
+        constexpr int PEND = SLOTS - 2 * PL < 4 ? SLOTS - 2 * PL : 4;
+        static_assert(PEND >= 1, "a ring of more than two tiles");
+        uint32_t told = 0;
+        auto tell = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.full[told % SLOTS]));
+            ++told;
+        };
+        for (int seq = 0; seq < 2 * nt; ++seq) {
+            bool value;
+            const int tile = tile_of(seq, value);
+            if (w == 0) list_states(min((tile + 1) * KT, keys));
+            // the list is written; and all three have read it for the tile before
+            named_sync<2, 96>();
+            int state[(KT / 4 + 2) / 3];
+            rows_of(tile, w, Warps<3>{}, state);
+            for (int p = PL - 1; p >= 0; --p, ++issued) {
+                const uint32_t slot = issued % SLOTS, round = issued / SLOTS;
+                if (issued > PEND) {
+                    cp_async_wait<PEND>();
+                    tell();
+                }
+                if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
+                copy_rows(slot, value, p, w, Warps<3>{}, state);
+                cp_async_commit();
+            }
+        }
+        cp_async_wait<0>();
+        while (told < issued) tell();
+    };
+
+    int ahead = 0;   // tiles whose copies are issued before the CTA's barrier
+    if (warp == 8) {
+        for (int i = lane; i < BARS; i += 32) mbar_init(smem_u32(&sh.full[0]) + 8 * i, i < MAX_SLOTS ? (mb ? 3 : 1) : (i < BARS_ONE ? 1 : 4));
+        if (lane == 0) sh.abort = 0;
+        fence_mbar_init();
+        __syncwarp();
+        if (lane == 0 && nt > 0) {
+            // row tiles: tokens and heads past the end read as zero
+            mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(QT * PL * DB * g.gb * g.tb * 128));
+            for (int i = 0; i < QT; ++i) {
+                const int rt = unit * QT + i;
+                const int tok = rt / g.gblocks * g.tb, gh = rt % g.gblocks * g.gb;
+                for (int p = 0; p < PL; ++p)
+                    for (int d = 0; d < DB; ++d)
+                        tma_load_5d(q_smem + ((i * PL + p) * DB + d) * BLK, &mq, d * 64, gh, tok, g.packed ? nh : h,
+                                    g.packed ? p : n, smem_u32(&sh.q_full));
+            }
+        }
+        __syncwarp();
+        // with a mask the number of tiles is not known yet
+        if (!mb)
+            for (; ahead < 2 * nt && (ahead + 1) * PL <= SLOTS; ++ahead) load_tile(ahead);
+    } else if (warp == 9) {
+        tc::tmem_alloc(smem_u32(&sh.tmem), 512);
+    }
+    if (mb) {
+        const int c = __reduce_add_sync(0xffffffffu, count_part(mb + key_begin, keys, tid));
+        if (lane == 0) sh.counts[warp] = c;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
+    const int q_tiles = nt;   // the row tiles have been asked for
+    if (mb) {
+        keys = 0;
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) keys += sh.counts[i];
+        nt = (keys + KT - 1) / KT;
+    }
+    constexpr int P1 = KT, P2 = DP == 64 ? KT / 2 : KT + KT / 2, TO = 256 - DP;   // columns of a stream
+    auto p_plane = [](int p) { return p == 0 ? 0 : (p == 1 ? P1 : P2); };
 
     if (warp >= 8) {
         // one instruction for the four warps, as its form asks
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_OTHER));
         if (warp == 8) {
-            if (lane == 0 && nt > 0) {
-                // row tiles: tokens and heads past the end read as zero
-                mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(QT * PL * DB * g.gb * g.tb * 128));
-                for (int i = 0; i < QT; ++i) {
-                    const int rt = unit * QT + i;
-                    const int tok = rt / g.gblocks * g.tb, gh = rt % g.gblocks * g.gb;
-                    for (int p = 0; p < PL; ++p)
-                        for (int d = 0; d < DB; ++d)
-                            tma_load_5d(q_smem + ((i * PL + p) * DB + d) * BLK, &mq, d * 64, gh, tok, PL == 1 ? h : nh,
-                                        PL == 1 ? n : p, smem_u32(&sh.q_full));
-                }
-                // (h, n) of the tensor; 0 on an axis that all share (the planes share none)
-                const int kh = PL > 1 || a.ks.h ? h : 0, kn = PL > 1 || a.ks.n ? n : 0;
-                const int vh = PL > 1 || a.vs.h ? h : 0, vn = PL > 1 || a.vs.n ? n : 0;
-                auto load = [&](const CUtensorMap *map, int tile, int ch, int cn) {
-                    for (int p = PL - 1; p >= 0; --p, ++issued) {   // the smallest plane first
-                        const uint32_t slot = issued % g.slots, round = issued / g.slots;
-                        if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
-                        if (*abort_flag) return;
-                        mbar_arrive_expect_tx(smem_u32(&sh.full[slot]), SLOT);
-                        for (int d = 0; d < DB; ++d)
-                            tma_load_5d(ring + slot * SLOT + d * KBLK, map, d * 64, (t_begin + tile) * KT, ch, cn, p,
-                                        smem_u32(&sh.full[slot]));
-                    }
-                };
-                for (int j = 0; j < LAG && j < nt; ++j) load(&mk, j, kh, kn);
-                for (int j = 0; j < nt; ++j) {
-                    load(&mv, j, vh, vn);
-                    if (j + LAG < nt) load(&mk, j + LAG, kh, kn);
-                }
+            if (mb) {
+#pragma unroll
+                for (int b = 0; b < AHEAD; ++b) read_mask(b);
+                copy_tiles(0);
+            } else {
+                for (int seq = ahead; seq < 2 * nt; ++seq) load_tile(seq);
             }
+            // a mask that leaves nothing: no one else waits for the row tiles
+            if (nt == 0 && q_tiles > 0) wait(sh.q_full, 0);
             __syncwarp();
         } else if (warp == 9) {
             if (nt > 0) {
@@ -328,8 +505,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 auto mma_s = [&](int i, uint32_t c, bool release) {
 #pragma unroll
                     for (int pk = PL - 1; pk >= 0; --pk, ++c) {
-                        const uint32_t slot = c % g.slots;
-                        wait(sh.full[slot], (c / g.slots) & 1);
+                        const uint32_t slot = c % SLOTS;
+                        wait(sh.full[slot], (c / SLOTS) & 1);
                         tc::fence_after_sync();
                         const uint32_t kb = ((ring + slot * SLOT) >> 4) | DESC_LO_K;
 #pragma unroll
@@ -348,17 +525,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 };
                 // O of stream i = P V (fp32 tensors), or += P V; use = the stream's count of P tiles so far
                 // P comes in two halves of the key tile: the first half's products run while the second is made
-                auto mma_v = [&](int i, uint32_t c, int j, uint32_t use, bool release, bool last) {
+                auto mma_v = [&](int i, uint32_t c, uint32_t use, bool release, bool last) {
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
                         wait(sh.p_full[i][part], use & 1);
-                        if (part == 0 && ragged) wait(sh.vclean[j % VC], (j / VC) & 1);
                         tc::fence_after_sync();
 #pragma unroll
                         for (int pv = PL - 1; pv >= 0; --pv) {
-                            const uint32_t e = c + (PL - 1 - pv), slot = e % g.slots;
+                            const uint32_t e = c + (PL - 1 - pv), slot = e % SLOTS;
                             if (part == 0) {
-                                wait(sh.full[slot], (e / g.slots) & 1);
+                                wait(sh.full[slot], (e / SLOTS) & 1);
                                 tc::fence_after_sync();
                             }
                             const uint32_t vb = ((ring + slot * SLOT) >> 4) | desc_lo_v(KT);
@@ -380,9 +556,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t c = PL;
                     for (int j = 0; j < nt; ++j) {
                         const bool more = j + 1 < nt;
-                        mma_v(0, c, j, j, false, !more);
+                        mma_v(0, c, j, false, !more);
                         if (more) mma_s(0, c + PL, false);
-                        mma_v(1, c, j, j, true, !more);
+                        mma_v(1, c, j, true, !more);
                         if (more) mma_s(1, c + PL, true);
                         c += more ? 2 * PL : PL;
                     }
@@ -392,7 +568,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t c = nt > 1 ? 2 * PL : PL;
                     for (int j = 0; j < nt; ++j) {
                         const bool more = j + 2 < nt;
-                        mma_v(j & 1, c, j, j >> 1, true, !more);
+                        mma_v(j & 1, c, j >> 1, true, !more);
                         c += PL;
                         if (more) {
                             mma_s(j & 1, c, true);
@@ -402,46 +578,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             __syncwarp();
-        } else {
-            // value rows that are not valid: zero, in every plane and block
-            if (ragged) {
-                // every entry of the ring is waited for in turn, the key tiles' too: a
-                // barrier's parity tells a round only from its neighbours
-                uint32_t c = 0;
-                auto pass = [&]() {
-                    for (int p = 0; p < PL; ++p, ++c) wait(sh.full[c % g.slots], (c / g.slots) & 1);
-                };
-                for (int j = 0; j < LAG && j < nt; ++j) pass();
-                const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
-                constexpr int KW = KT / 64;   // keys of a lane: two warps share the tile
-                for (int j = 0; j < nt; ++j) {
-                    const int row0 = (warp - 10) * 32 * KW + lane;
-                    bool bad[KW];
-#pragma unroll
-                    for (int i = 0; i < KW; ++i) {
-                        const int key = (t_begin + j) * KT + row0 + i * 32;
-                        // states past Tk are not in the tensor and read as zero
-                        bad[i] = key < a.Tk && (key >= len || (mb && mb[key] == 0));
-                    }
-                    for (int p = 0; p < PL; ++p, ++c) {
-                        const uint32_t slot = c % g.slots;
-                        wait(sh.full[slot], (c / g.slots) & 1);
-#pragma unroll
-                        for (int i = 0; i < KW; ++i) {
-                            if (!bad[i]) continue;
-                            const uint32_t at = ring + slot * SLOT + (row0 + i * 32) * 128;
-                            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)   // from chunk `lane` on: no two lanes in one bank
-                                    tc::st_shared_v4(at + d * KBLK + ((e + lane) & 7) * 16, 0u, 0u, 0u, 0u);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.vclean[j % VC]));
-                    if (j + LAG < nt) pass();
-                }
-            }
+        } else if (mb) {
+            copy_tiles(warp - 9);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS_SOFTMAX));
@@ -455,15 +593,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         float acc[PL == 3 ? DP : 1];    // fp32 tensors: the row's sums, relative to m
 #pragma unroll
         for (int d = 0; d < (PL == 3 ? DP : 1); ++d) acc[d] = 0.f;
-        const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
         constexpr int KW = KT / 32;     // words of a tile's valid bits
         int use = 0;
-        // this thread's byte of key tile j: 0 where the state is not valid
-        auto mask_byte = [&](int j) {
-            const int key = (t_begin + j) * KT + row;
-            return row < KT && j < nt && key < len ? (int)mb[key] : 0;
-        };
-        int next = mb ? mask_byte(PAIR ? 0 : i) : 0;
         // half of a key tile's P is in tensor memory
         auto hand_over = [&](int part) {
             tmem_wait_st();
@@ -482,34 +613,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         };
         for (int j = PAIR ? 0 : i; j < nt; j += step, ++use) {
-            const int key0 = (t_begin + j) * KT;
+            // only the last tile has scores that are not valid
+            const bool masked = (j + 1) * KT > keys;
             uint32_t w[KW];
 #pragma unroll
-            for (int e = 0; e < KW; ++e) w[e] = ~0u;
-            bool masked = key0 + KT > len;
-            if (mb) {
-                // one key per thread, a word per warp; the next tile's byte is
-                // read a tile ahead (its latency was a third of a masked tile's time)
-                const uint32_t word = __ballot_sync(0xffffffffu, next != 0);
-                next = mask_byte(j + step);
-                if (lane == 0) sh.words[i][use & 1][warp & 3] = word;
-                if (i == 0)
-                    named_sync<1, 128>();
-                else
-                    named_sync<2, 128>();
-                uint32_t all = ~0u;
-#pragma unroll
-                for (int e = 0; e < KW; ++e) {
-                    w[e] = sh.words[i][use & 1][e];
-                    all &= w[e];
-                }
-                masked = all != ~0u;
-            } else if (masked) {
-#pragma unroll
-                for (int e = 0; e < KW; ++e) {
-                    const int left = len - key0 - 32 * e;
-                    w[e] = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
-                }
+            for (int e = 0; e < KW; ++e) {
+                const int left = keys - j * KT - 32 * e;
+                w[e] = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
             }
             wait(sh.s_full[i], use & 1);
             tc::fence_after_sync();
@@ -681,9 +791,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                named_sync<3, 256>();
+                named_sync<1, 256>();
             } else {
-                named_sync<3, 256>();
+                named_sync<1, 256>();
                 const float m1 = sh.m[row], l1 = sh.l[row];
                 const float mm = fmaxf(m, m1), ms = mm == -INFINITY ? 0.f : mm;
                 f0 = ex2(m - ms);
@@ -745,10 +855,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         // give the copies and products in flight their time to end before the
         // shared and tensor memory are given back
         if (tid == 0) atomicExch(status, kDeviceTimeout);
-        if (warp == 8 && lane == 0 && nt > 0) {
-            (void)mbar_wait_bounded(smem_u32(&sh.q_full), 0, timeout_ns);
-            for (uint32_t e = issued > (uint32_t)g.slots ? issued - g.slots : 0; e < issued; ++e)
-                (void)mbar_wait_bounded(smem_u32(&sh.full[e % g.slots]), (e / g.slots) & 1, timeout_ns);
+        if (warp == 8 && lane == 0) {
+            if (q_tiles > 0) (void)mbar_wait_bounded(smem_u32(&sh.q_full), 0, timeout_ns);
+            // (copies by row have been waited for by their threads)
+            for (uint32_t e = issued > (uint32_t)SLOTS ? issued - SLOTS : 0; e < issued && !mb; ++e)
+                (void)mbar_wait_bounded(smem_u32(&sh.full[e % SLOTS]), (e / SLOTS) & 1, timeout_ns);
         }
         if (warp == 9 && lane == 0) {
             tc::mma_commit(smem_u32(&sh.drain));
@@ -792,20 +903,21 @@ bool encode_map(CUtensorMap *m, const void *base, int D, const long long (&size)
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
 template <int DP, int PL, bool PAIR>
-cudaError_t launch(const AttnArgs &a, Geom g, const CUtensorMap (&maps)[3], const AttnPartials &part, cudaStream_t st)
+cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPartials &part, cudaStream_t st)
 {
-    constexpr int SLOT = DP / 64 * key_tile<DP, PL>() * 128;
-    const size_t fixed = q_region<DP, PL, PAIR>() + sizeof(Shared);
-    g.slots = (int)((SMEM_CAP - fixed) / SLOT);
-    if (g.slots > MAX_SLOTS) g.slots = MAX_SLOTS;
-    g.smem = (uint32_t)(fixed + (size_t)g.slots * SLOT);
+    constexpr int SMEM = q_region<DP, PL, PAIR>() + ring_slots<DP, PL, PAIR>() * (DP / 64 * key_tile<DP, PL>() * 128) +
+                         (int)sizeof(Shared<PAIR>);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     static KernelCache cache;
-    e = ensure_dynamic_smem(cache, dev, attn_tc_kernel<DP, PL, PAIR>, (int)g.smem);
+    e = ensure_dynamic_smem(cache, dev, attn_tc_kernel<DP, PL, PAIR>, SMEM);
     if (e != cudaSuccess) return e;
     // the register split is of REGS_LAUNCH a thread: with fewer, a warp would wait for registers that never come
     static const int regs = [] {
@@ -817,7 +929,7 @@ cudaError_t launch(const AttnArgs &a, Geom g, const CUtensorMap (&maps)[3], cons
     if (!status) return cudaErrorInvalidDevice;
     const long long grid = (long long)a.N * a.Hkv * g.units * g.splits;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    attn_tc_kernel<DP, PL, PAIR><<<(unsigned)grid, THREADS, g.smem, st>>>(maps[0], maps[1], maps[2], a, g, part, status,
+    attn_tc_kernel<DP, PL, PAIR><<<(unsigned)grid, THREADS, SMEM, st>>>(m.q, m.k, m.v, a, g, part, status,
                                                                        1000000000ull);
     return cudaGetLastError();
 }
@@ -827,11 +939,6 @@ cudaError_t launch(const AttnArgs &a, Geom g, const CUtensorMap (&maps)[3], cons
 cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
 {
     if (!at::encoder()) return cudaErrorNotSupported;
-    // a shared axis (stride 0) of bf16 keys or values is one coordinate of the
-    // map; the row tiles, and key tiles, need their own axes
-    if (bf16 && ((a.G > 1 && a.qs.h == 0) || (a.Tq > 1 && a.qs.t == 0) || (a.Hkv > 1 && a.qs.h == 0) ||
-                 (a.N > 1 && a.qs.n == 0) || (a.Tk > 1 && (a.ks.t == 0 || a.vs.t == 0))))
-        return cudaErrorNotSupported;
     at::Geom g = {};
     g.gb = a.G < at::TILE ? a.G : at::TILE;
     g.tb = at::TILE / g.gb;
@@ -851,13 +958,24 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
     if (splits < 1) splits = 1;
     g.splits = (int)splits;
 
-    // workspace: partial results, and the planes of fp32 tensors
+    // fp32 tensors are split into planes; bf16 ones are used as they lie where
+    // the TMA copies can address them: axes of the row and key tiles that are
+    // not shared
+    g.packed = !bf16 || (a.G > 1 && a.qs.h == 0) || (a.Tq > 1 && a.qs.t == 0) || (a.Hkv > 1 && a.qs.h == 0) ||
+               (a.N > 1 && a.qs.n == 0) || (a.Tk > 1 && (a.ks.t == 0 || a.vs.t == 0));
     const int planes = bf16 ? 1 : 3;
     const long long rows = (long long)a.N * a.Hq * a.Tq, keys = (long long)a.N * a.Hkv * a.Tk;
+    g.k_axes[0] = g.packed || a.ks.h != 0;
+    g.k_axes[1] = g.packed || a.ks.n != 0;
+    g.v_axes[0] = g.packed || a.vs.h != 0;
+    g.v_axes[1] = g.packed || a.vs.n != 0;
+
+    // workspace: partial results, and the packed tensors
     auto pad = [](size_t b) { return (b + 255) & ~(size_t)255; };
     const size_t po = g.splits > 1 ? pad((size_t)g.splits * rows * a.D * 4) : 0;
     const size_t pml = g.splits > 1 ? pad((size_t)g.splits * rows * sizeof(float2)) : 0;
-    const size_t pq = bf16 ? 0 : pad((size_t)rows * a.D * 6), pk = bf16 ? 0 : pad((size_t)keys * a.D * 6);
+    const size_t pq = g.packed ? pad((size_t)rows * a.D * 2 * planes) : 0;
+    const size_t pk = g.packed ? pad((size_t)keys * a.D * 2 * planes) : 0;
     char *ws = nullptr;
     if (po + pml + pq + pk > 0) {
         const cudaError_t e = workspace_alloc(reinterpret_cast<void **>(&ws), po + pml + pq + 2 * pk, st);
@@ -867,40 +985,46 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
     if (g.splits > 1) part = AttnPartials{reinterpret_cast<float *>(ws), reinterpret_cast<float2 *>(ws + po), g.splits};
     void *const plane[3] = {ws + po + pml, ws + po + pml + pq, ws + po + pml + pq + pk};
 
-    CUtensorMap maps[3];
+    at::Maps m;
+    std::memset(&m, 0, sizeof(m));
     bool ok;
-    if (bf16) {
-        const long long size[4] = {a.G, a.Tq, a.Hkv, a.N};
-        const long long stride[4] = {a.qs.h * 2, a.qs.t * 2, a.qs.h * a.G * 2, a.qs.n * 2};
-        ok = at::encode_map(&maps[0], a.q, a.D, size, stride, g.gb, g.tb);
-    } else {
+    g.k = g.packed ? plane[1] : a.k;
+    g.v = g.packed ? plane[2] : a.v;
+    const long long packed_row[4] = {a.D, (long long)a.D * a.Tk, (long long)a.D * a.Tk * a.Hkv, (long long)a.D * keys};
+    const long long k_row[4] = {a.ks.t, a.ks.h, a.ks.n, 0}, v_row[4] = {a.vs.t, a.vs.h, a.vs.n, 0};
+    std::memcpy(g.k_row, g.packed ? packed_row : k_row, sizeof(k_row));
+    std::memcpy(g.v_row, g.packed ? packed_row : v_row, sizeof(v_row));
+    if (g.packed) {
         const long long size[4] = {a.G, a.Tq, (long long)a.N * a.Hkv, planes}, d = a.D * 2LL;
         const long long stride[4] = {d, d * a.G, d * a.G * a.Tq, d * rows};
-        ok = at::encode_map(&maps[0], plane[0], a.D, size, stride, g.gb, g.tb);
-    }
-    for (int i = 0; i < 2 && ok; ++i) {
-        if (bf16) {
+        ok = at::encode_map(&m.q, plane[0], a.D, size, stride, g.gb, g.tb);
+        const long long ksize[4] = {a.Tk, a.Hkv, a.N, planes};
+        const long long kstride[4] = {d, d * a.Tk, d * a.Tk * a.Hkv, d * keys};
+        ok = ok && at::encode_map(&m.k, g.k, a.D, ksize, kstride, kt, 1) &&
+             at::encode_map(&m.v, g.v, a.D, ksize, kstride, kt, 1);
+    } else {
+        const long long size[4] = {a.G, a.Tq, a.Hkv, a.N};
+        const long long stride[4] = {a.qs.h * 2, a.qs.t * 2, a.qs.h * a.G * 2, a.qs.n * 2};
+        ok = at::encode_map(&m.q, a.q, a.D, size, stride, g.gb, g.tb);
+        // a shared axis (stride 0) of the keys or values is one coordinate of the map
+        for (int i = 0; i < 2; ++i) {
             const HeadStrides &s = i ? a.vs : a.ks;
-            const long long size[4] = {a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1};
-            const long long stride[4] = {s.t * 2, s.h * 2, s.n * 2, 16};
-            ok = at::encode_map(&maps[1 + i], i ? a.v : a.k, a.D, size, stride, kt, 1);
-        } else {
-            const long long size[4] = {a.Tk, a.Hkv, a.N, planes}, d = a.D * 2LL;
-            const long long stride[4] = {d, d * a.Tk, d * a.Tk * a.Hkv, d * keys};
-            ok = at::encode_map(&maps[1 + i], plane[1 + i], a.D, size, stride, kt, 1);
+            const long long ksize[4] = {a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1};
+            const long long kstride[4] = {s.t * 2, s.h * 2, s.n * 2, 16};
+            ok = ok && at::encode_map(i ? &m.v : &m.k, i ? g.v : g.k, a.D, ksize, kstride, kt, 1);
         }
     }
-    cudaError_t e = ok ? cudaSuccess : cudaErrorNotSupported;
-    if (e == cudaSuccess && !bf16) e = launch_attn_split(a, plane, st);
+    cudaError_t e = ok ? cudaSuccess : cudaErrorInvalidValue;
+    if (e == cudaSuccess && g.packed) e = launch_attn_split(a, bf16, plane, st);
     if (e == cudaSuccess) {
         if (bf16 && a.D <= 64)
-            e = pair ? at::launch<64, 1, true>(a, g, maps, part, st) : at::launch<64, 1, false>(a, g, maps, part, st);
+            e = pair ? at::launch<64, 1, true>(a, g, m, part, st) : at::launch<64, 1, false>(a, g, m, part, st);
         else if (bf16)
-            e = pair ? at::launch<128, 1, true>(a, g, maps, part, st) : at::launch<128, 1, false>(a, g, maps, part, st);
+            e = pair ? at::launch<128, 1, true>(a, g, m, part, st) : at::launch<128, 1, false>(a, g, m, part, st);
         else if (a.D <= 64)
-            e = pair ? at::launch<64, 3, true>(a, g, maps, part, st) : at::launch<64, 3, false>(a, g, maps, part, st);
+            e = pair ? at::launch<64, 3, true>(a, g, m, part, st) : at::launch<64, 3, false>(a, g, m, part, st);
         else
-            e = at::launch<128, 3, false>(a, g, maps, part, st);
+            e = at::launch<128, 3, false>(a, g, m, part, st);
     }
     if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st);
     if (ws) {

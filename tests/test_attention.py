@@ -240,6 +240,28 @@ def test_other_stream_and_repeatable(sc, dtype, Tq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(9, 1, 700, 2, 2, 64), (2, 3, 3000, 8, 2, 128), (1, 16, 5000, 2, 2, 64), (4, 50, 900, 4, 2, 64),
+                                   (2, 300, 700, 2, 2, 128)])
+def test_same_bits_every_time(sc, shape, dtype):
+    """Many calls one after the other, lengths and masks among them: no CTA, warp or copy may be late or early."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, dtype, N, Tq, Hq, D, seed=30, gain=2.0)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=31), make(torch, dtype, N, Tk, Hkv, D, seed=32)
+    lens = torch.tensor([Tk - 37 * i for i in range(N)], dtype=torch.int32).cuda()
+    mask = (torch.rand(N, Tk, generator=torch.Generator().manual_seed(33)) < 0.6).to(torch.uint8).cuda()
+    for kw in (dict(), dict(k_len=lens), dict(key_mask=mask)):
+        outs = [torch.full_like(q, float("nan")) for _ in range(60)]
+        for o in outs:
+            sc.check(sc.cross_attention_fwd(q, k, v, o, N, Tq, Tk, Hq, Hkv, D, D ** -0.5, dtype, **kw))
+        sc.check(sc.sc_last_device_status())
+        assert torch.isfinite(outs[0]).all()
+        for i, o in enumerate(outs):
+            assert torch.equal(o, outs[0]), f"call {i} differs"
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("Tq", [1, 140])
 def test_nan_in_a_valid_state_is_not_hidden(sc, Tq):
     import torch
