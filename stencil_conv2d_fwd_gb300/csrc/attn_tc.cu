@@ -21,16 +21,14 @@
 // rescaled only when a row's maximum has grown by more than 2^8 since the last
 // rescaling (P then stays below 256); the division at the end cancels the
 // common factor.  Warp 8 issues the TMA copies, warp 9 the MMAs.
-//
-// States that a mask leaves out are not read and not computed with: the CTA
-// counts the valid states of its share, warp 8 lists them tile by tile, and
-// warps 8, 10 and 11 copy their rows, 16 bytes a lane (cp.async, into the
-// places where a TMA copy would put them), so that the key tiles are dense
-// and only the last one has scores to leave out.  The last tile of a length is
-// copied the same way.  Rows past the last valid state are zero: what is
-// stored there does not reach a product.  (TMA gathers of four rows took 118
-// us where these copies take MASKED_US, 32 x 77 queries over masked 56 x 56
-// maps, 8 heads of 64.)
+// Warps 10 and 11 clear the value rows of states that a length or a mask
+// leaves out (their weight is 0, but 0 times an infinity would not be).  Key
+// tiles without a valid state are neither read nor computed with: the CTA
+// first looks through its share of the mask and lists the others.  (To gather
+// the valid states' rows alone, so that every tile is dense, cost more than
+// the states left out: 32 x 77 queries over padded 56 x 56 maps, half of whose
+// states are valid, 118 us by TMA gathers of four rows, 60 us by 16-byte
+// copies, MASKED_US us in place.)
 //
 // Accumulators, softmax and sums are fp32.  bf16 tensors: P is rounded to bf16
 // for the second product (a relative error of 2^-8 of single terms, the size
@@ -69,7 +67,8 @@ constexpr int key_tile() { return PL == 3 && DP == 128 ? 64 : 128; }
 constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 216, REGS_OTHER = 72;
 constexpr int THREADS = 384;
 constexpr int MAX_SLOTS = 12;
-constexpr int LIST = 512;              // listed states: a tile in use, two ahead and a piece of 128
+constexpr int VC = 8;                  // barriers of cleared value tiles: more than the ring holds
+constexpr int LIST = 512;              // key tiles of a share that are looked through; a longer share keeps all
 constexpr float GROW = 8.f;            // log2 growth of a row's maximum that rescales O
 constexpr size_t SMEM_CAP = 227 * 1024;
 
@@ -80,8 +79,6 @@ struct Geom {
     int splits;           // CTAs that share a row unit's keys
     bool packed;          // q, k and v are the workspace's copies (attn_split.cu)
     int k_axes[2], v_axes[2];        // whether the maps' (h, n) are axes (1), or shared by all (0)
-    const void *k, *v;               // bf16 keys and values (of plane 0), for copies by row,
-    long long k_row[4], v_row[4];    // and their strides: token, head, sequence, plane
 };
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, int c0, int c1, int c2, int c3, int c4,
@@ -197,39 +194,19 @@ constexpr uint32_t desc_lo_v(int key_tile) { return (uint32_t)(key_tile * 128 >>
 
 template <bool PAIR>
 struct Shared {
-    // barriers of one arrival (full: with a mask three), then those of the four warps of a stream
+    // barriers of one arrival, of the two clearing warps, and of a stream's four
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], q_full, s_full[2], o_full[2], drain;
+    uint64_t vclean[VC];
     uint64_t p_full[2][2];
-    int list[LIST];   // states of the coming tiles
+    uint32_t words[2][2][4];           // valid bits of a key tile, per stream, two tiles deep
     float m[PAIR ? 1 : TILE], l[PAIR ? 1 : TILE];   // stream 1's, at the end
-    int counts[THREADS / 32];
+    uint16_t tiles[LIST];              // the share's key tiles that have a valid state
+    uint8_t any[LIST];                 // whether a tile has one
+    int count;
     uint32_t tmem;
     int abort;
 };
-constexpr int BARS_ONE = 2 * MAX_SLOTS + 6, BARS = BARS_ONE + 4;
-
-template <int N>
-struct Warps {
-    static constexpr int value = N;
-};
-
-// How many of the n bytes at p are not 0, over the CTA's threads (each one's
-// part).
-__device__ __forceinline__ int count_part(const unsigned char *p, int n, int tid)
-{
-    const int head = min(n, (int)(-reinterpret_cast<uintptr_t>(p) & 15u));
-    const int body = (n - head) / 16, tail = n - head - 16 * body;
-    int c = 0;
-    if (tid < head) c += p[tid] != 0;
-    if (tid < tail) c += p[head + 16 * body + tid] != 0;
-    const uint4 *v = reinterpret_cast<const uint4 *>(p + head);
-#pragma unroll 4
-    for (int i = tid; i < body; i += THREADS) {
-        const uint4 w = v[i];
-        c += __popc(__vsetne4(w.x, 0u)) + __popc(__vsetne4(w.y, 0u)) + __popc(__vsetne4(w.z, 0u)) + __popc(__vsetne4(w.w, 0u));
-    }
-    return c;
-}
+constexpr int BARS_ONE = 2 * MAX_SLOTS + 6, BARS_TWO = BARS_ONE + VC, BARS = BARS_TWO + 4;
 
 // Shared memory: row tiles (of one row tile at least the room of its 128 x DP
 // fp32 sums, which the streams' join uses), the ring, then Shared.
@@ -283,8 +260,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int t_end = (int)((long long)tiles_all * (split + 1) / g.splits);
     const int key_begin = t_begin * KT, key_end = min(len, t_end * KT);   // this CTA's share
     const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
-    int keys = max(0, key_end - key_begin);   // valid states of the share
-    int nt = (keys + KT - 1) / KT;            // and key tiles
+    int nt = max(0, (key_end - key_begin + KT - 1) / KT);   // its key tiles, then those with a valid state
+    const bool look = mb && nt <= LIST;
+    auto tile_key = [&](int j) -> int { return key_begin + (look ? (int)sh.tiles[j] : j) * KT; };
 
     // A wait that runs out marks the CTA: every later wait returns at once and
     // all loops, which are finite, run to their end.
@@ -306,142 +284,27 @@ __global__ void __launch_bounds__(THREADS, 1)
     // first LAG key tiles, then value tile j and key tile j + LAG in turn.
     constexpr int LAG = PAIR ? 1 : 2;
     uint32_t issued = 0;          // ring entries whose copies have been issued
-    int listed = 0, scan = key_begin;   // states listed, and the next one to look at
-    constexpr int AHEAD = 4;      // pieces of 128 bytes of the mask that are read ahead,
-    int byte[AHEAD][4];           // four bytes a lane
-    auto read_mask = [&](int b) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = scan + 128 * b + 32 * i + lane;
-            byte[b][i] = key < key_end ? (int)mb[key] : 0;
-        }
-    };
-    // The seq-th tile: its kind and number.
-    auto tile_of = [&](int seq, bool &value) -> int {
-        const int l0 = min(LAG, nt), both = 2 * (nt - l0), s = seq - l0;
-        value = seq >= l0 && (s >= both || (s & 1) == 0);
-        return seq < l0 ? seq : (s >= both ? nt - l0 + s - both : (value ? s / 2 : l0 + s / 2));
-    };
-    // Copies by row: a warp's part (w of `warps`) of a tile is every warps-th
-    // group of four rows, eight lanes a row.  The rows' states, -1 past the last:
-    const int r4 = lane >> 3, chunk = lane & 7;
-    auto rows_of = [&](int tile, int w, auto warps, auto &state) {
-        constexpr int W = decltype(warps)::value;
-#pragma unroll
-        for (int i = 0; i < (KT / 4 + W - 1) / W; ++i) {
-            const int at = tile * KT + 4 * (w + W * i) + r4;
-            state[i] = -1;
-            // (in range whatever the list holds, should the mask change under the call)
-            if (w + W * i < KT / 4 && at < keys)
-                state[i] = mb ? (int)min((uint32_t)sh.list[at % LIST], (uint32_t)a.Tk - 1u) : key_begin + at;
-        }
-    };
-    // ... and their copies to ring entry `slot`, plane p.  (The states are in
-    // registers by then: between two copies nothing is read.)
-    auto copy_rows = [&](uint32_t slot, bool value, int p, int w, auto warps, const auto &state) {
-        constexpr int W = decltype(warps)::value;
-        const long long *st = value ? g.v_row : g.k_row;
-        const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(value ? g.v : g.k);
-        const __nv_bfloat16 *src = base + n * st[2] + h * st[1] + p * st[3] + chunk * 8;
-        const long long pitch = st[0];
-        const uint32_t dst = ring + slot * SLOT + r4 * 128;
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-            const bool on = d * 64 + chunk * 8 < a.D;
-#pragma unroll
-            for (int i = 0; i < (KT / 4 + W - 1) / W; ++i) {
-                const int rows4 = w + W * i;   // rows 4 rows4 + r4
-                if (rows4 >= KT / 4) break;
-                const bool live = on && state[i] >= 0;
-                cp_async16(dst + d * KBLK + rows4 * 512 + ((chunk ^ ((4 * rows4 + r4) & 7)) << 4),
-                           live ? src + state[i] * pitch + d * 64 : base, live ? 16 : 0);
-            }
-        }
-    };
-    // Lists states until `need` of them are listed.
-    auto list_states = [&](int need) {
-        while (listed < need && scan < key_end) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t ok = __ballot_sync(0xffffffffu, byte[0][i] != 0);
-                if (byte[0][i] != 0) sh.list[(listed + __popc(ok & ((1u << lane) - 1u))) % LIST] = scan + 32 * i + lane;
-                listed += __popc(ok);
-#pragma unroll
-                for (int b = 0; b + 1 < AHEAD; ++b) byte[b][i] = byte[b + 1][i];
-            }
-            scan += 128;
-            read_mask(AHEAD - 1);
-        }
-    };
-    // Without a mask: the TMA copies of the seq-th tile (the last tile of a
-    // length by row); the whole of warp 8 calls it.
+    // The copies of the seq-th tile.
     auto load_tile = [&](int seq) {
-        bool value;
-        const int tile = tile_of(seq, value), key0 = key_begin + tile * KT;
-        const bool whole = key0 + KT <= key_end || key_end == a.Tk;   // rows past the tensor's end read as zero
+        const int l0 = min(LAG, nt), both = 2 * (nt - l0), s = seq - l0;
+        const bool value = seq >= l0 && (s >= both || (s & 1) == 0);
+        const int tile = seq < l0 ? seq : (s >= both ? nt - l0 + s - both : (value ? s / 2 : l0 + s / 2));
+        const int *ax = value ? g.v_axes : g.k_axes;
+        const int key0 = tile_key(tile);
         for (int p = PL - 1; p >= 0; --p, ++issued) {   // the smallest plane first
             const uint32_t slot = issued % SLOTS, round = issued / SLOTS;
             const uint32_t bar = smem_u32(&sh.full[slot]);
             if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
             if (*abort_flag) return;
-            if (whole) {
-                const int *ax = value ? g.v_axes : g.k_axes;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, SLOT);
-                    for (int d = 0; d < DB; ++d)
-                        tma_load_5d(ring + slot * SLOT + d * KBLK, value ? &mv : &mk, d * 64, key0, h * ax[0], n * ax[1], p, bar);
-                }
-            } else {
-                int state[KT / 4];
-                rows_of(tile, 0, Warps<1>{}, state);
-                copy_rows(slot, value, p, 0, Warps<1>{}, state);
-                cp_async_commit();
-                cp_async_wait<0>();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar);
-            }
+            mbar_arrive_expect_tx(bar, SLOT);
+            for (int d = 0; d < DB; ++d)
+                tma_load_5d(ring + slot * SLOT + d * KBLK, value ? &mv : &mk, d * 64, key0, h * ax[0], n * ax[1], p, bar);
         }
-    };
-    // With a mask: warp w of three copies its part of every tile, PEND ring
-    // entries behind which it tells the MMA warp of the one that has landed.
-    // (An entry is released once the 2 PL after it have been multiplied.)
-    auto copy_tiles = [&](int w) {
-        constexpr int PEND = SLOTS - 2 * PL < 4 ? SLOTS - 2 * PL : 4;
-        static_assert(PEND >= 1, "a ring of more than two tiles");
-        uint32_t told = 0;
-        auto tell = [&]() {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.full[told % SLOTS]));
-            ++told;
-        };
-        for (int seq = 0; seq < 2 * nt; ++seq) {
-            bool value;
-            const int tile = tile_of(seq, value);
-            if (w == 0) list_states(min((tile + 1) * KT, keys));
-            // the list is written; and all three have read it for the tile before
-            named_sync<2, 96>();
-            int state[(KT / 4 + 2) / 3];
-            rows_of(tile, w, Warps<3>{}, state);
-            for (int p = PL - 1; p >= 0; --p, ++issued) {
-                const uint32_t slot = issued % SLOTS, round = issued / SLOTS;
-                if (issued > PEND) {
-                    cp_async_wait<PEND>();
-                    tell();
-                }
-                if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
-                copy_rows(slot, value, p, w, Warps<3>{}, state);
-                cp_async_commit();
-            }
-        }
-        cp_async_wait<0>();
-        while (told < issued) tell();
     };
 
     int ahead = 0;   // tiles whose copies are issued before the CTA's barrier
     if (warp == 8) {
-        for (int i = lane; i < BARS; i += 32) mbar_init(smem_u32(&sh.full[0]) + 8 * i, i < MAX_SLOTS ? (mb ? 3 : 1) : (i < BARS_ONE ? 1 : 4));
+        for (int i = lane; i < BARS; i += 32) mbar_init(smem_u32(&sh.full[0]) + 8 * i, i < BARS_ONE ? 1 : (i < BARS_TWO ? 2 : 4));
         if (lane == 0) sh.abort = 0;
         fence_mbar_init();
         __syncwarp();
@@ -457,28 +320,45 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     g.packed ? p : n, smem_u32(&sh.q_full));
             }
         }
-        __syncwarp();
-        // with a mask the number of tiles is not known yet
-        if (!mb)
+        // (with a mask the tiles are not known yet)
+        if (lane == 0 && !look)
             for (; ahead < 2 * nt && (ahead + 1) * PL <= SLOTS; ++ahead) load_tile(ahead);
+        __syncwarp();
     } else if (warp == 9) {
         tc::tmem_alloc(smem_u32(&sh.tmem), 512);
     }
-    if (mb) {
-        const int c = __reduce_add_sync(0xffffffffu, count_part(mb + key_begin, keys, tid));
-        if (lane == 0) sh.counts[warp] = c;
+    if (look) {
+#pragma unroll 2
+        for (int j = warp; j < nt; j += THREADS / 32) {
+            int any = 0;
+#pragma unroll
+            for (int i = 0; i < KT / 32; ++i) {
+                const int key = key_begin + j * KT + 32 * i + lane;
+                any |= key < key_end ? (int)mb[key] : 0;
+            }
+            any = __any_sync(0xffffffffu, any != 0);
+            if (lane == 0) sh.any[j] = (uint8_t)any;
+        }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
     const int q_tiles = nt;   // the row tiles have been asked for
-    if (mb) {
-        keys = 0;
-#pragma unroll
-        for (int i = 0; i < THREADS / 32; ++i) keys += sh.counts[i];
-        nt = (keys + KT - 1) / KT;
+    if (look) {
+        if (warp == 8) {
+            int count = 0;
+            for (int j0 = 0; j0 < nt; j0 += 32) {
+                const uint32_t on = __ballot_sync(0xffffffffu, j0 + lane < nt && sh.any[j0 + lane] != 0);
+                if (on >> lane & 1u) sh.tiles[count + __popc(on & ((1u << lane) - 1u))] = (uint16_t)(j0 + lane);
+                count += __popc(on);
+            }
+            if (lane == 0) sh.count = count;
+        }
+        __syncthreads();
+        nt = sh.count;
     }
+    const bool ragged = mb || len < a.Tk;   // value rows to clear
     constexpr int P1 = KT, P2 = DP == 64 ? KT / 2 : KT + KT / 2, TO = 256 - DP;   // columns of a stream
     auto p_plane = [](int p) { return p == 0 ? 0 : (p == 1 ? P1 : P2); };
 
@@ -486,15 +366,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         // one instruction for the four warps, as its form asks
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_OTHER));
         if (warp == 8) {
-            if (mb) {
-#pragma unroll
-                for (int b = 0; b < AHEAD; ++b) read_mask(b);
-                copy_tiles(0);
-            } else {
+            if (lane == 0) {
                 for (int seq = ahead; seq < 2 * nt; ++seq) load_tile(seq);
+                // a mask that leaves nothing: no one else waits for the row tiles
+                if (nt == 0 && q_tiles > 0) wait(sh.q_full, 0);
             }
-            // a mask that leaves nothing: no one else waits for the row tiles
-            if (nt == 0 && q_tiles > 0) wait(sh.q_full, 0);
             __syncwarp();
         } else if (warp == 9) {
             if (nt > 0) {
@@ -525,10 +401,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 };
                 // O of stream i = P V (fp32 tensors), or += P V; use = the stream's count of P tiles so far
                 // P comes in two halves of the key tile: the first half's products run while the second is made
-                auto mma_v = [&](int i, uint32_t c, uint32_t use, bool release, bool last) {
+                auto mma_v = [&](int i, uint32_t c, int j, uint32_t use, bool release, bool last) {
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
                         wait(sh.p_full[i][part], use & 1);
+                        if (part == 0 && ragged) wait(sh.vclean[j % VC], (j / VC) & 1);
                         tc::fence_after_sync();
 #pragma unroll
                         for (int pv = PL - 1; pv >= 0; --pv) {
@@ -556,9 +433,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t c = PL;
                     for (int j = 0; j < nt; ++j) {
                         const bool more = j + 1 < nt;
-                        mma_v(0, c, j, false, !more);
+                        mma_v(0, c, j, j, false, !more);
                         if (more) mma_s(0, c + PL, false);
-                        mma_v(1, c, j, true, !more);
+                        mma_v(1, c, j, j, true, !more);
                         if (more) mma_s(1, c + PL, true);
                         c += more ? 2 * PL : PL;
                     }
@@ -568,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t c = nt > 1 ? 2 * PL : PL;
                     for (int j = 0; j < nt; ++j) {
                         const bool more = j + 2 < nt;
-                        mma_v(j & 1, c, j >> 1, true, !more);
+                        mma_v(j & 1, c, j, j >> 1, true, !more);
                         c += PL;
                         if (more) {
                             mma_s(j & 1, c, true);
@@ -578,8 +455,44 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             __syncwarp();
-        } else if (mb) {
-            copy_tiles(warp - 9);
+        } else if (ragged) {
+            // value rows that are not valid: zero, in every plane and block.
+            // Every entry of the ring is waited for in turn, the key tiles' too: a
+            // barrier's parity tells a round only from its neighbours.
+            uint32_t c = 0;
+            auto pass = [&]() {
+                for (int p = 0; p < PL; ++p, ++c) wait(sh.full[c % SLOTS], (c / SLOTS) & 1);
+            };
+            for (int j = 0; j < LAG && j < nt; ++j) pass();
+            constexpr int KL = KT / 64;   // keys of a lane: two warps share the tile
+            const int row0 = (warp - 10) * 32 * KL + lane;
+            for (int j = 0; j < nt; ++j) {
+                const int key0 = tile_key(j);
+                bool bad[KL];
+#pragma unroll
+                for (int i = 0; i < KL; ++i) {
+                    const int key = key0 + row0 + i * 32;
+                    // states past Tk are not in the tensor and read as zero
+                    bad[i] = key < a.Tk && (key >= len || (mb && mb[key] == 0));
+                }
+                for (int p = 0; p < PL; ++p, ++c) {
+                    const uint32_t slot = c % SLOTS;
+                    wait(sh.full[slot], (c / SLOTS) & 1);
+#pragma unroll
+                    for (int i = 0; i < KL; ++i) {
+                        if (!bad[i]) continue;
+                        const uint32_t at = ring + slot * SLOT + (row0 + i * 32) * 128;
+                        for (int d = 0; d < DB; ++d)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)   // from chunk `lane` on: no two lanes in one bank
+                                tc::st_shared_v4(at + d * KBLK + ((e + lane) & 7) * 16, 0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.vclean[j % VC]));
+                if (j + LAG < nt) pass();
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS_SOFTMAX));
@@ -595,6 +508,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int d = 0; d < (PL == 3 ? DP : 1); ++d) acc[d] = 0.f;
         constexpr int KW = KT / 32;     // words of a tile's valid bits
         int use = 0;
+        // this thread's byte of key tile j: 0 where the state is not valid
+        auto mask_byte = [&](int j) {
+            if (j >= nt || row >= KT) return 0;
+            const int key = tile_key(j) + row;
+            return key < len ? (int)mb[key] : 0;
+        };
+        int next = mb ? mask_byte(PAIR ? 0 : i) : 0;
         // half of a key tile's P is in tensor memory
         auto hand_over = [&](int part) {
             tmem_wait_st();
@@ -613,13 +533,32 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         };
         for (int j = PAIR ? 0 : i; j < nt; j += step, ++use) {
-            // only the last tile has scores that are not valid
-            const bool masked = (j + 1) * KT > keys;
+            const int key0 = tile_key(j);
             uint32_t w[KW];
+            bool masked = key0 + KT > len;
+            if (mb) {
+                // one key per thread, a word per warp; the next tile's byte is
+                // read a tile ahead (its latency was a third of a masked tile's time)
+                const uint32_t word = __ballot_sync(0xffffffffu, next != 0);
+                next = mask_byte(j + step);
+                if (lane == 0) sh.words[i][use & 1][warp & 3] = word;
+                if (i == 0)
+                    named_sync<1, 128>();
+                else
+                    named_sync<2, 128>();
+                uint32_t all = ~0u;
 #pragma unroll
-            for (int e = 0; e < KW; ++e) {
-                const int left = keys - j * KT - 32 * e;
-                w[e] = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
+                for (int e = 0; e < KW; ++e) {
+                    w[e] = sh.words[i][use & 1][e];
+                    all &= w[e];
+                }
+                masked = all != ~0u;
+            } else {
+#pragma unroll
+                for (int e = 0; e < KW; ++e) {
+                    const int left = len - key0 - 32 * e;
+                    w[e] = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
+                }
             }
             wait(sh.s_full[i], use & 1);
             tc::fence_after_sync();
@@ -791,9 +730,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                named_sync<1, 256>();
+                named_sync<3, 256>();
             } else {
-                named_sync<1, 256>();
+                named_sync<3, 256>();
                 const float m1 = sh.m[row], l1 = sh.l[row];
                 const float mm = fmaxf(m, m1), ms = mm == -INFINITY ? 0.f : mm;
                 f0 = ex2(m - ms);
@@ -857,8 +796,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (tid == 0) atomicExch(status, kDeviceTimeout);
         if (warp == 8 && lane == 0) {
             if (q_tiles > 0) (void)mbar_wait_bounded(smem_u32(&sh.q_full), 0, timeout_ns);
-            // (copies by row have been waited for by their threads)
-            for (uint32_t e = issued > (uint32_t)SLOTS ? issued - SLOTS : 0; e < issued && !mb; ++e)
+            for (uint32_t e = issued > (uint32_t)SLOTS ? issued - SLOTS : 0; e < issued; ++e)
                 (void)mbar_wait_bounded(smem_u32(&sh.full[e % SLOTS]), (e / SLOTS) & 1, timeout_ns);
         }
         if (warp == 9 && lane == 0) {
@@ -988,20 +926,15 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
     at::Maps m;
     std::memset(&m, 0, sizeof(m));
     bool ok;
-    g.k = g.packed ? plane[1] : a.k;
-    g.v = g.packed ? plane[2] : a.v;
-    const long long packed_row[4] = {a.D, (long long)a.D * a.Tk, (long long)a.D * a.Tk * a.Hkv, (long long)a.D * keys};
-    const long long k_row[4] = {a.ks.t, a.ks.h, a.ks.n, 0}, v_row[4] = {a.vs.t, a.vs.h, a.vs.n, 0};
-    std::memcpy(g.k_row, g.packed ? packed_row : k_row, sizeof(k_row));
-    std::memcpy(g.v_row, g.packed ? packed_row : v_row, sizeof(v_row));
+    const void *k = g.packed ? plane[1] : a.k, *v = g.packed ? plane[2] : a.v;
     if (g.packed) {
         const long long size[4] = {a.G, a.Tq, (long long)a.N * a.Hkv, planes}, d = a.D * 2LL;
         const long long stride[4] = {d, d * a.G, d * a.G * a.Tq, d * rows};
         ok = at::encode_map(&m.q, plane[0], a.D, size, stride, g.gb, g.tb);
         const long long ksize[4] = {a.Tk, a.Hkv, a.N, planes};
         const long long kstride[4] = {d, d * a.Tk, d * a.Tk * a.Hkv, d * keys};
-        ok = ok && at::encode_map(&m.k, g.k, a.D, ksize, kstride, kt, 1) &&
-             at::encode_map(&m.v, g.v, a.D, ksize, kstride, kt, 1);
+        ok = ok && at::encode_map(&m.k, k, a.D, ksize, kstride, kt, 1) &&
+             at::encode_map(&m.v, v, a.D, ksize, kstride, kt, 1);
     } else {
         const long long size[4] = {a.G, a.Tq, a.Hkv, a.N};
         const long long stride[4] = {a.qs.h * 2, a.qs.t * 2, a.qs.h * a.G * 2, a.qs.n * 2};
@@ -1011,7 +944,7 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
             const HeadStrides &s = i ? a.vs : a.ks;
             const long long ksize[4] = {a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1};
             const long long kstride[4] = {s.t * 2, s.h * 2, s.n * 2, 16};
-            ok = ok && at::encode_map(i ? &m.v : &m.k, i ? g.v : g.k, a.D, ksize, kstride, kt, 1);
+            ok = ok && at::encode_map(i ? &m.v : &m.k, i ? v : k, a.D, ksize, kstride, kt, 1);
         }
     }
     cudaError_t e = ok ? cudaSuccess : cudaErrorInvalidValue;
