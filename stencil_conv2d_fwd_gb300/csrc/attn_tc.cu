@@ -885,7 +885,9 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
     if (rt > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
     g.row_tiles = (int)rt;
     // two row tiles of three planes of 128 columns do not fit in shared memory
-    const bool pair = g.row_tiles > 1 && (bf16 || a.D <= 64);
+    // (nor is there a reason to pair them where each has an SM of its own)
+    const bool pair = (bf16 || a.D <= 64) && g.row_tiles > 1 &&
+                      (long long)a.N * a.Hkv * g.row_tiles > device_sm_count();
     g.units = pair ? (g.row_tiles + 1) / 2 : g.row_tiles;
     // CTAs per row unit: fill the GPU, at least four key tiles each
     const long long blocks = (long long)a.N * a.Hkv * g.units;
