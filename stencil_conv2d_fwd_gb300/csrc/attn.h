@@ -37,10 +37,11 @@ struct AttnPartials {
     int parts;
 };
 
-// Up to 16 bf16 rows per key head: keys streamed through warp-wide MMAs
+// Few rows per key head: keys streamed through warp-wide MMAs
 // (attn_mma.cu).
-cudaError_t launch_attn_mma(const AttnArgs &a, cudaStream_t st);
-// Few fp32 rows per key head: keys streamed through registers (attn_rows.cu).
+cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, cudaStream_t st);
+// Up to three fp32 rows per key head: keys streamed through registers
+// (attn_rows.cu).
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t st);
 // Many rows per key head: tensor cores (attn_tc.cu).
 cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st);

@@ -281,7 +281,7 @@ int cross_attention_fwd(const void *q, const void *k, const void *v, void *out, 
     const bool bf16 = dtype == SC_BF16;
     const long long rows = (long long)Tq * a.G;
     if (rows > 16) return from_cuda(sc::launch_attn_tc(a, bf16, st));
-    return from_cuda(bf16 ? sc::launch_attn_mma(a, st) : sc::launch_attn_rows(a, st));
+    return from_cuda(!bf16 && rows <= 3 ? sc::launch_attn_rows(a, st) : sc::launch_attn_mma(a, bf16, st));
 }
 
 }  // extern "C"

@@ -1,30 +1,37 @@
-// Attention of up to 16 bf16 rows per key head over many keys: a decoder's
-// next token with its group of query heads, a short draft.  Bound by reading
-// K and V once; the products run on warp-wide m16n8k16 MMAs, which take the
-// rows as M, so that a 16-row block costs what one row does (some 35
+// Attention of few rows per key head over many keys: a decoder's next token
+// with its group of query heads, a short draft.  Bound by reading K and V
+// once; the products run on warp-wide m16n8k16 bf16 MMAs, which take the rows
+// as M, so that a block of 8 or 16 rows costs what one row does (bf16: some 35
 // instructions per KB of K and V; multiplied out in registers it was 210 for
 // four rows, and the issue slots were the bound).
 //
 //   S = Q K^T,  P = 2^(c S - m),  O = P V,  out = O / sum P,   c = scale log2 e
 //
-// One pass, running m and sum of a row, as in attn_rows.cu.  Each warp has a
-// ring of its own in shared memory, STAGES pieces of 16 keys and values that
-// its lanes copy there asynchronously, 16 bytes each, so that some 100 KB are
-// under way on an SM at any time without a register held for them and without
-// a barrier between warps.  States that are not valid are not read (their
-// bytes are zero-filled): whatever is stored there does not reach a sum.
-// Operands go from there to the MMA's registers 16 bytes a lane:
+// One pass over the keys, m and the sum running values of a row.  Each warp
+// has a ring of its own in shared memory, ENTRIES pieces of 16 keys or 16
+// values that its lanes copy there asynchronously, 16 bytes each, so that some
+// 100 to 200 KB are under way on an SM at any time without a register held
+// for them and without a barrier between warps.  States that are not valid are
+// not read (their bytes are zero-filled): whatever is stored there does not
+// reach a sum.  Operands go from there to the MMA's registers 16 bytes a lane:
 //   * a product's order of summation over d is free, so lane (g, t) of a quad
-//     takes its key's elements 8 (4 c + t) .. + 8 as its share of k, the same
-//     for Q, with no transposition;
+//     takes its key's 16-byte chunks 4 i + t as its share of k, the same for
+//     Q, with no transposition;
 //   * the columns of V's product are free as well: lane (g, t) reads one chunk
-//     of 8 elements of each of the four keys that its share of P stands for,
-//     and pairs two keys' elements with one byte permutation each.
-// 16-byte chunk x of a row y lies at chunk x XOR (y mod 8).  Column g of the
-// scores is key g / 2 + 4 (g mod 2), and chunk column g of V is chunk
-// g / 2 + 4 (g mod 2), so that every quarter-warp's reads fall in eight
-// different bank groups.  The scores' registers are P's operand registers as
-// they are; P is rounded to bf16 (a relative error of 2^-8 of single terms).
+//     at a time of each of the four keys that its share of P stands for, and
+//     pairs two keys' elements.
+// Chunk x of a row y lies at chunk x XOR (y mod 8).  Column g of the scores is
+// key g / 2 + 4 (g mod 2), and chunk column g of V is chunk g / 2 + 4 (g mod 2),
+// so that every quarter-warp's reads fall in eight different bank groups.  The
+// scores' registers are P's operand registers as they are.
+//
+// bf16 tensors: P is rounded to bf16 (a relative error of 2^-8 of single
+// terms).  fp32 tensors: Q, K, P and V are split into three bf16 planes in
+// registers, x = x0 + x1 + x2 to 24 bits, a product the six of planes
+// i + j <= 2: in four MMAs, since rows 8 to 15 of an operand Q or P take its
+// second plane.  The MMAs cut sums short instead of rounding them, so the large
+// product of the scores and the small ones have accumulators of their own, and
+// O is moved to sums outside the MMAs every FLUSH steps.
 // A warp's pieces are every 8th of the CTA's share.
 #include "attn_rows.cuh"
 #include "launch.h"
@@ -46,20 +53,41 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 
 constexpr int KEYS = 16;   // keys of a step
+constexpr int FLUSH = 4;
 
 // Index of column g of a product (see above).
 __device__ __forceinline__ int spread(int g) { return (g >> 1) + 4 * (g & 1); }
 
-// DP: head width rounded up to 64 or 128.  RH: 1 for up to 8 rows, 2 for 16.
-constexpr int STAGES = 3;   // of 16 + 16 rows; a step's valid bits are 16 of a 64-bit word: at most 4
+// Two floats as three pairs of bf16, x = x0 + x1 + x2.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3])
+{
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        p[i] = tc::pack_bf16(x, y);
+        x -= __uint_as_float(p[i] << 16);
+        y -= __uint_as_float(p[i] & 0xffff0000u);
+    }
+}
+
+// DP: head width rounded up to 64 or 128 (fp32: 32, 64 or 128).  RH: 1 for up
+// to 8 rows, 2 for 16 (bf16 only: fp32 has no registers for them).
+template <class T, int DP>
+struct Rows {
+    static constexpr bool F32 = sizeof(T) == 4;
+    static constexpr int EPC = 16 / sizeof(T);   // elements of a chunk
+    static constexpr int CH = DP / EPC;          // chunks of a row
+    // entries of a warp's ring (its step's valid bits are 16 of a 64-bit word: at most 7)
+    static constexpr int ENTRIES = F32 && DP == 128 ? 3 : 6;
+    static constexpr int CTAS = 16 * CH * 16 * ENTRIES * kRowWarps <= 96 * 1024 ? 2 : 1;   // an SM
+};
 
 // The rings' memory becomes the sums' at the end.  With 8 rows the cluster's
 // sums have their own: the first CTA's place is then free from the start, and
 // no CTA waits for another's loop.  With 16 there is no room.
-template <int DP, int RH>
+template <class T, int DP, int RH>
 struct MmaShared {
     union {
-        uint4 ring[kRowWarps][STAGES][2][KEYS][DP / 8];   // K, V
+        uint4 ring[kRowWarps][Rows<T, DP>::ENTRIES][KEYS][Rows<T, DP>::CH];
         struct {
             WarpSums<8 * RH, DP> warps;
             CtaSums<RH == 1 ? 1 : 8 * RH, RH == 1 ? 1 : DP> shared_ctas;
@@ -75,19 +103,22 @@ struct MmaShared {
     }
 };
 
-template <int DP, int RH>
-__global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
+template <class T, int DP, int RH>
+__global__ void __launch_bounds__(kRowThreads, Rows<T, DP>::CTAS)
     attn_mma_kernel(const AttnArgs a, const RowsGeom g, const AttnPartials part)
 {
+    using RT = Rows<T, DP>;
+    constexpr bool F32 = RT::F32;
     constexpr int R = 8 * RH;
-    constexpr int ST = STAGES;
-    constexpr int KC = DP / 32;          // 16-byte chunks of a key per lane
-    constexpr int VC = DP / 64;          // of a value per lane
-    constexpr int CH = DP / 8;           // chunks of a row
-    constexpr int RPL = 32 / CH;         // rows of a warp-wide copy
+    constexpr int EN = RT::ENTRIES, EPC = RT::EPC, CH = RT::CH;
+    constexpr int KC = CH / 4;           // chunks of a key per lane
+    constexpr int VC = CH / 8;           // of a value per lane
+    constexpr int NT = VC * EPC;         // products of 8 columns of O
+    constexpr int RPL = CH >= 32 ? 1 : 32 / CH;   // rows of a warp-wide copy
     constexpr int COPIES = KEYS / RPL;
+    static_assert(CH <= 32 && (!F32 || RH == 1), "one row at most a copy; fp32: 8 rows");
     extern __shared__ __align__(128) unsigned char dyn[];
-    MmaShared<DP, RH> &sm = *reinterpret_cast<MmaShared<DP, RH> *>(dyn);
+    MmaShared<T, DP, RH> &sm = *reinterpret_cast<MmaShared<T, DP, RH> *>(dyn);
 
     pdl_trigger();   // the join kernel may be set up; it waits for this grid's end
     if (RH == 1 && g.cluster > 1) cluster_arrive();
@@ -99,19 +130,32 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
     const int n = nh / a.Hkv, h = nh - n * a.Hkv;
     const int rows = a.Tq * a.G;
 
-    // the rows' queries (a row past the last one is 0), as stored: the scale
-    // is applied to the fp32 scores
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint4 q[RH][KC];
+    // the rows' queries (a row past the last one is 0), as stored, or in planes:
+    // the scale is applied to the fp32 scores
+    constexpr int PL = F32 ? 3 : 1, QW = F32 ? 2 : 4;   // planes; words of a chunk's operand
+    uint32_t q[RH][PL][KC][QW];
 #pragma unroll
     for (int r = 0; r < RH; ++r)
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-            const int row = row0 + r * 8 + gq, d = (c * 4 + t) * 8;
-            q[r][c] = zero;
+            const int row = row0 + r * 8 + gq, d = (c * 4 + t) * EPC;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (row < rows && d < a.D) {
                 const int tok = row / a.G, hq = h * a.G + row % a.G;
-                q[r][c] = ldg16(static_cast<const __nv_bfloat16 *>(a.q) + n * a.qs.n + tok * a.qs.t + hq * a.qs.h + d);
+                v = ldg16(static_cast<const T *>(a.q) + n * a.qs.n + tok * a.qs.t + hq * a.qs.h + d);
+            }
+            if constexpr (F32) {
+                uint32_t p0[3], p1[3];
+                split3(__uint_as_float(v.x), __uint_as_float(v.y), p0);
+                split3(__uint_as_float(v.z), __uint_as_float(v.w), p1);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    q[r][i][c][0] = p0[i];
+                    q[r][i][c][1] = p1[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[r][0][c][i] = word(v, i);
             }
         }
 
@@ -125,98 +169,131 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
     constexpr int STEP = kRowWarps * KEYS;
     const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
 
-    // the lane's part of a step's copies: row crow + RPL i, chunk cch
+    // the lane's part of a piece's copies: row crow + RPL i, chunk cch
     const int crow = lane / CH, cch = lane % CH;
-    const bool cact = cch * 8 < a.D;   // chunks past D are zero-filled
-    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k) + n * a.ks.n + h * a.ks.h +
-                              (long long)(key0 + crow) * a.ks.t + (cact ? cch * 8 : 0);
-    const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v) + n * a.vs.n + h * a.vs.h +
-                              (long long)(key0 + crow) * a.vs.t + (cact ? cch * 8 : 0);
-    const __nv_bfloat16 *kbase = static_cast<const __nv_bfloat16 *>(a.k), *vbase = static_cast<const __nv_bfloat16 *>(a.v);
-    uint4 *ring = &sm.ring[warp][0][0][0][0];
-    constexpr int STAGE = 2 * KEYS * CH;   // in 16-byte units
-    uint32_t dst[COPIES];
-#pragma unroll
-    for (int i = 0; i < COPIES; ++i) {
-        const int row = crow + i * RPL;
-        dst[i] = smem_u32(ring + row * CH + (cch ^ (row & 7)));
-    }
+    const bool cact = cch * EPC < a.D;   // chunks past D are zero-filled
+    const T *kbase = static_cast<const T *>(a.k), *vbase = static_cast<const T *>(a.v);
+    const T *kp = kbase + n * a.ks.n + h * a.ks.h + (long long)(key0 + crow) * a.ks.t + (cact ? cch * EPC : 0);
+    const T *vp = vbase + n * a.vs.n + h * a.vs.h + (long long)(key0 + crow) * a.vs.t + (cact ? cch * EPC : 0);
+    uint4 *ring = &sm.ring[warp][0][0][0];
+    constexpr int ENTRY = KEYS * CH;   // in 16-byte units
 
-    // Valid bits of a step's keys.  The mask's byte is read two steps ahead of
-    // its copies.
+    // Valid bits of a step's keys.  The mask's byte is read a step ahead.
     auto mask_byte = [&](int step) -> int {
         const int key = key0 + step * STEP + lane;
         return step < steps && lane < KEYS && key < len ? (mb ? (int)mb[key] : 1) : 0;
     };
-    auto copy = [&](int stage, uint32_t ok) {
-        const uint32_t at = stage * STAGE * 16;
-        const __nv_bfloat16 *k = kp, *v = vp;
+    auto copy = [&](int entry, const T *&p, long long pitch, const T *base, uint32_t ok) {
+        const uint32_t at = smem_u32(ring + entry * ENTRY);
+        const T *src = p;
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i, k += RPL * a.ks.t, v += RPL * a.vs.t) {
-            const bool on = cact && (ok >> (crow + i * RPL) & 1u);
-            cp_async16(dst[i] + at, on ? k : kbase, on ? 16 : 0);
-            cp_async16(dst[i] + at + KEYS * CH * 16, on ? v : vbase, on ? 16 : 0);
+        for (int i = 0; i < COPIES; ++i, src += RPL * pitch) {
+            const int row = crow + i * RPL;
+            const bool on = cact && (ok >> row & 1u);
+            cp_async16(at + (row * CH + (cch ^ (row & 7))) * 16, on ? src : base, on ? 16 : 0);
         }
         cp_async_commit();
-        kp += STEP * a.ks.t;
-        vp += STEP * a.vs.t;
+        p += STEP * pitch;
     };
-    // steps 0 .. ST - 2 under way; their valid bits, 16 each, the oldest lowest
+    // Pieces in order: keys of step 0, values of step 0, keys of step 1, ...
+    // EN - 1 of them are under way; the valid bits of the current step and
+    // those after it, 16 each, the current lowest.
     unsigned long long okq = 0;
+    constexpr int LEAD = EN / 2;   // steps whose keys are under way
+    int byte;
     {
-        int byte[ST - 1];
+        constexpr int FIRST = (EN - 1 + 1) / 2;   // steps begun before the loop
+        int b[FIRST];
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i) byte[i] = mask_byte(i);
+        for (int i = 0; i < FIRST; ++i) b[i] = mask_byte(i);
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i) {
-            const uint32_t ok = __ballot_sync(0xffffffffu, byte[i] != 0);
+        for (int i = 0; i < FIRST; ++i) {
+            const uint32_t ok = __ballot_sync(0xffffffffu, b[i] != 0);
             okq |= (unsigned long long)ok << (16 * i);
-            copy(i, ok);
+            copy(2 * i, kp, a.ks.t, kbase, ok);
+            if (2 * i + 1 < EN - 1) copy(2 * i + 1, vp, a.vs.t, vbase, ok);
         }
+        byte = mask_byte(FIRST);
     }
-    int byte = mask_byte(ST - 1);
+    auto next_keys = [&](int entry, int step) {   // keys of the step LEAD ahead of the current, which is `step`
+        const uint32_t ok = __ballot_sync(0xffffffffu, byte != 0);
+        byte = mask_byte(step + LEAD + 1);
+        okq |= (unsigned long long)ok << (16 * LEAD);
+        copy(entry, kp, a.ks.t, kbase, ok);
+    };
+    auto next_values = [&](int entry) {   // values of the step (EN - 1) / 2 ahead
+        copy(entry, vp, a.vs.t, vbase, (uint32_t)(okq >> (16 * ((EN - 1) / 2))) & 0xffffu);
+    };
 
     const float sc = a.scale * kLog2e;
-    float m[RH], l[RH], o[VC * 8][4];
+    float m[RH], l[RH], o[NT][4], sums[F32 ? NT : 1][2];
 #pragma unroll
     for (int r = 0; r < RH; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < VC * 8; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
-
-    int stage = 0, fill = ST - 1;
-    for (int step = 0; step < steps; ++step) {
-        cp_async_wait<ST - 2>();
-        __syncwarp();
-        // the step ST - 1 ahead goes where the last step was read (the barrier
-        // above is behind those reads)
-        {
-            const uint32_t ok = __ballot_sync(0xffffffffu, byte != 0);
-            byte = mask_byte(step + ST);
-            okq |= (unsigned long long)ok << (16 * (ST - 1));
-            copy(fill, ok);
-            fill = fill + 1 == ST ? 0 : fill + 1;
+#pragma unroll
+    for (int j = 0; j < (F32 ? NT : 1); ++j) sums[j][0] = sums[j][1] = 0.f;
+    auto flush = [&](float f) {
+        if constexpr (F32) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                sums[j][0] = (sums[j][0] + (o[j][0] + o[j][2])) * f;
+                sums[j][1] = (sums[j][1] + (o[j][1] + o[j][3])) * f;
+                o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+            }
         }
+    };
+
+    int entry = 0, fill = EN - 1;   // ring entries of the piece in use and of the next one to be asked for
+    auto advance = [&]() {
+        entry = entry + 1 == EN ? 0 : entry + 1;
+        fill = fill + 1 == EN ? 0 : fill + 1;
+    };
+    for (int step = 0; step < steps; ++step) {
         const uint32_t ok = (uint32_t)okq & 0xffffu;
-        okq >>= 16;
-        const uint4 *kt = ring + stage * STAGE, *vt = kt + KEYS * CH;
-        stage = stage + 1 == ST ? 0 : stage + 1;
+        cp_async_wait<EN - 2>();
+        __syncwarp();
+        // the next piece goes where the last one was read (the barrier above is behind those reads)
+        if constexpr (EN % 2 == 0)
+            next_values(fill);
+        else
+            next_keys(fill, step);
+        const uint4 *kt = ring + entry * ENTRY;
+        advance();
 
         float s[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+            float lo[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+            const int key = spread(gq);
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
-                const int key = spread(gq);
                 const uint4 k = kt[(i * 8 + key) * CH + ((c * 4 + t) ^ key)];
-                mma16816(s[i], q[0][c].x, RH == 2 ? q[RH - 1][c].x : 0u, q[0][c].y, RH == 2 ? q[RH - 1][c].y : 0u, k.x, k.y);
-                mma16816(s[i], q[0][c].z, RH == 2 ? q[RH - 1][c].z : 0u, q[0][c].w, RH == 2 ? q[RH - 1][c].w : 0u, k.z, k.w);
+                if constexpr (F32) {
+                    uint32_t b0[3], b1[3];
+                    split3(__uint_as_float(k.x), __uint_as_float(k.y), b0);
+                    split3(__uint_as_float(k.z), __uint_as_float(k.w), b1);
+                    mma16816(lo, q[0][0][c][0], 0u, q[0][0][c][1], 0u, b0[2], b1[2]);
+                    mma16816(lo, q[0][2][c][0], 0u, q[0][2][c][1], 0u, b0[0], b1[0]);
+                    mma16816(lo, q[0][0][c][0], q[0][1][c][0], q[0][0][c][1], q[0][1][c][1], b0[1], b1[1]);
+                    mma16816(s[i], q[0][0][c][0], q[0][1][c][0], q[0][0][c][1], q[0][1][c][1], b0[0], b1[0]);
+                } else {
+                    mma16816(s[i], q[0][0][c][0], RH == 2 ? q[RH - 1][0][c][0] : 0u, q[0][0][c][1],
+                             RH == 2 ? q[RH - 1][0][c][1] : 0u, k.x, k.y);
+                    mma16816(s[i], q[0][0][c][2], RH == 2 ? q[RH - 1][0][c][2] : 0u, q[0][0][c][3],
+                             RH == 2 ? q[RH - 1][0][c][3] : 0u, k.z, k.w);
+                }
+            }
+            if constexpr (F32) {
+                s[i][0] += (lo[0] + lo[2]) + s[i][2];
+                s[i][1] += (lo[1] + lo[3]) + s[i][3];
             }
         }
         // scores of row g (and g + 8) for the keys 8 i + t and 8 i + t + 4
@@ -237,20 +314,27 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
             top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
             grow |= top[r] > m[r];
         }
-        if (__any_sync(0xffffffffu, grow)) {
+        const bool any_grow = __any_sync(0xffffffffu, grow);
+        if (any_grow) {
 #pragma unroll
             for (int r = 0; r < RH; ++r) {
                 const float f = top[r] == -INFINITY ? 1.f : ex2(m[r] - top[r]);
                 m[r] = top[r];
                 l[r] *= f;
+                if constexpr (F32) {
+                    flush(f);
+                } else {
 #pragma unroll
-                for (int j = 0; j < VC * 8; ++j) {
-                    o[j][2 * r] *= f;
-                    o[j][2 * r + 1] *= f;
+                    for (int j = 0; j < NT; ++j) {
+                        o[j][2 * r] *= f;
+                        o[j][2 * r + 1] *= f;
+                    }
                 }
             }
+        } else if (F32 && step % FLUSH == FLUSH - 1) {
+            flush(1.f);
         }
-        uint32_t p[2][RH];
+        uint32_t p[2][RH][PL];
 #pragma unroll
         for (int r = 0; r < RH; ++r) {
             const float ms = m[r] == -INFINITY ? 0.f : m[r];
@@ -258,9 +342,20 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
             for (int i = 0; i < 2; ++i) {
                 const float x = ex2(s[i][2 * r] - ms), y = ex2(s[i][2 * r + 1] - ms);
                 l[r] += x + y;
-                p[i][r] = tc::pack_bf16(x, y);
+                if constexpr (F32)
+                    split3(x, y, p[i][r]);
+                else
+                    p[i][r][0] = tc::pack_bf16(x, y);
             }
         }
+        cp_async_wait<EN - 2>();
+        __syncwarp();
+        if constexpr (EN % 2 == 0)
+            next_keys(fill, step);
+        else
+            next_values(fill);
+        const uint4 *vt = ring + entry * ENTRY;
+        advance();
 #pragma unroll
         for (int c = 0; c < VC; ++c) {
             // keys t, t + 4, t + 8, t + 12
@@ -269,14 +364,27 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = vt[(t + 4 * i) * CH + (x ^ ((t + 4 * i) & 7))];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-                const uint32_t b0 = __byte_perm(word(v[0], j / 2), word(v[1], j / 2), sel);
-                const uint32_t b1 = __byte_perm(word(v[2], j / 2), word(v[3], j / 2), sel);
-                mma16816(o[c * 8 + j], p[0][0], RH == 2 ? p[0][RH - 1] : 0u, p[1][0], RH == 2 ? p[1][RH - 1] : 0u, b0, b1);
+            for (int j = 0; j < EPC; ++j) {
+                float(&acc)[4] = o[c * EPC + j];
+                if constexpr (F32) {
+                    uint32_t b0[3], b1[3];
+                    split3(__uint_as_float(word(v[0], j)), __uint_as_float(word(v[1], j)), b0);
+                    split3(__uint_as_float(word(v[2], j)), __uint_as_float(word(v[3], j)), b1);
+                    mma16816(acc, p[0][0][0], 0u, p[1][0][0], 0u, b0[2], b1[2]);
+                    mma16816(acc, p[0][0][2], 0u, p[1][0][2], 0u, b0[0], b1[0]);
+                    mma16816(acc, p[0][0][0], p[0][0][1], p[1][0][0], p[1][0][1], b0[1], b1[1]);
+                    mma16816(acc, p[0][0][0], p[0][0][1], p[1][0][0], p[1][0][1], b0[0], b1[0]);
+                } else {
+                    const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+                    const uint32_t b0 = __byte_perm(word(v[0], j / 2), word(v[1], j / 2), sel);
+                    const uint32_t b1 = __byte_perm(word(v[2], j / 2), word(v[3], j / 2), sel);
+                    mma16816(acc, p[0][0][0], RH == 2 ? p[0][RH - 1][0] : 0u, p[1][0][0], RH == 2 ? p[1][RH - 1][0] : 0u, b0, b1);
+                }
             }
         }
+        okq >>= 16;
     }
+    flush(1.f);
     cp_async_wait<0>();
     __syncthreads();   // the rings' memory becomes the sums'
     if (RH == 2 && g.cluster > 1) cluster_arrive();
@@ -293,35 +401,40 @@ __global__ void __launch_bounds__(kRowThreads, DP == 64 ? 2 : 1)
 #pragma unroll
         for (int c = 0; c < VC; ++c)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < EPC; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    sm.sums.warps.o[warp][r * 8 + gq][(c * 8 + spread(2 * t + e)) * 8 + j] = o[c * 8 + j][2 * r + e];
+                    sm.sums.warps.o[warp][r * 8 + gq][(c * 8 + spread(2 * t + e)) * EPC + j] =
+                        F32 ? sums[F32 ? c * EPC + j : 0][e] : o[c * EPC + j][2 * r + e];
     }
-    finish_rows<__nv_bfloat16, R, DP>(sm.sums.warps, sm.ctas(), a, g, part, nh, row0, split);
+    finish_rows<T, R, DP>(sm.sums.warps, sm.ctas(), a, g, part, nh, row0, split);
 }
 
-template <int DP, int RH>
+template <class T, int DP, int RH>
 cudaError_t launch_mma(const AttnArgs &a, cudaStream_t st)
 {
-    const int smem = (int)sizeof(MmaShared<DP, RH>);
+    const int smem = (int)sizeof(MmaShared<T, DP, RH>);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     static KernelCache cache;
-    e = ensure_dynamic_smem(cache, dev, attn_mma_kernel<DP, RH>, smem);
+    e = ensure_dynamic_smem(cache, dev, attn_mma_kernel<T, DP, RH>, smem);
     if (e != cudaSuccess) return e;
-    return launch_rows_kernel(attn_mma_kernel<DP, RH>, a, true, 8 * RH, kRowWarps * KEYS, smem, st);
+    return launch_rows_kernel(attn_mma_kernel<T, DP, RH>, a, sizeof(T) == 2, 8 * RH, kRowWarps * KEYS, smem, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_mma(const AttnArgs &a, cudaStream_t st)
+cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, cudaStream_t st)
 {
+    if (!bf16) {
+        if (a.D <= 32) return launch_mma<float, 32, 1>(a, st);
+        return a.D <= 64 ? launch_mma<float, 64, 1>(a, st) : launch_mma<float, 128, 1>(a, st);
+    }
     const bool few = (long long)a.Tq * a.G <= 8;
-    if (a.D <= 64) return few ? launch_mma<64, 1>(a, st) : launch_mma<64, 2>(a, st);
-    return few ? launch_mma<128, 1>(a, st) : launch_mma<128, 2>(a, st);
+    if (a.D <= 64) return few ? launch_mma<__nv_bfloat16, 64, 1>(a, st) : launch_mma<__nv_bfloat16, 64, 2>(a, st);
+    return few ? launch_mma<__nv_bfloat16, 128, 1>(a, st) : launch_mma<__nv_bfloat16, 128, 2>(a, st);
 }
 
 }  // namespace sc

@@ -1,6 +1,11 @@
-// Attention of a few fp32 query rows over many keys (a decoder's next token, a
-// short draft): every key and value is used by R <= 4 rows, so the kernel is
-// bound by reading K and V once.
+// Attention of up to three fp32 query rows per key head over many keys (a
+// decoder's next token, a short draft): every key and value is used by R <= 3
+// rows, so the kernel is bound by reading K and V once.  (The MMA kernel,
+// attn_mma.cu, splits fp32 operands into bf16 planes, which costs the same for
+// one row as for eight.  8 x 4 key heads of 32 over 16384 states: 1 to 3 rows
+// 31.4 us here and 39.6 there, 4 rows 45.7 and 39.6; 32 x 8 key heads of 64
+// over 3136: 1 row 72.4 and 92.7, 4 rows 117 and 92.8; 4 x 8 of 128 over 5000:
+// 1 row 35.5 and 66.2, 4 rows 62.1 and 70.3.)
 //
 //   s_j = scale * q . k_j,  m = max_j s_j,  l = sum_j 2^((s_j - m) log2 e),
 //   o = sum_j 2^((s_j - m) log2 e) v_j,     out = o / l
@@ -223,8 +228,7 @@ cudaError_t launch_rows_r(const AttnArgs &a, cudaStream_t st)
     constexpr int STEP = kRowWarps * (32 / LPK) * U;
     if (rows == 1) return launch_rows_kernel(attn_rows_kernel<LPK, 1, U>, a, false, 1, STEP, 0, st);
     if (rows == 2) return launch_rows_kernel(attn_rows_kernel<LPK, 2, U>, a, false, 2, STEP, 0, st);
-    if (rows == 3) return launch_rows_kernel(attn_rows_kernel<LPK, 3, U>, a, false, 3, STEP, 0, st);
-    return launch_rows_kernel(attn_rows_kernel<LPK, 4, U>, a, false, 4, STEP, 0, st);
+    return launch_rows_kernel(attn_rows_kernel<LPK, 3, U>, a, false, 3, STEP, 0, st);
 }
 
 }  // namespace
