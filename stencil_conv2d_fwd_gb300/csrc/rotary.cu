@@ -14,9 +14,10 @@
 // norm's weights in registers and all its loads issued first, and keeps what
 // it loaded as stored until each head's turn: with floats for all four heads
 // (116 registers, 16 warps an SM) 131072 tokens of 8 x 128 bf16 took 149.6 us,
-// now (32 warps an SM) 97.3 (6.2 TB/s); 65536 + 14400 tokens of 16 x 128 fp32
-// with the norm 210 and 193 us (6.8 TB/s).  Two heads a thread read the table
-// twice as often: 100 and 218 us at the same occupancy.
+// now (32 warps an SM) 92.8 (6.5 TB/s); 65536 + 14400 tokens of 16 x 128 fp32
+// with the norm 210 and 192 us (6.8 TB/s); 2464 + 100352 of 8 x 64 bf16 with the
+// norm 67.6 and 41.1 us (5.1 TB/s; half-heads of 64 bytes).  Two heads a thread
+// read the table twice as often: 100, 200 and 45 us.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -28,13 +29,13 @@ namespace sc {
 
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 128;
 constexpr int kHeads = 4;     // heads of a token per thread
-// CTAs an SM: at most 64 registers a thread, 80 where eight weights' and eight
-// angles' floats of each chunk are held (64 spill them: 90 us, not 47, for the
-// keys of 32 maps of 56 x 56, 8 x 64 bf16).
+// CTAs an SM: at most 64 registers a thread, 96 where eight weights and angles
+// of each chunk are held (64 spill them: 91 us, not 41, for the keys of 32 maps
+// of 56 x 56, 8 x 64 bf16, and their prompts' queries).
 template <int V, bool NORM>
-constexpr int rot_ctas() { return V == 8 && NORM ? 3 : 4; }
+constexpr int rot_ctas() { return V == 8 && NORM ? 5 : 8; }
 
 // V elements (16 bytes, or 8 for four bf16) as stored, and as floats.
 template <class T, int V>
@@ -62,7 +63,7 @@ struct Packed {
         else
             *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
     }
-    __device__ __forceinline__ void unpack(float (&f)[V]) const
+    __device__ __forceinline__ void unpack(float *f) const
     {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
@@ -74,7 +75,7 @@ struct Packed {
             }
         }
     }
-    __device__ __forceinline__ void pack(const float (&f)[V])
+    __device__ __forceinline__ void pack(const float *f)
     {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
@@ -90,7 +91,7 @@ struct Packed {
 
 // V floats at p, 16-byte aligned, of a table that every CTA reads.
 template <int V>
-__device__ __forceinline__ void load_floats(const float *p, float (&f)[V])
+__device__ __forceinline__ void load_floats(const float *p, float *f)
 {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
@@ -105,6 +106,7 @@ __device__ __forceinline__ void load_floats(const float *p, float (&f)[V])
 struct RotGeom {
     int lanes;           // threads per row: a power of two >= D / (2 V)
     int slots;           // D / (2 V)
+    float inv_d;         // 1 / D
     long long blocks0;   // CTAs of part[0]; the others do part[1]
 };
 
@@ -151,8 +153,9 @@ __global__ void __launch_bounds__(kRotThreads, rot_ctas<V, NORM>()) rotary_kerne
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
         if (i < nh) {
-            ra[i].load(x + i * P.x_h + ca);
-            rb[i].load(x + i * P.x_h + cb);
+            ra[i].load(x + ca);
+            rb[i].load(x + cb);
+            x += P.x_h;
         } else {
 #pragma unroll
             for (int j = 0; j < Packed<T, V>::W; ++j) ra[i].w[j] = rb[i].w[j] = 0u;
@@ -182,58 +185,77 @@ __global__ void __launch_bounds__(kRotThreads, rot_ctas<V, NORM>()) rotary_kerne
             for (int j = 0; j < V; ++j) cs[j] = sn[j] = __int_as_float(0x7fc00000);
         }
     }
-    float wa[V], wb[V];
+    // Pair p of the thread is (fa[p], fb[p]), or with adjacent pairs (2p, 2p + 1)
+    // of fa and fb in turn.  With the norm, the weights go into the factors:
+    //   x -> rs (x wx cos - y wy sin),  y -> rs (y wy cos + x wx sin)
+    auto px = [](int p) { return INTERLEAVED ? 2 * p : p; };
+    auto py = [](int p) { return INTERLEAVED ? 2 * p + 1 : V + p; };
+    // and where nothing is turned kx and ky are the weights.
+    float kx[V], ky[V];   // wx cos, wy cos (wx sin and wy sin are cs and sn afterwards)
     if constexpr (NORM) {
+        float w[2 * V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) wa[j] = wb[j] = 1.f;
+        for (int j = 0; j < 2 * V; ++j) w[j] = 1.f;
         if (act && P.weight) {
-            load_floats<V>(P.weight + ca, wa);
-            load_floats<V>(P.weight + cb, wb);
+            load_floats<V>(P.weight + ca, w);
+            load_floats<V>(P.weight + cb, w + V);
+        }
+#pragma unroll
+        for (int p = 0; p < V; ++p) {
+            kx[p] = w[px(p)];
+            ky[p] = w[py(p)];
+            if (turn) {
+                const float c = cs[p], s = sn[p];
+                cs[p] = kx[p] * s;
+                sn[p] = ky[p] * s;
+                kx[p] *= c;
+                ky[p] *= c;
+            }
         }
     }
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-        float fa[V], fb[V];
-        ra[i].unpack(fa);
-        rb[i].unpack(fb);
+        float f[2 * V];   // the thread's elements: chunk a, then chunk b
+        ra[i].unpack(f);
+        rb[i].unpack(f + V);
+        float rs = 1.f;
         if constexpr (NORM) {
             float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) ss = fmaf(fa[j], fa[j], fmaf(fb[j], fb[j], ss));
-            for (int off = g.lanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            const float rs = rsqrtf(ss / (float)a.D + a.eps);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                fa[j] *= rs * wa[j];
-                fb[j] *= rs * wb[j];
-            }
+            for (int j = 0; j < 2 * V; ++j) ss = fmaf(f[j], f[j], ss);
+            if (g.lanes > 16) ss += __shfl_xor_sync(0xffffffffu, ss, 16);
+            if (g.lanes > 8) ss += __shfl_xor_sync(0xffffffffu, ss, 8);
+            if (g.lanes > 4) ss += __shfl_xor_sync(0xffffffffu, ss, 4);
+            if (g.lanes > 2) ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+            if (g.lanes > 1) ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            rs = rsqrtf(fmaf(ss, g.inv_d, a.eps));
         }
         if (i >= nh) continue;
         if (turn) {
-            if (INTERLEAVED) {
-                // pairs (0, 1), (2, 3), ... of the 2 V adjacent elements
 #pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    const float p = fa[j], q = fa[j + 1];
-                    fa[j] = p * cs[j / 2] - q * sn[j / 2];
-                    fa[j + 1] = q * cs[j / 2] + p * sn[j / 2];
-                    const float r = fb[j], u = fb[j + 1];
-                    fb[j] = r * cs[V / 2 + j / 2] - u * sn[V / 2 + j / 2];
-                    fb[j + 1] = u * cs[V / 2 + j / 2] + r * sn[V / 2 + j / 2];
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float p = fa[j], q = fb[j];
-                    fa[j] = p * cs[j] - q * sn[j];
-                    fb[j] = q * cs[j] + p * sn[j];
+            for (int p = 0; p < V; ++p) {
+                float &x = f[px(p)], &y = f[py(p)];
+                const float u = x, v = y;
+                if constexpr (NORM) {
+                    x = rs * (u * kx[p] - v * sn[p]);
+                    y = rs * (v * ky[p] + u * cs[p]);
+                } else {
+                    x = u * cs[p] - v * sn[p];
+                    y = v * cs[p] + u * sn[p];
                 }
             }
+        } else if constexpr (NORM) {
+#pragma unroll
+            for (int p = 0; p < V; ++p) {
+                f[px(p)] *= rs * kx[p];
+                f[py(p)] *= rs * ky[p];
+            }
         }
-        ra[i].pack(fa);
-        rb[i].pack(fb);
-        ra[i].store(y + i * P.y_h + ca);
-        rb[i].store(y + i * P.y_h + cb);
+        ra[i].pack(f);
+        rb[i].pack(f + V);
+        ra[i].store(y + ca);
+        rb[i].store(y + cb);
+        y += P.y_h;
     }
 }
 
@@ -242,6 +264,7 @@ cudaError_t launch_rot(const RotaryArgs &a, cudaStream_t st)
 {
     RotGeom g;
     g.slots = a.D / (2 * V);
+    g.inv_d = 1.f / (float)a.D;
     g.lanes = 1;
     while (g.lanes < g.slots) g.lanes *= 2;
     const int per_cta = kRotThreads / g.lanes;
