@@ -7,20 +7,16 @@
 //
 //   S = Q K^T,  P = 2^(c S - m),  O = P V,  out = O / sum P,   c = scale log2 e
 //
-// One pass over the keys, m and the sum running values of a row.  Each warp
-// has a ring of its own in shared memory, ENTRIES pieces of 16 keys or 16
-// values that its lanes copy there asynchronously, 16 bytes each, so that some
-// 100 to 200 KB are under way on an SM at any time without a register held
-// for them and without a barrier between warps.  States that are not valid are
-// not read (their bytes are zero-filled): whatever is stored there does not
-// reach a sum.  Operands go from there to the MMA's registers 16 bytes a lane:
+// One pass over the keys, m and the sum running values of a row.  Keys and
+// values come through a ring of each warp's own in shared memory (PieceRing),
+// and from there to the MMA's registers 16 bytes a lane:
 //   * a product's order of summation over d is free, so lane (g, t) of a quad
 //     takes its key's 16-byte chunks 4 i + t as its share of k, the same for
 //     Q, with no transposition;
 //   * the columns of V's product are free as well: lane (g, t) reads one chunk
 //     at a time of each of the four keys that its share of P stands for, and
 //     pairs two keys' elements.
-// Chunk x of a row y lies at chunk x XOR (y mod 8).  Column g of the scores is
+// Column g of the scores is
 // key g / 2 + 4 (g mod 2), and chunk column g of V is chunk g / 2 + 4 (g mod 2),
 // so that every quarter-warp's reads fall in eight different bank groups.  The
 // scores' registers are P's operand registers as they are.
@@ -32,7 +28,6 @@
 // second plane.  The MMAs cut sums short instead of rounding them, so the large
 // product of the scores and the small ones have accumulators of their own, and
 // O is moved to sums outside the MMAs every FLUSH steps.
-// A warp's pieces are every 8th of the CTA's share.
 #include "attn_rows.cuh"
 #include "launch.h"
 #include "tc_common.cuh"
@@ -52,7 +47,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 
-constexpr int KEYS = 16;   // keys of a step
 constexpr int FLUSH = 4;
 
 // Index of column g of a product (see above).
@@ -70,53 +64,27 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3])
 }
 
 // DP: head width rounded up to 64 or 128 (fp32: 32, 64 or 128).  RH: 1 for up
-// to 8 rows, 2 for 16 (bf16 only: fp32 has no registers for them).
+// to 8 rows, 2 for 16 (bf16 only: fp32 has no registers for them, and 16 rows'
+// cluster sums no shared memory of their own).
 template <class T, int DP>
-struct Rows {
-    static constexpr bool F32 = sizeof(T) == 4;
-    static constexpr int EPC = 16 / sizeof(T);   // elements of a chunk
-    static constexpr int CH = DP / EPC;          // chunks of a row
-    // entries of a warp's ring (its step's valid bits are 16 of a 64-bit word: at most 7)
-    static constexpr int ENTRIES = F32 && DP == 128 ? 3 : 6;
-    static constexpr int CTAS = 16 * CH * 16 * ENTRIES * kRowWarps <= 96 * 1024 ? 2 : 1;   // an SM
-};
-
-// The rings' memory becomes the sums' at the end.  With 8 rows the cluster's
-// sums have their own: the first CTA's place is then free from the start, and
-// no CTA waits for another's loop.  With 16 there is no room.
+constexpr int entries() { return sizeof(T) == 4 && DP == 128 ? 3 : 6; }
+template <class T, int DP>
+constexpr int ctas_per_sm() { return PieceRing<T, DP, entries<T, DP>()>::CH == 8 ? 2 : 1; }
 template <class T, int DP, int RH>
-struct MmaShared {
-    union {
-        uint4 ring[kRowWarps][Rows<T, DP>::ENTRIES][KEYS][Rows<T, DP>::CH];
-        struct {
-            WarpSums<8 * RH, DP> warps;
-            CtaSums<RH == 1 ? 1 : 8 * RH, RH == 1 ? 1 : DP> shared_ctas;
-        } sums;
-    };
-    CtaSums<RH == 1 ? 8 : 1, RH == 1 ? DP : 1> own_ctas;
-    __device__ __forceinline__ CtaSums<8 * RH, DP> &ctas()
-    {
-        if constexpr (RH == 1)
-            return own_ctas;
-        else
-            return sums.shared_ctas;
-    }
-};
+using MmaShared = RowsShared<T, DP, entries<T, DP>(), 8 * RH, RH == 1>;
 
 template <class T, int DP, int RH>
-__global__ void __launch_bounds__(kRowThreads, Rows<T, DP>::CTAS)
+__global__ void __launch_bounds__(kRowThreads, ctas_per_sm<T, DP>())
     attn_mma_kernel(const AttnArgs a, const RowsGeom g, const AttnPartials part)
 {
-    using RT = Rows<T, DP>;
-    constexpr bool F32 = RT::F32;
+    using Ring = PieceRing<T, DP, entries<T, DP>()>;
+    constexpr bool F32 = sizeof(T) == 4;
     constexpr int R = 8 * RH;
-    constexpr int EN = RT::ENTRIES, EPC = RT::EPC, CH = RT::CH;
+    constexpr int EPC = Ring::EPC, CH = Ring::CH;
     constexpr int KC = CH / 4;           // chunks of a key per lane
     constexpr int VC = CH / 8;           // of a value per lane
     constexpr int NT = VC * EPC;         // products of 8 columns of O
-    constexpr int RPL = CH >= 32 ? 1 : 32 / CH;   // rows of a warp-wide copy
-    constexpr int COPIES = KEYS / RPL;
-    static_assert(CH <= 32 && (!F32 || RH == 1), "one row at most a copy; fp32: 8 rows");
+    static_assert(!F32 || RH == 1, "fp32: 8 rows");
     extern __shared__ __align__(128) unsigned char dyn[];
     MmaShared<T, DP, RH> &sm = *reinterpret_cast<MmaShared<T, DP, RH> *>(dyn);
 
@@ -159,71 +127,8 @@ __global__ void __launch_bounds__(kRowThreads, Rows<T, DP>::CTAS)
             }
         }
 
-    int len = a.Tk;
-    if (a.k_len) len = max(0, min(len, a.k_len[n]));
-    // this CTA's keys: an equal share of the sequence's own length, in pieces
-    const int pieces = (len + KEYS - 1) / KEYS;
-    const int p0 = (int)((long long)pieces * split / g.splits), p1 = (int)((long long)pieces * (split + 1) / g.splits);
-    const int steps = p1 - p0 > warp ? (p1 - p0 - warp + kRowWarps - 1) / kRowWarps : 0;   // of this warp
-    const int key0 = (p0 + warp) * KEYS;
-    constexpr int STEP = kRowWarps * KEYS;
-    const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
-
-    // the lane's part of a piece's copies: row crow + RPL i, chunk cch
-    const int crow = lane / CH, cch = lane % CH;
-    const bool cact = cch * EPC < a.D;   // chunks past D are zero-filled
-    const T *kbase = static_cast<const T *>(a.k), *vbase = static_cast<const T *>(a.v);
-    const T *kp = kbase + n * a.ks.n + h * a.ks.h + (long long)(key0 + crow) * a.ks.t + (cact ? cch * EPC : 0);
-    const T *vp = vbase + n * a.vs.n + h * a.vs.h + (long long)(key0 + crow) * a.vs.t + (cact ? cch * EPC : 0);
-    uint4 *ring = &sm.ring[warp][0][0][0];
-    constexpr int ENTRY = KEYS * CH;   // in 16-byte units
-
-    // Valid bits of a step's keys.  The mask's byte is read a step ahead.
-    auto mask_byte = [&](int step) -> int {
-        const int key = key0 + step * STEP + lane;
-        return step < steps && lane < KEYS && key < len ? (mb ? (int)mb[key] : 1) : 0;
-    };
-    auto copy = [&](int entry, const T *&p, long long pitch, const T *base, uint32_t ok) {
-        const uint32_t at = smem_u32(ring + entry * ENTRY);
-        const T *src = p;
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i, src += RPL * pitch) {
-            const int row = crow + i * RPL;
-            const bool on = cact && (ok >> row & 1u);
-            cp_async16(at + (row * CH + (cch ^ (row & 7))) * 16, on ? src : base, on ? 16 : 0);
-        }
-        cp_async_commit();
-        p += STEP * pitch;
-    };
-    // Pieces in order: keys of step 0, values of step 0, keys of step 1, ...
-    // EN - 1 of them are under way; the valid bits of the current step and
-    // those after it, 16 each, the current lowest.
-    unsigned long long okq = 0;
-    constexpr int LEAD = EN / 2;   // steps whose keys are under way
-    int byte;
-    {
-        constexpr int FIRST = (EN - 1 + 1) / 2;   // steps begun before the loop
-        int b[FIRST];
-#pragma unroll
-        for (int i = 0; i < FIRST; ++i) b[i] = mask_byte(i);
-#pragma unroll
-        for (int i = 0; i < FIRST; ++i) {
-            const uint32_t ok = __ballot_sync(0xffffffffu, b[i] != 0);
-            okq |= (unsigned long long)ok << (16 * i);
-            copy(2 * i, kp, a.ks.t, kbase, ok);
-            if (2 * i + 1 < EN - 1) copy(2 * i + 1, vp, a.vs.t, vbase, ok);
-        }
-        byte = mask_byte(FIRST);
-    }
-    auto next_keys = [&](int entry, int step) {   // keys of the step LEAD ahead of the current, which is `step`
-        const uint32_t ok = __ballot_sync(0xffffffffu, byte != 0);
-        byte = mask_byte(step + LEAD + 1);
-        okq |= (unsigned long long)ok << (16 * LEAD);
-        copy(entry, kp, a.ks.t, kbase, ok);
-    };
-    auto next_values = [&](int entry) {   // values of the step (EN - 1) / 2 ahead
-        copy(entry, vp, a.vs.t, vbase, (uint32_t)(okq >> (16 * ((EN - 1) / 2))) & 0xffffu);
-    };
+    Ring ring;
+    ring.begin(sm.ring[warp], a, n, h, split, g.splits, warp);
 
     const float sc = a.scale * kLog2e;
     float m[RH], l[RH], o[NT][4], sums[F32 ? NT : 1][2];
@@ -249,22 +154,9 @@ __global__ void __launch_bounds__(kRowThreads, Rows<T, DP>::CTAS)
         }
     };
 
-    int entry = 0, fill = EN - 1;   // ring entries of the piece in use and of the next one to be asked for
-    auto advance = [&]() {
-        entry = entry + 1 == EN ? 0 : entry + 1;
-        fill = fill + 1 == EN ? 0 : fill + 1;
-    };
-    for (int step = 0; step < steps; ++step) {
-        const uint32_t ok = (uint32_t)okq & 0xffffu;
-        cp_async_wait<EN - 2>();
-        __syncwarp();
-        // the next piece goes where the last one was read (the barrier above is behind those reads)
-        if constexpr (EN % 2 == 0)
-            next_values(fill);
-        else
-            next_keys(fill, step);
-        const uint4 *kt = ring + entry * ENTRY;
-        advance();
+    for (int step = 0; step < ring.steps; ++step) {
+        const uint32_t ok = ring.valid();
+        const uint4 *kt = ring.template piece<true>(step);
 
         float s[2][4];
 #pragma unroll
@@ -348,14 +240,7 @@ __global__ void __launch_bounds__(kRowThreads, Rows<T, DP>::CTAS)
                     p[i][r][0] = tc::pack_bf16(x, y);
             }
         }
-        cp_async_wait<EN - 2>();
-        __syncwarp();
-        if constexpr (EN % 2 == 0)
-            next_keys(fill, step);
-        else
-            next_values(fill);
-        const uint4 *vt = ring + entry * ENTRY;
-        advance();
+        const uint4 *vt = ring.template piece<false>(step);
 #pragma unroll
         for (int c = 0; c < VC; ++c) {
             // keys t, t + 4, t + 8, t + 12
@@ -382,7 +267,7 @@ __global__ void __launch_bounds__(kRowThreads, Rows<T, DP>::CTAS)
                 }
             }
         }
-        okq >>= 16;
+        ring.next_step();
     }
     flush(1.f);
     cp_async_wait<0>();
@@ -413,15 +298,9 @@ __global__ void __launch_bounds__(kRowThreads, Rows<T, DP>::CTAS)
 template <class T, int DP, int RH>
 cudaError_t launch_mma(const AttnArgs &a, cudaStream_t st)
 {
-    const int smem = (int)sizeof(MmaShared<T, DP, RH>);
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     static KernelCache cache;
-    e = ensure_dynamic_smem(cache, dev, attn_mma_kernel<T, DP, RH>, smem);
-    if (e != cudaSuccess) return e;
-    return launch_rows_kernel(attn_mma_kernel<T, DP, RH>, a, sizeof(T) == 2, 8 * RH, kRowWarps * KEYS, smem, st);
+    return launch_rows_kernel(attn_mma_kernel<T, DP, RH>, cache, a, sizeof(T) == 2, 8 * RH,
+                              (int)sizeof(MmaShared<T, DP, RH>), st);
 }
 
 }  // namespace

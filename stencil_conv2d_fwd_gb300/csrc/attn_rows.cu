@@ -2,7 +2,8 @@
 // decoder's next token, a short draft): every key and value is used by R <= 3
 // rows, so the kernel is bound by reading K and V once.  (The MMA kernel,
 // attn_mma.cu, splits fp32 operands into bf16 planes, which costs the same for
-// one row as for eight.  8 x 4 key heads of 32 over 16384 states: 1 to 3 rows
+// one row as for eight; and asynchronous copies to shared memory, as there, took
+// 35.5, 80.5 and 48.8 us for one row of the cases below.  8 x 4 key heads of 32 over 16384 states: 1 to 3 rows
 // 31.4 us here and 39.6 there, 4 rows 45.7 and 39.6; 32 x 8 key heads of 64
 // over 3136: 1 row 72.4 and 92.7, 4 rows 117 and 92.8; 4 x 8 of 128 over 5000:
 // 1 row 35.5 and 66.2, 4 rows 62.1 and 70.3.)
@@ -221,14 +222,19 @@ __global__ void __launch_bounds__(kRowThreads, 2) attn_rows_kernel(const AttnArg
     finish_rows<float, R, DP>(sm, cs, a, g, part, nh, row0, split);
 }
 
+template <int LPK, int R, int U>
+cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
+{
+    static KernelCache cache;
+    return launch_rows_kernel(attn_rows_kernel<LPK, R, U>, cache, a, false, R, 0, st);
+}
+
 template <int LPK, int U>
 cudaError_t launch_rows_r(const AttnArgs &a, cudaStream_t st)
 {
     const long long rows = (long long)a.Tq * a.G;
-    constexpr int STEP = kRowWarps * (32 / LPK) * U;
-    if (rows == 1) return launch_rows_kernel(attn_rows_kernel<LPK, 1, U>, a, false, 1, STEP, 0, st);
-    if (rows == 2) return launch_rows_kernel(attn_rows_kernel<LPK, 2, U>, a, false, 2, STEP, 0, st);
-    return launch_rows_kernel(attn_rows_kernel<LPK, 3, U>, a, false, 3, STEP, 0, st);
+    if (rows == 1) return launch_rows<LPK, 1, U>(a, st);
+    return rows == 2 ? launch_rows<LPK, 2, U>(a, st) : launch_rows<LPK, 3, U>(a, st);
 }
 
 }  // namespace
