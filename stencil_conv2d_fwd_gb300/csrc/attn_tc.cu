@@ -69,6 +69,7 @@ constexpr int THREADS = 384;
 constexpr int MAX_SLOTS = 12;
 constexpr int VC = 8;                  // barriers of cleared value tiles: more than the ring holds
 constexpr int LIST = 512;              // key tiles of a share that are looked through; a longer share keeps all
+constexpr int GRID_Y = 32768;          // (sequence, key head) pairs of a grid's y axis
 constexpr float GROW = 8.f;            // log2 growth of a row's maximum that rescales O
 constexpr size_t SMEM_CAP = 227 * 1024;
 
@@ -184,6 +185,16 @@ __device__ __forceinline__ void named_sync()
 {
     asm volatile("bar.sync %0, %1;\n" ::"n"(ID), "n"(N) : "memory");
 }
+template <int ID, int N>
+__device__ __forceinline__ void named_arrive()
+{
+    asm volatile("bar.arrive %0, %1;\n" ::"n"(ID), "n"(N) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m)
+{
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<unsigned long long>(m)) : "memory");
+}
 
 // Matrix descriptors' high words: 128-byte swizzle, 8-row groups 1024 bytes
 // apart.  Low words: the start address; the second operand V is N-major, its
@@ -223,13 +234,18 @@ constexpr int ring_slots()
     return n < MAX_SLOTS ? n : MAX_SLOTS;
 }
 
+template <bool B>
+struct Bool {
+    static constexpr bool value = B;
+};
+
 // PL operand planes: 1 (bf16 tensors), or 3 (fp32 tensors split into three
 // bf16 planes, see attn_split.cu).
 template <int DP, int PL, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                   const __grid_constant__ CUtensorMap mv, const AttnArgs a, const Geom g, const AttnPartials part,
-                   int *status, unsigned long long timeout_ns)
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const AttnArgs a,
+                   const Geom g, const AttnPartials part, int *status, unsigned long long timeout_ns)
 {
     constexpr int DB = DP / 64;                 // 64-column blocks of a head
     constexpr int QT = PAIR ? 2 : 1;            // row tiles
@@ -249,10 +265,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 
     // what this CTA does
-    const int split = blockIdx.x % g.splits;
-    const int unit = (blockIdx.x / g.splits) % g.units;
-    const int nh = blockIdx.x / g.splits / g.units;
+    const int nh = blockIdx.y + blockIdx.z * GRID_Y;
+    if (nh >= a.N * a.Hkv) return;
+    const int unit = g.splits == 1 ? blockIdx.x : blockIdx.x / g.splits;
+    const int split = blockIdx.x - unit * g.splits;
     const int n = nh / a.Hkv, h = nh - n * a.Hkv;
+    if (warp == 8 && lane < 4) prefetch_map(lane == 0 ? &mq : (lane == 1 ? &mk : (lane == 2 ? &mv : &mo)));
     int len = a.Tk;
     if (a.k_len) len = max(0, min(len, a.k_len[n]));
     const int tiles_all = (len + KT - 1) / KT;
@@ -302,7 +320,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     };
 
-    int ahead = 0;   // tiles whose copies are issued before the CTA's barrier
     if (warp == 8) {
         for (int i = lane; i < BARS; i += 32) mbar_init(smem_u32(&sh.full[0]) + 8 * i, i < BARS_ONE ? 1 : (i < BARS_TWO ? 2 : 4));
         if (lane == 0) sh.abort = 0;
@@ -320,9 +337,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     g.packed ? p : n, smem_u32(&sh.q_full));
             }
         }
-        // (with a mask the tiles are not known yet)
-        if (lane == 0 && !look)
-            for (; ahead < 2 * nt && (ahead + 1) * PL <= SLOTS; ++ahead) load_tile(ahead);
         __syncwarp();
     } else if (warp == 9) {
         tc::tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -341,7 +355,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
     tc::fence_before_sync();
-    __syncthreads();
+    // the copying warp goes on: the first copies' latency runs beside the
+    // allocation, and the others do not wait until it has issued them
+    if (warp == 8 && !look)
+        named_arrive<4, THREADS>();
+    else
+        named_sync<4, THREADS>();
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
     const int q_tiles = nt;   // the row tiles have been asked for
@@ -367,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_OTHER));
         if (warp == 8) {
             if (lane == 0) {
-                for (int seq = ahead; seq < 2 * nt; ++seq) load_tile(seq);
+                for (int seq = 0; seq < 2 * nt; ++seq) load_tile(seq);
                 // a mask that leaves nothing: no one else waits for the row tiles
                 if (nt == 0 && q_tiles > 0) wait(sh.q_full, 0);
             }
@@ -745,44 +764,75 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool any = nt > 0, two = !PAIR && nt > 1;
             const bool final_out = part.parts == 0;
             const float inv = final_out ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            const long long prow = ((long long)split * a.N * a.Hkv + nh) * ((long long)a.Tq * a.G) + (long long)tok * a.G + gh;
+            // The row tile goes to memory by TMA (rows and columns past the
+            // tensor's end are left out), from shared memory that is free by
+            // now: the stream's own row tile of Q (its scores' products are
+            // complete), or with one row tile the ring.  (16-byte stores of 128
+            // rows to 128 lines each took 2 us of a CTA's 22.)
+            if (nt == 0 && q_tiles > 0) wait(sh.q_full, 0);
+            unsigned char *tile = dyn + (PAIR ? i * PL * DB * BLK : q_region<DP, PL, PAIR>());
+            constexpr int ROOM = PAIR ? PL * DB : SLOTS * SLOT / BLK;   // blocks of 128 rows of 128 bytes
+            auto store = [&](auto out_bf16) {
+                constexpr bool OB = decltype(out_bf16)::value;
+                constexpr int CB = OB ? 64 : 32, NB = DP / CB;   // columns of a block, blocks
+                constexpr int GRP = NB < ROOM ? NB : ROOM;       // blocks at a time
 #pragma unroll
-            for (int d = 0; d < DP; d += 32) {
-                if (d >= a.D) continue;
-                float y[32];
-                if (any) {
-                    row_sums(d, y);
-                } else {
+                for (int b0 = 0; b0 < NB; b0 += GRP) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) y[k] = 0.f;
+                    for (int d = b0 * CB; d < (b0 + GRP) * CB; d += 32) {
+                        if (d >= a.D) continue;
+                        float y[32];
+                        if (any) {
+                            row_sums(d, y);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) y[k] = 0.f;
+                        }
+                        uint32_t w[OB ? 16 : 32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            float v = y[k] * f0;
+                            if (two) v = fmaf(stage[(d + k) * TILE + row], f1, v);
+                            y[k] = l == 0.f ? 0.f : v * inv;
+                        }
+#pragma unroll
+                        for (int k = 0; k < (OB ? 16 : 32); ++k)
+                            w[k] = OB ? tc::pack_bf16(y[OB ? 2 * k : k], y[OB ? 2 * k + 1 : k]) : __float_as_uint(y[k]);
+                        const uint32_t at = smem_u32(tile) + (d / CB - b0) * BLK + row * 128;
+                        const int c0 = d % CB * (OB ? 2 : 4) / 16;   // 16-byte chunks, swizzled as the copies expect
+#pragma unroll
+                        for (int k = 0; k < (OB ? 4 : 8); ++k)
+                            tc::st_shared_v4(at + (((c0 + k) ^ (row & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    }
+                    fence_proxy_async_smem();
+                    if (i == 0)
+                        named_sync<1, 128>();
+                    else
+                        named_sync<2, 128>();
+                    if (row == 0 && rt < g.row_tiles) {
+                        const int tok0 = rt / g.gblocks * g.tb, gh0 = rt % g.gblocks * g.gb;
+                        for (int b = b0; b < b0 + GRP && b * CB < a.D; ++b)
+                            tma_store_5d(&mo, smem_u32(tile) + (b - b0) * BLK, b * CB, gh0, tok0, final_out ? h : nh,
+                                         final_out ? n : split);
+                        bulk_commit();
+                        bulk_wait_read<0>();   // the writes end with the grid, the reads of shared memory before the CTA
+                    }
+                    if (b0 + GRP < NB) {   // the blocks are written over
+                        if (i == 0)
+                            named_sync<1, 128>();
+                        else
+                            named_sync<2, 128>();
+                    }
                 }
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    float v = y[k] * f0;
-                    if (two) v = fmaf(stage[(d + k) * TILE + row], f1, v);
-                    y[k] = l == 0.f ? 0.f : v * inv;
-                }
-                if (!live) continue;
-                if (final_out && PL == 1) {
-                    __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.out) + n * a.os.n + tok * a.os.t + hq * a.os.h + d;
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        if (d + k < a.D)
-                            *reinterpret_cast<uint4 *>(op + k) =
-                                make_uint4(tc::pack_bf16(y[k], y[k + 1]), tc::pack_bf16(y[k + 2], y[k + 3]),
-                                           tc::pack_bf16(y[k + 4], y[k + 5]), tc::pack_bf16(y[k + 6], y[k + 7]));
-                } else {
-                    float *op = final_out ? static_cast<float *>(a.out) + n * a.os.n + tok * a.os.t + hq * a.os.h + d
-                                          : part.o + prow * a.D + d;
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        if (d + k < a.D)
-                            *reinterpret_cast<float4 *>(op + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-                }
-            }
+            };
+            if (PL == 1 && final_out)
+                store(Bool<PL == 1>{});
+            else
+                store(Bool<false>{});
             if (live) {
                 if (!final_out)
-                    part.ml[prow] = make_float2(m, l);
+                    part.ml[((long long)split * a.N * a.Hkv + nh) * ((long long)a.Tq * a.G) + (long long)tok * a.G + gh] =
+                        make_float2(m, l);
                 else if (a.lse)
                     a.lse[((long long)n * a.Hq + hq) * a.Tq + tok] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
             }
@@ -823,8 +873,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return fn;
 }
 
-// A map of bf16 rows of D elements with four outer axes (strides in bytes).
-bool encode_map(CUtensorMap *m, const void *base, int D, const long long (&size)[4], const long long (&stride)[4],
+// A map of rows of D elements with four outer axes (strides in bytes), boxes of
+// 128 bytes of box1 x box2 rows.
+bool encode_map(CUtensorMap *m, bool bf16, const void *base, int D, const long long (&size)[4], const long long (&stride)[4],
                 int box1, int box2)
 {
     cuuint64_t dims[5] = {(cuuint64_t)D}, strides[4];
@@ -834,15 +885,16 @@ bool encode_map(CUtensorMap *m, const void *base, int D, const long long (&size)
         // multiple of 16 above zero
         strides[i] = size[i] == 1 ? 16 : (cuuint64_t)stride[i];
     }
-    const cuuint32_t box[5] = {64, (cuuint32_t)box1, (cuuint32_t)box2, 1, 1};
+    const cuuint32_t box[5] = {bf16 ? 64u : 32u, (cuuint32_t)box1, (cuuint32_t)box2, 1, 1};
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return encoder()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 5,
+                     const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
 };
 
 template <int DP, int PL, bool PAIR>
@@ -865,9 +917,10 @@ cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPa
     if (regs != REGS_LAUNCH) return cudaErrorNotSupported;
     int *status = device_status_ptr();
     if (!status) return cudaErrorInvalidDevice;
-    const long long grid = (long long)a.N * a.Hkv * g.units * g.splits;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    attn_tc_kernel<DP, PL, PAIR><<<(unsigned)grid, THREADS, SMEM, st>>>(m.q, m.k, m.v, a, g, part, status,
+    const long long x = (long long)g.units * g.splits, nh = (long long)a.N * a.Hkv;
+    if (x > 0x7fffffffLL || nh > (long long)GRID_Y * 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)x, (unsigned)(nh < GRID_Y ? nh : GRID_Y), (unsigned)((nh + GRID_Y - 1) / GRID_Y));
+    attn_tc_kernel<DP, PL, PAIR><<<grid, THREADS, SMEM, st>>>(m.q, m.k, m.v, m.out, a, g, part, status,
                                                                        1000000000ull);
     return cudaGetLastError();
 }
@@ -932,22 +985,32 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
     if (g.packed) {
         const long long size[4] = {a.G, a.Tq, (long long)a.N * a.Hkv, planes}, d = a.D * 2LL;
         const long long stride[4] = {d, d * a.G, d * a.G * a.Tq, d * rows};
-        ok = at::encode_map(&m.q, plane[0], a.D, size, stride, g.gb, g.tb);
+        ok = at::encode_map(&m.q, true, plane[0], a.D, size, stride, g.gb, g.tb);
         const long long ksize[4] = {a.Tk, a.Hkv, a.N, planes};
         const long long kstride[4] = {d, d * a.Tk, d * a.Tk * a.Hkv, d * keys};
-        ok = ok && at::encode_map(&m.k, k, a.D, ksize, kstride, kt, 1) &&
-             at::encode_map(&m.v, v, a.D, ksize, kstride, kt, 1);
+        ok = ok && at::encode_map(&m.k, true, k, a.D, ksize, kstride, kt, 1) &&
+             at::encode_map(&m.v, true, v, a.D, ksize, kstride, kt, 1);
     } else {
         const long long size[4] = {a.G, a.Tq, a.Hkv, a.N};
         const long long stride[4] = {a.qs.h * 2, a.qs.t * 2, a.qs.h * a.G * 2, a.qs.n * 2};
-        ok = at::encode_map(&m.q, a.q, a.D, size, stride, g.gb, g.tb);
+        ok = at::encode_map(&m.q, true, a.q, a.D, size, stride, g.gb, g.tb);
         // a shared axis (stride 0) of the keys or values is one coordinate of the map
         for (int i = 0; i < 2; ++i) {
             const HeadStrides &s = i ? a.vs : a.ks;
             const long long ksize[4] = {a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1};
             const long long kstride[4] = {s.t * 2, s.h * 2, s.n * 2, 16};
-            ok = ok && at::encode_map(i ? &m.v : &m.k, i ? v : k, a.D, ksize, kstride, kt, 1);
+            ok = ok && at::encode_map(i ? &m.v : &m.k, true, i ? v : k, a.D, ksize, kstride, kt, 1);
         }
+    }
+    if (part.parts > 0) {
+        const long long size[4] = {a.G, a.Tq, (long long)a.N * a.Hkv, g.splits}, d = a.D * 4LL;
+        const long long stride[4] = {d, d * a.G, d * a.G * a.Tq, d * rows};
+        ok = ok && at::encode_map(&m.out, false, part.o, a.D, size, stride, g.gb, g.tb);
+    } else {
+        const int es = bf16 ? 2 : 4;
+        const long long size[4] = {a.G, a.Tq, a.Hkv, a.N};
+        const long long stride[4] = {a.os.h * es, a.os.t * es, a.os.h * a.G * es, a.os.n * es};
+        ok = ok && at::encode_map(&m.out, bf16, a.out, a.D, size, stride, g.gb, g.tb);
     }
     cudaError_t e = ok ? cudaSuccess : cudaErrorInvalidValue;
     if (e == cudaSuccess && g.packed) e = launch_attn_split(a, bf16, plane, st);
