@@ -13,7 +13,9 @@
 //   * Two row tiles (PAIR): stream i is row tile i, and every key tile is used
 //     by both.
 //   * One row tile: stream i takes every other key tile; the two (m, sum, O)
-//     are joined at the end.  For calls with at most 128 rows per key head.
+//     are joined at the end.  Where every row tile has an SM of its own.
+// P is handed over in two halves of the key tile, so that the first half's
+// products run while the second half is made.
 // Warps 0-3 and 4-7 are the streams' softmax, one thread per row (a warp
 // reads the quadrant of tensor memory that it may address): scores from
 // tensor memory, masked, 2^x, and P back to tensor memory as the second
@@ -28,7 +30,7 @@
 // the valid states' rows alone, so that every tile is dense, cost more than
 // the states left out: 32 x 77 queries over padded 56 x 56 maps, half of whose
 // states are valid, 118 us by TMA gathers of four rows, 60 us by 16-byte
-// copies, MASKED_US us in place.)
+// copies, 46 us in place.)
 //
 // Accumulators, softmax and sums are fp32.  bf16 tensors: P is rounded to bf16
 // for the second product (a relative error of 2^-8 of single terms, the size
@@ -39,6 +41,20 @@
 // accumulator that adds up (1e-5 of the result at 3136 keys); so there O holds
 // one key tile's product at a time, which the softmax threads add to sums of
 // their own in registers.
+//
+// Bound (4 x 16384 queries over 3600 states, 16 heads of 128 bf16: 1.285 ms,
+// 1.50 PFLOP/s, 0.78 of the 1.94 that a large library product reaches here): the
+// products' reads of shared memory.  A 128 x 128 x 16 product takes 64 clocks
+// and reads 8 KB for S (the row and the key tile's slices), 4 KB for O, and the
+// copies write 64 KB a pair of tiles, together what 128 bytes a clock allow;
+// a pair of 128 x 128 tiles takes some 2800 clocks against 2048 of products
+// alone, and starting and ending a CTA 6 of 85 thousand.  Two threads a row
+// (20 warps) made it 6% slower: the softmax is not what is waited for.  With 64
+// columns or fewer a product takes the same 64 clocks, so the O products of
+// 64-wide heads run at half rate: fp32 prompts (2 x 1001 queries over 3136
+// states, 8 heads of 64: 82 us, 157 TFLOP/s of the formula, 6 times that in
+// products) are bound by them.  Few row tiles are bound by reading keys and
+// values (6.7 TB/s while the tiles run) and by a CTA's start and end, 4 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
