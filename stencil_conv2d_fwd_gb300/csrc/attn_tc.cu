@@ -958,13 +958,16 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
     const bool pair = (bf16 || a.D <= 64) && g.row_tiles > 1 &&
                       (long long)a.N * a.Hkv * g.row_tiles > device_sm_count();
     g.units = pair ? (g.row_tiles + 1) / 2 : g.row_tiles;
-    // CTAs per row unit: fill the GPU, at least four key tiles each
+    // CTAs per row unit: fill the GPU, at least four key tiles each (2 x 8 key
+    // heads, 77 rows, 25 tiles: 19.1 us, at least eight 20.1, sixteen 27.3; two of
+    // 9000 keys, 17 rows: 18.1, 20.1, 26.3), and none for fewer than
+    // twelve tiles, whose join costs what it saves
     const long long blocks = (long long)a.N * a.Hkv * g.units;
     const int kt = bf16 ? at::key_tile<64, 1>() : (a.D <= 64 ? at::key_tile<64, 3>() : at::key_tile<128, 3>());
     const long long tiles = (a.Tk + kt - 1) / kt;
     long long splits = device_sm_count() / blocks;
     if (splits > tiles / 4) splits = tiles / 4;
-    if (splits < 1) splits = 1;
+    if (splits < 1 || tiles < 12) splits = 1;
     g.splits = (int)splits;
 
     // fp32 tensors are split into planes; bf16 ones are used as they lie where

@@ -85,6 +85,9 @@ SHAPES = [
     (1, 257, 385, 5, 1, 104),
     (1, 300, 1300, 4, 4, 128),
     (1, 1000, 300, 2, 2, 56),
+    (1, 500, 900, 3, 3, 64),
+    (2, 260, 4100, 4, 1, 24),
+    (1, 40, 20000, 2, 2, 72),
 ]
 
 
@@ -144,6 +147,59 @@ def test_masks(sc, dtype, Tq, G, D):
     v[bad & (torch.arange(Tk, device="cuda") % 2 == 0)] = float("nan")
     out, lse = run_and_check(torch, sc, q, k, v, dtype, k_len=lens, key_mask=mask)
     assert (out[0] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("G,D", [(1, 64), (3, 40), (1, 128)])
+@pytest.mark.parametrize("kind", ["all", "lengths", "mask"])
+def test_more_row_tiles_than_sms(sc, dtype, G, D, kind):
+    """Three row tiles of each of 66 (sequence, key head) pairs, the last of them partly full: tiles in pairs."""
+    import torch
+    N, Tk, Hkv = 11, 700, 6
+    Tq = 300 // G
+    lens = mask = None
+    rng = np.random.default_rng(35)
+    if kind == "lengths":
+        lens = [0, 1, 127, 128, 129, 300, 384, 511, 640, 699, 700]
+    elif kind == "mask":
+        mask = (rng.random((N, Tk)) < 0.5).astype(np.uint8)
+        mask[0] = 0
+        mask[1, :400] = 0
+        mask[2, 128:640] = 0
+        mask[3] = 0
+        mask[3, 699] = 1
+    q = make(torch, dtype, N, Tq, Hkv * G, D, seed=36, gain=2.0)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=37), make(torch, dtype, N, Tk, Hkv, D, seed=38)
+    if kind != "all":
+        bad = torch.as_tensor(~valid_of(N, Tk, lens, mask)).cuda()
+        k[bad] = float("nan")
+        v[bad] = float("inf")
+    run_and_check(torch, sc, q, k, v, dtype, k_len=lens, key_mask=mask)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Tq", [20, 300])
+def test_long_masked_share(sc, Tq):
+    """A mask over more states than a CTA looks through beforehand (no tile is skipped)."""
+    import torch
+    N, Tk, H, D = 20, 70001, 8, 64
+    g = torch.Generator(device="cuda").manual_seed(39)
+    q = torch.randn(N, Tq, H, D, device="cuda", generator=g).bfloat16()
+    k, v = (torch.randn(N, Tk, H, D, device="cuda", generator=g).bfloat16() for _ in range(2))
+    mask = (torch.rand(N, Tk, device="cuda", generator=g) < 0.5).to(torch.uint8)
+    mask[-1, :-3000] = 0
+    bad = mask == 0
+    k[bad] = float("nan")
+    v[bad] = float("nan")
+    out = torch.empty_like(q)
+    sc.check(sc.cross_attention_fwd(q, k, v, out, N, Tq, Tk, H, H, D, 0.125, BF16, key_mask=mask))
+    sc.check(sc.sc_last_device_status())
+    for n, h in ((0, 0), (N - 1, H - 1)):
+        keep = mask[n].bool()
+        o, z, wabs, mag = ref.attention(f64(q[n:n + 1, :, h:h + 1]), f64(k[n:n + 1, keep, h:h + 1]),
+                                        f64(v[n:n + 1, keep, h:h + 1]), 0.125)
+        assert (np.abs(f64(out[n:n + 1, :, h:h + 1]) - o) <= ref.out_bound(o, wabs, mag, D, Tk, True)).all()
 
 
 @pytest.mark.gpu
