@@ -34,6 +34,7 @@ struct SplitArgs {
 template <bool BF16>
 __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitArgs a)
 {
+    pdl_trigger();   // the attention kernel may be set up; its copies wait for this grid's end
     const SplitPart &p = a.p[blockIdx.y];
     const long long stride = (long long)gridDim.x * kSplitThreads;
     for (long long e = (long long)blockIdx.x * kSplitThreads + threadIdx.x; e < p.chunks; e += stride) {

@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) sh.abort = 0;
         fence_mbar_init();
         __syncwarp();
+        if (g.packed) pdl_wait();   // the copies read what the launch before has written
         if (lane == 0 && nt > 0) {
             // row tiles: tokens and heads past the end read as zero
             mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(QT * PL * DB * g.gb * g.tb * 128));
@@ -936,9 +937,17 @@ cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPa
     const long long x = (long long)g.units * g.splits, nh = (long long)a.N * a.Hkv;
     if (x > 0x7fffffffLL || nh > (long long)GRID_Y * 65535) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)x, (unsigned)(nh < GRID_Y ? nh : GRID_Y), (unsigned)((nh + GRID_Y - 1) / GRID_Y));
-    attn_tc_kernel<DP, PL, PAIR><<<grid, THREADS, SMEM, st>>>(m.q, m.k, m.v, m.out, a, g, part, status,
-                                                                       1000000000ull);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = g.packed ? 1 : 0;   // behind attn_split's launch
+    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, PL, PAIR>, m.q, m.k, m.v, m.out, a, g, part, status, 1000000000ull);
 }
 
 }  // namespace at
