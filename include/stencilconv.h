@@ -487,6 +487,19 @@ int sc_test_stencil_wait_expiry(const float *in, float *out, int H, int W, int d
                                 int timeout_us, sc_stream_t stream);
 
 /*
+ * sc_test_attn_wait_expiry: test hook for the device-status path, not part
+ * of the operation.  Runs cross_attention_fwd's tensor-core kernel (bf16,
+ * packed, scale 1) with copy `drop_copy` (0-based, in each CTA's issue order)
+ * never issued, so the time-bounded waits for it expire after `timeout_us`
+ * microseconds.  The kernel then records SC_ERR_DEVICE_TIMEOUT (read and
+ * cleared by sc_last_device_status), waits for its other copies and products
+ * and returns; the context stays usable.  `out` is left with no defined
+ * values.
+ */
+int sc_test_attn_wait_expiry(const void *q, const void *k, const void *v, void *out, int N, int Tq, int Tk, int Hq,
+                             int Hkv, int D, int drop_copy, int timeout_us, sc_stream_t stream);
+
+/*
  * sc_test_workspace_allocs: test hook, not part of the operation.  The
  * number of temporary device buffers the library has taken from its memory
  * pool since it was loaded (conv2d_fwd with SC_NCHW takes one per call);

@@ -72,6 +72,7 @@ SIGNATURES = {
     "sc_test_workspace_allocs": (ctypes.c_longlong, []),
     "conv2d_chain_fwd_host": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "cross_attention_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P]),
+    "sc_test_attn_wait_expiry": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "rotary_table_fwd": (_I, [_P, _I, _I, _D, _I, _D, _D, _P]),
     "rotary_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "qk_norm_rotary_fwd": (_I, [_P, _P, _P, _I, _I, _I, _F, _I, _I, _I, _P]),
@@ -338,6 +339,12 @@ def sc_test_workspace_allocs() -> int:
 
 def sc_test_conv_wait_expiry(x, w, b, y, N, H, W, Cin, Cout, drop_copy, timeout_us, stream=None) -> int:
     return load().sc_test_conv_wait_expiry(_ptr(x), _ptr(w), _ptr(b), _ptr(y), N, H, W, Cin, Cout, drop_copy,
+                                           timeout_us, _stream(stream))
+
+
+def sc_test_attn_wait_expiry(q, k, v, out, N, Tq, Tk, Hq, Hkv, D, drop_copy, timeout_us, stream=None) -> int:
+    """Test hook: cross_attention_fwd's tensor-core kernel with one copy never issued (see the header)."""
+    return load().sc_test_attn_wait_expiry(_ptr(q), _ptr(k), _ptr(v), _ptr(out), N, Tq, Tk, Hq, Hkv, D, drop_copy,
                                            timeout_us, _stream(stream))
 
 

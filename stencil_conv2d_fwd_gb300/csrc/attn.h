@@ -44,7 +44,11 @@ cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, cudaStream_t st);
 // (attn_rows.cu).
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t st);
 // Many rows per key head: tensor cores (attn_tc.cu).
-cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st);
+// drop_copy >= 0 leaves that ring entry of every CTA un-issued so that its
+// bounded wait expires (tests of the device-status path); timeout_ns bounds
+// each wait.
+cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, int drop_copy = -1,
+                           unsigned long long timeout_ns = 1000000000ull);
 // Copies of q ([plane][N][Hkv][Tq][G][D]), k and v ([plane][N][Hkv][Tk][D]) for
 // it: fp32 tensors as three bf16 planes, bf16 ones as one (attn_split.cu).
 cudaError_t launch_attn_split(const AttnArgs &a, bool bf16, void *const (&planes)[3], cudaStream_t st);

@@ -179,6 +179,62 @@ int rotate_heads(const sc_norm_heads *t0, const sc_norm_heads *t1, const float *
     return from_cuda(sc::launch_rotary(a, dtype == SC_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// cross_attention_fwd's argument checks; SC_OK with `a` filled in when the
+// call may launch.
+int take_attention(const void *q, const void *k, const void *v, void *out, float *lse, const int *k_len,
+                   const unsigned char *key_mask, int N, int Tq, int Tk, int Hq, int Hkv, int D, float scale, int dtype,
+                   const sc_attn_strides *strides, sc::AttnArgs &a)
+{
+    if (!q || !k || !v || !out) return SC_ERR_NULL;
+    if (product(N, Tq, Hq, D) < 0 || product(N, Tk, Hkv, D) < 0) return SC_ERR_SHAPE;
+    if (Tq > (1 << 30) || Tk > (1 << 30)) return SC_ERR_SHAPE;
+    if (product(N, Tq, Hq) > (1 << 30)) return SC_ERR_SHAPE;   // one index of 32 bits for a row
+    if (dtype != SC_F32 && dtype != SC_BF16) return SC_ERR_UNSUPPORTED;
+    if (Hq % Hkv != 0 || D % 8 != 0 || D > sc::kAttnMaxD) return SC_ERR_UNSUPPORTED;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return SC_ERR_UNSUPPORTED;
+    const int es = dtype == SC_BF16 ? 2 : 4;
+    a = sc::AttnArgs{};
+    if (take_strides(strides ? &strides->q : nullptr, N, Tq, Hq, D, a.qs) != SC_OK ||
+        take_strides(strides ? &strides->k : nullptr, N, Tk, Hkv, D, a.ks) != SC_OK ||
+        take_strides(strides ? &strides->v : nullptr, N, Tk, Hkv, D, a.vs) != SC_OK ||
+        take_strides(strides ? &strides->out : nullptr, N, Tq, Hq, D, a.os) != SC_OK)
+        return SC_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+        !aligned(k_len, 4))
+        return SC_ERR_ALIGN;
+    if (!strides_aligned(a.qs, N, Tq, Hq, es) || !strides_aligned(a.ks, N, Tk, Hkv, es) ||
+        !strides_aligned(a.vs, N, Tk, Hkv, es) || !strides_aligned(a.os, N, Tq, Hq, es))
+        return SC_ERR_ALIGN;
+    const Region rq = region(q, N, Tq, Hq, D, a.qs, es), rk = region(k, N, Tk, Hkv, D, a.ks, es);
+    const Region rv = region(v, N, Tk, Hkv, D, a.vs, es), ro = region(out, N, Tq, Hq, D, a.os, es);
+    const long long lse_bytes = lse ? 4LL * N * Hq * Tq : 0;
+    if (!rows_distinct(ro) || may_overlap(ro, rq) || may_overlap(ro, rk) || may_overlap(ro, rv) ||
+        flat_overlap(ro, k_len, 4LL * N) || flat_overlap(ro, key_mask, (long long)N * Tk) ||
+        flat_overlap(ro, lse, lse_bytes) || flat_overlap(rq, lse, lse_bytes) || flat_overlap(rk, lse, lse_bytes) ||
+        flat_overlap(rv, lse, lse_bytes))
+        return SC_ERR_ALIAS;
+    if (lse) {
+        const Region rl{reinterpret_cast<uintptr_t>(lse), 1, 1, 1, lse_bytes, 0, lse_bytes, 0};
+        if (flat_overlap(rl, k_len, 4LL * N) || flat_overlap(rl, key_mask, (long long)N * Tk)) return SC_ERR_ALIAS;
+    }
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.out = out;
+    a.lse = lse;
+    a.k_len = k_len;
+    a.key_mask = key_mask;
+    a.N = N;
+    a.Tq = Tq;
+    a.Tk = Tk;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.G = Hq / Hkv;
+    a.scale = scale;
+    return SC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -230,53 +286,9 @@ int cross_attention_fwd(const void *q, const void *k, const void *v, void *out, 
                         const unsigned char *key_mask, int N, int Tq, int Tk, int Hq, int Hkv, int D, float scale,
                         int dtype, const sc_attn_strides *strides, sc_stream_t stream)
 {
-    if (!q || !k || !v || !out) return SC_ERR_NULL;
-    if (product(N, Tq, Hq, D) < 0 || product(N, Tk, Hkv, D) < 0) return SC_ERR_SHAPE;
-    if (Tq > (1 << 30) || Tk > (1 << 30)) return SC_ERR_SHAPE;
-    if (product(N, Tq, Hq) > (1 << 30)) return SC_ERR_SHAPE;   // one index of 32 bits for a row
-    if (dtype != SC_F32 && dtype != SC_BF16) return SC_ERR_UNSUPPORTED;
-    if (Hq % Hkv != 0 || D % 8 != 0 || D > sc::kAttnMaxD) return SC_ERR_UNSUPPORTED;
-    if (!(scale > 0.f) || !std::isfinite(scale)) return SC_ERR_UNSUPPORTED;
-    const int es = dtype == SC_BF16 ? 2 : 4;
-    sc::AttnArgs a = {};
-    if (take_strides(strides ? &strides->q : nullptr, N, Tq, Hq, D, a.qs) != SC_OK ||
-        take_strides(strides ? &strides->k : nullptr, N, Tk, Hkv, D, a.ks) != SC_OK ||
-        take_strides(strides ? &strides->v : nullptr, N, Tk, Hkv, D, a.vs) != SC_OK ||
-        take_strides(strides ? &strides->out : nullptr, N, Tq, Hq, D, a.os) != SC_OK)
-        return SC_ERR_SHAPE;
-    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
-        !aligned(k_len, 4))
-        return SC_ERR_ALIGN;
-    if (!strides_aligned(a.qs, N, Tq, Hq, es) || !strides_aligned(a.ks, N, Tk, Hkv, es) ||
-        !strides_aligned(a.vs, N, Tk, Hkv, es) || !strides_aligned(a.os, N, Tq, Hq, es))
-        return SC_ERR_ALIGN;
-    const Region rq = region(q, N, Tq, Hq, D, a.qs, es), rk = region(k, N, Tk, Hkv, D, a.ks, es);
-    const Region rv = region(v, N, Tk, Hkv, D, a.vs, es), ro = region(out, N, Tq, Hq, D, a.os, es);
-    const long long lse_bytes = lse ? 4LL * N * Hq * Tq : 0;
-    if (!rows_distinct(ro) || may_overlap(ro, rq) || may_overlap(ro, rk) || may_overlap(ro, rv) ||
-        flat_overlap(ro, k_len, 4LL * N) || flat_overlap(ro, key_mask, (long long)N * Tk) ||
-        flat_overlap(ro, lse, lse_bytes) || flat_overlap(rq, lse, lse_bytes) || flat_overlap(rk, lse, lse_bytes) ||
-        flat_overlap(rv, lse, lse_bytes))
-        return SC_ERR_ALIAS;
-    if (lse) {
-        const Region rl{reinterpret_cast<uintptr_t>(lse), 1, 1, 1, lse_bytes, 0, lse_bytes, 0};
-        if (flat_overlap(rl, k_len, 4LL * N) || flat_overlap(rl, key_mask, (long long)N * Tk)) return SC_ERR_ALIAS;
-    }
-    a.q = q;
-    a.k = k;
-    a.v = v;
-    a.out = out;
-    a.lse = lse;
-    a.k_len = k_len;
-    a.key_mask = key_mask;
-    a.N = N;
-    a.Tq = Tq;
-    a.Tk = Tk;
-    a.Hq = Hq;
-    a.Hkv = Hkv;
-    a.D = D;
-    a.G = Hq / Hkv;
-    a.scale = scale;
+    sc::AttnArgs a;
+    const int rc = take_attention(q, k, v, out, lse, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, scale, dtype, strides, a);
+    if (rc != SC_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SC_BF16;
     const long long rows = (long long)Tq * a.G;
@@ -288,6 +300,17 @@ int cross_attention_fwd(const void *q, const void *k, const void *v, void *out, 
     const double products = (double)N * Hq * Tq * (double)Tk * D;
     if (rows > 16 && (bf16 || products > 48e6)) return from_cuda(sc::launch_attn_tc(a, bf16, st));
     return from_cuda(!bf16 && rows <= 3 ? sc::launch_attn_rows(a, st) : sc::launch_attn_mma(a, bf16, st));
+}
+
+int sc_test_attn_wait_expiry(const void *q, const void *k, const void *v, void *out, int N, int Tq, int Tk, int Hq,
+                             int Hkv, int D, int drop_copy, int timeout_us, sc_stream_t stream)
+{
+    sc::AttnArgs a;
+    const int rc = take_attention(q, k, v, out, nullptr, nullptr, nullptr, N, Tq, Tk, Hq, Hkv, D, 1.f, SC_BF16, nullptr, a);
+    if (rc != SC_OK) return rc;
+    if (drop_copy < 0 || timeout_us < 1) return SC_ERR_SHAPE;
+    return from_cuda(sc::launch_attn_tc(a, true, reinterpret_cast<cudaStream_t>(stream), drop_copy,
+                                        1000ull * (unsigned long long)timeout_us));
 }
 
 }  // extern "C"

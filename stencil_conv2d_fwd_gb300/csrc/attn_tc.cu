@@ -261,7 +261,7 @@ template <int DP, int PL, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const AttnArgs a,
-                   const Geom g, const AttnPartials part, int *status, unsigned long long timeout_ns)
+                   const Geom g, const AttnPartials part, int *status, unsigned long long timeout_ns, int drop_copy)
 {
     constexpr int DB = DP / 64;                 // 64-column blocks of a head
     constexpr int QT = PAIR ? 2 : 1;            // row tiles
@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t bar = smem_u32(&sh.full[slot]);
             if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
             if (*abort_flag) return;
+            if ((int)issued == drop_copy) continue;
             mbar_arrive_expect_tx(bar, SLOT);
             for (int d = 0; d < DB; ++d)
                 tma_load_5d(ring + slot * SLOT + d * KBLK, value ? &mv : &mk, d * 64, key0, h * ax[0], n * ax[1], p, bar);
@@ -866,9 +867,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (uint32_t e = issued > (uint32_t)SLOTS ? issued - SLOTS : 0; e < issued; ++e)
                 (void)mbar_wait_bounded(smem_u32(&sh.full[e % SLOTS]), (e / SLOTS) & 1, timeout_ns);
         }
-        if (warp == 9 && lane == 0) {
-            tc::mma_commit(smem_u32(&sh.drain));
+        if (warp == 9) {
+            mma_commit(elect_one(), smem_u32(&sh.drain));   // by the thread that issued the products
             (void)mbar_wait_bounded(smem_u32(&sh.drain), 0, timeout_ns);
+            __syncwarp();
         }
         __syncthreads();
     }
@@ -915,7 +917,8 @@ struct Maps {
 };
 
 template <int DP, int PL, bool PAIR>
-cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPartials &part, cudaStream_t st)
+cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPartials &part, cudaStream_t st, int drop_copy,
+                   unsigned long long timeout_ns)
 {
     constexpr int SMEM = q_region<DP, PL, PAIR>() + ring_slots<DP, PL, PAIR>() * (DP / 64 * key_tile<DP, PL>() * 128) +
                          (int)sizeof(Shared<PAIR>);
@@ -947,12 +950,13 @@ cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPa
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = g.packed ? 1 : 0;   // behind attn_split's launch
-    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, PL, PAIR>, m.q, m.k, m.v, m.out, a, g, part, status, 1000000000ull);
+    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, PL, PAIR>, m.q, m.k, m.v, m.out, a, g, part, status, timeout_ns,
+                              drop_copy);
 }
 
 }  // namespace at
 
-cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
+cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, int drop_copy, unsigned long long timeout_ns)
 {
     if (!at::encoder()) return cudaErrorNotSupported;
     at::Geom g = {};
@@ -1044,13 +1048,13 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st)
     if (e == cudaSuccess && g.packed) e = launch_attn_split(a, bf16, plane, st);
     if (e == cudaSuccess) {
         if (bf16 && a.D <= 64)
-            e = pair ? at::launch<64, 1, true>(a, g, m, part, st) : at::launch<64, 1, false>(a, g, m, part, st);
+            e = pair ? at::launch<64, 1, true>(a, g, m, part, st, drop_copy, timeout_ns) : at::launch<64, 1, false>(a, g, m, part, st, drop_copy, timeout_ns);
         else if (bf16)
-            e = pair ? at::launch<128, 1, true>(a, g, m, part, st) : at::launch<128, 1, false>(a, g, m, part, st);
+            e = pair ? at::launch<128, 1, true>(a, g, m, part, st, drop_copy, timeout_ns) : at::launch<128, 1, false>(a, g, m, part, st, drop_copy, timeout_ns);
         else if (a.D <= 64)
-            e = pair ? at::launch<64, 3, true>(a, g, m, part, st) : at::launch<64, 3, false>(a, g, m, part, st);
+            e = pair ? at::launch<64, 3, true>(a, g, m, part, st, drop_copy, timeout_ns) : at::launch<64, 3, false>(a, g, m, part, st, drop_copy, timeout_ns);
         else
-            e = at::launch<128, 3, false>(a, g, m, part, st);
+            e = at::launch<128, 3, false>(a, g, m, part, st, drop_copy, timeout_ns);
     }
     if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st);
     if (ws) {

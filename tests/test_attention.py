@@ -328,6 +328,23 @@ def test_nan_in_a_valid_state_is_not_hidden(sc, Tq):
     assert torch.isnan(out).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 140, 1000, 2, 2, 64), (11, 300, 700, 6, 6, 64), (1, 40, 20000, 2, 2, 128)])
+@pytest.mark.parametrize("drop_copy", [0, 1, 3])
+def test_expired_wait_is_reported(sc, shape, drop_copy):
+    """A copy that never comes: its waits run out, the status says so, and the next call is right."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, BF16, N, Tq, Hq, D, seed=40)
+    k, v = make(torch, BF16, N, Tk, Hkv, D, seed=41), make(torch, BF16, N, Tk, Hkv, D, seed=42)
+    out = torch.empty_like(q)
+    sc.check(sc.sc_last_device_status())
+    sc.check(sc.sc_test_attn_wait_expiry(q, k, v, out, N, Tq, Tk, Hq, Hkv, D, drop_copy, 300))
+    assert sc.sc_last_device_status() == scl.SC_ERR_DEVICE_TIMEOUT
+    assert sc.sc_last_device_status() == scl.SC_OK
+    run_and_check(torch, sc, q, k, v, BF16)
+
+
 A, B, C, O = 1 << 30, 1 << 32, 1 << 34, 1 << 36   # fake, aligned, far apart: never dereferenced
 
 
@@ -377,3 +394,10 @@ def test_refusals(change, expect):
                                  a["scale"], a["dtype"], k_len=a["k_len"], key_mask=a["key_mask"], lse=a["lse"],
                                  strides=a["strides"], stream=0)
     assert rc == expect, scl.sc_status_string(rc)
+
+
+def test_wait_expiry_hook_refusals():
+    assert scl.sc_test_attn_wait_expiry(None, B, C, O, 1, 8, 20, 4, 2, 64, 0, 10, stream=0) == scl.SC_ERR_NULL
+    assert scl.sc_test_attn_wait_expiry(A, B, C, O, 1, 8, 20, 4, 2, 64, -1, 10, stream=0) == scl.SC_ERR_SHAPE
+    assert scl.sc_test_attn_wait_expiry(A, B, C, O, 1, 8, 20, 4, 2, 64, 0, 0, stream=0) == scl.SC_ERR_SHAPE
+    assert scl.sc_test_attn_wait_expiry(A, B, C, O, 1, 8, 20, 4, 3, 64, 0, 10, stream=0) == scl.SC_ERR_UNSUPPORTED
