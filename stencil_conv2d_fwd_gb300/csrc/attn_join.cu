@@ -14,6 +14,7 @@ namespace sc {
 namespace {
 
 constexpr int kJoinThreads = 256;
+constexpr int kAhead = 8;
 
 // m, l, o <- joined with (m2, l2, o2)
 __device__ __forceinline__ void join4(float &m, float &l, float4 &o, float m2, float l2, const float4 &o2)
@@ -48,11 +49,33 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (act) {
-#pragma unroll 4
-        for (int i = grp; i < p.parts; i += g.groups) {
-            const long long at = i * nrow + at0;
-            const float2 ml = p.ml[at];
-            join4(m, l, o, ml.x, ml.y, *reinterpret_cast<const float4 *>(p.o + at * a.D + 4 * c));
+        // kAhead parts' loads at a time
+        for (int i0 = grp; i0 < p.parts; i0 += kAhead * g.groups) {
+            float2 ml[kAhead];
+            float4 q[kAhead];
+            float mm = m;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * g.groups;
+                const long long at = i * nrow + at0;
+                ml[k] = i < p.parts ? p.ml[at] : make_float2(-INFINITY, 0.f);
+                q[k] = i < p.parts ? *reinterpret_cast<const float4 *>(p.o + at * a.D + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) mm = fmaxf(mm, ml[k].x);
+            const float ms = mm == -INFINITY ? 0.f : mm, f0 = ex2(m - ms);
+            l *= f0;
+            o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+            m = mm;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const float f = ex2(ml[k].x - ms);
+                l = fmaf(ml[k].y, f, l);
+                o.x = fmaf(q[k].x, f, o.x);
+                o.y = fmaf(q[k].y, f, o.y);
+                o.z = fmaf(q[k].z, f, o.z);
+                o.w = fmaf(q[k].w, f, o.w);
+            }
         }
     }
     if (g.groups > 1) {
