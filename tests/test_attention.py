@@ -88,6 +88,10 @@ SHAPES = [
     (1, 500, 900, 3, 3, 64),
     (2, 260, 4100, 4, 1, 24),
     (1, 40, 20000, 2, 2, 72),
+    (1, 1, 300, 150, 1, 32),
+    (2, 3, 500, 200, 1, 64),
+    (1, 10, 2000, 150, 1, 64),
+    (1, 5, 1500, 260, 2, 128),
 ]
 
 
@@ -315,6 +319,33 @@ def test_same_bits_every_time(sc, shape, dtype):
         assert torch.isfinite(outs[0]).all()
         for i, o in enumerate(outs):
             assert torch.equal(o, outs[0]), f"call {i} differs"
+
+
+@pytest.mark.gpu
+def test_calls_on_several_streams_at_once(sc):
+    """Every kernel on streams of its own, side by side: workspaces, tensor memory and launch caches are not shared."""
+    import torch
+    cases = []
+    for i, (dtype, N, Tq, Tk, Hq, Hkv, D) in enumerate([
+            (BF16, 2, 300, 5000, 8, 4, 64), (F32, 2, 200, 3000, 4, 2, 64), (BF16, 4, 1, 9000, 8, 2, 128), (F32, 3, 2, 8000, 2, 2, 64),
+            (BF16, 1, 40, 40000, 2, 2, 64), (F32, 2, 9, 4000, 4, 4, 128), (BF16, 3, 200, 900, 8, 8, 128), (F32, 1, 150, 6000, 2, 2, 96)]):
+        q = make(torch, dtype, N, Tq, Hq, D, seed=50 + i, gain=2.0)
+        k, v = make(torch, dtype, N, Tk, Hkv, D, seed=60 + i), make(torch, dtype, N, Tk, Hkv, D, seed=70 + i)
+        want = torch.empty_like(q)
+        call = (N, Tq, Tk, Hq, Hkv, D, D ** -0.5, dtype)
+        sc.check(sc.cross_attention_fwd(q, k, v, want, *call))
+        cases.append((q, k, v, want, call, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(6):
+        for q, k, v, want, call, s in cases:
+            out = torch.empty_like(q)
+            sc.check(sc.cross_attention_fwd(q, k, v, out, *call, stream=s))
+            outs.append((out, want))
+    torch.cuda.synchronize()
+    sc.check(sc.sc_last_device_status())
+    for out, want in outs:
+        assert torch.equal(out, want)
 
 
 @pytest.mark.gpu
