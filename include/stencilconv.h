@@ -410,9 +410,9 @@ int sc_version(void);
 
 /*
  * sc_release_workspace: hand the memory of the library's temporary buffers
- * back to the driver.  Those buffers (the NCHW repack of conv2d_fwd) come
- * from a library-private
- * stream-ordered memory pool per device that otherwise keeps freed memory
+ * back to the driver.  Those buffers (the NCHW repack of conv2d_fwd,
+ * the partial results and split operands of cross_attention_fwd) come from a
+ * library-private stream-ordered memory pool per device that otherwise keeps freed memory
  * for the next call.  Memory still in use by queued work is not affected.
  * Returns SC_OK.
  */
