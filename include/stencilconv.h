@@ -500,6 +500,18 @@ int sc_test_attn_wait_expiry(const void *q, const void *k, const void *v, void *
                              int Hkv, int D, int drop_copy, int timeout_us, sc_stream_t stream);
 
 /*
+ * sc_test_attn_slow_clear: test hook, not part of the operation.  Runs
+ * cross_attention_fwd's tensor-core kernel (packed, scale 1, whatever the
+ * number of rows) with the warps that clear the value rows of states that are
+ * not valid held up `delay_us` (0 to 1000) microseconds before each entry of
+ * the ring.  The result is cross_attention_fwd's.  One of k_len and key_mask
+ * is needed.
+ */
+int sc_test_attn_slow_clear(const void *q, const void *k, const void *v, void *out, const int *k_len,
+                            const unsigned char *key_mask, int N, int Tq, int Tk, int Hq, int Hkv, int D, int dtype,
+                            int delay_us, sc_stream_t stream);
+
+/*
  * sc_test_workspace_allocs: test hook, not part of the operation.  The
  * number of temporary device buffers the library has taken from its memory
  * pool since it was loaded (conv2d_fwd with SC_NCHW takes one per call);

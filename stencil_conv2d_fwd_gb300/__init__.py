@@ -73,6 +73,7 @@ SIGNATURES = {
     "conv2d_chain_fwd_host": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "cross_attention_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P]),
     "sc_test_attn_wait_expiry": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "sc_test_attn_slow_clear": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "rotary_table_fwd": (_I, [_P, _I, _I, _D, _I, _D, _D, _P]),
     "rotary_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "qk_norm_rotary_fwd": (_I, [_P, _P, _P, _I, _I, _I, _F, _I, _I, _I, _P]),
@@ -346,6 +347,12 @@ def sc_test_attn_wait_expiry(q, k, v, out, N, Tq, Tk, Hq, Hkv, D, drop_copy, tim
     """Test hook: cross_attention_fwd's tensor-core kernel with one copy never issued (see the header)."""
     return load().sc_test_attn_wait_expiry(_ptr(q), _ptr(k), _ptr(v), _ptr(out), N, Tq, Tk, Hq, Hkv, D, drop_copy,
                                            timeout_us, _stream(stream))
+
+
+def sc_test_attn_slow_clear(q, k, v, out, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, dtype, delay_us, stream=None) -> int:
+    """Test hook: cross_attention_fwd's tensor-core kernel with its clearing warps held up (see the header)."""
+    return load().sc_test_attn_slow_clear(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(k_len), _ptr(key_mask), N, Tq, Tk,
+                                          Hq, Hkv, D, dtype, delay_us, _stream(stream))
 
 
 def sc_test_stencil_wait_expiry(inp, out, H, W, drop_copy, timeout_us, stream=None) -> int:

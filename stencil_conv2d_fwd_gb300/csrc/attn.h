@@ -46,9 +46,14 @@ cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t st);
 // Many rows per key head: tensor cores (attn_tc.cu).
 // drop_copy >= 0 leaves that ring entry of every CTA un-issued so that its
 // bounded wait expires (tests of the device-status path); timeout_ns bounds
-// each wait.
-cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, int drop_copy = -1,
-                           unsigned long long timeout_ns = 1000000000ull);
+// each wait; clear_delay_ns holds the warps that clear value rows up before
+// each entry (tests of the ring's order).
+struct TcTest {
+    int drop_copy = -1;
+    unsigned clear_delay_ns = 0;
+    unsigned long long timeout_ns = 1000000000ull;
+};
+cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, const TcTest &test = TcTest());
 // Copies of q ([plane][N][Hkv][Tq][G][D]), k and v ([plane][N][Hkv][Tk][D]) for
 // it: fp32 tensors as three bf16 planes, bf16 ones as one (attn_split.cu).
 cudaError_t launch_attn_split(const AttnArgs &a, bool bf16, void *const (&planes)[3], cudaStream_t st);

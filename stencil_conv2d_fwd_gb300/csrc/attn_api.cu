@@ -309,8 +309,24 @@ int sc_test_attn_wait_expiry(const void *q, const void *k, const void *v, void *
     const int rc = take_attention(q, k, v, out, nullptr, nullptr, nullptr, N, Tq, Tk, Hq, Hkv, D, 1.f, SC_BF16, nullptr, a);
     if (rc != SC_OK) return rc;
     if (drop_copy < 0 || timeout_us < 1) return SC_ERR_SHAPE;
-    return from_cuda(sc::launch_attn_tc(a, true, reinterpret_cast<cudaStream_t>(stream), drop_copy,
-                                        1000ull * (unsigned long long)timeout_us));
+    sc::TcTest test;
+    test.drop_copy = drop_copy;
+    test.timeout_ns = 1000ull * (unsigned long long)timeout_us;
+    return from_cuda(sc::launch_attn_tc(a, true, reinterpret_cast<cudaStream_t>(stream), test));
+}
+
+int sc_test_attn_slow_clear(const void *q, const void *k, const void *v, void *out, const int *k_len,
+                            const unsigned char *key_mask, int N, int Tq, int Tk, int Hq, int Hkv, int D, int dtype,
+                            int delay_us, sc_stream_t stream)
+{
+    sc::AttnArgs a;
+    const int rc = take_attention(q, k, v, out, nullptr, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, 1.f, dtype, nullptr, a);
+    if (rc != SC_OK) return rc;
+    if (!k_len && !key_mask) return SC_ERR_NULL;
+    if (delay_us < 0 || delay_us > 1000) return SC_ERR_SHAPE;
+    sc::TcTest test;
+    test.clear_delay_ns = 1000u * (unsigned)delay_us;
+    return from_cuda(sc::launch_attn_tc(a, dtype == SC_BF16, reinterpret_cast<cudaStream_t>(stream), test));
 }
 
 }  // extern "C"

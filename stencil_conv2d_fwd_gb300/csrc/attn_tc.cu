@@ -221,7 +221,9 @@ constexpr uint32_t desc_lo_v(int key_tile) { return (uint32_t)(key_tile * 128 >>
 
 template <bool PAIR>
 struct Shared {
-    // barriers of one arrival, of the two clearing warps, and of a stream's four
+    // barriers of one arrival (`empty`: of the MMA warp and, where value rows
+    // are cleared, the two clearing warps), of the two clearing warps, and of a
+    // stream's four
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], q_full, s_full[2], o_full[2], drain;
     uint64_t vclean[VC];
     uint64_t p_full[2][2];
@@ -261,7 +263,7 @@ template <int DP, int PL, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const AttnArgs a,
-                   const Geom g, const AttnPartials part, int *status, unsigned long long timeout_ns, int drop_copy)
+                   const Geom g, const AttnPartials part, int *status, const TcTest test)
 {
     constexpr int DB = DP / 64;                 // 64-column blocks of a head
     constexpr int QT = PAIR ? 2 : 1;            // row tiles
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const unsigned long long t0 = global_ns();
         while (!mbar_try_wait(b, parity)) {
             if (*abort_flag) return;
-            if (global_ns() - t0 > timeout_ns) {
+            if (global_ns() - t0 > test.timeout_ns) {
                 *abort_flag = 1;
                 return;
             }
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t bar = smem_u32(&sh.full[slot]);
             if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
             if (*abort_flag) return;
-            if ((int)issued == drop_copy) continue;
+            if ((int)issued == test.drop_copy) continue;
             mbar_arrive_expect_tx(bar, SLOT);
             for (int d = 0; d < DB; ++d)
                 tma_load_5d(ring + slot * SLOT + d * KBLK, value ? &mv : &mk, d * 64, key0, h * ax[0], n * ax[1], p, bar);
@@ -338,7 +340,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
 
     if (warp == 8) {
-        for (int i = lane; i < BARS; i += 32) mbar_init(smem_u32(&sh.full[0]) + 8 * i, i < BARS_ONE ? 1 : (i < BARS_TWO ? 2 : 4));
+        const int release = mb || len < a.Tk ? 3 : 1;   // arrivals of `empty`: 3 where value rows are cleared (`ragged` below)
+        for (int i = lane; i < BARS; i += 32)
+            mbar_init(smem_u32(&sh.full[0]) + 8 * i,
+                      i < BARS_ONE ? (i >= MAX_SLOTS && i < 2 * MAX_SLOTS ? release : 1) : (i < BARS_TWO ? 2 : 4));
         if (lane == 0) sh.abort = 0;
         fence_mbar_init();
         __syncwarp();
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncthreads();
         nt = sh.count;
     }
-    const bool ragged = mb || len < a.Tk;   // value rows to clear
+    const bool ragged = mb || len < a.Tk;
     constexpr int P1 = KT, P2 = DP == 64 ? KT / 2 : KT + KT / 2, TO = 256 - DP;   // columns of a stream
     auto p_plane = [](int p) { return p == 0 ? 0 : (p == 1 ? P1 : P2); };
 
@@ -494,11 +499,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
         } else if (ragged) {
             // value rows that are not valid: zero, in every plane and block.
-            // Every entry of the ring is waited for in turn, the key tiles' too: a
-            // barrier's parity tells a round only from its neighbours.
+            // A barrier's parity tells a round only from its neighbours, so these
+            // warps wait for every entry of the ring in turn, the key tiles' too,
+            // and each entry's release waits for them: a slot's next copy is not
+            // asked for before both have seen this one, however late they are.
             uint32_t c = 0;
-            auto pass = [&]() {
-                for (int p = 0; p < PL; ++p, ++c) wait(sh.full[c % SLOTS], (c / SLOTS) & 1);
+            auto seen = [&]() {   // the next entry's copy
+                if (test.clear_delay_ns > 0)
+                    for (const unsigned long long t0 = global_ns(); global_ns() - t0 < test.clear_delay_ns;) {}
+                wait(sh.full[c % SLOTS], (c / SLOTS) & 1);
+            };
+            auto release = [&](uint32_t entry) { mbar_arrive(smem_u32(&sh.empty[entry % SLOTS])); };
+            auto pass = [&]() {   // a key tile
+#pragma unroll 1   // (unrolled, these loops cost the softmax warps of the three-plane pairs 300 bytes of spills)
+                for (int p = 0; p < PL; ++p, ++c) {
+                    seen();
+                    __syncwarp();
+                    if (lane == 0) release(c);
+                }
             };
             for (int j = 0; j < LAG && j < nt; ++j) pass();
             constexpr int KL = KT / 64;   // keys of a lane: two warps share the tile
@@ -512,9 +530,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     // states past Tk are not in the tensor and read as zero
                     bad[i] = key < a.Tk && (key >= len || (mb && mb[key] == 0));
                 }
+#pragma unroll 1
                 for (int p = 0; p < PL; ++p, ++c) {
                     const uint32_t slot = c % SLOTS;
-                    wait(sh.full[slot], (c / SLOTS) & 1);
+                    seen();
 #pragma unroll
                     for (int i = 0; i < KL; ++i) {
                         if (!bad[i]) continue;
@@ -527,7 +546,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.vclean[j % VC]));
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh.vclean[j % VC]));
+#pragma unroll 1
+                    for (int p = 1; p <= PL; ++p) release(c - p);
+                }
                 if (j + LAG < nt) pass();
             }
         }
@@ -863,13 +886,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         // shared and tensor memory are given back
         if (tid == 0) atomicExch(status, kDeviceTimeout);
         if (warp == 8 && lane == 0) {
-            if (q_tiles > 0) (void)mbar_wait_bounded(smem_u32(&sh.q_full), 0, timeout_ns);
+            if (q_tiles > 0) (void)mbar_wait_bounded(smem_u32(&sh.q_full), 0, test.timeout_ns);
             for (uint32_t e = issued > (uint32_t)SLOTS ? issued - SLOTS : 0; e < issued; ++e)
-                (void)mbar_wait_bounded(smem_u32(&sh.full[e % SLOTS]), (e / SLOTS) & 1, timeout_ns);
+                (void)mbar_wait_bounded(smem_u32(&sh.full[e % SLOTS]), (e / SLOTS) & 1, test.timeout_ns);
         }
         if (warp == 9) {
             mma_commit(elect_one(), smem_u32(&sh.drain));   // by the thread that issued the products
-            (void)mbar_wait_bounded(smem_u32(&sh.drain), 0, timeout_ns);
+            (void)mbar_wait_bounded(smem_u32(&sh.drain), 0, test.timeout_ns);
             __syncwarp();
         }
         __syncthreads();
@@ -917,8 +940,8 @@ struct Maps {
 };
 
 template <int DP, int PL, bool PAIR>
-cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPartials &part, cudaStream_t st, int drop_copy,
-                   unsigned long long timeout_ns)
+cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPartials &part, cudaStream_t st,
+                   const TcTest &test)
 {
     constexpr int SMEM = q_region<DP, PL, PAIR>() + ring_slots<DP, PL, PAIR>() * (DP / 64 * key_tile<DP, PL>() * 128) +
                          (int)sizeof(Shared<PAIR>);
@@ -950,13 +973,12 @@ cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPa
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = g.packed ? 1 : 0;   // behind attn_split's launch
-    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, PL, PAIR>, m.q, m.k, m.v, m.out, a, g, part, status, timeout_ns,
-                              drop_copy);
+    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, PL, PAIR>, m.q, m.k, m.v, m.out, a, g, part, status, test);
 }
 
 }  // namespace at
 
-cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, int drop_copy, unsigned long long timeout_ns)
+cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, const TcTest &test)
 {
     if (!at::encoder()) return cudaErrorNotSupported;
     at::Geom g = {};
@@ -1048,13 +1070,13 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, int dr
     if (e == cudaSuccess && g.packed) e = launch_attn_split(a, bf16, plane, st);
     if (e == cudaSuccess) {
         if (bf16 && a.D <= 64)
-            e = pair ? at::launch<64, 1, true>(a, g, m, part, st, drop_copy, timeout_ns) : at::launch<64, 1, false>(a, g, m, part, st, drop_copy, timeout_ns);
+            e = pair ? at::launch<64, 1, true>(a, g, m, part, st, test) : at::launch<64, 1, false>(a, g, m, part, st, test);
         else if (bf16)
-            e = pair ? at::launch<128, 1, true>(a, g, m, part, st, drop_copy, timeout_ns) : at::launch<128, 1, false>(a, g, m, part, st, drop_copy, timeout_ns);
+            e = pair ? at::launch<128, 1, true>(a, g, m, part, st, test) : at::launch<128, 1, false>(a, g, m, part, st, test);
         else if (a.D <= 64)
-            e = pair ? at::launch<64, 3, true>(a, g, m, part, st, drop_copy, timeout_ns) : at::launch<64, 3, false>(a, g, m, part, st, drop_copy, timeout_ns);
+            e = pair ? at::launch<64, 3, true>(a, g, m, part, st, test) : at::launch<64, 3, false>(a, g, m, part, st, test);
         else
-            e = at::launch<128, 3, false>(a, g, m, part, st, drop_copy, timeout_ns);
+            e = at::launch<128, 3, false>(a, g, m, part, st, test);
     }
     if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st);
     if (ws) {

@@ -376,6 +376,38 @@ def test_expired_wait_is_reported(sc, shape, drop_copy):
     run_and_check(torch, sc, q, k, v, BF16)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,shape", [
+    (BF16, (2, 140, 2500, 2, 2, 128)), (BF16, (11, 300, 1300, 6, 6, 128)), (BF16, (2, 140, 3300, 2, 2, 64)),
+    (BF16, (11, 300, 2100, 6, 6, 40)), (F32, (2, 140, 1300, 4, 2, 128)), (F32, (2, 140, 1300, 2, 2, 64)),
+    (F32, (11, 300, 900, 6, 6, 64))])
+@pytest.mark.parametrize("kind", ["lengths", "mask"])
+def test_late_clearing_warps(sc, shape, dtype, kind):
+    """The warps that clear value rows far behind the products: no slot of the ring is refilled before they have
+    seen its copy, so the result is the same, and no wait runs out."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, dtype, N, Tq, Hq, D, seed=80, gain=0.3)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=81), make(torch, dtype, N, Tk, Hkv, D, seed=82)
+    lens = mask = None
+    if kind == "lengths":
+        lens = torch.tensor([Tk - 3 - 90 * (n % 3) for n in range(N)], dtype=torch.int32).cuda()
+    else:
+        mask = (torch.rand(N, Tk, generator=torch.Generator().manual_seed(83)) < 0.5).to(torch.uint8).cuda()
+    valid = torch.as_tensor(valid_of(N, Tk, None if lens is None else lens.cpu().numpy(),
+                                     None if mask is None else mask.cpu().numpy())).cuda()
+    k[~valid] = float("nan")
+    v[~valid] = float("inf")
+    outs = []
+    for delay in (0, 20):
+        outs.append(torch.full_like(q, float("nan")))
+        sc.check(sc.sc_test_attn_slow_clear(q, k, v, outs[-1], lens, mask, N, Tq, Tk, Hq, Hkv, D, dtype, delay))
+        sc.check(sc.sc_last_device_status(), "device status")
+    o, z, wabs, mag = ref.attention(f64(q), f64(k), f64(v), 1.0, valid.cpu().numpy())
+    assert (np.abs(f64(outs[0]) - o) <= ref.out_bound(o, wabs, mag, D, Tk, dtype == BF16)).all()
+    assert torch.equal(outs[0], outs[1])
+
+
 A, B, C, O = 1 << 30, 1 << 32, 1 << 34, 1 << 36   # fake, aligned, far apart: never dereferenced
 
 
@@ -432,3 +464,12 @@ def test_wait_expiry_hook_refusals():
     assert scl.sc_test_attn_wait_expiry(A, B, C, O, 1, 8, 20, 4, 2, 64, -1, 10, stream=0) == scl.SC_ERR_SHAPE
     assert scl.sc_test_attn_wait_expiry(A, B, C, O, 1, 8, 20, 4, 2, 64, 0, 0, stream=0) == scl.SC_ERR_SHAPE
     assert scl.sc_test_attn_wait_expiry(A, B, C, O, 1, 8, 20, 4, 3, 64, 0, 10, stream=0) == scl.SC_ERR_UNSUPPORTED
+
+
+def test_slow_clear_hook_refusals():
+    L = 1 << 38
+    assert scl.sc_test_attn_slow_clear(None, B, C, O, L, None, 1, 8, 20, 4, 2, 64, BF16, 10, stream=0) == scl.SC_ERR_NULL
+    assert scl.sc_test_attn_slow_clear(A, B, C, O, None, None, 1, 8, 20, 4, 2, 64, BF16, 10, stream=0) == scl.SC_ERR_NULL
+    assert scl.sc_test_attn_slow_clear(A, B, C, O, L, None, 1, 8, 20, 4, 2, 64, BF16, -1, stream=0) == scl.SC_ERR_SHAPE
+    assert scl.sc_test_attn_slow_clear(A, B, C, O, L, None, 1, 8, 20, 4, 2, 64, BF16, 1001, stream=0) == scl.SC_ERR_SHAPE
+    assert scl.sc_test_attn_slow_clear(A, B, C, O, L, None, 1, 8, 20, 4, 3, 64, BF16, 10, stream=0) == scl.SC_ERR_UNSUPPORTED
