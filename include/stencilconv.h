@@ -304,8 +304,9 @@ int rotary_table_fwd(float *table, int positions, int pairs, double base, int ru
  *   turned by p = pos[t], the second by p = pos[tokens + t], each with the
  *   table's pairs from the first.
  * x, y : [tokens][heads][D] of `dtype`, 16-byte aligned, packed unless
- *   strides are given (their batch stride is not used).  y may be x (with
- *   the same strides), else it overlaps no input.
+ *   strides are given (their batch stride is not used; 0 on an axis of x that
+ *   shares one row, 0 on both included).  y's rows are distinct; y may be x
+ *   (with the same strides), else it overlaps no input.
  * table : positions * pairs * 2 floats of rotary_table_fwd.  pos : axes *
  *   tokens ints in device memory; for a position outside [0, positions) the
  *   head's turned elements become NaN and sc_last_device_status returns
@@ -319,8 +320,9 @@ int rotary_fwd(const void *x, void *y, const float *table, const int *pos, int t
                const sc_head_strides *y_strides, sc_stream_t stream);
 
 /* One tensor of qk_norm_rotary_fwd: x and y as in rotary_fwd (token and head
- * strides in elements; both 0: packed), weight D floats (16-byte aligned) or
- * NULL for ones. */
+ * strides in elements; both 0: packed, so that tokens that share one row need
+ * a head stride above 0, also with one head), weight D floats (16-byte
+ * aligned) or NULL for ones. */
 typedef struct {
     const void *x;
     void *y;

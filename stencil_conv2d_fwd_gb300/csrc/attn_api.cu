@@ -115,16 +115,23 @@ int from_cuda(cudaError_t e)
     return sc::record_cuda_error(e);
 }
 
+// One tensor of a norm or rotation, and whether x and y are packed, whatever
+// their strides say (two strides of 0 may be a row that all tokens and heads share).
+struct Heads {
+    sc_norm_heads t;
+    bool packed_x, packed_y;
+};
+
 // The arguments of one tensor of a norm or rotation.
-int take_heads(const sc_norm_heads &t, int D, int rot, int axes, int esize, sc::NormHeads &out, Region &rx, Region &ry)
+int take_heads(const Heads &heads, int D, int rot, int axes, int esize, sc::NormHeads &out, Region &rx, Region &ry)
 {
+    const sc_norm_heads &t = heads.t;
     if (!t.x || !t.y || (rot > 0 && !t.pos)) return SC_ERR_NULL;
     if (product(t.tokens, t.heads, D) < 0) return SC_ERR_SHAPE;
     const sc_head_strides sx{0, t.x_token_stride, t.x_head_stride}, sy{0, t.y_token_stride, t.y_head_stride};
-    const bool px = sx.token == 0 && sx.head == 0, py = sy.token == 0 && sy.head == 0;
     sc::HeadStrides hx, hy;
-    if (take_strides(px ? nullptr : &sx, 1, t.tokens, t.heads, D, hx) != SC_OK) return SC_ERR_SHAPE;
-    if (take_strides(py ? nullptr : &sy, 1, t.tokens, t.heads, D, hy) != SC_OK) return SC_ERR_SHAPE;
+    if (take_strides(heads.packed_x ? nullptr : &sx, 1, t.tokens, t.heads, D, hx) != SC_OK) return SC_ERR_SHAPE;
+    if (take_strides(heads.packed_y ? nullptr : &sy, 1, t.tokens, t.heads, D, hy) != SC_OK) return SC_ERR_SHAPE;
     if (!aligned(t.x, 16) || !aligned(t.y, 16) || !aligned(t.weight, 16) || !aligned(t.pos, 4)) return SC_ERR_ALIGN;
     if (!strides_aligned(hx, 1, t.tokens, t.heads, esize) || !strides_aligned(hy, 1, t.tokens, t.heads, esize))
         return SC_ERR_ALIGN;
@@ -139,7 +146,7 @@ int take_heads(const sc_norm_heads &t, int D, int rot, int axes, int esize, sc::
 }
 
 // What rotary_fwd and qk_norm_rotary_fwd have in common.
-int rotate_heads(const sc_norm_heads *t0, const sc_norm_heads *t1, const float *table, int D, int rot_dim, int positions,
+int rotate_heads(const Heads *t0, const Heads *t1, const float *table, int D, int rot_dim, int positions,
                  bool norm, float eps, int mode, int axes, int inverse, int dtype, sc_stream_t stream)
 {
     if (!t0 && !t1) return SC_ERR_NULL;
@@ -161,7 +168,7 @@ int rotate_heads(const sc_norm_heads *t0, const sc_norm_heads *t1, const float *
     a.inverse = inverse != 0;
     a.norm = norm;
     a.eps = eps;
-    const sc_norm_heads *t[2] = {t0 ? t0 : t1, t0 ? t1 : nullptr};
+    const Heads *t[2] = {t0 ? t0 : t1, t0 ? t1 : nullptr};
     Region rx[2], ry[2];
     const long long table_bytes = rot_dim > 0 ? (long long)positions * (rot_dim / axes) * 4 : 0;
     for (int i = 0; i < 2 && t[i]; ++i) {
@@ -172,8 +179,8 @@ int rotate_heads(const sc_norm_heads *t0, const sc_norm_heads *t1, const float *
     if (t[1]) {
         if (may_overlap(ry[0], rx[1]) || may_overlap(ry[1], rx[0]) || may_overlap(ry[0], ry[1])) return SC_ERR_ALIAS;
         for (int i = 0; i < 2; ++i)
-            if (flat_overlap(ry[i], t[1 - i]->weight, 4LL * D) ||
-                flat_overlap(ry[i], t[1 - i]->pos, rot_dim > 0 ? 4LL * axes * t[1 - i]->tokens : 0))
+            if (flat_overlap(ry[i], t[1 - i]->t.weight, 4LL * D) ||
+                flat_overlap(ry[i], t[1 - i]->t.pos, rot_dim > 0 ? 4LL * axes * t[1 - i]->t.tokens : 0))
                 return SC_ERR_ALIAS;
     }
     return from_cuda(sc::launch_rotary(a, dtype == SC_BF16, reinterpret_cast<cudaStream_t>(stream)));
@@ -259,7 +266,10 @@ int rotary_fwd(const void *x, void *y, const float *table, const int *pos, int t
                int positions, int mode, int axes, int inverse, int dtype, const sc_head_strides *x_strides,
                const sc_head_strides *y_strides, sc_stream_t stream)
 {
-    sc_norm_heads t = {};
+    Heads xy = {};
+    xy.packed_x = !x_strides;
+    xy.packed_y = !y_strides;
+    sc_norm_heads &t = xy.t;
     t.x = x;
     t.y = y;
     t.pos = pos;
@@ -273,13 +283,20 @@ int rotary_fwd(const void *x, void *y, const float *table, const int *pos, int t
         t.y_token_stride = y_strides->token;
         t.y_head_stride = y_strides->head;
     }
-    return rotate_heads(&t, nullptr, table, D, rot_dim, positions, false, 0.f, mode, axes, inverse, dtype, stream);
+    return rotate_heads(&xy, nullptr, table, D, rot_dim, positions, false, 0.f, mode, axes, inverse, dtype, stream);
 }
 
 int qk_norm_rotary_fwd(const sc_norm_heads *q, const sc_norm_heads *k, const float *table, int D, int rot_dim,
                        int positions, float eps, int mode, int axes, int dtype, sc_stream_t stream)
 {
-    return rotate_heads(q, k, table, D, rot_dim, positions, true, eps, mode, axes, 0, dtype, stream);
+    const sc_norm_heads *t[2] = {q, k};
+    Heads heads[2];
+    for (int i = 0; i < 2; ++i)
+        if (t[i])
+            heads[i] = Heads{*t[i], t[i]->x_token_stride == 0 && t[i]->x_head_stride == 0,
+                             t[i]->y_token_stride == 0 && t[i]->y_head_stride == 0};
+    return rotate_heads(q ? &heads[0] : nullptr, k ? &heads[1] : nullptr, table, D, rot_dim, positions, true, eps, mode,
+                        axes, 0, dtype, stream);
 }
 
 int cross_attention_fwd(const void *q, const void *k, const void *v, void *out, float *lse, const int *k_len,

@@ -155,6 +155,31 @@ def test_fused_projection_in_place(sc, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens,heads,shared", [(40, 6, "both"), (1, 5, "both"), (7, 1, "both"), (1, 1, "both"),
+                                                 (40, 6, "tokens"), (40, 6, "heads")])
+def test_rows_shared_by_stride_zero(sc, tokens, heads, shared, dtype):
+    """One row for all tokens and heads (both strides 0), one for all tokens, one for all heads of a token; memory
+    right behind the shared rows is someone else's."""
+    import torch
+    D, positions = 64, 50
+    rows = {"both": (1, 1), "tokens": (1, heads), "heads": (tokens, 1)}[shared]
+    store = torch.full((rows[0] * rows[1] + tokens * heads, D), float("nan"),
+                       dtype=torch.bfloat16 if dtype == BF16 else torch.float32, device="cuda")
+    base = store[:rows[0] * rows[1]].view(*rows, D)
+    base.copy_(make(torch, dtype, *rows, D, seed=17))
+    x = base.expand(tokens, heads, D)
+    xs = (0 if rows[0] == 1 else heads * D if shared == "tokens" else D, D if shared == "tokens" else 0)
+    pos = positions_for(torch, 1, tokens, positions, 18)
+    t = table_for(torch, sc, positions, D // 2)
+    y = store[rows[0] * rows[1]:].view(tokens, heads, D)     # next to x: overlaps the one only if the other is packed
+    sc.check(sc.rotary_fwd(base, y, t, pos, tokens, heads, D, D, positions, dtype=dtype, x_strides=xs))
+    f, m = ref.frequencies(D // 2)
+    want, mag = ref.rotate(f64(x), pos.cpu().numpy(), D, HALF, 1, f)
+    assert (np.abs(f64(y) - want) <= bound(mag, want, D, dtype == BF16, False)).all()
+
+
+@pytest.mark.gpu
 def test_long_context_positions(sc):
     """The last positions of a long scaled context: the angle is not lost to 32 bits."""
     import torch
@@ -254,6 +279,11 @@ A, B, T, P, W = 1 << 30, 1 << 32, 1 << 34, 1 << 36, 1 << 38   # fake, aligned, f
     (dict(xs=(258, 64)), scl.SC_ERR_ALIGN),
     (dict(ys=(256, -64)), scl.SC_ERR_SHAPE),
     (dict(ys=(256, 32)), scl.SC_ERR_ALIAS),
+    (dict(ys=(0, 0)), scl.SC_ERR_ALIAS),
+    (dict(ys=(256, 0)), scl.SC_ERR_ALIAS),
+    (dict(ys=(0, 64)), scl.SC_ERR_ALIAS),
+    (dict(y=A, xs=(0, 0), ys=(0, 0)), scl.SC_ERR_ALIAS),
+    (dict(y=A, xs=(0, 0)), scl.SC_ERR_ALIAS),
     (dict(y=A + 64), scl.SC_ERR_ALIAS),
     (dict(y=A, ys=(512, 64)), scl.SC_ERR_ALIAS),
     (dict(table=B + 64), scl.SC_ERR_ALIAS),
