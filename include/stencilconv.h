@@ -256,7 +256,12 @@ typedef struct {
  * Supported: Hq % Hkv == 0; D % 8 == 0, D <= 128; scale > 0; Tq, Tk and
  *   N*Tq*Hq up to 2^30.
  * Scores, softmax and sums are fp32; bf16 outputs are rounded once (to
- * nearest even).
+ * nearest even).  Infinities and NaN in queries and valid states follow the
+ * formula, but that a row whose scores are all -infinity counts as one without
+ * a valid state.  fp32 tensors with more than 3 rows a key head (Tq * Hq / Hkv) are
+ * multiplied in three bf16 planes of 24 bits in all: there an infinity times
+ * another, or a key's times a query's element above 256, may be NaN, and an
+ * element below 2^-110 keeps 2^-134, not 24 bits.
  * A call may take a stream-ordered temporary buffer (see
  * sc_release_workspace).  Returns SC_OK or a negative sc_status.
  */

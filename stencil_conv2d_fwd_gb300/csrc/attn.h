@@ -95,6 +95,14 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two floats -> two bf16 (to nearest even, at most bf16's largest finite
+// value; NaN stays), `lo` at the lower address.
+__device__ __forceinline__ uint32_t pack_bf16_finite(float lo, float hi)
+{
+    uint32_t y;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Programmatic dependent launch: let the next kernel on the stream start its

@@ -52,15 +52,28 @@ constexpr int FLUSH = 4;
 // Index of column g of a product (see above).
 __device__ __forceinline__ int spread(int g) { return (g >> 1) + 4 * (g & 1); }
 
-// Two floats as three pairs of bf16, x = x0 + x1 + x2.
+// Two floats as three pairs of bf16, x = x0 + x1 + x2.  The first two planes
+// stay finite: fp32 values above bf16's largest, M, leave the rest to the
+// second, and an infinity is (M, M, infinity), of which the last meets the first
+// plane of the other operand only, so that 0 times it or a difference of two
+// does not arise (attn_split.cu's (0, 0, infinity) would take three more
+// instructions an element here).  For the same reason rows 8 to 15 of its
+// product are not 0: both halves of the rows take half of that first plane.
 __device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3])
 {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        p[i] = tc::pack_bf16(x, y);
+        p[i] = i < 2 ? pack_bf16_finite(x, y) : tc::pack_bf16(x, y);
         x -= __uint_as_float(p[i] << 16);
         y -= __uint_as_float(p[i] & 0xffff0000u);
     }
+}
+
+// Half of two bf16.
+__device__ __forceinline__ uint32_t half_of(uint32_t x)
+{
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), __float2bfloat162_rn(0.5f));
+    return *reinterpret_cast<const uint32_t *>(&y);
 }
 
 // DP: head width rounded up to 64 or 128 (fp32: 32, 64 or 128).  RH: 1 for up
@@ -172,7 +185,8 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm<T, DP>())
                     uint32_t b0[3], b1[3];
                     split3(__uint_as_float(k.x), __uint_as_float(k.y), b0);
                     split3(__uint_as_float(k.z), __uint_as_float(k.w), b1);
-                    mma16816(lo, q[0][0][c][0], 0u, q[0][0][c][1], 0u, b0[2], b1[2]);
+                    const uint32_t h0 = half_of(q[0][0][c][0]), h1 = half_of(q[0][0][c][1]);
+                    mma16816(lo, h0, h0, h1, h1, b0[2], b1[2]);
                     mma16816(lo, q[0][2][c][0], 0u, q[0][2][c][1], 0u, b0[0], b1[0]);
                     mma16816(lo, q[0][0][c][0], q[0][1][c][0], q[0][0][c][1], q[0][1][c][1], b0[1], b1[1]);
                     mma16816(s[i], q[0][0][c][0], q[0][1][c][0], q[0][0][c][1], q[0][1][c][1], b0[0], b1[0]);
@@ -240,6 +254,7 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm<T, DP>())
                     p[i][r][0] = tc::pack_bf16(x, y);
             }
         }
+        const uint32_t ph[2] = {half_of(p[0][0][0]), half_of(p[1][0][0])};   // fp32
         const uint4 *vt = ring.template piece<false>(step);
 #pragma unroll
         for (int c = 0; c < VC; ++c) {
@@ -255,7 +270,7 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm<T, DP>())
                     uint32_t b0[3], b1[3];
                     split3(__uint_as_float(word(v[0], j)), __uint_as_float(word(v[1], j)), b0);
                     split3(__uint_as_float(word(v[2], j)), __uint_as_float(word(v[3], j)), b1);
-                    mma16816(acc, p[0][0][0], 0u, p[1][0][0], 0u, b0[2], b1[2]);
+                    mma16816(acc, ph[0], ph[0], ph[1], ph[1], b0[2], b1[2]);
                     mma16816(acc, p[0][0][2], 0u, p[1][0][2], 0u, b0[0], b1[0]);
                     mma16816(acc, p[0][0][0], p[0][0][1], p[1][0][0], p[1][0][1], b0[1], b1[1]);
                     mma16816(acc, p[0][0][0], p[0][0][1], p[1][0][0], p[1][0][1], b0[0], b1[0]);

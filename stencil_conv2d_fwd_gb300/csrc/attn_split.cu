@@ -2,10 +2,14 @@
 // cores' tiles: fp32 ones split into three bf16 planes, bf16 ones (whose
 // strides the tiles' copies cannot address) as they are.
 //   x0 = bf16(x), x1 = bf16(x - x0), x2 = bf16(x - x0 - x1)
-// so that x = x0 + x1 + x2 to 24 bits (the differences are exact).  A product
-// x y is then x0 y0 + x0 y1 + x1 y0 + (x0 y2 + x1 y1 + x2 y0), the terms left
-// out below 2^-24 |x y| (bf16 has fp32's range, so nothing over- or underflows
-// that fp32 holds).  Bound by memory: 4 bytes read and 6 written an element.
+// so that x = x0 + x1 + x2 to 24 bits (the differences are exact; under 2^-110
+// the last planes are subnormal, and x keeps 2^-134).  A product x y is then
+// x0 y0 + x0 y1 + x1 y0 + (x0 y2 + x1 y1 + x2 y0), the terms left out below
+// 2^-24 |x y|.  x0 is at most bf16's largest value, which lies below fp32's; the
+// rest goes to x1.  An infinity (or NaN) is (0, 0, x): the last plane meets the
+// first of the other operand only, so that a finite y gives the infinity of y's
+// sign, as in x y, and not the NaN of an infinity times a plane that is 0 or has
+// the other sign.  Bound by memory: 4 bytes read and 6 written an element.
 #include <cuda_bf16.h>
 
 #include "attn.h"
@@ -52,14 +56,21 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitAr
         }
         const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + at);
         const float4 v0 = src[0], v1 = src[1];
-        float f[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        const float x[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = fabsf(x[i]) < INFINITY ? x[i] : 0.f;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                if (k == 2) {
+                    f[2 * i] = fabsf(x[2 * i]) < INFINITY ? f[2 * i] : x[2 * i];
+                    f[2 * i + 1] = fabsf(x[2 * i + 1]) < INFINITY ? f[2 * i + 1] : x[2 * i + 1];
+                }
                 const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                w[i] = k == 0 ? pack_bf16_finite(f[2 * i], f[2 * i + 1]) : *reinterpret_cast<const uint32_t *>(&b);
                 f[2 * i] -= __uint_as_float(w[i] << 16);
                 f[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
             }

@@ -359,6 +359,150 @@ def test_nan_in_a_valid_state_is_not_hidden(sc, Tq):
     assert torch.isnan(out).all()
 
 
+# (N, Tq, Tk, Hq, Hkv, D): 1, 3, 8, 16, 40 rows a key head on the kernels for few rows, 40 and 120 on the tensor cores
+ROWS = [(1, 1, 500, 4, 4, 64), (2, 3, 700, 2, 2, 64), (2, 2, 500, 8, 2, 64), (1, 16, 900, 2, 2, 128), (1, 40, 600, 4, 4, 64),
+        (1, 40, 6000, 4, 4, 64), (2, 40, 3000, 6, 2, 128)]
+
+
+def check_close(torch, got, lse, q, k, v, dtype, skip=None, valid=None):
+    """Against the 64-bit form at its bounds, but for the elements where skip holds."""
+    D, Tk = q.shape[3], k.shape[1]
+    o, z, wabs, mag = ref.attention(f64(q), f64(k), f64(v), D ** -0.5, valid)
+    ok = np.abs(f64(got) - o) <= ref.out_bound(o, wabs, mag, D, Tk, dtype == BF16)
+    assert (ok if skip is None else ok | skip).all()
+    zok = np.abs(f64(lse) - z) <= ref.lse_bound(z, mag, D, Tk)
+    assert (zok if skip is None else zok | skip.any(axis=3).transpose(0, 2, 1)).all()
+
+
+def call(torch, sc, q, k, v, dtype):
+    N, Tq, Hq, D = q.shape
+    out, lse = torch.zeros_like(q), torch.zeros(N, Hq, Tq, device="cuda")
+    sc.check(sc.cross_attention_fwd(q, k, v, out, N, Tq, k.shape[1], Hq, k.shape[2], D, D ** -0.5, dtype, lse=lse))
+    sc.check(sc.sc_last_device_status())
+    return out, lse
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", ROWS)
+def test_largest_fp32_values(sc, shape):
+    """A value, and a key where its queries are 0, above bf16's largest: finite results, as accurate as any."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, F32, N, Tq, Hq, D, seed=90)
+    k, v = make(torch, F32, N, Tk, Hkv, D, seed=91), make(torch, F32, N, Tk, Hkv, D, seed=92)
+    q[..., 2] = 0
+    k[:, 301, :, 2] = 3.4e38
+    v[:, 77, 0, 7] = 3.4e38
+    v[:, 78, -1, D - 1] = -3.402e38
+    out, lse = call(torch, sc, q, k, v, F32)
+    check_close(torch, out, lse, q, k, v, F32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("exponent", [-100, -112, -126])
+@pytest.mark.parametrize("shape", ROWS)
+def test_smallest_fp32_values(sc, shape, exponent):
+    """Values under 2^-110: their last bf16 planes are subnormal, an element keeps 2^-134 (half of the least of them);
+    the weights add up to 1 and their fp32 sums round by 2^-150 a term."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, F32, N, Tq, Hq, D, seed=105)
+    k, v = make(torch, F32, N, Tk, Hkv, D, seed=106), make(torch, F32, N, Tk, Hkv, D, seed=107, gain=2.0 ** exponent)
+    out, lse = call(torch, sc, q, k, v, F32)
+    o, z, wabs, mag = ref.attention(f64(q), f64(k), f64(v), D ** -0.5)
+    bound = ref.out_bound(o, wabs, mag, D, Tk, False) - 1e-30 + 2.0 ** -134 + Tk * 2.0 ** -150
+    assert (np.abs(f64(out) - o) <= bound).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", ROWS)
+def test_infinite_values(sc, shape, dtype):
+    """An infinity in a valid state's value: its column is that infinity, and no other is touched."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, dtype, N, Tq, Hq, D, seed=93)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=94), make(torch, dtype, N, Tk, Hkv, D, seed=95)
+    plain = v.clone()
+    v[0, 77, 0, 5] = math.inf
+    v[0, 411, -1, 9] = -math.inf
+    out, lse = call(torch, sc, q, k, v, dtype)
+    G = Hq // Hkv
+    assert (out[0, :, :G, 5] == math.inf).all() and (out[0, :, -G:, 9] == -math.inf).all()
+    skip = np.zeros(out.shape, bool)
+    skip[0, :, :G, 5] = skip[0, :, -G:, 9] = True
+    o, z, wabs, mag = ref.attention(f64(q), f64(k), f64(plain), D ** -0.5)
+    assert (np.abs(np.where(skip, 0, f64(out)) - np.where(skip, 0, o)) <=
+            ref.out_bound(o, wabs, mag, D, Tk, dtype == BF16)).all()
+    assert (np.abs(f64(lse) - z) <= ref.lse_bound(z, mag, D, Tk)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", ROWS)
+def test_infinite_key(sc, shape, dtype):
+    """A valid state whose score is -infinity has weight 0: the results are those without it."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, dtype, N, Tq, Hq, D, seed=96)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=97), make(torch, dtype, N, Tk, Hkv, D, seed=98)
+    q[..., 3] = q[..., 3].abs() + 0.125
+    k[:, 200, :, 3] = -math.inf
+    out, lse = call(torch, sc, q, k, v, dtype)
+    valid = np.ones((N, Tk), bool)
+    valid[:, 200] = False
+    check_close(torch, out, lse, q, torch.nan_to_num(k, neginf=0.0), v, dtype, valid=valid)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", ROWS)
+def test_every_score_minus_infinity(sc, shape, dtype):
+    """As without a valid state."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, dtype, N, Tq, Hq, D, seed=108)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=109), make(torch, dtype, N, Tk, Hkv, D, seed=110)
+    q[..., 3] = q[..., 3].abs() + 0.125
+    k[..., 3] = -math.inf
+    out, lse = call(torch, sc, q, k, v, dtype)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", ROWS)
+def test_infinite_query(sc, shape, dtype):
+    """An infinity in a query: scores of both infinities, NaN in that row and no other."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, dtype, N, Tq, Hq, D, seed=99)
+    k, v = make(torch, dtype, N, Tk, Hkv, D, seed=100), make(torch, dtype, N, Tk, Hkv, D, seed=101)
+    plain = q.clone()
+    q[0, -1, 0, 4] = math.inf
+    out, lse = call(torch, sc, q, k, v, dtype)
+    assert torch.isnan(out[0, -1, 0]).all() and torch.isnan(lse[0, 0, -1])
+    skip = np.zeros(out.shape, bool)
+    skip[0, -1, 0] = True
+    check_close(torch, out, lse, plain, k, v, dtype, skip=skip)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", ROWS)
+def test_nan_in_a_valid_fp32_state_is_not_hidden(sc, shape):
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    q = make(torch, F32, N, Tq, Hq, D, seed=102)
+    k, v = make(torch, F32, N, Tk, Hkv, D, seed=103), make(torch, F32, N, Tk, Hkv, D, seed=104)
+    k[:, 300, :, 1] = math.nan
+    out, lse = call(torch, sc, q, k, v, F32)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+    k[:, 300, :, 1] = 0
+    v[:, 300, :, 1] = math.nan
+    out, lse = call(torch, sc, q, k, v, F32)
+    assert torch.isnan(out[..., 1]).all() and torch.isfinite(out[..., 2:]).all() and torch.isfinite(lse).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(1, 140, 1000, 2, 2, 64), (11, 300, 700, 6, 6, 64), (1, 40, 20000, 2, 2, 128)])
 @pytest.mark.parametrize("drop_copy", [0, 1, 3])
