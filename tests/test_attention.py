@@ -251,6 +251,52 @@ def test_strides(sc, dtype, Tq):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(2, 2, 300, 6, 2, 64), (3, 50, 700, 4, 2, 72), (2, 200, 700, 4, 2, 64), (2, 160, 900, 4, 4, 128)])
+@pytest.mark.parametrize("which,axes", [("q", (0,)), ("q", (1,)), ("q", (2,)), ("q", (0, 1, 2)), ("k", (0,)), ("k", (2,)),
+                                        ("v", (0,)), ("v", (2,)), ("kv", (0, 2)), ("k", (1,)), ("v", (1,)), ("qkv", (0,))])
+@pytest.mark.parametrize("kind", ["all", "lengths", "mask"])
+def test_shared_axes(sc, shape, dtype, which, axes, kind):
+    """Strides of 0: queries, keys or values that the batch (0), the tokens or states (1) or the heads (2) share."""
+    import torch
+    N, Tq, Tk, Hq, Hkv, D = shape
+    lens = [Tk, 130, 1][:N] if kind == "lengths" else None
+    mask = None
+    if kind == "mask":
+        mask = (np.random.default_rng(111).random((N, Tk)) < 0.4).astype(np.uint8)
+        mask[0, 128:300] = 0
+    x, strides = {}, []
+    for i, (name, T, H) in enumerate((("q", Tq, Hq), ("k", Tk, Hkv), ("v", Tk, Hkv))):
+        size = [N, T, H]
+        for a in axes if name in which else ():
+            size[a] = 1
+        x[name] = make(torch, dtype, *size, D, seed=112 + i, gain=2.0 if name == "q" else 1.0)
+        if name != "q" and kind != "all" and size[:2] == [N, T]:     # states of its own: what is left out holds anything
+            x[name][torch.as_tensor(~valid_of(N, Tk, lens, mask)).cuda()] = math.nan if name == "k" else math.inf
+        x[name] = x[name].expand(N, T, H, D)
+        strides.append([0 if size[j] == 1 else x[name].stride(j) for j in range(3)])
+    out = torch.full((N, Tq, Hq, D), math.nan, dtype=x["q"].dtype, device="cuda")
+    run_and_check(torch, sc, x["q"], x["k"], x["v"], dtype, k_len=lens, key_mask=mask, strides=strides + [out.stride()[:3]],
+                  out=out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["all", "mask"])
+@pytest.mark.parametrize("axis", [0, 1, 2])
+def test_shared_queries_in_paired_tiles(sc, axis, kind):
+    """Queries that the batch, the tokens or the heads share, more row tiles than SMs."""
+    import torch
+    N, Tq, Tk, H, D = 11, 300, 700, 6, 64
+    size = [N, Tq, H]
+    size[axis] = 1
+    q = make(torch, BF16, *size, D, seed=115, gain=2.0).expand(N, Tq, H, D)
+    k, v = make(torch, BF16, N, Tk, H, D, seed=116), make(torch, BF16, N, Tk, H, D, seed=117)
+    mask = (np.random.default_rng(118).random((N, Tk)) < 0.4).astype(np.uint8) if kind == "mask" else None
+    out = torch.full((N, Tq, H, D), math.nan, dtype=q.dtype, device="cuda")
+    run_and_check(torch, sc, q, k, v, BF16, key_mask=mask, strides=[t.stride()[:3] for t in (q, k, v, out)], out=out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("Tq,Hq,Hkv", [(1, 4, 1), (33, 3, 3)])
 def test_offsets_beyond_32_bits(sc, dtype, Tq, Hq, Hkv):
     """Keys and values of more than 2^31 elements; the valid states are the last ones."""
