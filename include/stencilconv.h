@@ -255,13 +255,18 @@ typedef struct {
  *   as Tk), or NULL for Tk.  key_mask : N*Tk bytes, or NULL.
  * Supported: Hq % Hkv == 0; D % 8 == 0, D <= 128; scale > 0; Tq, Tk and
  *   N*Tq*Hq up to 2^30.
- * Scores, softmax and sums are fp32; bf16 outputs are rounded once (to
- * nearest even).  Infinities and NaN in queries and valid states follow the
- * formula, but that a row whose scores are all -infinity counts as one without
- * a valid state.  fp32 tensors with more than 3 rows a key head (Tq * Hq / Hkv) are
- * multiplied in three bf16 planes of 24 bits in all: there an infinity times
- * another, or a key's times a query's element above 256, may be NaN, and an
- * element below 2^-110 keeps 2^-134, not 24 bits.
+ * Scores, weights exp(s_j - m) and sums are fp32.  bf16 tensors: each weight
+ * is rounded to bf16 (a relative error up to 2^-8) where it multiplies a value,
+ * the sum that divides is one of unrounded weights, and the output is rounded
+ * once (to nearest even).  The sums of weight times value have to stay within
+ * fp32's range, m being the row's largest score so far, or for bf16 tensors up
+ * to 8 log 2 below it.
+ * Infinities and NaN in queries and valid states follow the formula, but that
+ * a row whose scores are all -infinity counts as one without a valid state.
+ * fp32 tensors with more than 3 rows a key head (Tq * Hq / Hkv) are multiplied
+ * in three bf16 planes of 24 bits in all: there an infinity times another, or
+ * a key's times a query's element above 256, may be NaN, and an element below
+ * 2^-110 keeps 2^-134, not 24 bits.
  * A call may take a stream-ordered temporary buffer (see
  * sc_release_workspace).  Returns SC_OK or a negative sc_status.
  */
