@@ -319,8 +319,8 @@ int rotary_table_fwd(float *table, int positions, int pairs, double base, int ru
  *   (with the same strides), else it overlaps no input.
  * table : positions * pairs * 2 floats of rotary_table_fwd.  pos : axes *
  *   tokens ints in device memory; for a position outside [0, positions) the
- *   head's turned elements become NaN and sc_last_device_status returns
- *   SC_ERR_RANGE.
+ *   elements that it turns become NaN (with axes 2, those of its axis's pairs)
+ *   and sc_last_device_status returns SC_ERR_RANGE.
  * Supported: D % 8 == 0, D <= 256; rot_dim <= D, rot_dim % (8 * axes) == 0
  *   (with rot_dim 0, table and pos may be NULL).
  * Returns SC_OK or a negative sc_status.

@@ -237,6 +237,42 @@ def test_position_outside_the_table(sc, bad):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("mode", [HALF, INTER])
+@pytest.mark.parametrize("bad_axes", [(0,), (1,), (0, 1)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_position_outside_the_table_on_one_axis(sc, norm, bad_axes, mode, dtype):
+    """Two axes: NaN where the bad position turns, the other axis's pairs and the rest of the head are right."""
+    import torch
+    tokens, heads, D, rot, positions = 9, 5, 80, 64, 40
+    t = table_for(torch, sc, positions, rot // 4)
+    pos = positions_for(torch, 2, tokens, positions, 19)
+    for a in bad_axes:
+        pos[a, 4] = positions
+    x = make(torch, dtype, tokens, heads, D, seed=20)
+    y = torch.zeros_like(x)
+    sc.check(sc.sc_last_device_status())
+    if norm:
+        sc.check(sc.qk_norm_rotary_fwd((x, y, None, pos, tokens, heads), None, t, D, rot, positions, 1e-6, mode, 2, dtype))
+    else:
+        sc.check(sc.rotary_fwd(x, y, t, pos, tokens, heads, D, rot, positions, mode, 2, dtype=dtype))
+    assert sc.sc_last_device_status() == scl.SC_ERR_RANGE
+    pair = np.arange(rot // 2)
+    a, b = (pair, pair + rot // 2) if mode == HALF else (2 * pair, 2 * pair + 1)
+    bad = np.zeros((tokens, heads, D), bool)
+    for axis in bad_axes:
+        mine = pair // (rot // 4) == axis
+        bad[4][:, np.concatenate([a[mine], b[mine]])] = True
+    got = f64(y)
+    assert np.isnan(got[bad]).all()
+    f, m = ref.frequencies(rot // 4)
+    src = ref.rms_norm(f64(x), None, 1e-6) if norm else f64(x)
+    want, mag = ref.rotate(src, pos.cpu().numpy() % positions, rot, mode, 2, f)
+    ok = np.abs(got - want) <= bound(mag, want, D, dtype == BF16, norm)
+    assert (ok | bad).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_offsets_beyond_32_bits(sc, dtype):
     import torch
     tokens, heads, D, positions = (1 << 31) // (16 * 128) + 77, 16, 128, 64
