@@ -311,9 +311,9 @@ int cross_attention_fwd(const void *q, const void *k, const void *v, void *out, 
     const long long rows = (long long)Tq * a.G;
     // More than 16 rows go to the tensor cores, except small fp32 calls: their
     // planes are a launch of their own there, and the warp-wide MMAs take row
-    // blocks of 8 (4 heads of 64, 20 rows over 300 states 12.9 against 22.2 us; 8
-    // heads, 77 rows over 1000 27.3 and 28.4; 4 x 8 heads, 40 rows over 1000, 82 M
-    // products, 37.5 and 32.4).
+    // blocks of 8 (4 heads of 64, 20 rows over 300 states 10.2 against 15.9 us; 8
+    // heads, 77 rows over 1000 24.6 and 26.6; 4 x 8 heads, 40 rows over 1000, 82 M
+    // products, 33.3 and 31.6).
     const double products = (double)N * Hq * Tq * (double)Tk * D;
     if (rows > 16 && (bf16 || products > 48e6)) return from_cuda(sc::launch_attn_tc(a, bf16, st));
     return from_cuda(!bf16 && rows <= 3 ? sc::launch_attn_rows(a, st) : sc::launch_attn_mma(a, bf16, st));

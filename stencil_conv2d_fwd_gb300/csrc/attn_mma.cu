@@ -27,7 +27,9 @@
 // i + j <= 2: in four MMAs, since rows 8 to 15 of an operand Q or P take its
 // second plane.  The MMAs cut sums short instead of rounding them, so the large
 // product of the scores and the small ones have accumulators of their own, and
-// O is moved to sums outside the MMAs every FLUSH steps.
+// O is moved to sums outside the MMAs every FLUSH steps.  (At 128 columns these
+// accumulators, Q's planes and the sums fill 255 registers, and 48 bytes a
+// thread are spilled.)
 #include "attn_rows.cuh"
 #include "launch.h"
 #include "tc_common.cuh"

@@ -1,12 +1,14 @@
 // Attention of up to three fp32 query rows per key head over many keys (a
 // decoder's next token, a short draft): every key and value is used by R <= 3
-// rows, so the kernel is bound by reading K and V once.  (The MMA kernel,
+// rows, so the kernel is bound by reading K and V once.  The MMA kernel,
 // attn_mma.cu, splits fp32 operands into bf16 planes, which costs the same for
-// one row as for eight; and asynchronous copies to shared memory, as there, took
-// 35.5, 80.5 and 48.8 us for one row of the cases below.  8 x 4 key heads of 32 over 16384 states: 1 to 3 rows
-// 31.4 us here and 39.6 there, 4 rows 45.7 and 39.6; 32 x 8 key heads of 64
-// over 3136: 1 row 72.4 and 92.7, 4 rows 117 and 92.8; 4 x 8 of 128 over 5000:
-// 1 row 35.5 and 66.2, 4 rows 62.1 and 70.3.)
+// one row as for eight.  Calls among others on changing inputs, 1, 3 and 4 rows
+// (4 in two blocks here):
+//   8 x 4 key heads of 32 over 16384 states: 25.5, 27.2, 40.8 us; there 30.8
+//   32 x 8 key heads of 64 over 3136:        64.9, 68.2, 110;     there 78.6 to 80.5
+//   4 x 8 key heads of 128 over 5000:        30.1, 32.2, 48.8;    there 60.1 to 63.3
+// (Asynchronous copies to shared memory, as there, but with FFMA, took one row of
+// these a tenth to a third longer.)
 //
 //   s_j = scale * q . k_j,  m = max_j s_j,  l = sum_j 2^((s_j - m) log2 e),
 //   o = sum_j 2^((s_j - m) log2 e) v_j,     out = o / l

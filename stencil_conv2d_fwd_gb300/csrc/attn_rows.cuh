@@ -289,13 +289,12 @@ __device__ __forceinline__ void finish_rows(const WarpSums<R, DP> &sm, CtaSums<R
 // there is one for every SM, none with less than a step of keys.  Up to 8 CTAs
 // of a row block are a cluster, which joins their sums itself; more write
 // partial results for a second kernel, unless four steps each of eight CTAs are
-// enough (one bf16 row over 4000 states 10.9 us, with a second kernel 14.0).
-// Measured: 32 x 4 key heads over up to 3136 bf16 states 18.4 us (two CTAs for
-// every SM 20.7, four 28.4: a CTA's start and end cost what it reads in 1 us);
-// one key head over 921600 states 45.2 us (with a slower join 45.9, where two
-// took 50.7 and clusters of 8, which leave SMs of a processing cluster idle,
-// 67); 8 x 4 fp32 key heads over 16384 states in clusters 26.7 us, as
-// partial results 38.9.
+// enough.  Measured, calls among others on changing inputs:
+//   one key head of 64, one bf16 row over 4000 states: cluster 8.2 us, partial results 10.2
+//   8 x 4 of 64, one bf16 row over 16384: 28.6 and 32.5; 8 x 4 of 32, three fp32 rows: 27.1 and 37.9
+//   32 x 4 of 64, four bf16 rows over 3136: 23.7 and 26.3; two CTAs for every SM 27.2, four 33.3
+//   (a CTA's start and end cost what it reads in 1 us)
+//   one of 64, four bf16 rows over 921600: 45.0, two CTAs for every SM 48.1, four 54.9
 template <class K>
 cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const AttnArgs &a, bool bf16, int R, int smem, cudaStream_t st)
 {

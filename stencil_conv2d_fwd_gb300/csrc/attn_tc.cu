@@ -30,7 +30,7 @@
 // the valid states' rows alone, so that every tile is dense, cost more than
 // the states left out: 32 x 77 queries over padded 56 x 56 maps, half of whose
 // states are valid, 118 us by TMA gathers of four rows, 60 us by 16-byte
-// copies, 46 us in place.)
+// copies, 45 us in place.)
 //
 // Accumulators, softmax and sums are fp32.  bf16 tensors: P is rounded to bf16
 // for the second product (a relative error of 2^-8 of single terms, the size
@@ -42,8 +42,8 @@
 // one key tile's product at a time, which the softmax threads add to sums of
 // their own in registers.
 //
-// Bound (4 x 16384 queries over 3600 states, 16 heads of 128 bf16: 1.285 ms,
-// 1.50 PFLOP/s, 0.78 of the 1.94 that a large library product reaches here): the
+// Bound (4 x 16384 queries over 3600 states, 16 heads of 128 bf16: 1.27 to 1.31
+// ms, 1.50 PFLOP/s, 0.77 of the 1.94 that a large library product reaches here): the
 // products' reads of shared memory.  A 128 x 128 x 16 product takes 64 clocks
 // and reads 8 KB for S (the row and the key tile's slices), 4 KB for O, and the
 // copies write 64 KB a pair of tiles, together what 128 bytes a clock allow;
@@ -51,9 +51,14 @@
 // alone, and starting and ending a CTA 6 of 85 thousand.  Two threads a row
 // (20 warps) made it 6% slower: the softmax is not what is waited for.  With 64
 // columns or fewer a product takes the same 64 clocks, so the O products of
-// 64-wide heads run at half rate: fp32 prompts (2 x 1001 queries over 3136
-// states, 8 heads of 64: 82 us, 157 TFLOP/s of the formula, 6 times that in
-// products) are bound by them.  Few row tiles are bound by reading keys and
+// 64-wide heads run at half rate (the same queries over 16 heads of 64 bf16:
+// 1.06 ms, 0.91 PFLOP/s): fp32 prompts (2 x 1001 queries over 3136 states, 8
+// heads of 64: 80 us, 162 TFLOP/s of the formula, 6 times that in products) are
+// bound by them.  fp32 heads of more than 64 have key tiles of 64, and it is the
+// S products that run at half rate (8 heads of 128: 142 us, 182 TFLOP/s; 4 x
+// 2048 queries over 3600 states, 16 heads: 1.03 ms, 235).  The two-row-tile
+// form of the planes (PAIR) spills 80 bytes a softmax thread, the others less
+// than 32.  Few row tiles are bound by reading keys and
 // values (6.7 TB/s while the tiles run) and by a CTA's start and end, 4 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -994,8 +999,8 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, const 
                       (long long)a.N * a.Hkv * g.row_tiles > device_sm_count();
     g.units = pair ? (g.row_tiles + 1) / 2 : g.row_tiles;
     // CTAs per row unit: fill the GPU, at least four key tiles each (2 x 8 key
-    // heads, 77 rows, 25 tiles: 19.1 us, at least eight 20.1, sixteen 27.3; two of
-    // 9000 keys, 17 rows: 18.1, 20.1, 26.3), and none for fewer than
+    // heads, 77 rows, 25 tiles: 14.4 us, at least eight 16.4, sixteen 24.6; two of
+    // 9000 keys, 17 rows: 14.3, 16.4, 22.5), and none for fewer than
     // twelve tiles, whose join costs what it saves
     const long long blocks = (long long)a.N * a.Hkv * g.units;
     const int kt = bf16 ? at::key_tile<64, 1>() : (a.D <= 64 ? at::key_tile<64, 3>() : at::key_tile<128, 3>());

@@ -33,7 +33,8 @@ constexpr int kRotThreads = 128;
 constexpr int kHeads = 4;     // heads of a token per thread
 // CTAs an SM: at most 64 registers a thread, 96 where eight weights and angles
 // of each chunk are held (64 spill them: 91 us, not 41, for the keys of 32 maps
-// of 56 x 56, 8 x 64 bf16, and their prompts' queries).
+// of 56 x 56, 8 x 64 bf16, and their prompts' queries).  The rotation alone
+// spills 20 to 32 bytes of its eight angles at 64, and runs at the memory's rate.
 template <int V, bool NORM>
 constexpr int rot_ctas() { return V == 8 && NORM ? 5 : 8; }
 
