@@ -261,7 +261,8 @@ def _to_code(y, code):
     if code == "i8":
         return y.round().to(torch.int8)
     # spacing of the codes at |y|: 2^-3 of its power of two, 2^-9 below 2^-6
-    step = torch.ldexp(torch.ones_like(y), torch.frexp(y).exponent.clamp(min=-5) - 4)
+    # (made of its bits: a power by pow may be off by a little)
+    step = ((torch.frexp(y).exponent.clamp(min=-5).long() + 1019) << 52).view(torch.float64)
     return ((y / step).round() * step).float().to(torch.float8_e4m3fn)
 
 
