@@ -45,7 +45,12 @@ typedef enum {
 } sc_status;
 
 typedef enum { SC_NCHW = 0, SC_NHWC = 1 } sc_layout;
-typedef enum { SC_ACT_NONE = 0, SC_ACT_RELU = 1 } sc_act;
+typedef enum {
+    SC_ACT_NONE = 0,
+    SC_ACT_RELU = 1,
+    SC_ACT_GELU = 2,   /* v (1 + erf(v / sqrt 2)) / 2; linear_fwd only, as SC_ACT_SILU is */
+    SC_ACT_SILU = 3    /* v / (1 + exp(-v)) */
+} sc_act;
 typedef enum { SC_F32 = 0, SC_BF16 = 1 } sc_dtype;   /* element type of an activation tensor */
 
 /*
@@ -354,6 +359,150 @@ typedef struct {
  */
 int qk_norm_rotary_fwd(const sc_norm_heads *q, const sc_norm_heads *k, const float *table, int D, int rot_dim,
                        int positions, float eps, int mode, int axes, int dtype, sc_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------
+ * A decoder layer around the attention: its products, its norms, and the
+ * feature map's states held in 8 bits.
+ * ---------------------------------------------------------------------
+ */
+
+/* Strides, in elements, from one row of linear_fwd's tensors to the next. */
+typedef struct {
+    long long x, w, y, residual;
+} sc_linear_strides;
+
+/*
+ * linear_fwd: y = act(x w^T + b) + residual, a decoder's projections and MLP
+ * ("Attention Is All You Need", Sections 3.2.2 and 3.3) and the 1x1 convolution
+ * of a feature map whose pixels are the rows:
+ *   y[i][o] = act( sum_c x[i][c] w[o][c] + b[o] ) + residual[i][o]
+ * act : SC_ACT_NONE, SC_ACT_RELU, SC_ACT_GELU ("Gaussian Error Linear Units",
+ *   the form with erf) or SC_ACT_SILU.  A NaN stays one.
+ * x : [rows][Cin], w : [Cout][Cin] (the order of conv2d_fwd's 1x1 filters),
+ *   y, residual : [rows][Cout], all of `dtype` (SC_F32 or SC_BF16); b : Cout
+ *   floats, or NULL for none; residual NULL for none.  Packed if strides is
+ *   NULL.
+ * Rows of x and w are 16-byte aligned (Cin % 8 == 0, strides multiples of 16
+ *   bytes, at least Cin).  Rows of y and residual are aligned to an element
+ *   only, any Cout and strides; y's are distinct, a residual stride of 0 is a
+ *   row that all share.  y may be residual (with the same stride), else it
+ *   overlaps no input.
+ * Products and sums are fp32, and so is everything up to y, which is rounded
+ * once (to nearest even).  Up to 16 rows are multiplied in fp32 or, in bf16, on
+ * warp-wide MMAs; more go to the tensor cores, fp32 tensors in three bf16
+ * planes of 24 bits in all, where an infinity times another may be NaN and an
+ * element below 2^-110 keeps 2^-134.
+ * Supported: rows, Cin and Cout up to 2^30.  A call may take a stream-ordered
+ * temporary buffer (see sc_release_workspace).  Returns SC_OK or a negative
+ * sc_status.
+ */
+int linear_fwd(const void *x, const void *w, const float *b, const void *residual, void *y, int rows, int Cin, int Cout,
+               int act, int dtype, const sc_linear_strides *strides, sc_stream_t stream);
+
+typedef enum { SC_NORM_NONE = 0, SC_NORM_RMS = 1, SC_NORM_LAYER = 2 } sc_norm_kind;
+
+/* One norm of residual_norm_fwd: weight and bias C floats (16-byte aligned), or
+ * NULL for ones and zeros. */
+typedef struct {
+    int kind;
+    float eps;
+    const float *weight, *bias;
+} sc_norm;
+
+/* Strides, in elements, from one row of residual_norm_fwd's tensors to the next. */
+typedef struct {
+    long long x, residual, sum, y;
+} sc_residual_strides;
+
+/*
+ * residual_norm_fwd: the norm behind a block, its gate, the residual stream
+ * and the norm before the next block, in one pass:
+ *   t = post(x),  s = scale * residual + gate * t,  sum = s,  y = pre(s)
+ *   SC_NORM_NONE:  v
+ *   SC_NORM_RMS:   v * (mean(v^2) + eps)^(-1/2) * weight + bias
+ *   SC_NORM_LAYER: (v - mean(v)) * (mean((v - mean(v))^2) + eps)^(-1/2) * weight + bias
+ * ("Root Mean Square Layer Normalization"; "Layer Normalization"), over the C
+ * elements of a row.  y is of s as it is in fp32, before sum's rounding.
+ * x, residual, sum, y : [rows][C] of `dtype`, 16-byte aligned, packed if
+ *   strides is NULL (multiples of 16 bytes; 0 on x or residual is a row that
+ *   all share).  residual NULL: s = gate * t.  sum or y may be NULL, not both.
+ *   Either may be x or residual (with the same stride), else it overlaps no
+ *   input; they do not overlap one another.
+ * post, pre : NULL for SC_NORM_NONE.  (A pre that is SC_NORM_NONE makes y the
+ *   sum.)
+ * gate : [(rows + gate_rows - 1) / gate_rows][C] floats, 16-byte aligned: row i
+ *   takes gate row i / gate_rows (gate_rows the tokens of a sequence, or rows
+ *   for one gate).  NULL for ones.
+ * Supported: C % 8 == 0, C <= 16384; finite scale, eps >= 0 and finite.
+ * Sums, means and all that leads to an output are fp32; each output is rounded
+ * once (to nearest even).
+ * Returns SC_OK or a negative sc_status.
+ */
+int residual_norm_fwd(const void *x, const void *residual, void *sum, void *y, int rows, int C, const sc_norm *post,
+                      const sc_norm *pre, const float *gate, int gate_rows, float scale, int dtype,
+                      const sc_residual_strides *strides, sc_stream_t stream);
+
+/* What a byte of an 8-bit state stands for: an integer (-128 .. 127), or a
+ * float of 4 exponent and 3 mantissa bits without infinities (up to 448;
+ * 0x7f and 0xff are NaN). */
+typedef enum { SC_CODE_I8 = 0, SC_CODE_E4M3 = 1 } sc_code;
+
+/* One tensor of kv_quantize_fwd: x as in cross_attention_fwd, codes the same
+ * with one byte an element, scale [N][Hkv][(Tk + block - 1) / block] floats.
+ * packed_x, packed_codes != 0: packed, whatever the strides say. */
+typedef struct {
+    const void *x;
+    void *codes;
+    float *scale;
+    int packed_x, packed_codes;
+    sc_head_strides x_strides, code_strides;
+} sc_quant_states;
+
+/*
+ * kv_quantize_fwd: keys and values in 8 bits with one scale for each block of
+ * `block` states and head.  With a the largest |x| over the block's valid
+ * states and the head's D elements, and top = 127 (SC_CODE_I8) or 448
+ * (SC_CODE_E4M3):
+ *   scale = a / top,   code = the code nearest to top * x / a (a tie to the even one)
+ * the quotient as in exact arithmetic.  A block of zeros has scale 0 and codes
+ * 0; one with an infinity or NaN in a valid state has scale NaN and codes 0.
+ * State j of sequence n is valid if j < k_len[n] and key_mask[n][j] != 0
+ * (NULL: all).  Others are not read; their codes, and the scales of blocks
+ * without a valid state, are left as they were.
+ * x : [N][Tk][Hkv][D] of `dtype`; k or v may be NULL (not both).  x, codes and
+ *   scale do not overlap.  To append blocks of states to a cache, pass the
+ *   addresses of the first new block.
+ * Supported: D % 16 == 0, D <= 128; block 16, 32, 64 or 128; rows of x and of
+ *   codes 16-byte aligned.  Returns SC_OK or a negative sc_status.
+ */
+int kv_quantize_fwd(const sc_quant_states *k, const sc_quant_states *v, const int *k_len, const unsigned char *key_mask,
+                    int N, int Tk, int Hkv, int D, int block, int code, int dtype, sc_stream_t stream);
+
+/*
+ * cross_attention_q8_fwd: cross_attention_fwd over states held as
+ * kv_quantize_fwd leaves them,
+ *   k[n][j][h][d] = k_scale[n][h][j / block] * code(k[n][j][h][d]),  v likewise,
+ * which reads half the bytes of bf16 states.
+ * q, out : [N][Tq][Hq][D] of `dtype`.  k, v : [N][Tk][Hkv][D] bytes; strides'
+ *   k and v count bytes.  k_scale, v_scale : [N][Hkv][(Tk + block - 1) / block]
+ *   floats, 4-byte aligned.  Everything else as in cross_attention_fwd; what
+ *   states that are not valid hold, and the scales of blocks without a valid
+ *   state, have no effect.
+ * Codes are multiplied as they are; the scales enter the fp32 scores and, in
+ * fp32, the sums of weights times codes.  fp32 queries and weights are taken to
+ * 22 bits, in two planes of fp16 (queries with a power of two for each row); a
+ * query with an infinity or NaN gives NaN.  With bf16 tensors each weight is
+ * rounded to fp16 where it multiplies a code (a relative error up to 2^-11),
+ * and the output is rounded once (to nearest even).  A weight below 2^-28 of the
+ * largest one among its 16 or 32 neighbours keeps 2^-39 of that.
+ * Supported: D % 16 == 0, D <= 128; block 16, 32, 64 or 128; otherwise as
+ * cross_attention_fwd.  Returns SC_OK or a negative sc_status.
+ */
+int cross_attention_q8_fwd(const void *q, const void *k, const float *k_scale, const void *v, const float *v_scale,
+                           void *out, float *lse, const int *k_len, const unsigned char *key_mask, int N, int Tq, int Tk,
+                           int Hq, int Hkv, int D, float scale, int block, int code, int dtype,
+                           const sc_attn_strides *strides, sc_stream_t stream);
 
 /*
  * stencil_pipeline_fwd: three stencil stages fused in one pass over a

@@ -32,6 +32,8 @@ SC_NCHW = 0
 SC_NHWC = 1
 SC_ACT_NONE = 0
 SC_ACT_RELU = 1
+SC_ACT_GELU = 2
+SC_ACT_SILU = 3
 SC_F32 = 0
 SC_BF16 = 1
 SC_ROT_HALF = 0
@@ -40,6 +42,11 @@ SC_ROT_SCALE_NONE = 0
 SC_ROT_SCALE_LINEAR = 1
 SC_ROT_SCALE_NTK = 2
 SC_ROT_SCALE_BANDS = 3
+SC_NORM_NONE = 0
+SC_NORM_RMS = 1
+SC_NORM_LAYER = 2
+SC_CODE_I8 = 0
+SC_CODE_E4M3 = 1
 
 # Every symbol include/stencilconv.h declares, with (restype, argtypes).
 _P = ctypes.c_void_p
@@ -77,6 +84,10 @@ SIGNATURES = {
     "rotary_table_fwd": (_I, [_P, _I, _I, _D, _I, _D, _D, _P]),
     "rotary_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "qk_norm_rotary_fwd": (_I, [_P, _P, _P, _I, _I, _I, _F, _I, _I, _I, _P]),
+    "linear_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "residual_norm_fwd": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _I, _F, _I, _P, _P]),
+    "kv_quantize_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "cross_attention_q8_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P, _P]),
 }
 SC_CHAIN_MAX_LAYERS = 64
 
@@ -326,6 +337,74 @@ def qk_norm_rotary_fwd(q, k, table, D, rot_dim, positions, eps=1e-6, mode=SC_ROT
     y_head_stride]) or None."""
     return load().qk_norm_rotary_fwd(_norm_heads(q), _norm_heads(k), _ptr(table), D, rot_dim, positions, eps, mode,
                                      axes, dtype, _stream(stream))
+
+
+# sc_linear_strides and sc_residual_strides
+_FOUR_STRIDES = struct.Struct("@qqqq")
+
+
+def linear_fwd(x, w, b, y, rows, Cin, Cout, act=SC_ACT_NONE, dtype=SC_F32, residual=None, strides=None,
+               stream=None) -> int:
+    """y = act(x w^T + b) + residual, x [rows][Cin], w [Cout][Cin] (see the header).
+
+    strides: elements from row to row of (x, w, y, residual), or None (packed)."""
+    return load().linear_fwd(_ptr(x), _ptr(w), _ptr(b), _ptr(residual), _ptr(y), rows, Cin, Cout, act, dtype,
+                             None if strides is None else _FOUR_STRIDES.pack(*strides), _stream(stream))
+
+
+# sc_norm as bytes
+_NORM = struct.Struct("@ifPP")
+
+
+def _norm_of(t):
+    if t is None:
+        return None
+    kind, weight, bias, eps = t
+    return _NORM.pack(kind, eps, _ptr(weight) or 0, _ptr(bias) or 0)
+
+
+def residual_norm_fwd(x, residual, sum, y, rows, C, post=None, pre=None, gate=None, gate_rows=1, scale=1.0, dtype=SC_F32,
+                      strides=None, stream=None) -> int:
+    """sum = scale * residual + gate * post(x), y = pre(sum), in one pass (see the header).
+
+    post, pre: (kind, weight, bias, eps) or None; strides: elements from row to row of
+    (x, residual, sum, y), or None (packed)."""
+    return load().residual_norm_fwd(_ptr(x), _ptr(residual), _ptr(sum), _ptr(y), rows, C, _norm_of(post), _norm_of(pre),
+                                    _ptr(gate), gate_rows, scale, dtype,
+                                    None if strides is None else _FOUR_STRIDES.pack(*strides), _stream(stream))
+
+
+# sc_quant_states as bytes
+_QUANT_STATES = struct.Struct("@PPPiiqqqqqq")
+
+
+def _quant_states(t):
+    if t is None:
+        return None
+    x, codes, scale, *strides = t
+    xs, cs = strides or (None, None)
+    return _QUANT_STATES.pack(_ptr(x) or 0, _ptr(codes) or 0, _ptr(scale) or 0, xs is None, cs is None,
+                              *(xs or (0, 0, 0)), *(cs or (0, 0, 0)))
+
+
+def kv_quantize_fwd(k, v, N, Tk, Hkv, D, block, code=SC_CODE_I8, dtype=SC_F32, k_len=None, key_mask=None,
+                    stream=None) -> int:
+    """Keys and values in 8 bits, one scale for each block of states and head (see the header).
+
+    k, v: (x, codes, scale[, x_strides, code_strides]) or None; strides: (batch, token, head) in
+    elements, or None (packed)."""
+    return load().kv_quantize_fwd(_quant_states(k), _quant_states(v), _ptr(k_len), _ptr(key_mask), N, Tk, Hkv, D, block,
+                                  code, dtype, _stream(stream))
+
+
+def cross_attention_q8_fwd(q, k, k_scale, v, v_scale, out, N, Tq, Tk, Hq, Hkv, D, scale, block, code=SC_CODE_I8,
+                           dtype=SC_F32, k_len=None, key_mask=None, lse=None, strides=None, stream=None) -> int:
+    """cross_attention_fwd over states that kv_quantize_fwd has written (see the header)."""
+    if strides is not None:
+        strides = ctypes.byref(ScAttnStrides(*(ScHeadStrides(*s) for s in strides)))
+    return load().cross_attention_q8_fwd(_ptr(q), _ptr(k), _ptr(k_scale), _ptr(v), _ptr(v_scale), _ptr(out), _ptr(lse),
+                                         _ptr(k_len), _ptr(key_mask), N, Tq, Tk, Hq, Hkv, D, scale, block, code, dtype,
+                                         strides, _stream(stream))
 
 
 def sc_empty_kernel(blocks, threads, stream=None) -> int:

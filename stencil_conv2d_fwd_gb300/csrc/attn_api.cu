@@ -6,114 +6,20 @@
 #include "../../include/stencilconv.h"
 #include "attn.h"
 #include "launch.h"
+#include "operands.h"
 
 namespace {
 
-constexpr long long kMaxOffset = 1LL << 46;   // elements; keeps every byte offset far from 2^63
-
-// A [n][t][h][D] tensor in memory: base address, sizes, strides in bytes.
-struct Region {
-    uintptr_t base;
-    long long n, t, h, row;      // sizes; bytes of a row of D elements
-    long long sn, st, sh;
-};
-
-long long region_bytes(const Region &r) { return (r.n - 1) * r.sn + (r.t - 1) * r.st + (r.h - 1) * r.sh + r.row; }
-
-// Whether two tensors share a byte, or false only if they surely do not:
-// disjoint ranges, or rows of one common token pitch whose heads lie in
-// disjoint parts of the pitch (the queries and keys of one fused projection).
-bool may_overlap(const Region &a, const Region &b)
-{
-    const uintptr_t a1 = a.base + (uintptr_t)region_bytes(a), b1 = b.base + (uintptr_t)region_bytes(b);
-    if (a1 <= b.base || b1 <= a.base) return false;
-    const long long s = a.st;
-    const bool pitched = s > 0 && s == b.st && (a.n == 1 || a.sn % s == 0) && (b.n == 1 || b.sn % s == 0);
-    const long long ea = (a.h - 1) * a.sh + a.row, eb = (b.h - 1) * b.sh + b.row;
-    if (!pitched || ea > s || eb > s) return true;
-    const long long d = (long long)((b.base >= a.base ? b.base - a.base : s - (a.base - b.base) % s) % (uintptr_t)s);
-    return d < ea || d + eb > s;
-}
-
-bool flat_overlap(const Region &a, const void *p, long long bytes)
-{
-    if (!p || bytes <= 0) return false;
-    const Region b{reinterpret_cast<uintptr_t>(p), 1, 1, 1, bytes, 0, bytes, 0};
-    return may_overlap(a, b);
-}
-
-// Whether the rows of a tensor that is written are distinct: sorted by
-// stride, each axis steps over all of the smaller ones.
-bool rows_distinct(const Region &r)
-{
-    long long size[3] = {r.n, r.t, r.h}, stride[3] = {r.sn, r.st, r.sh};
-    for (int i = 0; i < 3; ++i)
-        for (int j = i + 1; j < 3; ++j)
-            if (stride[j] < stride[i]) {
-                const long long a = stride[i], b = size[i];
-                stride[i] = stride[j];
-                stride[j] = a;
-                size[i] = size[j];
-                size[j] = b;
-            }
-    long long extent = r.row;
-    for (int i = 0; i < 3; ++i) {
-        if (size[i] == 1) continue;
-        if (stride[i] < extent) return false;
-        extent += (size[i] - 1) * stride[i];
-    }
-    return true;
-}
-
-bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-// Product of sizes >= 1, or -1 if it passes the largest offset.
-long long product(long long a, long long b, long long c = 1, long long d = 1)
-{
-    const long long v[4] = {a, b, c, d};
-    long long n = 1;
-    for (long long x : v) {
-        if (x < 1 || n > kMaxOffset / x) return -1;
-        n *= x;
-    }
-    return n;
-}
-
-// Strides of a tensor: the caller's, or those of packed [n][t][h][D].
-// SC_ERR_SHAPE for a negative stride or one whose tensor is too large.
-int take_strides(const sc_head_strides *s, int N, int T, int H, int D, sc::HeadStrides &out)
-{
-    out.h = D;
-    out.t = (long long)H * D;
-    out.n = out.t * T;
-    if (s) {
-        out.n = s->batch;
-        out.t = s->token;
-        out.h = s->head;
-    }
-    const long long v[3] = {out.n, out.t, out.h}, size[3] = {N, T, H};
-    for (int i = 0; i < 3; ++i)
-        if (v[i] < 0 || (v[i] > 0 && size[i] - 1 > kMaxOffset / v[i])) return SC_ERR_SHAPE;
-    return SC_OK;
-}
-
-bool strides_aligned(const sc::HeadStrides &s, int N, int T, int H, int esize)
-{
-    const int v = 16 / esize;
-    return (N == 1 || s.n % v == 0) && (T == 1 || s.t % v == 0) && (H == 1 || s.h % v == 0);
-}
-
-Region region(const void *p, int N, int T, int H, int D, const sc::HeadStrides &s, int esize)
-{
-    return Region{reinterpret_cast<uintptr_t>(p), N, T, H, (long long)D * esize, s.n * esize, s.t * esize, s.h * esize};
-}
-
-int from_cuda(cudaError_t e)
-{
-    if (e == cudaSuccess) return SC_OK;
-    if (e == cudaErrorInvalidConfiguration) return SC_ERR_SHAPE;   // more CTAs than a grid holds
-    return sc::record_cuda_error(e);
-}
+using sc::aligned;
+using sc::flat_overlap;
+using sc::from_cuda;
+using sc::may_overlap;
+using sc::product;
+using sc::region;
+using sc::Region;
+using sc::rows_distinct;
+using sc::strides_aligned;
+using sc::take_strides;
 
 // One tensor of a norm or rotation, and whether x and y are packed, whatever
 // their strides say (two strides of 0 may be a row that all tokens and heads share).
@@ -186,21 +92,26 @@ int rotate_heads(const Heads *t0, const Heads *t1, const float *table, int D, in
     return from_cuda(sc::launch_rotary(a, dtype == SC_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// cross_attention_fwd's argument checks; SC_OK with `a` filled in when the
-// call may launch.
+}  // namespace
+
+namespace sc {
+
+// The argument checks of cross_attention_fwd and cross_attention_q8_fwd; SC_OK
+// with `a` filled in when the call may launch.  Queries and output are of
+// `dtype`, an element of a key or value has state_bytes bytes.
 int take_attention(const void *q, const void *k, const void *v, void *out, float *lse, const int *k_len,
                    const unsigned char *key_mask, int N, int Tq, int Tk, int Hq, int Hkv, int D, float scale, int dtype,
-                   const sc_attn_strides *strides, sc::AttnArgs &a)
+                   int state_bytes, const sc_attn_strides *strides, AttnArgs &a)
 {
     if (!q || !k || !v || !out) return SC_ERR_NULL;
     if (product(N, Tq, Hq, D) < 0 || product(N, Tk, Hkv, D) < 0) return SC_ERR_SHAPE;
     if (Tq > (1 << 30) || Tk > (1 << 30)) return SC_ERR_SHAPE;
     if (product(N, Tq, Hq) > (1 << 30)) return SC_ERR_SHAPE;   // one index of 32 bits for a row
     if (dtype != SC_F32 && dtype != SC_BF16) return SC_ERR_UNSUPPORTED;
-    if (Hq % Hkv != 0 || D % 8 != 0 || D > sc::kAttnMaxD) return SC_ERR_UNSUPPORTED;
+    if (Hq % Hkv != 0 || D % 8 != 0 || D > kAttnMaxD) return SC_ERR_UNSUPPORTED;
     if (!(scale > 0.f) || !std::isfinite(scale)) return SC_ERR_UNSUPPORTED;
-    const int es = dtype == SC_BF16 ? 2 : 4;
-    a = sc::AttnArgs{};
+    const int es = dtype == SC_BF16 ? 2 : 4, ss = state_bytes;
+    a = AttnArgs{};
     if (take_strides(strides ? &strides->q : nullptr, N, Tq, Hq, D, a.qs) != SC_OK ||
         take_strides(strides ? &strides->k : nullptr, N, Tk, Hkv, D, a.ks) != SC_OK ||
         take_strides(strides ? &strides->v : nullptr, N, Tk, Hkv, D, a.vs) != SC_OK ||
@@ -209,11 +120,11 @@ int take_attention(const void *q, const void *k, const void *v, void *out, float
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(k_len, 4))
         return SC_ERR_ALIGN;
-    if (!strides_aligned(a.qs, N, Tq, Hq, es) || !strides_aligned(a.ks, N, Tk, Hkv, es) ||
-        !strides_aligned(a.vs, N, Tk, Hkv, es) || !strides_aligned(a.os, N, Tq, Hq, es))
+    if (!strides_aligned(a.qs, N, Tq, Hq, es) || !strides_aligned(a.ks, N, Tk, Hkv, ss) ||
+        !strides_aligned(a.vs, N, Tk, Hkv, ss) || !strides_aligned(a.os, N, Tq, Hq, es))
         return SC_ERR_ALIGN;
-    const Region rq = region(q, N, Tq, Hq, D, a.qs, es), rk = region(k, N, Tk, Hkv, D, a.ks, es);
-    const Region rv = region(v, N, Tk, Hkv, D, a.vs, es), ro = region(out, N, Tq, Hq, D, a.os, es);
+    const Region rq = region(q, N, Tq, Hq, D, a.qs, es), rk = region(k, N, Tk, Hkv, D, a.ks, ss);
+    const Region rv = region(v, N, Tk, Hkv, D, a.vs, ss), ro = region(out, N, Tq, Hq, D, a.os, es);
     const long long lse_bytes = lse ? 4LL * N * Hq * Tq : 0;
     if (!rows_distinct(ro) || may_overlap(ro, rq) || may_overlap(ro, rk) || may_overlap(ro, rv) ||
         flat_overlap(ro, k_len, 4LL * N) || flat_overlap(ro, key_mask, (long long)N * Tk) ||
@@ -242,7 +153,7 @@ int take_attention(const void *q, const void *k, const void *v, void *out, float
     return SC_OK;
 }
 
-}  // namespace
+}  // namespace sc
 
 extern "C" {
 
@@ -304,7 +215,8 @@ int cross_attention_fwd(const void *q, const void *k, const void *v, void *out, 
                         int dtype, const sc_attn_strides *strides, sc_stream_t stream)
 {
     sc::AttnArgs a;
-    const int rc = take_attention(q, k, v, out, lse, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, scale, dtype, strides, a);
+    const int rc = sc::take_attention(q, k, v, out, lse, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, scale, dtype, dtype == SC_BF16 ? 2 : 4,
+                                  strides, a);
     if (rc != SC_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SC_BF16;
@@ -323,7 +235,7 @@ int sc_test_attn_wait_expiry(const void *q, const void *k, const void *v, void *
                              int Hkv, int D, int drop_copy, int timeout_us, sc_stream_t stream)
 {
     sc::AttnArgs a;
-    const int rc = take_attention(q, k, v, out, nullptr, nullptr, nullptr, N, Tq, Tk, Hq, Hkv, D, 1.f, SC_BF16, nullptr, a);
+    const int rc = sc::take_attention(q, k, v, out, nullptr, nullptr, nullptr, N, Tq, Tk, Hq, Hkv, D, 1.f, SC_BF16, 2, nullptr, a);
     if (rc != SC_OK) return rc;
     if (drop_copy < 0 || timeout_us < 1) return SC_ERR_SHAPE;
     sc::TcTest test;
@@ -337,7 +249,8 @@ int sc_test_attn_slow_clear(const void *q, const void *k, const void *v, void *o
                             int delay_us, sc_stream_t stream)
 {
     sc::AttnArgs a;
-    const int rc = take_attention(q, k, v, out, nullptr, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, 1.f, dtype, nullptr, a);
+    const int rc = sc::take_attention(q, k, v, out, nullptr, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, 1.f, dtype,
+                                  dtype == SC_BF16 ? 2 : 4, nullptr, a);
     if (rc != SC_OK) return rc;
     if (!k_len && !key_mask) return SC_ERR_NULL;
     if (delay_us < 0 || delay_us > 1000) return SC_ERR_SHAPE;

@@ -1,0 +1,516 @@
+// Attention of few rows per key head over states held as 8-bit codes with a
+// scale for each block of states and head: a decoder's next token with its group
+// of query heads, a short draft; more rows come in blocks of 8 or 16.
+//
+//   S = scale ks (Q Kc^T),  P = 2^(log2e S - top),  O = sum_groups vs 2^(top - m) (P Vc),
+//   l = sum_groups 2^(top - m) sum P,  out = O / l
+//
+// over groups of 16 keys (32 where they share a scale), top the group's largest
+// score and m the largest so far.
+//
+// Bound by reading the codes once.  The products run on warp-wide m16n8k16 fp16
+// MMAs: a code, integer or e4m3, is exact in fp16, so neither the codes nor their
+// scales are rounded.  Queries are fp16 times a power of two for each row (a bf16
+// query is exact; an fp32 one has two planes of 11 bits, the second as rows 8 to
+// 15 of the operand).  Weights are 2^14 P, so that fp16 holds them to 2^-11 of
+// themselves down to 2^-28 of the group's largest (fp32 tensors: two planes, 22 bits
+// of that largest); a group has one scale, so a small weight cannot meet a larger
+// one's scale.  A group's products start from zero and enter the sums in fp32 with
+// its scale, so that the MMAs' cut-off sums stay short.
+//
+// Keys and values come through a ring of each warp's own in shared memory,
+// copied there asynchronously, 16 bytes a lane, and go to the operands in
+// registers 8 or 16 bytes at a time:
+//   * the order of summation over d is free, so lane (g, t) takes whole 16-byte
+//     chunks of its key as its share of k, and Q is laid out to match;
+//   * the columns of V's product are free too: lane (g, t) takes the g-th eighth
+//     of the head of each of the four keys that its share of P stands for.
+// Integer codes become fp16 in 2.5 (K) or 3 (V) instructions for two: a byte
+// with its sign bit turned is the low byte of 1024 + 128 + x in fp16, from which
+// 1152 is taken.
+#include "attn_rows.cuh"
+#include "launch.h"
+#include "layer.h"
+#include "tc_common.cuh"
+
+namespace sc {
+
+namespace {
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t x)
+{
+    float2 y;
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.f32.f16 %0, l;\ncvt.f32.f16 %1, h;\n}\n" : "=f"(y.x), "=f"(y.y) : "r"(x));
+    return y;
+}
+
+// Four codes -> two pairs of fp16.  Integers: (bytes 0, 2) and (1, 3); e4m3:
+// (0, 1) and (2, 3).
+template <bool E4M3>
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t &p0, uint32_t &p1)
+{
+    if constexpr (E4M3) {
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+            : "=r"(p0), "=r"(p1)
+            : "r"(w));
+    } else {
+        // (w & 0x00ff00ff) ^ 0x64806480 is 1024 + (x + 128) in each half
+        uint32_t e, o;
+        asm("lop3.b32 %0, %1, 0x00ff00ff, %2, 0x6a;" : "=r"(e) : "r"(w), "r"(0x64806480u));
+        asm("lop3.b32 %0, %1, 0x00ff00ff, %2, 0x6a;" : "=r"(o) : "r"(w >> 8), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p0) : "r"(e), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p1) : "r"(o), "r"(0x64806480u));
+    }
+}
+// Which byte of four is element i of the pairs (p0.lo, p0.hi, p1.lo, p1.hi).
+template <bool E4M3>
+__host__ __device__ constexpr int byte_of(int i) { return E4M3 ? i : (i == 1 ? 2 : (i == 2 ? 1 : i)); }
+// The selector that gathers bytes 2 i and 2 i + 1 of two words so that the pairs
+// of to_f16 are (word 0, word 1) of byte 2 i, and of byte 2 i + 1.
+template <bool E4M3>
+__host__ __device__ constexpr uint32_t gather(int i) { return E4M3 ? (i ? 0x7362u : 0x5140u) : (i ? 0x7632u : 0x5410u); }
+
+// A warp's ring: STAGES steps of KP keys and as many values, rows of DP bytes,
+// and the step's scales.  A row's 16-byte chunks lie so that the reads below
+// fall in different bank groups: key r of eight in place 2 (r mod 4) + r / 4, chunk
+// c of places of 128 bytes at c XOR 4 (place mod 2); value r in place r, chunk c
+// at c XOR 2 (r mod 4), of 64-byte rows c XOR 2 (r / 2 mod 2).
+template <int DP>
+struct Q8Ring {
+    static constexpr int KP = DP == 64 ? 32 : 16;
+    static constexpr int GROUPS = KP / 16;              // of 16 keys, each with one scale
+    static constexpr int CH = DP / 16;                  // chunks of a row
+    static constexpr int RPL = 32 / CH;                 // rows of a warp-wide copy
+    static constexpr int STAGES = 3;
+    static constexpr int TILE = KP * CH;                // in 16-byte units
+    static constexpr int STAGE = 2 * TILE + 1;          // and one unit of scales: ks, ks, vs, vs
+    static constexpr int STEP = kRowWarps * KP;         // keys from a step to the next
+
+    const unsigned char *kp, *vp, *kbase, *vbase;
+    const float *scale;      // lanes 0 to 3: the scales of their part of a step
+    long long kst, vst;
+    const unsigned char *mb;
+    uint4 *ring;
+    int len, key0, steps, lane, crow, cch, log2_block, use, fill;
+    bool cact;
+    uint32_t ok[STAGES - 1];   // valid bits of the steps under way
+    int byte;                  // the mask's byte of the step after those
+
+    __device__ __forceinline__ int mask_byte(int step) const
+    {
+        const int key = key0 + step * STEP + lane;
+        return step < steps && lane < KP && key < len ? (mb ? (int)mb[key] : 1) : 0;
+    }
+    static __device__ __forceinline__ int key_at(int r, int c)
+    {
+        const int place = (r & ~7) | ((r & 3) << 1) | ((r >> 2) & 1);
+        return place * CH + (CH == 8 ? c ^ (4 * (place & 1)) : c);
+    }
+    static __device__ __forceinline__ int value_at(int r, int c)
+    {
+        return r * CH + (CH == 8 ? c ^ (2 * (r & 3)) : c ^ (2 * ((r >> 1) & 1)));
+    }
+    __device__ __forceinline__ void copy(int step, uint32_t valid)
+    {
+        uint4 *k = ring + fill * STAGE, *v = k + TILE;
+#pragma unroll
+        for (int i = 0; i < KP / RPL; ++i) {
+            const int row = crow + i * RPL;
+            const bool on = cact && (valid >> row & 1u);
+            cp_async16(smem_u32(k + key_at(row, cch)), on ? kp + i * RPL * kst : kbase, on ? 16 : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < KP / RPL; ++i) {
+            const int row = crow + i * RPL;
+            const bool on = cact && (valid >> row & 1u);
+            cp_async16(smem_u32(v + value_at(row, cch)), on ? vp + i * RPL * vst : vbase, on ? 16 : 0);
+        }
+        // scales of groups without a valid state are not read
+        if (lane < 2 * GROUPS) {
+            const int grp = lane % GROUPS;
+            const bool on = (valid >> (16 * grp) & 0xffffu) != 0;
+            const int blk = (key0 + step * STEP + 16 * grp) >> log2_block;
+            cp_async4(smem_u32(reinterpret_cast<float *>(k + 2 * TILE) + lane), scale + (on ? blk : 0), on ? 4 : 0);
+        }
+        cp_async_commit();
+        kp += STEP * kst;
+        vp += STEP * vst;
+        fill = fill + 1 == STAGES ? 0 : fill + 1;
+    }
+    __device__ __forceinline__ void begin(uint4 *memory, const AttnQ8Args &a, int n, int h, int split, int splits, int warp)
+    {
+        ring = memory;
+        lane = threadIdx.x & 31;
+        len = a.Tk;
+        if (a.k_len) len = max(0, min(len, a.k_len[n]));
+        const int pieces = (len + KP - 1) / KP;
+        const int p0 = (int)((long long)pieces * split / splits), p1 = (int)((long long)pieces * (split + 1) / splits);
+        steps = p1 - p0 > warp ? (p1 - p0 - warp + kRowWarps - 1) / kRowWarps : 0;
+        key0 = (p0 + warp) * KP;
+        mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
+        crow = lane / CH;
+        cch = lane % CH;
+        cact = cch * 16 < a.D;
+        kst = a.ks.t;
+        vst = a.vs.t;
+        kbase = static_cast<const unsigned char *>(a.k);
+        vbase = static_cast<const unsigned char *>(a.v);
+        kp = kbase + n * a.ks.n + h * a.ks.h + (long long)(key0 + crow) * kst + (cact ? cch * 16 : 0);
+        vp = vbase + n * a.vs.n + h * a.vs.h + (long long)(key0 + crow) * vst + (cact ? cch * 16 : 0);
+        scale = (lane < GROUPS ? a.k_scale : a.v_scale) + ((long long)n * a.Hkv + h) * a.blocks;
+        log2_block = a.log2_block;
+        use = fill = 0;
+        int b[STAGES - 1];
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) b[i] = mask_byte(i);
+        byte = mask_byte(STAGES - 1);
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) {
+            ok[i] = __ballot_sync(0xffffffffu, b[i] != 0);
+            copy(i, ok[i]);
+        }
+    }
+    // Waits for the step's stage and asks for the one STAGES - 1 ahead, which goes
+    // where the last one was read (the warp's barrier is behind those reads).
+    __device__ __forceinline__ const uint4 *next(int step, uint32_t &valid)
+    {
+        cp_async_wait<STAGES - 2>();
+        __syncwarp();
+        valid = ok[0];
+#pragma unroll
+        for (int i = 0; i + 1 < STAGES - 1; ++i) ok[i] = ok[i + 1];
+        ok[STAGES - 2] = __ballot_sync(0xffffffffu, byte != 0);
+        byte = mask_byte(step + STAGES);
+        copy(step + STAGES - 1, ok[STAGES - 2]);
+        const uint4 *s = ring + use * STAGE;
+        use = use + 1 == STAGES ? 0 : use + 1;
+        return s;
+    }
+};
+
+// The rings' memory becomes the warps' sums at the end; the cluster's sums have
+// their own.
+template <int DP, int R>
+struct Q8Shared {
+    union {
+        uint4 ring[kRowWarps][Q8Ring<DP>::STAGE * Q8Ring<DP>::STAGES];
+        WarpSums<R, DP> warps;
+    };
+    CtaSums<R, DP> ctas;
+};
+
+constexpr float kWeightLog2 = 14.f;   // weights are 2^14 P
+
+// T: float or bf16 queries; R: 8 rows, or with bf16 16.
+template <class T, int DP, bool E4M3, int R>
+__global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
+    attn_q8_kernel(const AttnQ8Args a, const RowsGeom g, const AttnPartials part)
+{
+    using Ring = Q8Ring<DP>;
+    constexpr bool F32 = sizeof(T) == 4;
+    constexpr int RH = R / 8;
+    constexpr int KC = Ring::CH / 4;     // chunks of a key per lane
+    constexpr int NT = DP / 8;           // products of 8 columns of O, one for each of the lane's bytes of a value
+    static_assert(!F32 || RH == 1, "fp32: rows 8 to 15 are the second plane");
+    extern __shared__ __align__(128) unsigned char dyn[];
+    Q8Shared<DP, R> &sm = *reinterpret_cast<Q8Shared<DP, R> *>(dyn);
+
+    pdl_trigger();   // the join kernel may be set up; it waits for this grid's end
+    if (g.cluster > 1) cluster_arrive();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t = lane & 3;
+    const int split = blockIdx.x % g.splits;
+    const int blk = blockIdx.x / g.splits;
+    const int row0 = (blk % g.row_blocks) * R;
+    const int nh = blk / g.row_blocks;
+    const int n = nh / a.Hkv, h = nh - n * a.Hkv;
+    const int rows = a.Tq * a.G;
+
+    Ring ring;
+    ring.begin(sm.ring[warp], a, n, h, split, g.splits, warp);
+
+    // the rows' queries times a power of two that puts a row's largest element in
+    // [2^12, 2^13); back[] undoes it and carries scale log2 e
+    uint32_t q[KC * 4][4];
+    float back[RH];
+    {
+        float f[RH][KC][16];
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+            const int row = row0 + r * 8 + gq;
+            const int tok = row / a.G, hq = h * a.G + row % a.G;
+            float mx = 0.f;
+            bool odd = false;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const int d = (c * 4 + t) * 16;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[r][c][i] = 0.f;
+                if (row < rows && d < a.D) {
+                    const T *p = static_cast<const T *>(a.q) + n * a.qs.n + tok * a.qs.t + hq * a.qs.h + d;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 16 / (int)sizeof(T)) {
+                        const uint4 v = ldg16(p + i);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if constexpr (F32) {
+                                f[r][c][i + j] = __uint_as_float(w[j]);
+                            } else {
+                                f[r][c][i + 2 * j] = __uint_as_float(w[j] << 16);
+                                f[r][c][i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    mx = fmaxf(mx, fabsf(f[r][c][i]));
+                    odd |= !(fabsf(f[r][c][i]) < INFINITY);
+                }
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const uint32_t odd_quad = __ballot_sync(0xffffffffu, odd) >> (lane & ~3) & 0xfu;
+            // 2^(12 - exponent), in two steps where a row is tiny
+            const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -126);
+            const int up = mx > 0.f ? 12 - e : 0;
+            const float u0 = __uint_as_float((uint32_t)(127 + up / 2) << 23), u1 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
+            const float d0 = __uint_as_float((uint32_t)(127 - up / 2) << 23), d1 = __uint_as_float((uint32_t)(127 - (up - up / 2)) << 23);
+            // an infinity or NaN makes the row NaN
+            back[r] = odd_quad ? __uint_as_float(0x7fffffffu) : a.scale * kLog2e * d0 * d1;
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[r][c][i] = odd_quad ? 0.f : f[r][c][i] * u0 * u1;
+        }
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {   // operand registers (0, 1), (2, 3): the two pairs of a word of codes
+                    const int i0 = 4 * w + byte_of<E4M3>(2 * p), i1 = 4 * w + byte_of<E4M3>(2 * p + 1);
+                    const uint32_t hi = pack_f16(f[0][c][i0], f[0][c][i1]);
+                    q[c * 4 + w][2 * p] = hi;
+                    if constexpr (F32) {
+                        const float2 x = unpack_f16(hi);
+                        q[c * 4 + w][2 * p + 1] = pack_f16(f[0][c][i0] - x.x, f[0][c][i1] - x.y);
+                    } else {
+                        q[c * 4 + w][2 * p + 1] = RH == 2 ? pack_f16(f[RH - 1][c][i0], f[RH - 1][c][i1]) : 0u;
+                    }
+                }
+    }
+
+    float m[RH], l[RH], o[NT][2 * RH];   // m: the largest top, to which l and o are relative
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2 * RH; ++i) o[j][i] = 0.f;
+
+    for (int step = 0; step < ring.steps; ++step) {
+        uint32_t ok;
+        const uint4 *kt = ring.next(step, ok);
+        const uint4 *vt = kt + Ring::TILE;
+        const float *sc = reinterpret_cast<const float *>(kt + 2 * Ring::TILE);
+
+        float s[2 * Ring::GROUPS][4];
+#pragma unroll
+        for (int i = 0; i < 2 * Ring::GROUPS; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+            // column g of the scores is key 8 i + (g / 2) + 4 (g mod 2), in place 8 i + g
+            const int place = 8 * i + gq;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const uint4 k = kt[place * Ring::CH + (KC == 2 ? (c * 4 + t) ^ (4 * (place & 1)) : t)];
+                const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t b0, b1;
+                    to_f16<E4M3>(w[x], b0, b1);
+                    mma_f16(s[i], q[c * 4 + x], b0, b1);
+                }
+            }
+        }
+        // scores of row g (and g + 8) for the keys 8 i + t and 8 i + t + 4; top: what
+        // a group's weights are relative to, its largest score less 14
+        const bool joint = Ring::GROUPS == 2 && a.log2_block > 4 && (ok >> 16) != 0 && (ok & 0xffffu) != 0;   // one scale
+        float top[Ring::GROUPS][RH];
+        bool grow = false;
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+#pragma unroll
+            for (int i = 0; i < Ring::GROUPS; ++i) {
+                const float f = back[r] * sc[i];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float &x = s[2 * i + e / 2][2 * r + e % 2];
+                    if constexpr (F32) x += s[2 * i + e / 2][2 + e % 2];
+                    x = (ok >> (16 * i + 8 * (e / 2) + t + 4 * (e % 2)) & 1u) ? x * f : -INFINITY;
+                    mx = fmaxf(mx, x);
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                top[i][r] = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) - kWeightLog2;
+                grow |= top[i][r] > m[r];
+            }
+            if (joint) top[0][r] = top[Ring::GROUPS - 1][r] = fmaxf(top[0][r], top[Ring::GROUPS - 1][r]);
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int r = 0; r < RH; ++r) {
+                const float mm = fmaxf(m[r], fmaxf(top[0][r], top[Ring::GROUPS - 1][r]));
+                const float f = mm == -INFINITY ? 1.f : ex2(m[r] - mm);
+                m[r] = mm;
+                l[r] *= f;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[j][2 * r] *= f;
+                    o[j][2 * r + 1] *= f;
+                }
+            }
+        }
+        uint32_t p[Ring::GROUPS][4];
+        float vs[Ring::GROUPS][RH];   // a group's factor: its scale, and its weights relative to m
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+            const float mr = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+            for (int i = 0; i < Ring::GROUPS; ++i) {
+                const float f = ex2(top[i][r] - mr), ms = top[i][r] == -INFINITY ? 0.f : top[i][r];
+                vs[i][r] = sc[Ring::GROUPS + i] * f;
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = ex2(s[2 * i + e][2 * r] - ms), y = ex2(s[2 * i + e][2 * r + 1] - ms);
+                    sum += x + y;
+                    const uint32_t hi = pack_f16(x, y);
+                    p[i][2 * e + r] = hi;
+                    if constexpr (F32) {
+                        const float2 z = unpack_f16(hi);
+                        p[i][2 * e + 1] = pack_f16(x - z.x, y - z.y);
+                    } else if constexpr (RH == 1) {
+                        p[i][2 * e + 1] = 0u;
+                    }
+                }
+                l[r] = fmaf(sum, f, l[r]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NT / 8; ++c) {
+            // the lane's eight bytes (half a chunk of 128-wide heads, whose 16 bytes come as two) of four keys a group
+            uint2 v[Ring::GROUPS][4];
+#pragma unroll
+            for (int i = 0; i < Ring::GROUPS; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 16 * i + t + 4 * e;
+                    if constexpr (DP == 64)
+                        v[i][e] = reinterpret_cast<const uint2 *>(vt + Ring::value_at(r, gq >> 1))[gq & 1];
+                    else
+                        v[i][e] = reinterpret_cast<const uint2 *>(vt + Ring::value_at(r, gq))[c];
+                }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {   // bytes 2 x and 2 x + 1
+                uint32_t b[Ring::GROUPS][2][2];
+#pragma unroll
+                for (int i = 0; i < Ring::GROUPS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint2 &u0 = v[i][2 * e], &u1 = v[i][2 * e + 1];
+                        const uint32_t w = x < 2 ? __byte_perm(u0.x, u1.x, gather<E4M3>(x)) : __byte_perm(u0.y, u1.y, gather<E4M3>(x - 2));
+                        to_f16<E4M3>(w, b[i][0][e], b[i][1][e]);
+                    }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    float(&sum)[2 * RH] = o[c * 8 + 2 * x + y];
+                    auto add = [&](const float (&acc)[4], const float (&f)[RH]) {
+                        if constexpr (F32) {
+                            sum[0] = fmaf(acc[0] + acc[2], f[0], sum[0]);
+                            sum[1] = fmaf(acc[1] + acc[3], f[0], sum[1]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 2 * RH; ++k) sum[k] = fmaf(acc[k], f[k / 2], sum[k]);
+                        }
+                    };
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16(acc, p[0], b[0][y][0], b[0][y][1]);
+                    if constexpr (Ring::GROUPS == 2) {
+                        if (!joint) {
+                            if (ok & 0xffffu) add(acc, vs[0]);
+                            acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+                        }
+                        mma_f16(acc, p[Ring::GROUPS - 1], b[Ring::GROUPS - 1][y][0], b[Ring::GROUPS - 1][y][1]);
+                        if (joint || (ok >> 16)) add(acc, vs[Ring::GROUPS - 1]);
+                    } else if (ok) {
+                        add(acc, vs[0]);
+                    }
+                }
+            }
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();   // the rings' memory becomes the sums'
+
+    // the warp's sums: row g (and g + 8); l over the quad
+#pragma unroll
+    for (int r = 0; r < RH; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (t == 0) {
+            sm.warps.m[warp][r * 8 + gq] = m[r];
+            sm.warps.l[warp][r * 8 + gq] = l[r];
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)   // column 2 t + e of product j is byte j of that lane group's part of the head
+                sm.warps.o[warp][r * 8 + gq][(2 * t + e) * (DP / 8) + j] = o[j][2 * r + e];
+    }
+    finish_rows<T, R, DP>(sm.warps, sm.ctas, a, g, part, nh, row0, split);
+}
+
+template <class T, int DP, bool E4M3, int R>
+cudaError_t launch_q8(const AttnQ8Args &a, cudaStream_t st)
+{
+    static KernelCache cache;
+    return launch_rows_kernel(attn_q8_kernel<T, DP, E4M3, R>, cache, a, sizeof(T) == 2, R, (int)sizeof(Q8Shared<DP, R>), st);
+}
+
+template <class T, bool E4M3>
+cudaError_t dispatch(const AttnQ8Args &a, cudaStream_t st)
+{
+    if constexpr (sizeof(T) == 2) {
+        if ((long long)a.Tq * a.G > 8) return a.D <= 64 ? launch_q8<T, 64, E4M3, 16>(a, st) : launch_q8<T, 128, E4M3, 16>(a, st);
+    }
+    return a.D <= 64 ? launch_q8<T, 64, E4M3, 8>(a, st) : launch_q8<T, 128, E4M3, 8>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st)
+{
+    if (bf16) return e4m3 ? dispatch<__nv_bfloat16, true>(a, st) : dispatch<__nv_bfloat16, false>(a, st);
+    return e4m3 ? dispatch<float, true>(a, st) : dispatch<float, false>(a, st);
+}
+
+}  // namespace sc

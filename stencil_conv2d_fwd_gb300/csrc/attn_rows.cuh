@@ -295,8 +295,8 @@ __device__ __forceinline__ void finish_rows(const WarpSums<R, DP> &sm, CtaSums<R
 //   32 x 4 of 64, four bf16 rows over 3136: 23.7 and 26.3; two CTAs for every SM 27.2, four 33.3
 //   (a CTA's start and end cost what it reads in 1 us)
 //   one of 64, four bf16 rows over 921600: 45.0, two CTAs for every SM 48.1, four 54.9
-template <class K>
-cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const AttnArgs &a, bool bf16, int R, int smem, cudaStream_t st)
+template <class K, class A>
+cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const A &a, bool bf16, int R, int smem, cudaStream_t st)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

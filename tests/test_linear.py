@@ -1,0 +1,228 @@
+"""linear_fwd against the plain 64-bit form, and its refusals (bounds: layer_ref.py)."""
+import pytest
+
+import layer_ref as ref
+import stencil_conv2d_fwd_gb300 as scl
+
+BF16, F32 = scl.SC_BF16, scl.SC_F32
+
+
+def tensors(torch, dtype, rows, Cin, Cout, seed=0, bias=True, residual=True):
+    g = torch.Generator().manual_seed(seed)
+    t = torch.bfloat16 if dtype == BF16 else torch.float32
+    x = torch.randn(rows, Cin, generator=g).to(t).cuda()
+    w = (torch.randn(Cout, Cin, generator=g) * Cin ** -0.5).to(t).cuda()
+    b = torch.randn(Cout, generator=g).cuda() if bias else None
+    r = torch.randn(rows, Cout, generator=g).to(t).cuda() if residual else None
+    return x, w, b, r
+
+
+def check(torch, y, x, w, b, r, act, dtype):
+    want, mag, a = ref.linear(x, w, b, r, act)
+    bound = ref.linear_bound(want, mag, a, x.shape[1], dtype == BF16)
+    err = (y.double() - want).abs()
+    assert torch.isfinite(y.float()).all()
+    worst = (err / bound).max().item()
+    assert worst <= 1, f"{worst:.2f} of its bound at {(err / bound).argmax().item()} of {tuple(y.shape)}"
+
+
+def run(torch, sc, x, w, b, r, act, dtype, stream=None):
+    (rows, Cin), Cout = x.shape, w.shape[0]
+    y = torch.full((rows, Cout), float("nan"), dtype=x.dtype, device="cuda")
+    sc.check(sc.linear_fwd(x, w, b, y, rows, Cin, Cout, act, dtype, residual=r, stream=stream), "linear_fwd")
+    sc.check(sc.sc_last_device_status(stream), "device status")
+    return y
+
+
+# (rows, Cin, Cout): one row to many, around tiles, odd rows and outputs, narrow and long sums
+SHAPES = [
+    (1, 8, 1), (1, 64, 7), (1, 1024, 1024), (1, 4096, 257), (2, 520, 1000), (3, 512, 4001), (4, 1024, 1024), (5, 72, 33),
+    (8, 2048, 515), (9, 136, 129), (15, 1000, 64), (16, 512, 2048), (17, 512, 2048), (17, 8, 1), (31, 264, 77), (33, 64, 128),
+    (64, 1024, 63), (77, 512, 512), (100, 2000, 1001), (127, 1024, 127), (128, 64, 256), (129, 128, 257), (255, 640, 513),
+    (300, 320, 129), (513, 72, 640), (1001, 512, 300), (4000, 256, 130), (2, 32, 20001), (700, 2048, 2051), (130, 4104, 70),
+    (20000, 64, 24),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_shapes(sc, shape, dtype):
+    import torch
+    x, w, b, r = tensors(torch, dtype, *shape)
+    check(torch, run(torch, sc, x, w, b, r, sc.SC_ACT_NONE, dtype), x, w, b, r, sc.SC_ACT_NONE, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("act", [ref.ACT_NONE, ref.ACT_RELU, ref.ACT_GELU, ref.ACT_SILU])
+@pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("shape", [(3, 256, 130), (140, 256, 200), (700, 128, 515)])
+def test_epilogues(sc, shape, bias, residual, act, dtype):
+    import torch
+    x, w, b, r = tensors(torch, dtype, *shape, seed=1, bias=bias, residual=residual)
+    if b is not None:
+        b *= 3   # arguments of the activations from -10 to 10
+    check(torch, run(torch, sc, x, w, b, r, act, dtype), x, w, b, r, act, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(3, 128, 50), (16, 256, 100), (200, 128, 131), (513, 512, 264)])
+@pytest.mark.parametrize("pad", [8, 40])
+def test_strides(sc, shape, pad, dtype):
+    """Rows inside wider ones (a fused projection), y at an odd address and pitch, guard bytes around y."""
+    import torch
+    rows, Cin, Cout = shape
+    x, w, b, r = tensors(torch, dtype, *shape, seed=2)
+    xw, ww = torch.full((rows, Cin + pad), float("nan"), dtype=x.dtype, device="cuda"), \
+        torch.full((Cout, Cin + pad), float("nan"), dtype=x.dtype, device="cuda")
+    xw[:, 8:8 + Cin], ww[:, :Cin] = x, w
+    for off, pitch in ((0, Cout + 8), (1, Cout + 3)):
+        buf = torch.full((rows * pitch + 16,), 7.0, dtype=x.dtype, device="cuda")
+        rbuf = torch.full((rows * pitch + 16,), 7.0, dtype=x.dtype, device="cuda")
+        view = buf[off:off + rows * pitch].view(rows, pitch)
+        rbuf[off:off + rows * pitch].view(rows, pitch)[:, :Cout] = r
+        sc.check(sc.linear_fwd(xw[0, 8:], ww, b, view, rows, Cin, Cout, 0, dtype,
+                               residual=rbuf[off:], strides=(Cin + pad, Cin + pad, pitch, pitch)), "linear_fwd")
+        sc.check(sc.sc_last_device_status())
+        check(torch, view[:, :Cout], x, w, b, r, 0, dtype)
+        view[:, :Cout] = 7.0
+        assert (buf == 7.0).all(), "something outside y was written"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(4, 256, 512), (300, 256, 515)])
+def test_residual_in_place_and_shared(sc, shape, dtype):
+    import torch
+    rows, Cin, Cout = shape
+    x, w, b, r = tensors(torch, dtype, *shape, seed=3)
+    y = r.clone()
+    sc.check(sc.linear_fwd(x, w, b, y, rows, Cin, Cout, 0, dtype, residual=y), "linear_fwd")
+    check(torch, y, x, w, b, r, 0, dtype)
+    y = torch.empty_like(r)
+    sc.check(sc.linear_fwd(x, w, b, y, rows, Cin, Cout, sc.SC_ACT_SILU, dtype, residual=r,
+                           strides=(Cin, Cin, Cout, 0)), "linear_fwd")
+    check(torch, y, x, w, b, r[:1].expand(rows, -1), sc.SC_ACT_SILU, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [2, 40])
+def test_not_finite(sc, rows, dtype):
+    """An infinity or NaN reaches the outputs of its row (x) or column (w), and no others."""
+    import torch
+    x, w, b, r = tensors(torch, dtype, rows, 256, 140, seed=4)
+    clean = run(torch, sc, x, w, b, r, sc.SC_ACT_RELU, dtype)
+    x[1, 100] = float("nan")
+    w[9, 30] = float("inf")
+    y = run(torch, sc, x, w, b, r, sc.SC_ACT_NONE, dtype)
+    assert y[1].isnan().all()
+    col = y[:, 9]
+    want = torch.where(x[:, 30] > 0, float("inf"), float("-inf")).to(col.dtype)
+    assert (col[0] == want[0]) and (col[2:] == want[2:]).all() and col[1].isnan()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[1], keep[:, 9] = False, False
+    again = run(torch, sc, x, w, b, r, sc.SC_ACT_RELU, dtype)
+    assert torch.equal(again[keep], clean[keep])
+    assert again[1].isnan().all()   # a NaN passes the activation
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [3, 100])
+@pytest.mark.parametrize("big", [3e38, 1e-30])
+def test_ends_of_fp32(sc, rows, big):
+    """Values above bf16's largest, and products near fp32's smallest."""
+    import torch
+    x, w, b, r = tensors(torch, F32, rows, 64, 40, seed=5, bias=False, residual=False)
+    if big > 1:
+        x = torch.where(torch.arange(64, device="cuda") == 5, big * torch.sign(x), 0 * x)
+        x[:, 5] *= 1.13   # 3.39e38: between bf16's largest and fp32's
+        w = w.clamp(-1, 1)
+    else:
+        x, w = x * 1e-20, w * 1e-8
+    y = run(torch, sc, x, w, None, None, 0, F32)
+    want, mag, a = ref.linear(x, w, None, None, 0)
+    assert ((y.double() - want).abs() <= ref.linear_bound(want, mag, a, 64, False)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(4, 512, 700), (200, 1024, 300), (1500, 512, 1100)])
+def test_streams_graph_and_same_bits(sc, shape, dtype):
+    """Two streams at once, a captured call replayed on other inputs, and the same bits every time."""
+    import torch
+    x, w, b, r = tensors(torch, dtype, *shape, seed=6)
+    first = run(torch, sc, x, w, b, r, sc.SC_ACT_GELU, dtype)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [torch.empty_like(first) for _ in range(12)]
+    torch.cuda.synchronize()
+    for i, y in enumerate(outs):
+        sc.check(sc.linear_fwd(x, w, b, y, *x.shape, w.shape[0], sc.SC_ACT_GELU, dtype, residual=r,
+                               stream=streams[i % 3]), "linear_fwd")
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, first) for y in outs)
+    y, z, xin = torch.empty_like(first), torch.empty_like(first), torch.zeros_like(x)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph, out in zip(graphs, (y, z)):   # two graphs, each with its own temporary buffers
+        with torch.cuda.graph(graph):
+            sc.check(sc.linear_fwd(xin, w, b, out, *x.shape, w.shape[0], sc.SC_ACT_GELU, dtype, residual=r), "linear_fwd")
+    xin.copy_(x)
+    torch.cuda.synchronize()
+    for graph, s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, first) and torch.equal(z, first)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,rows", [(F32, 2), (BF16, 2), (BF16, 40)])
+def test_offsets_beyond_32_bits(sc, dtype, rows):
+    """The last row of x, w and y lies more than 2^31 elements behind the first."""
+    import torch
+    Cin, Cout = 64, 24
+    x, w, b, r = tensors(torch, dtype, rows, Cin, Cout, seed=7)
+    big = ((1 << 31) // (rows - 1) + 8192) // 64 * 64
+    buf = torch.empty(big * (rows - 1) + 128, dtype=x.dtype, device="cuda")
+    for i in range(rows):
+        buf[i * big:i * big + Cin] = x[i]
+        buf[i * big + Cin:i * big + Cin + Cout] = 7.0
+    y = buf[Cin:]
+    sc.check(sc.linear_fwd(buf, w, b, y, rows, Cin, Cout, 0, dtype, residual=r, strides=(big, Cin, big, Cout)), "linear_fwd")
+    sc.check(sc.sc_last_device_status())
+    got = torch.stack([y[i * big:i * big + Cout] for i in range(rows)])
+    check(torch, got, x, w, b, r, 0, dtype)
+
+
+A, B, C, D_ = 1 << 20, 1 << 24, 1 << 28, 1 << 32   # addresses, 16-byte aligned, never dereferenced
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(x=None), scl.SC_ERR_NULL), (dict(w=None), scl.SC_ERR_NULL), (dict(y=None), scl.SC_ERR_NULL),
+    (dict(rows=0), scl.SC_ERR_SHAPE), (dict(Cin=-8), scl.SC_ERR_SHAPE), (dict(Cout=0), scl.SC_ERR_SHAPE),
+    (dict(rows=(1 << 30) + 1), scl.SC_ERR_SHAPE), (dict(rows=1 << 30, Cin=1 << 30), scl.SC_ERR_SHAPE),
+    (dict(Cin=12), scl.SC_ERR_UNSUPPORTED), (dict(act=4), scl.SC_ERR_UNSUPPORTED), (dict(act=-1), scl.SC_ERR_UNSUPPORTED),
+    (dict(dtype=2), scl.SC_ERR_UNSUPPORTED), (dict(x=A + 8), scl.SC_ERR_ALIGN), (dict(w=B + 4), scl.SC_ERR_ALIGN),
+    (dict(y=C + 2), scl.SC_ERR_ALIGN), (dict(b=D_ + 2), scl.SC_ERR_ALIGN), (dict(residual=D_ + 2), scl.SC_ERR_ALIGN),
+    (dict(strides=(66, 64, 32, 32)), scl.SC_ERR_ALIGN), (dict(strides=(64, 70, 32, 32)), scl.SC_ERR_ALIGN),
+    (dict(strides=(0, 64, 32, 32)), scl.SC_ERR_UNSUPPORTED), (dict(strides=(64, 56, 32, 32)), scl.SC_ERR_UNSUPPORTED),
+    (dict(strides=(-64, 64, 32, 32)), scl.SC_ERR_SHAPE), (dict(strides=(64, 64, 32, -1), residual=D_), scl.SC_ERR_SHAPE),
+    (dict(strides=(1 << 60, 64, 32, 32)), scl.SC_ERR_SHAPE),
+    (dict(strides=(64, 64, 31, 32)), scl.SC_ERR_ALIAS), (dict(strides=(64, 64, 0, 32)), scl.SC_ERR_ALIAS),
+    (dict(y=A + 64), scl.SC_ERR_ALIAS), (dict(y=B), scl.SC_ERR_ALIAS), (dict(y=C, b=C + 16), scl.SC_ERR_ALIAS),
+    (dict(residual=C + 4), scl.SC_ERR_ALIAS), (dict(residual=C, strides=(64, 64, 32, 40)), scl.SC_ERR_ALIAS),
+    (dict(residual=C, strides=(64, 64, 32, 0)), scl.SC_ERR_ALIAS),
+])
+def test_refusals(change, expect):
+    a = dict(x=A, w=B, b=None, y=C, rows=5, Cin=64, Cout=32, act=0, dtype=F32, residual=None, strides=None)
+    a.update(change)
+    rc = scl.linear_fwd(a["x"], a["w"], a["b"], a["y"], a["rows"], a["Cin"], a["Cout"], a["act"], a["dtype"],
+                        residual=a["residual"], strides=a["strides"], stream=0)
+    assert rc == expect, scl.sc_status_string(rc)
+
+
+@pytest.mark.parametrize("act", [scl.SC_ACT_GELU, scl.SC_ACT_SILU])
+def test_convolutions_take_no_other_activation(act):
+    assert scl.conv2d_fwd(A, B, None, C, 1, 8, 8, 8, 8, 1, 1, scl.SC_NHWC, act, stream=0) == scl.SC_ERR_UNSUPPORTED
