@@ -19,7 +19,16 @@ struct LinearArgs {
     int rows, Cin, Cout, act;
     long long xs, ws, ys, rs;   // row strides in elements
 };
-cudaError_t launch_linear(const LinearArgs &a, bool bf16, cudaStream_t st);
+// Up to 16 rows (linear_rows.cu).
+cudaError_t launch_linear_rows(const LinearArgs &a, bool bf16, cudaStream_t st);
+// More: tensor cores (linear_tc.cu).  drop_copy >= 0 leaves that stage's copies
+// of every CTA un-issued so that the bounded wait for them expires (tests of the
+// device-status path); timeout_ns bounds each wait.
+struct LinearTest {
+    int drop_copy = -1;
+    unsigned long long timeout_ns = 1000000000ull;
+};
+cudaError_t launch_linear_tc(const LinearArgs &a, bool bf16, cudaStream_t st, const LinearTest &test = LinearTest());
 
 // One norm: kind as sc_norm_kind.
 struct NormArgs {

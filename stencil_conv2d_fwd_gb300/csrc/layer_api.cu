@@ -84,7 +84,9 @@ int linear_fwd(const void *x, const void *w, const float *b, const void *residua
         const Region rr = rows_region(residual, rows, Cout, a.rs, es);
         if (!same_rows(ry, rr) && sc::may_overlap(ry, rr)) return SC_ERR_ALIAS;
     }
-    return sc::from_cuda(sc::launch_linear(a, dtype == SC_BF16, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool bf16 = dtype == SC_BF16;
+    return sc::from_cuda(rows <= 16 ? sc::launch_linear_rows(a, bf16, st) : sc::launch_linear_tc(a, bf16, st));
 }
 
 int residual_norm_fwd(const void *x, const void *residual, void *sum, void *y, int rows, int C, const sc_norm *post,

@@ -1,0 +1,54 @@
+// What the kernels of linear_fwd share: activations, and loads and stores of
+// both element types.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "layer.h"
+
+namespace sc {
+
+// act as sc_act; a NaN stays one.
+__device__ __forceinline__ float activate(float v, int act)
+{
+    if (act == 1) return v < 0.f ? 0.f : v;
+    if (act == 2) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    if (act == 3) return v / (1.f + expf(-v));
+    return v;
+}
+__device__ __forceinline__ void activate32(float (&v)[32], int act)
+{
+    if (act == 0) return;
+    if (act == 1) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], 1);
+    } else if (act == 2) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], 2);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], 3);
+    }
+}
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+}  // namespace sc

@@ -2,21 +2,11 @@
 #include <cuda_bf16.h>
 
 #include "layer.h"
+#include "linear.cuh"
 
 namespace sc {
 
 namespace {
-
-template <class T>
-__device__ __forceinline__ float as_float(T v) { return (float)v; }
-
-__device__ __forceinline__ float activate(float v, int act)
-{
-    if (act == 1) return v < 0.f ? 0.f : v;
-    if (act == 2) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    if (act == 3) return v / (1.f + expf(-v));
-    return v;
-}
 
 template <class T>
 __global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a)
@@ -52,7 +42,7 @@ __global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a)
 
 }  // namespace
 
-cudaError_t launch_linear(const LinearArgs &a, bool bf16, cudaStream_t st)
+cudaError_t launch_linear_rows(const LinearArgs &a, bool bf16, cudaStream_t st)
 {
     const long long x = ((long long)a.Cout + 63) / 64, y = ((long long)a.rows + 63) / 64;
     if (y > 65535) return cudaErrorInvalidConfiguration;
