@@ -489,13 +489,16 @@ int kv_quantize_fwd(const sc_quant_states *k, const sc_quant_states *v, const in
  *   floats, 4-byte aligned.  Everything else as in cross_attention_fwd; what
  *   states that are not valid hold, and the scales of blocks without a valid
  *   state, have no effect.
- * Codes are multiplied as they are; the scales enter the fp32 scores and, in
- * fp32, the sums of weights times codes.  fp32 queries and weights are taken to
+ * Codes are multiplied as they are; the scales enter in fp32.
+ * Up to 16 rows a key head (Tq * Hq / Hkv): fp32 queries and weights are taken to
  * 22 bits, in two planes of fp16 (queries with a power of two for each row); a
  * query with an infinity or NaN gives NaN.  With bf16 tensors each weight is
- * rounded to fp16 where it multiplies a code (a relative error up to 2^-11),
- * and the output is rounded once (to nearest even).  A weight below 2^-28 of the
- * largest one among its 16 or 32 neighbours keeps 2^-39 of that.
+ * rounded to fp16 where it multiplies a code (a relative error up to 2^-11).  A
+ * weight below 2^-28 of the largest one among its 16 or 32 neighbours keeps 2^-39
+ * of that.
+ * More rows: as in cross_attention_fwd, but that it is a weight times its state's
+ * scale that is rounded to bf16, or taken in three planes.
+ * The output is rounded once (to nearest even).
  * Supported: D % 16 == 0, D <= 128; block 16, 32, 64 or 128; otherwise as
  * cross_attention_fwd.  Returns SC_OK or a negative sc_status.
  */

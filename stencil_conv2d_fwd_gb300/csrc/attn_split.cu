@@ -14,6 +14,7 @@
 
 #include "attn.h"
 #include "launch.h"
+#include "layer.h"
 
 namespace sc {
 
@@ -36,19 +37,17 @@ struct SplitArgs {
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitArgs a)
+__device__ __forceinline__ void split_part(const SplitPart &p, int D8)
 {
-    pdl_trigger();   // the attention kernel may be set up; its copies wait for this grid's end
-    const SplitPart &p = a.p[blockIdx.y];
     const long long stride = (long long)gridDim.x * kSplitThreads;
     for (long long e = (long long)blockIdx.x * kSplitThreads + threadIdx.x; e < p.chunks; e += stride) {
-        const long long row = e / a.D8;
-        const int c = (int)(e - row * a.D8);
+        const long long row = e / D8;
+        const int c = (int)(e - row * D8);
         const long long nt = row / p.H;
         const int h = (int)(row - nt * p.H), n = (int)(nt / p.T), t = (int)(nt - (long long)n * p.T);
         const long long at = n * p.s.n + t * p.s.t + h * p.s.h + c * 8;
         const long long orow = (((long long)n * (p.H / p.G) + h / p.G) * p.T + t) * p.G + h % p.G;
-        uint32_t *dst = p.y + (orow * a.D8 + c) * 4;
+        uint32_t *dst = p.y + (orow * D8 + c) * 4;
         if constexpr (BF16) {
             *reinterpret_cast<uint4 *>(dst) =
                 *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) + at);
@@ -79,6 +78,120 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitAr
     }
 }
 
+template <bool BF16>
+__global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitArgs a)
+{
+    pdl_trigger();   // the attention kernel may be set up; its copies wait for this grid's end
+    split_part<BF16>(a.p[blockIdx.y], a.D8);
+}
+
+// 8-bit states for the tensor cores: codes as bf16, which holds every one exactly
+// (0 for states that are not valid), and the factor of each 16 keys, which lie in
+// one block:
+//   keys    |scale of the block| * scale * log2 e, at least fp32's smallest normal number (so that it times
+//           minus infinity, the score of a key that is not valid, is not NaN); a negative scale turns the codes
+//   values  the block's scale
+// Groups without a valid state get that smallest number and 0, whatever their scale
+// is.  Bound by memory: a byte read and two written an element.
+struct ExpandArgs {
+    AttnQ8Args a;
+    SplitPart q;                 // chunks 0: not copied
+    int D8;
+    uint32_t *k, *v;
+    float *k_factor, *v_factor;
+    int groups;
+    long long rows;              // N * Hkv * Tk
+    float scale;                 // scale log2 e
+};
+
+template <bool E4M3>
+__device__ __forceinline__ uint32_t pair_to_bf16(uint32_t two)   // the two low bytes
+{
+    if constexpr (E4M3) {
+        uint32_t h;
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(h) : "r"(two));
+        float lo, hi;
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.f32.f16 %0, l;\ncvt.f32.f16 %1, h;\n}\n" : "=f"(lo), "=f"(hi) : "r"(h));
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&b);
+    } else {
+        // 2^23 + (x + 128) in fp32, less 2^23 + 128: exact, and its upper half is the bf16
+        const uint32_t u = two ^ 0x8080u;
+        const float lo = __uint_as_float(0x4b000000u | (u & 0xffu)) - 8388736.f;
+        const float hi = __uint_as_float(0x4b000000u | (u >> 8 & 0xffu)) - 8388736.f;
+        return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+    }
+}
+
+template <bool BF16, bool E4M3>
+__global__ void __launch_bounds__(kSplitThreads) attn_expand_kernel(const ExpandArgs x)
+{
+    pdl_trigger();   // the attention kernel may be set up; its copies wait for this grid's end
+    if (blockIdx.y == 3) {
+        split_part<BF16>(x.q, x.D8);
+        return;
+    }
+    const AttnQ8Args &a = x.a;
+    const long long stride = (long long)gridDim.x * kSplitThreads, first = (long long)blockIdx.x * kSplitThreads + threadIdx.x;
+    auto length = [&](int n) { return a.k_len ? max(0, min(a.Tk, a.k_len[n])) : a.Tk; };
+    if (blockIdx.y == 2) {
+        const long long all = (long long)a.N * a.Hkv * x.groups;
+        for (long long e = first; e < all; e += stride) {
+            const long long nh = e / x.groups;
+            const int grp = (int)(e - nh * x.groups), n = (int)(nh / a.Hkv);
+            const int t0 = grp * 16, t1 = min(t0 + 16, length(n));
+            bool any = t0 < t1;
+            if (any && a.key_mask) {
+                any = false;
+                for (int t = t0; t < t1; ++t) any |= a.key_mask[(long long)n * a.Tk + t] != 0;
+            }
+            float kf = 0x1p-126f, vf = 0.f;
+            if (any) {
+                const long long at = nh * a.blocks + (t0 >> a.log2_block);
+                kf = fabsf(a.k_scale[at]) * x.scale;
+                if (kf < 0x1p-126f) kf = 0x1p-126f;   // (a NaN stays)
+                vf = a.v_scale[at];
+            }
+            x.k_factor[e] = kf;
+            x.v_factor[e] = vf;
+        }
+        return;
+    }
+    const bool value = blockIdx.y == 1;
+    const unsigned char *src = static_cast<const unsigned char *>(value ? a.v : a.k);
+    const HeadStrides &s = value ? a.vs : a.ks;
+    uint32_t *dst = value ? x.v : x.k;
+    const int chunks = a.D / 16;
+    const long long all = x.rows * chunks;
+    for (long long e = first; e < all; e += stride) {
+        const long long row = e / chunks, nh = row / a.Tk;
+        const int c = (int)(e - row * chunks), t = (int)(row - nh * a.Tk), n = (int)(nh / a.Hkv), h = (int)(nh - (long long)n * a.Hkv);
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t sign = 0;
+        const bool on = t < length(n) && (!a.key_mask || a.key_mask[(long long)n * a.Tk + t] != 0);
+        if (on) {
+            w = __ldg(reinterpret_cast<const uint4 *>(src + n * s.n + t * s.t + h * s.h + c * 16));
+            if (!value && a.k_scale[nh * a.blocks + (t >> a.log2_block)] < 0.f) sign = 0x80008000u;
+        }
+        const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+        uint32_t y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[2 * i] = on ? pair_to_bf16<E4M3>(b[i] & 0xffffu) ^ sign : 0u;
+            y[2 * i + 1] = on ? pair_to_bf16<E4M3>(b[i] >> 16) ^ sign : 0u;
+        }
+        uint4 *out = reinterpret_cast<uint4 *>(dst + e * 8);
+        out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+}
+
+SplitPart split_part_of(const void *x, void *y, const HeadStrides &s, int N, int T, int H, int G, int D)
+{
+    const long long rows = (long long)N * T * H;
+    return SplitPart{x, static_cast<uint32_t *>(y), rows * D / 2, s, T, H, G, rows * (D / 8)};
+}
+
 }  // namespace
 
 cudaError_t launch_attn_split(const AttnArgs &a, bool bf16, void *const (&planes)[3], cudaStream_t st)
@@ -89,17 +202,8 @@ cudaError_t launch_attn_split(const AttnArgs &a, bool bf16, void *const (&planes
     const HeadStrides hs[3] = {a.qs, a.ks, a.vs};
     long long most = 0;
     for (int i = 0; i < 3; ++i) {
-        SplitPart &p = s.p[i];
-        p.x = x[i];
-        p.y = static_cast<uint32_t *>(planes[i]);
-        p.s = hs[i];
-        p.T = i ? a.Tk : a.Tq;
-        p.H = i ? a.Hkv : a.Hq;
-        p.G = i ? 1 : a.G;
-        const long long rows = (long long)a.N * p.T * p.H;
-        p.chunks = rows * s.D8;
-        p.plane_words = rows * a.D / 2;
-        if (p.chunks > most) most = p.chunks;
+        s.p[i] = split_part_of(x[i], planes[i], hs[i], a.N, i ? a.Tk : a.Tq, i ? a.Hkv : a.Hq, i ? 1 : a.G, a.D);
+        if (s.p[i].chunks > most) most = s.p[i].chunks;
     }
     long long blocks = (most + kSplitThreads - 1) / kSplitThreads;
     const long long cap = 16LL * device_sm_count();
@@ -108,6 +212,40 @@ cudaError_t launch_attn_split(const AttnArgs &a, bool bf16, void *const (&planes
         attn_split_kernel<true><<<dim3((unsigned)blocks, 3), kSplitThreads, 0, st>>>(s);
     else
         attn_split_kernel<false><<<dim3((unsigned)blocks, 3), kSplitThreads, 0, st>>>(s);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_expand(const AttnQ8Args &a, bool bf16, bool e4m3, void *q, void *k, void *v, float *k_factor, float *v_factor,
+                               int groups, cudaStream_t st)
+{
+    ExpandArgs x;
+    x.a = a;
+    x.D8 = a.D / 8;
+    x.q = q ? split_part_of(a.q, q, a.qs, a.N, a.Tq, a.Hq, a.G, a.D) : SplitPart{};
+    x.k = static_cast<uint32_t *>(k);
+    x.v = static_cast<uint32_t *>(v);
+    x.k_factor = k_factor;
+    x.v_factor = v_factor;
+    x.groups = groups;
+    x.rows = (long long)a.N * a.Hkv * a.Tk;
+    x.scale = a.scale * kLog2e;
+    long long most = x.rows * (a.D / 16);
+    if (x.q.chunks > most) most = x.q.chunks;
+    long long blocks = (most + kSplitThreads - 1) / kSplitThreads;
+    const long long cap = 16LL * device_sm_count();
+    if (blocks > cap) blocks = cap;
+    const dim3 grid((unsigned)blocks, q ? 4 : 3);
+    if (bf16) {
+        if (e4m3)
+            attn_expand_kernel<true, true><<<grid, kSplitThreads, 0, st>>>(x);
+        else
+            attn_expand_kernel<true, false><<<grid, kSplitThreads, 0, st>>>(x);
+    } else {
+        if (e4m3)
+            attn_expand_kernel<false, true><<<grid, kSplitThreads, 0, st>>>(x);
+        else
+            attn_expand_kernel<false, false><<<grid, kSplitThreads, 0, st>>>(x);
+    }
     return cudaGetLastError();
 }
 

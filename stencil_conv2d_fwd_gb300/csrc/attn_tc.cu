@@ -69,6 +69,7 @@
 
 #include "attn.h"
 #include "launch.h"
+#include "layer.h"
 #include "tc_common.cuh"
 
 namespace sc {
@@ -99,7 +100,11 @@ struct Geom {
     int units;            // CTAs' row units of it: pairs of row tiles, or row tiles
     int tb, gb, gblocks;  // tokens and group heads of a row tile; blocks of gb heads
     int splits;           // CTAs that share a row unit's keys
-    bool packed;          // q, k and v are the workspace's copies (attn_split.cu)
+    bool packed;          // q is the workspace's copy (attn_split.cu)
+    bool behind;          // k and v, or q, are written by the launch before
+    // 8-bit states: factors of 16 keys each, [N * Hkv][groups] (attn_split.cu)
+    const float *k_factor, *v_factor;
+    int groups;
     int k_axes[2], v_axes[2];        // whether the maps' (h, n) are axes (1), or shared by all (0)
 };
 
@@ -224,7 +229,7 @@ constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t DESC_LO_K = 1u << 16;
 constexpr uint32_t desc_lo_v(int key_tile) { return (uint32_t)(key_tile * 128 >> 4) << 16; }
 
-template <bool PAIR>
+template <bool PAIR, bool Q8>
 struct Shared {
     // barriers of one arrival (`empty`: of the MMA warp and, where value rows
     // are cleared, the two clearing warps), of the two clearing warps, and of a
@@ -233,6 +238,7 @@ struct Shared {
     uint64_t vclean[VC];
     uint64_t p_full[2][2];
     uint32_t words[2][2][4];           // valid bits of a key tile, per stream, two tiles deep
+    float factors[Q8 ? 2 : 1][Q8 ? 2 : 1][Q8 ? 16 : 1];   // 8-bit states: a key tile's factors of keys, then of values
     float m[PAIR ? 1 : TILE], l[PAIR ? 1 : TILE];   // stream 1's, at the end
     uint16_t tiles[LIST];              // the share's key tiles that have a valid state
     uint8_t any[LIST];                 // whether a tile has one
@@ -250,10 +256,10 @@ constexpr int q_region()
     return (PAIR ? 2 * PL : (PL > 2 ? PL : 2)) * (DP / 64) * BLK;   // a multiple of 1024
 }
 
-template <int DP, int PL, bool PAIR>
+template <int DP, int PL, bool PAIR, bool Q8>
 constexpr int ring_slots()
 {
-    const int n = ((int)SMEM_CAP - q_region<DP, PL, PAIR>() - (int)sizeof(Shared<PAIR>)) / (DP / 64 * key_tile<DP, PL>() * 128);
+    const int n = ((int)SMEM_CAP - q_region<DP, PL, PAIR>() - (int)sizeof(Shared<PAIR, Q8>)) / (DP / 64 * key_tile<DP, PL>() * 128);
     return n < MAX_SLOTS ? n : MAX_SLOTS;
 }
 
@@ -264,7 +270,10 @@ struct Bool {
 
 // PL operand planes: 1 (bf16 tensors), or 3 (fp32 tensors split into three
 // bf16 planes, see attn_split.cu).
-template <int DP, int PL, bool PAIR>
+// Q8: 8-bit states.  Keys and values are one plane of codes, exact in bf16
+// (attn_split.cu), and the scales enter the scores and the weights in fp32, 16
+// keys at a time.
+template <int DP, int PL, bool PAIR, bool Q8>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const AttnArgs a,
@@ -273,11 +282,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int DB = DP / 64;                 // 64-column blocks of a head
     constexpr int QT = PAIR ? 2 : 1;            // row tiles
     constexpr int KT = key_tile<DP, PL>();
+    constexpr int KPL = Q8 ? 1 : PL;            // planes of keys and values
+    constexpr int KG = KT / 16;                 // groups of keys with one scale
     constexpr int KBLK = KT * 128;              // bytes of a key tile's rows of 64 bf16
     constexpr int SLOT = DB * KBLK;
-    constexpr int SLOTS = ring_slots<DP, PL, PAIR>();
+    constexpr int SLOTS = ring_slots<DP, PL, PAIR, Q8>();
     extern __shared__ __align__(1024) unsigned char dyn[];
-    Shared<PAIR> &sh = *reinterpret_cast<Shared<PAIR> *>(dyn + q_region<DP, PL, PAIR>() + SLOTS * SLOT);
+    Shared<PAIR, Q8> &sh = *reinterpret_cast<Shared<PAIR, Q8> *>(dyn + q_region<DP, PL, PAIR>() + SLOTS * SLOT);
 
     // (the shuffle makes the warp's number, and all that follows from it, uniform)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -332,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int tile = seq < l0 ? seq : (s >= both ? nt - l0 + s - both : (value ? s / 2 : l0 + s / 2));
         const int *ax = value ? g.v_axes : g.k_axes;
         const int key0 = tile_key(tile);
-        for (int p = PL - 1; p >= 0; --p, ++issued) {   // the smallest plane first
+        for (int p = KPL - 1; p >= 0; --p, ++issued) {   // the smallest plane first
             const uint32_t slot = issued % SLOTS, round = issued / SLOTS;
             const uint32_t bar = smem_u32(&sh.full[slot]);
             if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
@@ -345,14 +356,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
 
     if (warp == 8) {
-        const int release = mb || len < a.Tk ? 3 : 1;   // arrivals of `empty`: 3 where value rows are cleared (`ragged` below)
+        const int release = !Q8 && (mb || len < a.Tk) ? 3 : 1;   // arrivals of `empty`: 3 where value rows are cleared (`ragged` below)
         for (int i = lane; i < BARS; i += 32)
             mbar_init(smem_u32(&sh.full[0]) + 8 * i,
                       i < BARS_ONE ? (i >= MAX_SLOTS && i < 2 * MAX_SLOTS ? release : 1) : (i < BARS_TWO ? 2 : 4));
         if (lane == 0) sh.abort = 0;
         fence_mbar_init();
         __syncwarp();
-        if (g.packed) pdl_wait();   // the copies read what the launch before has written
+        if (g.behind) pdl_wait();   // the copies read what the launch before has written
         if (lane == 0 && nt > 0) {
             // row tiles: tokens and heads past the end read as zero
             mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(QT * PL * DB * g.gb * g.tb * 128));
@@ -405,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncthreads();
         nt = sh.count;
     }
-    const bool ragged = mb || len < a.Tk;
+    const bool ragged = !Q8 && (mb || len < a.Tk);   // (expanded codes of states that are not valid are 0)
     constexpr int P1 = KT, P2 = DP == 64 ? KT / 2 : KT + KT / 2, TO = 256 - DP;   // columns of a stream
     auto p_plane = [](int p) { return p == 0 ? 0 : (p == 1 ? P1 : P2); };
 
@@ -427,7 +438,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // S of stream i from the key tile whose first plane is ring entry c
                 auto mma_s = [&](int i, uint32_t c, bool release) {
 #pragma unroll
-                    for (int pk = PL - 1; pk >= 0; --pk, ++c) {
+                    for (int pk = KPL - 1; pk >= 0; --pk, ++c) {
                         const uint32_t slot = c % SLOTS;
                         wait(sh.full[slot], (c / SLOTS) & 1);
                         tc::fence_after_sync();
@@ -440,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 if (k * 16 < a.D)
                                     mma_ss(one, tmem + i * 256, qb + ((k >> 2) * BLK + (k & 3) * 32) / 16, DESC_HI,
                                            kb + ((k >> 2) * KBLK + (k & 3) * 32) / 16, DESC_HI, idesc_s,
-                                           pk != PL - 1 || pq != PL - 1 - pk || k > 0);
+                                           pk != KPL - 1 || pq != PL - 1 - pk || k > 0);
                         }
                         if (release) mma_commit(one, smem_u32(&sh.empty[slot]));
                     }
@@ -455,8 +466,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (part == 0 && ragged) wait(sh.vclean[j % VC], (j / VC) & 1);
                         tc::fence_after_sync();
 #pragma unroll
-                        for (int pv = PL - 1; pv >= 0; --pv) {
-                            const uint32_t e = c + (PL - 1 - pv), slot = e % SLOTS;
+                        for (int pv = KPL - 1; pv >= 0; --pv) {
+                            const uint32_t e = c + (KPL - 1 - pv), slot = e % SLOTS;
                             if (part == 0) {
                                 wait(sh.full[slot], (e / SLOTS) & 1);
                                 tc::fence_after_sync();
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 for (int k = part * KT / 32; k < (part + 1) * KT / 32; ++k)
                                     mma_ts(one, tmem + i * 256 + TO, tmem + i * 256 + p_plane(pp) + k * 8, vb + k * 128,
                                            DESC_HI, idesc_v,
-                                           pv != PL - 1 || pp != PL - 1 - pv || k > 0 || (PL == 1 && use > 0));
+                                           pv != KPL - 1 || pp != PL - 1 - pv || k > 0 || (PL == 1 && use > 0));
                             if (part == 1 && release) mma_commit(one, smem_u32(&sh.empty[slot]));
                         }
                     }
@@ -477,26 +488,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if constexpr (PAIR) {
                     mma_s(0, 0, false);
                     mma_s(1, 0, true);
-                    uint32_t c = PL;
+                    uint32_t c = KPL;
                     for (int j = 0; j < nt; ++j) {
                         const bool more = j + 1 < nt;
                         mma_v(0, c, j, j, false, !more);
-                        if (more) mma_s(0, c + PL, false);
+                        if (more) mma_s(0, c + KPL, false);
                         mma_v(1, c, j, j, true, !more);
-                        if (more) mma_s(1, c + PL, true);
-                        c += more ? 2 * PL : PL;
+                        if (more) mma_s(1, c + KPL, true);
+                        c += more ? 2 * KPL : KPL;
                     }
                 } else {
                     mma_s(0, 0, true);
-                    if (nt > 1) mma_s(1, PL, true);
-                    uint32_t c = nt > 1 ? 2 * PL : PL;
+                    if (nt > 1) mma_s(1, KPL, true);
+                    uint32_t c = nt > 1 ? 2 * KPL : KPL;
                     for (int j = 0; j < nt; ++j) {
                         const bool more = j + 2 < nt;
                         mma_v(j & 1, c, j, j >> 1, true, !more);
-                        c += PL;
+                        c += KPL;
                         if (more) {
                             mma_s(j & 1, c, true);
-                            c += PL;
+                            c += KPL;
                         }
                     }
                 }
@@ -580,6 +591,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             return key < len ? (int)mb[key] : 0;
         };
         int next = mb ? mask_byte(PAIR ? 0 : i) : 0;
+        // 8-bit states: this thread's factor of key tile j
+        auto factor = [&](int j) {
+            if (j >= nt || row >= 2 * KG) return 0.f;
+            const float *f = row < KG ? g.k_factor : g.v_factor;
+            return __ldg(f + (long long)nh * g.groups + tile_key(j) / 16 + row % KG);
+        };
+        if (Q8 && g.behind) pdl_wait();   // the factors are the launch before's
+        float next_factor = Q8 ? factor(PAIR ? 0 : i) : 0.f;
         // half of a key tile's P is in tensor memory
         auto hand_over = [&](int part) {
             tmem_wait_st();
@@ -601,16 +620,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int key0 = tile_key(j);
             uint32_t w[KW];
             bool masked = key0 + KT > len;
+            if constexpr (Q8) {
+                if (row < 2 * KG) sh.factors[i][use & 1][row] = next_factor;
+                next_factor = factor(j + step);
+            }
             if (mb) {
                 // one key per thread, a word per warp; the next tile's byte is
                 // read a tile ahead (its latency was a third of a masked tile's time)
                 const uint32_t word = __ballot_sync(0xffffffffu, next != 0);
                 next = mask_byte(j + step);
                 if (lane == 0) sh.words[i][use & 1][warp & 3] = word;
+            }
+            if (mb || Q8) {
                 if (i == 0)
                     named_sync<1, 128>();
                 else
                     named_sync<2, 128>();
+            }
+            if (mb) {
                 uint32_t all = ~0u;
 #pragma unroll
                 for (int e = 0; e < KW; ++e) {
@@ -625,6 +652,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                     w[e] = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
                 }
             }
+            // the factor of 16 keys' scores, and of their weights
+            float kf[Q8 ? KG : 1], vf[Q8 ? KG : 1];
+            if constexpr (Q8) {
+#pragma unroll
+                for (int e = 0; e < KG; ++e) {
+                    kf[e] = sh.factors[i][use & 1][e];
+                    vf[e] = sh.factors[i][use & 1][KG + e];
+                }
+            }
+            auto key_factor = [&](int k) { return Q8 ? kf[Q8 ? k / 16 : 0] : c; };   // of key k of the tile
             wait(sh.s_full[i], use & 1);
             tc::fence_after_sync();
             if constexpr (PL == 1) {
@@ -648,7 +685,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                         mx[e] = max3(mx[e], __uint_as_float(s[e][k]), __uint_as_float(s[e][k + 1]));
                     mx[e] = fmaxf(mx[e], __uint_as_float(s[e][31]));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                if constexpr (Q8) {
+                    top = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < KG; ++e) {
+                        float z = max3(__uint_as_float(s[e / 2][e % 2 * 16]), __uint_as_float(s[e / 2][e % 2 * 16 + 1]),
+                                       __uint_as_float(s[e / 2][e % 2 * 16 + 2]));
+#pragma unroll
+                        for (int k = 3; k < 15; k += 2)
+                            z = max3(z, __uint_as_float(s[e / 2][e % 2 * 16 + k]), __uint_as_float(s[e / 2][e % 2 * 16 + k + 1]));
+                        top = fmaxf(top, fmaxf(z, __uint_as_float(s[e / 2][e % 2 * 16 + 15])) * kf[Q8 ? e : 0]);
+                    }
+                }
                 const bool grow = top - m > GROW;   // false where both are -infinity
                 float f = 1.f;
                 if (grow) {
@@ -675,10 +724,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t p[32];
 #pragma unroll
                     for (int k = 0; k < 64; k += 2) {
-                        const float x = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32]), c, -mc));
-                        const float y = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32 + 1]), c, -mc));
+                        const float f = key_factor(e * 32 + k);
+                        float x = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32]), f, -mc));
+                        float y = ex2(fmaf(__uint_as_float(s[e + k / 32][k % 32 + 1]), f, -mc));
                         sum[e + k / 32] += x;
                         sum[(e + k / 32) ^ 1] += y;
+                        if constexpr (Q8) {
+                            x *= vf[Q8 ? (e * 32 + k) / 16 : 0];
+                            y *= vf[Q8 ? (e * 32 + k) / 16 : 0];
+                        }
                         p[k / 2] = tc::pack_bf16(x, y);
                     }
                     tmem_st32(ts + e * 16, p);
@@ -690,21 +744,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // plane is written over it
                 constexpr int HOLD = DP == 64 ? KW / 2 : 0;
                 uint32_t hold[HOLD > 0 ? HOLD : 1][32];
-                float mx[2] = {-INFINITY, -INFINITY};
+                float mx[2] = {-INFINITY, -INFINITY}, top8 = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < KW; ++e) {
                     uint32_t s[32];
                     load_scores(e, s, w[e], masked);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
+                        if (Q8 && k % 16 == 0) mx[0] = mx[1] = -INFINITY;
                         mx[k / 2 & 1] = max3(mx[k / 2 & 1], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                        if (Q8 && k % 16 == 14) top8 = fmaxf(top8, fmaxf(mx[0], mx[1]) * key_factor(32 * e + k));
                         if (e >= KW - HOLD) {
                             hold[e - (KW - HOLD)][k] = s[k];
                             hold[e - (KW - HOLD)][k + 1] = s[k + 1];
                         }
                     }
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]) * c, m);
+                const float top = fmaxf(Q8 ? top8 : fmaxf(mx[0], mx[1]) * c, m);
                 const float mc = top == -INFINITY ? 0.f : top, f = ex2(m - mc);   // 1 or less; 0 at the first scores
                 m = top;
                 // the last tile's product, relative to the last maximum; it is
@@ -736,10 +792,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                         uint32_t p0[8], p1[8], p2[8];
 #pragma unroll
                         for (int k = 0; k < 16; k += 2) {
-                            float x = ex2(fmaf(__uint_as_float(s[q + k]), c, -mc));
-                            float y = ex2(fmaf(__uint_as_float(s[q + k + 1]), c, -mc));
+                            const float kfac = key_factor(32 * e + q + k);
+                            float x = ex2(fmaf(__uint_as_float(s[q + k]), kfac, -mc));
+                            float y = ex2(fmaf(__uint_as_float(s[q + k + 1]), kfac, -mc));
                             sum[0] += x;
                             sum[1] += y;
+                            if constexpr (Q8) {
+                                x *= vf[Q8 ? (32 * e + q) / 16 : 0];
+                                y *= vf[Q8 ? (32 * e + q) / 16 : 0];
+                            }
                             p0[k / 2] = tc::pack_bf16(x, y);
                             x -= __uint_as_float(p0[k / 2] << 16);
                             y -= __uint_as_float(p0[k / 2] & 0xffff0000u);
@@ -944,23 +1005,23 @@ struct Maps {
     CUtensorMap q, k, v, out;
 };
 
-template <int DP, int PL, bool PAIR>
+template <int DP, int PL, bool PAIR, bool Q8>
 cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPartials &part, cudaStream_t st,
                    const TcTest &test)
 {
-    constexpr int SMEM = q_region<DP, PL, PAIR>() + ring_slots<DP, PL, PAIR>() * (DP / 64 * key_tile<DP, PL>() * 128) +
-                         (int)sizeof(Shared<PAIR>);
+    constexpr int SMEM = q_region<DP, PL, PAIR>() + ring_slots<DP, PL, PAIR, Q8>() * (DP / 64 * key_tile<DP, PL>() * 128) +
+                         (int)sizeof(Shared<PAIR, Q8>);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     static KernelCache cache;
-    e = ensure_dynamic_smem(cache, dev, attn_tc_kernel<DP, PL, PAIR>, SMEM);
+    e = ensure_dynamic_smem(cache, dev, attn_tc_kernel<DP, PL, PAIR, Q8>, SMEM);
     if (e != cudaSuccess) return e;
     // the register split is of REGS_LAUNCH a thread: with fewer, a warp would wait for registers that never come
     static const int regs = [] {
         cudaFuncAttributes fa = {};
-        return cudaFuncGetAttributes(&fa, attn_tc_kernel<DP, PL, PAIR>) == cudaSuccess ? fa.numRegs : 0;
+        return cudaFuncGetAttributes(&fa, attn_tc_kernel<DP, PL, PAIR, Q8>) == cudaSuccess ? fa.numRegs : 0;
     }();
     if (regs != REGS_LAUNCH) return cudaErrorNotSupported;
     int *status = device_status_ptr();
@@ -977,13 +1038,28 @@ cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPa
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = g.packed ? 1 : 0;   // behind attn_split's launch
-    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, PL, PAIR>, m.q, m.k, m.v, m.out, a, g, part, status, test);
+    cfg.numAttrs = g.behind ? 1 : 0;   // behind attn_split's or attn_expand's launch
+    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, PL, PAIR, Q8>, m.q, m.k, m.v, m.out, a, g, part, status, test);
 }
 
 }  // namespace at
 
-cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, const TcTest &test)
+namespace at {
+
+template <bool Q8>
+cudaError_t dispatch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPartials &part, bool bf16, bool pair, cudaStream_t st,
+                     const TcTest &test)
+{
+    if (bf16 && a.D <= 64)
+        return pair ? launch<64, 1, true, Q8>(a, g, m, part, st, test) : launch<64, 1, false, Q8>(a, g, m, part, st, test);
+    if (bf16) return pair ? launch<128, 1, true, Q8>(a, g, m, part, st, test) : launch<128, 1, false, Q8>(a, g, m, part, st, test);
+    if (a.D <= 64) return pair ? launch<64, 3, true, Q8>(a, g, m, part, st, test) : launch<64, 3, false, Q8>(a, g, m, part, st, test);
+    return launch<128, 3, false, Q8>(a, g, m, part, st, test);
+}
+
+}  // namespace at
+
+static cudaError_t attn_tc(const AttnArgs &a, const AttnQ8Args *q8, bool e4m3, bool bf16, cudaStream_t st, const TcTest &test)
 {
     if (!at::encoder()) return cudaErrorNotSupported;
     at::Geom g = {};
@@ -1014,52 +1090,60 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, const 
     // the TMA copies can address them: axes of the row and key tiles that are
     // not shared
     g.packed = !bf16 || (a.G > 1 && a.qs.h == 0) || (a.Tq > 1 && a.qs.t == 0) || (a.Hkv > 1 && a.qs.h == 0) ||
-               (a.N > 1 && a.qs.n == 0) || (a.Tk > 1 && (a.ks.t == 0 || a.vs.t == 0));
-    const int planes = bf16 ? 1 : 3;
+               (a.N > 1 && a.qs.n == 0) || (!q8 && a.Tk > 1 && (a.ks.t == 0 || a.vs.t == 0));
+    // 8-bit states are expanded to one plane of bf16 codes
+    const bool kv_packed = g.packed || q8;
+    g.behind = kv_packed;
+    const int planes = bf16 ? 1 : 3, kv_planes = q8 ? 1 : planes;
     const long long rows = (long long)a.N * a.Hq * a.Tq, keys = (long long)a.N * a.Hkv * a.Tk;
-    g.k_axes[0] = g.packed || a.ks.h != 0;
-    g.k_axes[1] = g.packed || a.ks.n != 0;
-    g.v_axes[0] = g.packed || a.vs.h != 0;
-    g.v_axes[1] = g.packed || a.vs.n != 0;
+    g.k_axes[0] = kv_packed || a.ks.h != 0;
+    g.k_axes[1] = kv_packed || a.ks.n != 0;
+    g.v_axes[0] = kv_packed || a.vs.h != 0;
+    g.v_axes[1] = kv_packed || a.vs.n != 0;
 
     // workspace: partial results, and the packed tensors
     auto pad = [](size_t b) { return (b + 255) & ~(size_t)255; };
     const size_t po = g.splits > 1 ? pad((size_t)g.splits * rows * a.D * 4) : 0;
     const size_t pml = g.splits > 1 ? pad((size_t)g.splits * rows * sizeof(float2)) : 0;
     const size_t pq = g.packed ? pad((size_t)rows * a.D * 2 * planes) : 0;
-    const size_t pk = g.packed ? pad((size_t)keys * a.D * 2 * planes) : 0;
+    const size_t pk = kv_packed ? pad((size_t)keys * a.D * 2 * kv_planes) : 0;
+    // a key tile's groups, whole
+    g.groups = (int)((a.Tk + 127LL) / 128 * 8);
+    const size_t pf = q8 ? pad((size_t)a.N * a.Hkv * g.groups * 4) : 0;
     char *ws = nullptr;
     if (po + pml + pq + pk > 0) {
-        const cudaError_t e = workspace_alloc(reinterpret_cast<void **>(&ws), po + pml + pq + 2 * pk, st);
+        const cudaError_t e = workspace_alloc(reinterpret_cast<void **>(&ws), po + pml + pq + 2 * pk + 2 * pf, st);
         if (e != cudaSuccess) return e;
     }
     AttnPartials part{nullptr, nullptr, 0};
     if (g.splits > 1) part = AttnPartials{reinterpret_cast<float *>(ws), reinterpret_cast<float2 *>(ws + po), g.splits};
     void *const plane[3] = {ws + po + pml, ws + po + pml + pq, ws + po + pml + pq + pk};
+    float *const factor[2] = {reinterpret_cast<float *>(ws + po + pml + pq + 2 * pk),
+                              reinterpret_cast<float *>(ws + po + pml + pq + 2 * pk + pf)};
+    g.k_factor = factor[0];
+    g.v_factor = factor[1];
 
     at::Maps m;
     std::memset(&m, 0, sizeof(m));
     bool ok;
-    const void *k = g.packed ? plane[1] : a.k, *v = g.packed ? plane[2] : a.v;
+    const long long dq = a.D * 2LL;
     if (g.packed) {
-        const long long size[4] = {a.G, a.Tq, (long long)a.N * a.Hkv, planes}, d = a.D * 2LL;
-        const long long stride[4] = {d, d * a.G, d * a.G * a.Tq, d * rows};
+        const long long size[4] = {a.G, a.Tq, (long long)a.N * a.Hkv, planes};
+        const long long stride[4] = {dq, dq * a.G, dq * a.G * a.Tq, dq * rows};
         ok = at::encode_map(&m.q, true, plane[0], a.D, size, stride, g.gb, g.tb);
-        const long long ksize[4] = {a.Tk, a.Hkv, a.N, planes};
-        const long long kstride[4] = {d, d * a.Tk, d * a.Tk * a.Hkv, d * keys};
-        ok = ok && at::encode_map(&m.k, true, k, a.D, ksize, kstride, kt, 1) &&
-             at::encode_map(&m.v, true, v, a.D, ksize, kstride, kt, 1);
     } else {
         const long long size[4] = {a.G, a.Tq, a.Hkv, a.N};
         const long long stride[4] = {a.qs.h * 2, a.qs.t * 2, a.qs.h * a.G * 2, a.qs.n * 2};
         ok = at::encode_map(&m.q, true, a.q, a.D, size, stride, g.gb, g.tb);
+    }
+    for (int i = 0; i < 2; ++i) {
+        const HeadStrides &s = i ? a.vs : a.ks;
         // a shared axis (stride 0) of the keys or values is one coordinate of the map
-        for (int i = 0; i < 2; ++i) {
-            const HeadStrides &s = i ? a.vs : a.ks;
-            const long long ksize[4] = {a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1};
-            const long long kstride[4] = {s.t * 2, s.h * 2, s.n * 2, 16};
-            ok = ok && at::encode_map(i ? &m.v : &m.k, true, i ? v : k, a.D, ksize, kstride, kt, 1);
-        }
+        const long long packed[2][4] = {{a.Tk, a.Hkv, a.N, kv_planes}, {dq, dq * a.Tk, dq * a.Tk * a.Hkv, dq * keys}};
+        const long long lying[2][4] = {{a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1}, {s.t * 2, s.h * 2, s.n * 2, 16}};
+        const void *p = kv_packed ? plane[1 + i] : (i ? a.v : a.k);
+        const auto &map = kv_packed ? packed : lying;
+        ok = ok && at::encode_map(i ? &m.v : &m.k, true, p, a.D, map[0], map[1], kt, 1);
     }
     if (part.parts > 0) {
         const long long size[4] = {a.G, a.Tq, (long long)a.N * a.Hkv, g.splits}, d = a.D * 4LL;
@@ -1072,23 +1156,28 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, const 
         ok = ok && at::encode_map(&m.out, bf16, a.out, a.D, size, stride, g.gb, g.tb);
     }
     cudaError_t e = ok ? cudaSuccess : cudaErrorInvalidValue;
-    if (e == cudaSuccess && g.packed) e = launch_attn_split(a, bf16, plane, st);
-    if (e == cudaSuccess) {
-        if (bf16 && a.D <= 64)
-            e = pair ? at::launch<64, 1, true>(a, g, m, part, st, test) : at::launch<64, 1, false>(a, g, m, part, st, test);
-        else if (bf16)
-            e = pair ? at::launch<128, 1, true>(a, g, m, part, st, test) : at::launch<128, 1, false>(a, g, m, part, st, test);
-        else if (a.D <= 64)
-            e = pair ? at::launch<64, 3, true>(a, g, m, part, st, test) : at::launch<64, 3, false>(a, g, m, part, st, test);
-        else
-            e = at::launch<128, 3, false>(a, g, m, part, st, test);
-    }
+    if (e == cudaSuccess && q8)
+        e = launch_attn_expand(*q8, bf16, e4m3, g.packed ? plane[0] : nullptr, plane[1], plane[2], factor[0], factor[1], g.groups, st);
+    else if (e == cudaSuccess && g.packed)
+        e = launch_attn_split(a, bf16, plane, st);
+    if (e == cudaSuccess)
+        e = q8 ? at::dispatch<true>(a, g, m, part, bf16, pair, st, test) : at::dispatch<false>(a, g, m, part, bf16, pair, st, test);
     if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st);
     if (ws) {
         const cudaError_t ef = workspace_free(ws, st);
         if (e == cudaSuccess) e = ef;
     }
     return e;
+}
+
+cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, const TcTest &test)
+{
+    return attn_tc(a, nullptr, false, bf16, st, test);
+}
+
+cudaError_t launch_attn_tc_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st)
+{
+    return attn_tc(a, &a, e4m3, bf16, st, TcTest());
 }
 
 }  // namespace sc

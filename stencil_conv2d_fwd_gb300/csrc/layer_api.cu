@@ -216,7 +216,10 @@ int cross_attention_q8_fwd(const void *q, const void *k, const float *k_scale, c
         const Region rl{reinterpret_cast<uintptr_t>(lse), 1, 1, 1, lse_bytes, 0, lse_bytes, 0};
         if (sc::flat_overlap(rl, k_scale, bytes) || sc::flat_overlap(rl, v_scale, bytes)) return SC_ERR_ALIAS;
     }
-    return sc::from_cuda(sc::launch_attn_q8(a, dtype == SC_BF16, code == SC_CODE_E4M3, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool bf16 = dtype == SC_BF16, e4m3 = code == SC_CODE_E4M3;
+    const long long rows = (long long)Tq * a.G;
+    return sc::from_cuda(rows > 16 ? sc::launch_attn_tc_q8(a, bf16, e4m3, st) : sc::launch_attn_q8(a, bf16, e4m3, st));
 }
 
 }  // extern "C"
