@@ -18,8 +18,9 @@
 // one's scale.  A group's products start from zero and enter the sums in fp32 with
 // its scale, so that the MMAs' cut-off sums stay short.
 //
-// Keys and values come through a ring of each warp's own in shared memory,
-// copied there asynchronously, 16 bytes a lane, and go to the operands in
+// Keys and values come through a ring of each warp's own in shared memory, copied
+// there by TMA, one instruction for 16 or 32 rows (by 16-byte copies of the lanes
+// their addresses took a fifth of all instructions), and go to the operands in
 // registers 8 or 16 bytes at a time:
 //   * the order of summation over d is free, so lane (g, t) takes whole 16-byte
 //     chunks of its key as its share of k, and Q is laid out to match;
@@ -28,6 +29,12 @@
 // Integer codes become fp16 in 2.5 (K) or 3 (V) instructions for two: a byte
 // with its sign bit turned is the low byte of 1024 + 128 + x in fp16, from which
 // 1152 is taken.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+#include <mutex>
+
 #include "attn_rows.cuh"
 #include "launch.h"
 #include "layer.h"
@@ -84,76 +91,74 @@ __host__ __device__ constexpr int byte_of(int i) { return E4M3 ? i : (i == 1 ? 2
 template <bool E4M3>
 __host__ __device__ constexpr uint32_t gather(int i) { return E4M3 ? (i ? 0x7362u : 0x5140u) : (i ? 0x7632u : 0x5410u); }
 
-// A warp's ring: STAGES steps of KP keys and as many values, rows of DP bytes,
-// and the step's scales.  A row's 16-byte chunks lie so that the reads below
-// fall in different bank groups: key r of eight in place 2 (r mod 4) + r / 4, chunk
-// c of places of 128 bytes at c XOR 4 (place mod 2); value r in place r, chunk c
-// at c XOR 2 (r mod 4), of 64-byte rows c XOR 2 (r / 2 mod 2).
+// Tensor maps of the codes, [n][h][t][D], boxes of DP bytes of a step's rows,
+// swizzled; n_axis and h_axis are 0 where all share one (stride 0).
+struct Q8Maps {
+    CUtensorMap k, v;
+};
+struct Q8Axes {
+    int k_n, k_h, v_n, v_h;
+    int *status;
+};
+
+__device__ __forceinline__ void load_states(uint32_t dst, const CUtensorMap *m, int t, int h, int n, uint32_t bar)
+{
+    tma_load_4d(dst, m, 0, t, h, n, bar);
+}
+
+constexpr unsigned long long kWaitNs = 1000000000ull;
+
+// A warp's ring: STAGES steps of KP keys and as many values, rows of DP bytes
+// swizzled by the copy: 16-byte chunk c of row r lies at c XOR (r / 2 mod 4) of a
+// 64-byte row, at c XOR (r mod 8) of a 128-byte one.
 template <int DP>
 struct Q8Ring {
     static constexpr int KP = DP == 64 ? 32 : 16;
     static constexpr int GROUPS = KP / 16;              // of 16 keys, each with one scale
     static constexpr int CH = DP / 16;                  // chunks of a row
-    static constexpr int RPL = 32 / CH;                 // rows of a warp-wide copy
     static constexpr int STAGES = 3;
-    static constexpr int TILE = KP * CH;                // in 16-byte units
-    static constexpr int STAGE = 2 * TILE + 1;          // and one unit of scales: ks, ks, vs, vs
+    static constexpr int TILE = KP * DP;                // bytes
     static constexpr int STEP = kRowWarps * KP;         // keys from a step to the next
+    static constexpr uint32_t FULL = KP == 32 ? 0xffffffffu : 0xffffu;
 
-    const unsigned char *kp, *vp, *kbase, *vbase;
-    const float *scale;      // lanes 0 to 3: the scales of their part of a step
-    long long kst, vst;
+    const float *ks, *vs;
     const unsigned char *mb;
-    uint4 *ring;
-    int len, key0, steps, lane, crow, cch, log2_block, use, fill;
-    bool cact;
-    uint32_t ok[STAGES - 1];   // valid bits of the steps under way
-    int byte;                  // the mask's byte of the step after those
+    uint64_t *bars;
+    unsigned char *ring;
+    int len, key0, steps, lane, log2_block, byte, kn, kh, vn, vh;
+    float scales[2 * GROUPS];   // of the step after the current one
 
     __device__ __forceinline__ int mask_byte(int step) const
     {
         const int key = key0 + step * STEP + lane;
-        return step < steps && lane < KP && key < len ? (mb ? (int)mb[key] : 1) : 0;
+        return step < steps && lane < KP && key < len ? (int)mb[key] : 0;
     }
-    static __device__ __forceinline__ int key_at(int r, int c)
+    static __device__ __forceinline__ int chunk_at(int r, int c) { return r * CH + (CH == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)); }
+    __device__ __forceinline__ void copy(int step, const Q8Maps &m)
     {
-        const int place = (r & ~7) | ((r & 3) << 1) | ((r >> 2) & 1);
-        return place * CH + (CH == 8 ? c ^ (4 * (place & 1)) : c);
+        if (step >= steps || lane != 0) return;
+        const int slot = step % STAGES, t = key0 + step * STEP;
+        const uint32_t bar = smem_u32(bars + slot), at = smem_u32(ring + slot * 2 * TILE);
+        mbar_arrive_expect_tx(bar, 2 * TILE);
+        load_states(at, &m.k, t, kh, kn, bar);
+        load_states(at + TILE, &m.v, t, vh, vn, bar);
     }
-    static __device__ __forceinline__ int value_at(int r, int c)
+    // The scales of a step's groups: a group past the valid length takes the last
+    // valid state's, which is not used.
+    __device__ __forceinline__ void next_scales(int step)
     {
-        return r * CH + (CH == 8 ? c ^ (2 * (r & 3)) : c ^ (2 * ((r >> 1) & 1)));
-    }
-    __device__ __forceinline__ void copy(int step, uint32_t valid)
-    {
-        uint4 *k = ring + fill * STAGE, *v = k + TILE;
 #pragma unroll
-        for (int i = 0; i < KP / RPL; ++i) {
-            const int row = crow + i * RPL;
-            const bool on = cact && (valid >> row & 1u);
-            cp_async16(smem_u32(k + key_at(row, cch)), on ? kp + i * RPL * kst : kbase, on ? 16 : 0);
+        for (int i = 0; i < GROUPS; ++i) {
+            const int at = step < steps ? min(key0 + step * STEP + 16 * i, len - 1) >> log2_block : 0;
+            scales[i] = __ldg(ks + at);
+            scales[GROUPS + i] = __ldg(vs + at);
         }
-#pragma unroll
-        for (int i = 0; i < KP / RPL; ++i) {
-            const int row = crow + i * RPL;
-            const bool on = cact && (valid >> row & 1u);
-            cp_async16(smem_u32(v + value_at(row, cch)), on ? vp + i * RPL * vst : vbase, on ? 16 : 0);
-        }
-        // scales of groups without a valid state are not read
-        if (lane < 2 * GROUPS) {
-            const int grp = lane % GROUPS;
-            const bool on = (valid >> (16 * grp) & 0xffffu) != 0;
-            const int blk = (key0 + step * STEP + 16 * grp) >> log2_block;
-            cp_async4(smem_u32(reinterpret_cast<float *>(k + 2 * TILE) + lane), scale + (on ? blk : 0), on ? 4 : 0);
-        }
-        cp_async_commit();
-        kp += STEP * kst;
-        vp += STEP * vst;
-        fill = fill + 1 == STAGES ? 0 : fill + 1;
     }
-    __device__ __forceinline__ void begin(uint4 *memory, const AttnQ8Args &a, int n, int h, int split, int splits, int warp)
+    __device__ __forceinline__ void begin(unsigned char *memory, uint64_t *barriers, const AttnQ8Args &a, const Q8Maps &m,
+                                          const Q8Axes &ax, int n, int h, int split, int splits, int warp)
     {
         ring = memory;
+        bars = barriers;
         lane = threadIdx.x & 31;
         len = a.Tk;
         if (a.k_len) len = max(0, min(len, a.k_len[n]));
@@ -162,43 +167,36 @@ struct Q8Ring {
         steps = p1 - p0 > warp ? (p1 - p0 - warp + kRowWarps - 1) / kRowWarps : 0;
         key0 = (p0 + warp) * KP;
         mb = a.key_mask ? a.key_mask + (long long)n * a.Tk : nullptr;
-        crow = lane / CH;
-        cch = lane % CH;
-        cact = cch * 16 < a.D;
-        kst = a.ks.t;
-        vst = a.vs.t;
-        kbase = static_cast<const unsigned char *>(a.k);
-        vbase = static_cast<const unsigned char *>(a.v);
-        kp = kbase + n * a.ks.n + h * a.ks.h + (long long)(key0 + crow) * kst + (cact ? cch * 16 : 0);
-        vp = vbase + n * a.vs.n + h * a.vs.h + (long long)(key0 + crow) * vst + (cact ? cch * 16 : 0);
-        scale = (lane < GROUPS ? a.k_scale : a.v_scale) + ((long long)n * a.Hkv + h) * a.blocks;
-        log2_block = a.log2_block;
-        use = fill = 0;
-        int b[STAGES - 1];
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) b[i] = mask_byte(i);
-        byte = mask_byte(STAGES - 1);
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) {
-            ok[i] = __ballot_sync(0xffffffffu, b[i] != 0);
-            copy(i, ok[i]);
+        kn = n * ax.k_n, kh = h * ax.k_h, vn = n * ax.v_n, vh = h * ax.v_h;
+        if (lane == 0) {
+            for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(bars + i), 1);
+            fence_mbar_init();
         }
-    }
-    // Waits for the step's stage and asks for the one STAGES - 1 ahead, which goes
-    // where the last one was read (the warp's barrier is behind those reads).
-    __device__ __forceinline__ const uint4 *next(int step, uint32_t &valid)
-    {
-        cp_async_wait<STAGES - 2>();
         __syncwarp();
-        valid = ok[0];
 #pragma unroll
-        for (int i = 0; i + 1 < STAGES - 1; ++i) ok[i] = ok[i + 1];
-        ok[STAGES - 2] = __ballot_sync(0xffffffffu, byte != 0);
-        byte = mask_byte(step + STAGES);
-        copy(step + STAGES - 1, ok[STAGES - 2]);
-        const uint4 *s = ring + use * STAGE;
-        use = use + 1 == STAGES ? 0 : use + 1;
-        return s;
+        for (int i = 0; i < STAGES; ++i) copy(i, m);
+        log2_block = a.log2_block;
+        ks = a.k_scale + ((long long)n * a.Hkv + h) * a.blocks;
+        vs = a.v_scale + ((long long)n * a.Hkv + h) * a.blocks;
+        next_scales(0);
+        byte = mb ? mask_byte(0) : 0;
+    }
+    // Waits for a step's stage; valid: its states' bits, sc: its scales.
+    __device__ __forceinline__ const unsigned char *next(int step, uint32_t &valid, float (&sc)[2 * GROUPS], int *status)
+    {
+#pragma unroll
+        for (int i = 0; i < 2 * GROUPS; ++i) sc[i] = scales[i];
+        next_scales(step + 1);
+        if (mb) {
+            valid = __ballot_sync(0xffffffffu, byte != 0);
+            byte = mask_byte(step + 1);
+        } else {
+            const int left = len - (key0 + step * STEP);
+            valid = left >= KP ? FULL : (1u << left) - 1u;
+        }
+        const int slot = step % STAGES;
+        if (!mbar_wait_bounded(smem_u32(bars + slot), (step / STAGES) & 1, kWaitNs)) atomicExch(status, kDeviceTimeout);
+        return ring + slot * 2 * TILE;
     }
 };
 
@@ -207,18 +205,20 @@ struct Q8Ring {
 template <int DP, int R>
 struct Q8Shared {
     union {
-        uint4 ring[kRowWarps][Q8Ring<DP>::STAGE * Q8Ring<DP>::STAGES];
+        unsigned char ring[kRowWarps][2 * Q8Ring<DP>::TILE * Q8Ring<DP>::STAGES];
         WarpSums<R, DP> warps;
     };
     CtaSums<R, DP> ctas;
+    uint64_t bars[kRowWarps][Q8Ring<DP>::STAGES];
 };
 
+constexpr int kCtasPerSm = 1;
 constexpr float kWeightLog2 = 14.f;   // weights are 2^14 P
 
 // T: float or bf16 queries; R: 8 rows, or with bf16 16.
 template <class T, int DP, bool E4M3, int R>
 __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
-    attn_q8_kernel(const AttnQ8Args a, const RowsGeom g, const AttnPartials part)
+    attn_q8_kernel(const AttnQ8Args a, const RowsGeom g, const AttnPartials part, const __grid_constant__ Q8Maps maps, const Q8Axes axes)
 {
     using Ring = Q8Ring<DP>;
     constexpr bool F32 = sizeof(T) == 4;
@@ -226,9 +226,13 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
     constexpr int KC = Ring::CH / 4;     // chunks of a key per lane
     constexpr int NT = DP / 8;           // products of 8 columns of O, one for each of the lane's bytes of a value
     static_assert(!F32 || RH == 1, "fp32: rows 8 to 15 are the second plane");
-    extern __shared__ __align__(128) unsigned char dyn[];
+    extern __shared__ __align__(1024) unsigned char dyn[];
     Q8Shared<DP, R> &sm = *reinterpret_cast<Q8Shared<DP, R> *>(dyn);
 
+    if (smem_u32(dyn) & 1023u) {   // the swizzled tiles need it; there is no static shared memory before them
+        if (threadIdx.x == 0) atomicExch(axes.status, kDeviceTimeout);
+        return;
+    }
     pdl_trigger();   // the join kernel may be set up; it waits for this grid's end
     if (g.cluster > 1) cluster_arrive();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t = lane & 3;
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
     const int rows = a.Tq * a.G;
 
     Ring ring;
-    ring.begin(sm.ring[warp], a, n, h, split, g.splits, warp);
+    ring.begin(sm.ring[warp], sm.bars[warp], a, maps, axes, n, h, split, g.splits, warp);
 
     // the rows' queries times a power of two that puts a row's largest element in
     // [2^12, 2^13); back[] undoes it and carries scale log2 e
@@ -328,20 +332,30 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
 
     for (int step = 0; step < ring.steps; ++step) {
         uint32_t ok;
-        const uint4 *kt = ring.next(step, ok);
-        const uint4 *vt = kt + Ring::TILE;
-        const float *sc = reinterpret_cast<const float *>(kt + 2 * Ring::TILE);
+        float sc[2 * Ring::GROUPS];
+        unsigned char *tile = const_cast<unsigned char *>(ring.next(step, ok, sc, axes.status));
+        const uint4 *kt = reinterpret_cast<const uint4 *>(tile), *vt = reinterpret_cast<const uint4 *>(tile + Ring::TILE);
+        const bool full = ok == Ring::FULL;
+        if (E4M3 && !full) {
+            // values that are not valid: 0, as their weight times NaN is not
+            if (lane < Ring::KP && !(ok >> lane & 1u)) {
+                uint4 *row = reinterpret_cast<uint4 *>(tile + Ring::TILE) + lane * Ring::CH;
+#pragma unroll
+                for (int i = 0; i < Ring::CH; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();   // before the next copy to this place
+            __syncwarp();
+        }
 
         float s[2 * Ring::GROUPS][4];
 #pragma unroll
         for (int i = 0; i < 2 * Ring::GROUPS; ++i) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
-            // column g of the scores is key 8 i + (g / 2) + 4 (g mod 2), in place 8 i + g
-            const int place = 8 * i + gq;
+            // column g of the scores is key 8 i + g
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
-                const uint4 k = kt[place * Ring::CH + (KC == 2 ? (c * 4 + t) ^ (4 * (place & 1)) : t)];
+                const uint4 k = kt[Ring::chunk_at(8 * i + gq, c * 4 + t)];
                 const uint32_t w[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
                 }
             }
         }
-        // scores of row g (and g + 8) for the keys 8 i + t and 8 i + t + 4; top: what
+        // scores of row g (and g + 8) for the keys 8 i + 2 t and 8 i + 2 t + 1; top: what
         // a group's weights are relative to, its largest score less 14
         const bool joint = Ring::GROUPS == 2 && a.log2_block > 4 && (ok >> 16) != 0 && (ok & 0xffffu) != 0;   // one scale
         float top[Ring::GROUPS][RH];
@@ -366,7 +380,8 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
                 for (int e = 0; e < 4; ++e) {
                     float &x = s[2 * i + e / 2][2 * r + e % 2];
                     if constexpr (F32) x += s[2 * i + e / 2][2 + e % 2];
-                    x = (ok >> (16 * i + 8 * (e / 2) + t + 4 * (e % 2)) & 1u) ? x * f : -INFINITY;
+                    x *= f;
+                    if (!full) x = (ok >> (16 * i + 8 * (e / 2) + 2 * t + e % 2) & 1u) ? x : -INFINITY;
                     mx = fmaxf(mx, x);
                 }
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -423,11 +438,11 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
             for (int i = 0; i < Ring::GROUPS; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int r = 16 * i + t + 4 * e;
+                    const int r = 16 * i + 8 * (e / 2) + 2 * t + e % 2;
                     if constexpr (DP == 64)
-                        v[i][e] = reinterpret_cast<const uint2 *>(vt + Ring::value_at(r, gq >> 1))[gq & 1];
+                        v[i][e] = reinterpret_cast<const uint2 *>(vt + Ring::chunk_at(r, gq >> 1))[gq & 1];
                     else
-                        v[i][e] = reinterpret_cast<const uint2 *>(vt + Ring::value_at(r, gq))[c];
+                        v[i][e] = reinterpret_cast<const uint2 *>(vt + Ring::chunk_at(r, gq))[c];
                 }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {   // bytes 2 x and 2 x + 1
@@ -467,9 +482,10 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
                 }
             }
         }
+        __syncwarp();   // the stage has been read
+        ring.copy(step + Ring::STAGES, maps);
     }
-    cp_async_wait<0>();
-    __syncthreads();   // the rings' memory becomes the sums'
+    __syncthreads();   // the rings' memory becomes the sums': every copy has been waited for
 
     // the warp's sums: row g (and g + 8); l over the quad
 #pragma unroll
@@ -489,11 +505,43 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
     finish_rows<T, R, DP>(sm.warps, sm.ctas, a, g, part, nh, row0, split);
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+template <int DP>
+bool encode_map(CUtensorMap *m, const void *p, const HeadStrides &s, const AttnQ8Args &a)
+{
+    // an axis of one element may come with any stride, one of stride 0 has one: the map wants a multiple of 16 above zero
+    const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.Tk, (cuuint64_t)(s.h ? a.Hkv : 1), (cuuint64_t)(s.n ? a.N : 1)};
+    const cuuint64_t strides[3] = {a.Tk > 1 ? (cuuint64_t)s.t : 16, dims[2] > 1 ? (cuuint64_t)s.h : 16, dims[3] > 1 ? (cuuint64_t)s.n : 16};
+    const cuuint32_t box[4] = {DP, Q8Ring<DP>::KP, 1, 1}, one[4] = {1, 1, 1, 1};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     DP == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class T, int DP, bool E4M3, int R>
 cudaError_t launch_q8(const AttnQ8Args &a, cudaStream_t st)
 {
     static KernelCache cache;
-    return launch_rows_kernel(attn_q8_kernel<T, DP, E4M3, R>, cache, a, sizeof(T) == 2, R, (int)sizeof(Q8Shared<DP, R>), st);
+    Q8Axes ax{a.ks.n != 0, a.ks.h != 0, a.vs.n != 0, a.vs.h != 0, device_status_ptr()};
+    if (!ax.status) return cudaErrorInvalidDevice;
+    Q8Maps m;
+    std::memset(&m, 0, sizeof(m));
+    if (!encode_map<DP>(&m.k, a.k, a.ks, a) || !encode_map<DP>(&m.v, a.v, a.vs, a)) return cudaErrorInvalidValue;
+    return launch_rows_kernel(attn_q8_kernel<T, DP, E4M3, R>, cache, a, sizeof(T) == 2, R, (int)sizeof(Q8Shared<DP, R>), st, kCtasPerSm, m,
+                              ax);
 }
 
 template <class T, bool E4M3>
@@ -509,6 +557,7 @@ cudaError_t dispatch(const AttnQ8Args &a, cudaStream_t st)
 
 cudaError_t launch_attn_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st)
 {
+    if (!encoder()) return cudaErrorNotSupported;
     if (bf16) return e4m3 ? dispatch<__nv_bfloat16, true>(a, st) : dispatch<__nv_bfloat16, false>(a, st);
     return e4m3 ? dispatch<float, true>(a, st) : dispatch<float, false>(a, st);
 }

@@ -295,8 +295,11 @@ __device__ __forceinline__ void finish_rows(const WarpSums<R, DP> &sm, CtaSums<R
 //   32 x 4 of 64, four bf16 rows over 3136: 23.7 and 26.3; two CTAs for every SM 27.2, four 33.3
 //   (a CTA's start and end cost what it reads in 1 us)
 //   one of 64, four bf16 rows over 921600: 45.0, two CTAs for every SM 48.1, four 54.9
-template <class K, class A>
-cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const A &a, bool bf16, int R, int smem, cudaStream_t st)
+// per_sm: CTAs for every SM (8-bit states, whose conversion needs more warps than
+// their reading, take two: see attn_q8.cu).
+template <class K, class A, class... More>
+cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const A &a, bool bf16, int R, int smem, cudaStream_t st, int per_sm,
+                               const More &...more)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -309,7 +312,7 @@ cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const A &a, bool bf
     RowsGeom g;
     g.row_blocks = (int)((rows + R - 1) / R);
     const long long blocks = (long long)a.N * a.Hkv * g.row_blocks;
-    const long long want = (device_sm_count() + blocks - 1) / blocks;
+    const long long want = ((long long)per_sm * device_sm_count() + blocks - 1) / blocks;
     const long long most = ((long long)a.Tk + step - 1) / step;
     const long long s = want < most ? want : most;
     if (s <= kMaxCluster || most <= kMaxCluster * 4) {
@@ -342,7 +345,7 @@ cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const A &a, bool bf
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = g.cluster > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, a, g, part);
+    e = cudaLaunchKernelEx(&cfg, kernel, a, g, part, more...);
     if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st);
     if (ws) {
         const cudaError_t ef = workspace_free(ws, st);

@@ -3,16 +3,18 @@
 //   a = max |x| over the block's valid states,  scale = a / top,  code = nearest(top x / a)
 //
 // Bound by memory: 2 or 4 bytes read and one written an element.  A block is
-// read once into registers, four 8-element chunks a thread, its largest value
+// read once into registers, 16 elements a thread, its largest value
 // found as the largest of the magnitudes' bits (so that an infinity or NaN is
 // above every number), and the codes written from the registers.
 // The quotient is x times top / a in fp32, off by less than 2^-22 of itself; where
 // that leaves the code open (a value next to a border between two codes, every
-// 2^13th or so), it is taken in 64 bits, which decides every case: two operands of
-// 24 bits and a border of 8 cannot be closer than 2^-33 to it without lying on it.
+// 2^13th or so of fp32 values, and many bf16 ones, which lie on borders), top x is
+// compared with border times a in exact arithmetic made of fp32 FMAs.  (In 64 bits,
+// whose rate is 1/64 here, bf16 states took 794 us where they now take @@.)
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "divisor.cuh"
 #include "launch.h"
 #include "layer.h"
 
@@ -21,8 +23,12 @@ namespace sc {
 namespace {
 
 constexpr int kQuantThreads = 256;
-constexpr int kChunks = 4;   // of 8 elements, a thread's
+template <class T>
+constexpr int E = 16 / (int)sizeof(T);           // elements of a 16-byte chunk
+template <class T>
+constexpr int kChunks = 16 / E<T>;               // a thread's: 16 elements
 
+// (a warp's access is 512 bytes in a row whatever the type)
 __device__ __forceinline__ uint4 ld16(const void *p)
 {
     uint4 v;
@@ -32,13 +38,12 @@ __device__ __forceinline__ uint4 ld16(const void *p)
     return v;
 }
 
-__device__ __forceinline__ void load8(const float *p, float (&v)[8])
+__device__ __forceinline__ void load_chunk(const float *p, float (&v)[4])
 {
-    const uint4 a = ld16(p), b = ld16(p + 4);
+    const uint4 a = ld16(p);
     v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
+__device__ __forceinline__ void load_chunk(const __nv_bfloat16 *p, float (&v)[8])
 {
     const uint4 a = ld16(p);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -49,6 +54,17 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
     }
 }
 
+// The values of two positive e4m3 codes, added.
+__device__ __forceinline__ float e4m3_sum(uint32_t a, uint32_t b)
+{
+    float x, y;
+    asm("{\n.reg .b16 c, l, h;\n.reg .b32 p;\nmov.b32 {c, l}, %2;\ncvt.rn.f16x2.e4m3x2 p, c;\nmov.b32 {l, h}, p;\n"
+        "cvt.f32.f16 %0, l;\ncvt.f32.f16 %1, h;\n}\n"
+        : "=f"(x), "=f"(y)
+        : "r"(a | b << 8));
+    return x + y;
+}
+
 // Two floats -> two e4m3 codes (nearest, ties to even), `lo` in the low byte.
 __device__ __forceinline__ uint32_t to_e4m3(float lo, float hi)
 {
@@ -57,58 +73,65 @@ __device__ __forceinline__ uint32_t to_e4m3(float lo, float hi)
     return y;
 }
 
-// top x / a, rounded to 24 bits so that a second rounding to fewer bits is the
-// rounding of the quotient itself: to zero, the last bit set where it is inexact.
-__device__ __noinline__ float exact_quotient(float x, float a, float top)
+// The largest of m, |x| and |y|; NaN if one is.
+__device__ __forceinline__ float max_nan(float m, float x, float y)
 {
-    const double q = (double)x * (double)top / (double)a;
-    float f = __double2float_rz(q);
-    if ((double)f != q) f = __uint_as_float(__float_as_uint(f) | 1u);
-    return f;
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(x)), "f"(fabsf(y)));
+    return r;
 }
 
-template <bool E4M3>
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float a, float inv, bool tiny)
+// The sign of n |x| - m a in exact arithmetic, for integers n and m of up to 10 bits
+// and nearly equal products: a product's rounding error is one more FMA, the large
+// parts' difference is exact, and so is that of the errors, which have fewer than
+// ten bits between them.  a is in [1, 2).
+__device__ __forceinline__ float exact_difference(float n, float x, float m, float a)
 {
-    constexpr float top = E4M3 ? 448.f : 127.f;
-    float t[8];
-    uint32_t w[2] = {0u, 0u};
-    bool open = tiny;
+    const float p = n * x, q = m * a;
+    return (p - q) + (fmaf(n, x, -p) - fmaf(m, a, -q));
+}
+
+// The N codes of x / scale, a byte each; inv = top / a.  The quotient's two
+// ends are rounded; where they differ, the border between the two codes decides.
+template <bool E4M3, int N>
+__device__ __forceinline__ uint2 codes(const float (&x)[N], float a, float inv)
+{
+    constexpr float magic = 12582912.f;   // 1.5 * 2^23: the sum with it rounds to an integer, its low byte
+    const float inv0 = inv * (1.f - 0x1p-21f), inv1 = inv * (1.f + 0x1p-21f);
+    uint32_t w[2] = {0u, 0u}, v[2] = {0u, 0u};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = x[j] * inv;
-    if constexpr (E4M3) {
-        uint32_t other = 0;
+    for (int j = 0; j < N; j += 4) {
+        if constexpr (E4M3) {
+            w[j / 4] = __byte_perm(to_e4m3(x[j] * inv0, x[j + 1] * inv0), to_e4m3(x[j + 2] * inv0, x[j + 3] * inv0), 0x5410);
+            v[j / 4] = __byte_perm(to_e4m3(x[j] * inv1, x[j + 1] * inv1), to_e4m3(x[j + 2] * inv1, x[j + 3] * inv1), 0x5410);
+        } else {
+            uint32_t m[4], k[4];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            constexpr float lo = 1.f - 0x1p-21f, hi = 1.f + 0x1p-21f;
-            const uint32_t c = to_e4m3(t[j] * lo, t[j + 1] * lo);
-            other |= c ^ to_e4m3(t[j] * hi, t[j + 1] * hi);
-            w[j / 4] |= c << (8 * (j & 2));
+            for (int i = 0; i < 4; ++i) {
+                m[i] = __float_as_uint(fmaf(x[j + i], inv0, magic));
+                k[i] = __float_as_uint(fmaf(x[j + i], inv1, magic));
+            }
+            w[j / 4] = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
+            v[j / 4] = __byte_perm(__byte_perm(k[0], k[1], 0x0040), __byte_perm(k[2], k[3], 0x0040), 0x5410);
         }
-        open |= other != 0;
-    } else {
-        float near = 1.f;   // distance to the nearest border
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float r = rintf(t[j]);
-            near = fminf(near, fabsf(fabsf(t[j] - r) - 0.5f));
-            w[j / 4] |= ((uint32_t)(int)r & 0xffu) << (8 * (j & 3));
-        }
-        open |= near < 0x1p-14f;
     }
-    if (open) {
-        w[0] = w[1] = 0u;
-#pragma unroll 1
-        for (int j = 0; j < 8; ++j) {
-            float xj = x[0];   // (indexed by a constant, so that x stays in registers)
+    if ((w[0] ^ v[0]) | (w[1] ^ v[1])) {
+        const float unit = __uint_as_float((254u << 23) - (__float_as_uint(a) & 0x7f800000u)), an = a * unit;
 #pragma unroll
-            for (int i = 1; i < 8; ++i) xj = j == i ? x[i] : xj;
-            const float q = exact_quotient(xj, a, top);
-            const uint32_t c = E4M3 ? to_e4m3(q, 0.f) & 0xffu : (uint32_t)(int)rintf(q) & 0xffu;
-            if (j < 4)
-                w[0] |= c << (8 * j);
-            else
-                w[1] |= c << (8 * j - 32);
+        for (int j = 0; j < N; ++j) {
+            const uint32_t shift = 8 * (j & 3);
+            if (!((w[j / 4] ^ v[j / 4]) >> shift & 0xffu)) continue;
+            // w's code is the one nearer to zero, c of the magnitude; the border to the
+            // next one is half the sum of the two
+            if constexpr (E4M3) {
+                const uint32_t c = w[j / 4] >> shift & 0x7fu;
+                const float d = exact_difference(896.f, fabsf(x[j]) * unit, e4m3_sum(c, c + 1), an);
+                if (d > 0.f || (d == 0.f && (c & 1u))) w[j / 4] += 1u << shift;
+            } else {
+                const int c = abs((int)(signed char)(w[j / 4] >> shift & 0xffu));
+                const float d = exact_difference(254.f, fabsf(x[j]) * unit, 2.f * (float)c + 1.f, an);
+                if (d > 0.f || (d == 0.f && (c & 1))) w[j / 4] = (w[j / 4] & ~(0xffu << shift)) | (v[j / 4] & 0xffu << shift);
+            }
         }
     }
     return make_uint2(w[0], w[1]);
@@ -116,52 +139,60 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float a, float inv,
 
 // A unit: one block of one (sequence, head), `threads` of the CTA's.
 struct QuantGeom {
-    int threads;        // of a unit: 32 to 512
+    int threads;        // of a unit: 32 to 1024
+    int log2_threads;
     int per_cta;        // units
-    long long units;    // of a tensor
+    uint32_t units;     // of a tensor
+    Divisor heads, blocks, row_chunks;
 };
 
 template <class T, bool E4M3>
-__global__ void __launch_bounds__(512) kv_quantize_kernel(const QuantArgs a, const QuantGeom g)
+__global__ void __launch_bounds__(1024) kv_quantize_kernel(const QuantArgs a, const QuantGeom g)
 {
-    __shared__ uint32_t largest[16];   // of each warp
+    __shared__ uint32_t largest[32];   // of each warp
     const QuantPart &p = a.part[blockIdx.y];
-    const int tid = threadIdx.x % g.threads, slot = threadIdx.x / g.threads;
-    const long long unit = (long long)blockIdx.x * g.per_cta + slot;
+    const int tid = threadIdx.x & (g.threads - 1), slot = threadIdx.x >> g.log2_threads;
+    const uint32_t unit = blockIdx.x * g.per_cta + slot;
     const bool on = unit < g.units;
-    const int h = on ? (int)(unit % a.H) : 0;
-    const long long nb = on ? unit / a.H : 0;
-    const int n = (int)(nb / a.blocks), b = (int)(nb - (long long)n * a.blocks);
+    const uint32_t nb = on ? g.heads.quotient(unit) : 0u;
+    const int h = on ? (int)(unit - nb * a.H) : 0;
+    const int n = (int)g.blocks.quotient(nb), b = (int)nb - n * a.blocks;
     int len = a.T;
     if (a.k_len) len = max(0, min(len, a.k_len[n]));
-    const int row_chunks = a.D / 8, t0 = b * a.block;
+    const int row_chunks = a.D / E<T>, t0 = b * a.block;
     const int rows = on ? max(0, min(a.block, len - t0)) : 0;
     const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.T + t0 : nullptr;
-    float x[kChunks][8];
-    int row[kChunks], col[kChunks];
-    uint32_t top_bits = 0;
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int c = tid + i * g.threads;
-        row[i] = c / row_chunks;
-        col[i] = (c - row[i] * row_chunks) * 8;
-        if (row[i] >= rows || (mb && mb[row[i]] == 0)) {
-            row[i] = -1;
-            continue;
+    // this thread's chunks: `col` and `row` step by g.threads chunks
+    float x[kChunks<T>][E<T>];
+    const int dr = (int)g.row_chunks.quotient(g.threads), dc = g.threads - dr * row_chunks;
+    const T *xb = static_cast<const T *>(p.x) + n * p.xs.n + (long long)t0 * p.xs.t + h * p.xs.h;
+    unsigned char *cb = p.codes + n * p.cs.n + (long long)t0 * p.cs.t + h * p.cs.h;
+    const int row0 = (int)g.row_chunks.quotient(tid), col0 = tid - row0 * row_chunks;
+    auto next = [&](int &row, int &col) {
+        row += dr;
+        col += dc;
+        if (col >= row_chunks) {
+            col -= row_chunks;
+            ++row;
         }
-        any = true;
-        load8(static_cast<const T *>(p.x) + n * p.xs.n + (long long)(t0 + row[i]) * p.xs.t + h * p.xs.h + col[i], x[i]);
-    }
+    };
+    float top = 0.f;   // a NaN stays
+    uint32_t on_bits = 0;
+    int row = row0, col = col0;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-        if (row[i] >= 0) {
+    for (int i = 0; i < kChunks<T>; ++i, next(row, col))
+        if (row < rows && !(mb && mb[row] == 0)) {
+            on_bits |= 1u << i;
+            load_chunk(xb + row * p.xs.t + col * E<T>, x[i]);
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top_bits = max(top_bits, __float_as_uint(x[i][j]) & 0x7fffffffu);
+    for (int i = 0; i < kChunks<T>; ++i)
+        if (on_bits >> i & 1u) {
+#pragma unroll
+            for (int j = 0; j < E<T>; j += 2) top = max_nan(top, x[i][j], x[i][j + 1]);
         }
     // bit 31: a state is valid
-    top_bits |= any ? 0x80000000u : 0u;
-    uint32_t m = __reduce_max_sync(0xffffffffu, top_bits);
+    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top) | (on_bits ? 0x80000000u : 0u));
     if (g.threads > 32) {
         if ((threadIdx.x & 31) == 0) largest[threadIdx.x >> 5] = m;
         __syncthreads();
@@ -171,19 +202,30 @@ __global__ void __launch_bounds__(512) kv_quantize_kernel(const QuantArgs a, con
     }
     if (!(m >> 31)) return;
     m &= 0x7fffffffu;
-    constexpr float top = E4M3 ? 448.f : 127.f;
+    constexpr float largest_code = E4M3 ? 448.f : 127.f;
     const bool finite = m < 0x7f800000u;
-    const float amax = __uint_as_float(m);
+    float amax = __uint_as_float(m);
     if (tid == 0)
-        p.scale[((long long)n * a.H + h) * a.blocks + b] = finite ? __fdiv_rn(amax, top) : __uint_as_float(0x7fffffffu);
+        p.scale[((long long)n * a.H + h) * a.blocks + b] = finite ? __fdiv_rn(amax, largest_code) : __uint_as_float(0x7fffffffu);
     const bool zero = m == 0 || !finite;
-    const float inv = zero ? 0.f : __fdiv_rn(top, amax);
-    const bool tiny = !zero && amax < 0x1p-100f;   // top / a may not be finite
+    // far from 1 in size, top / a or top x may not be finite: all times a power of two
+    const float move = amax < 0x1p-100f ? 0x1p100f : (amax > 0x1p100f ? 0x1p-60f : 1.f);
+    amax *= move;
+    const float inv = zero ? 0.f : __fdiv_rn(largest_code, amax);
+    row = row0, col = col0;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        if (row[i] < 0) continue;
-        const uint2 w = zero ? make_uint2(0u, 0u) : codes8<E4M3>(x[i], amax, inv, tiny);
-        *reinterpret_cast<uint2 *>(p.codes + n * p.cs.n + (long long)(t0 + row[i]) * p.cs.t + h * p.cs.h + col[i]) = w;
+    for (int i = 0; i < kChunks<T>; ++i, next(row, col)) {
+        if (!(on_bits >> i & 1u)) continue;
+        if (move != 1.f) {
+#pragma unroll
+            for (int j = 0; j < E<T>; ++j) x[i][j] *= move;
+        }
+        const uint2 w = zero ? make_uint2(0u, 0u) : codes<E4M3>(x[i], amax, inv);
+        unsigned char *to = cb + row * p.cs.t + col * E<T>;
+        if constexpr (E<T> == 8)
+            *reinterpret_cast<uint2 *>(to) = w;
+        else
+            *reinterpret_cast<uint32_t *>(to) = w.x;
     }
 }
 
@@ -192,13 +234,19 @@ __global__ void __launch_bounds__(512) kv_quantize_kernel(const QuantArgs a, con
 cudaError_t launch_kv_quantize(const QuantArgs &a, bool bf16, bool e4m3, cudaStream_t st)
 {
     QuantGeom g;
-    const int chunks = a.block * a.D / 8;
     g.threads = 32;
-    while (g.threads * kChunks < chunks) g.threads *= 2;   // at most 512: 128 states of 128
+    while (g.threads * 16 < a.block * a.D) g.threads *= 2;   // at most 1024: 128 states of 128
     g.per_cta = g.threads < kQuantThreads ? kQuantThreads / g.threads : 1;
-    g.units = (long long)a.N * a.blocks * a.H;
-    const long long ctas = (g.units + g.per_cta - 1) / g.per_cta;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    // (2^31 units are 512 GB of codes)
+    const long long units = (long long)a.N * a.blocks * a.H;
+    if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    g.units = (uint32_t)units;
+    g.log2_threads = 5;
+    while (1 << g.log2_threads < g.threads) ++g.log2_threads;
+    g.heads = make_divisor(a.H);
+    g.blocks = make_divisor(a.blocks);
+    g.row_chunks = make_divisor(a.D / (bf16 ? 8 : 4));
+    const long long ctas = (units + g.per_cta - 1) / g.per_cta;
     const dim3 grid((unsigned)ctas, a.parts), block(g.threads * g.per_cta);
     if (bf16) {
         if (e4m3)

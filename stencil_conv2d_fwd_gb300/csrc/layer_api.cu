@@ -11,6 +11,8 @@ namespace {
 using sc::Region;
 
 constexpr int kMaxRows = 1 << 30;
+constexpr int kFewRowsF32 = 64;
+constexpr long long kMaxMapStride = 1LL << 40;   // bytes
 
 // [rows][cols] with a row stride in elements.
 Region rows_region(const void *p, int rows, int cols, long long stride, int esize)
@@ -76,6 +78,8 @@ int linear_fwd(const void *x, const void *w, const float *b, const void *residua
     if (!sc::aligned(x, 16) || !sc::aligned(w, 16) || !sc::aligned(y, es) || !sc::aligned(residual, es) || !sc::aligned(b, 4))
         return SC_ERR_ALIGN;
     if (a.xs % (16 / es) != 0 || a.ws % (16 / es) != 0) return SC_ERR_ALIGN;
+    if (a.xs * es >= kMaxMapStride || a.ws * es >= kMaxMapStride || a.ys * es >= kMaxMapStride || a.rs * es >= kMaxMapStride)
+        return SC_ERR_UNSUPPORTED;
     const Region rx = rows_region(x, rows, Cin, a.xs, es), rw = rows_region(w, Cout, Cin, a.ws, es);
     const Region ry = rows_region(y, rows, Cout, a.ys, es);
     if (!sc::rows_distinct(ry) || sc::may_overlap(ry, rx) || sc::may_overlap(ry, rw) || sc::flat_overlap(ry, b, 4LL * Cout))
@@ -86,7 +90,7 @@ int linear_fwd(const void *x, const void *w, const float *b, const void *residua
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SC_BF16;
-    return sc::from_cuda(rows <= 16 ? sc::launch_linear_rows(a, bf16, st) : sc::launch_linear_tc(a, bf16, st));
+    return sc::from_cuda(rows <= (bf16 ? 16 : kFewRowsF32) ? sc::launch_linear_rows(a, bf16, st) : sc::launch_linear_tc(a, bf16, st));
 }
 
 int residual_norm_fwd(const void *x, const void *residual, void *sum, void *y, int rows, int C, const sc_norm *post,
@@ -203,6 +207,10 @@ int cross_attention_q8_fwd(const void *q, const void *k, const float *k_scale, c
     rc = sc::take_attention(q, k, v, out, lse, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, scale, dtype, 1, strides, a);
     if (rc != SC_OK) return rc;
     if (!sc::aligned(k_scale, 4) || !sc::aligned(v_scale, 4)) return SC_ERR_ALIGN;
+    // a tensor map's strides
+    if (a.ks.n >= kMaxMapStride || a.ks.t >= kMaxMapStride || a.ks.h >= kMaxMapStride || a.vs.n >= kMaxMapStride ||
+        a.vs.t >= kMaxMapStride || a.vs.h >= kMaxMapStride)
+        return SC_ERR_UNSUPPORTED;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.block = block;
@@ -219,7 +227,9 @@ int cross_attention_q8_fwd(const void *q, const void *k, const float *k_scale, c
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SC_BF16, e4m3 = code == SC_CODE_E4M3;
     const long long rows = (long long)Tq * a.G;
-    return sc::from_cuda(rows > 16 ? sc::launch_attn_tc_q8(a, bf16, e4m3, st) : sc::launch_attn_q8(a, bf16, e4m3, st));
+    // (states that share one row by a stride of 0 cannot be copied tile by tile)
+    const bool few = rows <= 16 && (Tk == 1 || (a.ks.t > 0 && a.vs.t > 0));
+    return sc::from_cuda(few ? sc::launch_attn_q8(a, bf16, e4m3, st) : sc::launch_attn_tc_q8(a, bf16, e4m3, st));
 }
 
 }  // extern "C"

@@ -28,6 +28,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "divisor.cuh"
 #include "launch.h"
 #include "layer.h"
 #include "linear.cuh"
@@ -68,7 +69,8 @@ constexpr int smem_bytes() { return stages<CG, BN>() * stage_bytes<CG, BN>() + E
 struct Geom {
     int tiles_m, tiles_n, splits;
     int steps;          // stages of Cin: ceil(Cin / 64)
-    long long items;    // tiles_m * tiles_n * splits
+    int items;          // tiles_m * tiles_n * splits
+    Divisor per_split, per_group, tail_rows, parts;   // tiles; tiles of a group; row tiles of the last group; splits
     int box;            // columns of y that a TMA store takes: 64 (bf16) or 32; 0: rows by the warp
     bool residual_tma;
     float *part;        // splits > 1: [splits][rows][part_ld]
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         return;
     }
     const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;
-    const long long first = blockIdx.x / CG, stride = gridDim.x / CG;
+    const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
     volatile int *abort_flag = &sh.abort;
     auto wait = [&](uint64_t &bar, uint32_t parity) {
@@ -252,17 +254,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     struct Item {
         int m, n, k0, k1, split;
     };
-    auto item = [&](long long i) {
+    // (by multiplications: with divisions the products waited 3 us for each tile)
+    auto item = [&](int i) {
         Item r;
-        const int per = g.tiles_m * g.tiles_n;
-        r.split = (int)(i / per);
-        const int t = (int)(i - (long long)r.split * per);
-        const int grp = t / (GROUP_M * g.tiles_n), in = t - grp * GROUP_M * g.tiles_n;
-        const int rows = min(GROUP_M, g.tiles_m - grp * GROUP_M);
-        r.n = in / rows;
-        r.m = grp * GROUP_M + in - r.n * rows;
-        r.k0 = (int)((long long)g.steps * r.split / g.splits);
-        r.k1 = (int)((long long)g.steps * (r.split + 1) / g.splits);
+        r.split = g.splits == 1 ? 0 : (int)g.per_split.quotient(i);
+        const int t = i - r.split * (int)g.per_split.d;
+        const int grp = (int)g.per_group.quotient(t), in = t - grp * (int)g.per_group.d;
+        const bool tail = (grp + 1) * GROUP_M > g.tiles_m;
+        r.n = tail ? (int)g.tail_rows.quotient(in) : in / GROUP_M;
+        r.m = grp * GROUP_M + in - r.n * (tail ? (int)g.tail_rows.d : GROUP_M);
+        r.k0 = g.splits == 1 ? 0 : (int)g.parts.quotient(g.steps * r.split);
+        r.k1 = g.splits == 1 ? g.steps : (int)g.parts.quotient(g.steps * (r.split + 1));
         return r;
     };
     constexpr int PRODUCTS = F32 ? 6 : 1;
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 8) {
             if (F32) pdl_wait();   // the planes are the launch before's
             if (lane == 0) {
-                for (long long i = first; i < g.items; i += stride) {
+                for (int i = first; i < g.items; i += stride) {
                     const Item it = item(i);
                     const int row = (it.m * CG + rank) * TILE, col = it.n * BN + rank * (BN / CG);
                     for (int c0 = it.k0; c0 < it.k1; c0 += F32 ? KCHUNK : it.k1) {
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp == 9 && rank == 0) {
             const uint32_t one = elect_one();
             uint32_t c = 0, use = 0;   // stages and accumulators used
-            for (long long i = first; i < g.items; i += stride) {
+            for (int i = first; i < g.items; i += stride) {
                 const Item it = item(i);
                 for (int c0 = it.k0; c0 < it.k1; c0 += F32 ? KCHUNK : it.k1, ++use) {
                     const int n = (F32 ? min(c0 + KCHUNK, it.k1) - c0 : it.k1 - c0) * PRODUCTS;
@@ -356,10 +358,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int col_part = COLS == BN ? 0 : part * COLS;
         const bool active = COLS < BN || part == 0;   // tiles of 64 columns: the first four warps
         uint32_t use = 0, loads = 0;
-        for (long long i = first; i < g.items; i += stride) {
+        for (int i = first; i < g.items; i += stride) {
             const Item it = item(i);
             const int row0 = (it.m * CG + rank) * TILE + quad * 32, row = row0 + lane;
             const int col0 = it.n * BN + col_part;
+            // the columns' biases, a lane's each
+            float bias[COLS / 32];
+#pragma unroll
+            for (int j = 0; j < COLS / 32; ++j) {
+                const int col = col0 + j * 32 + lane;
+                bias[j] = a.b && col < a.Cout ? __ldg(a.b + col) : 0.f;
+            }
             float acc[F32 ? COLS : 1];
             auto columns = [&](int at, float (&v)[32]) {   // this row's 32 columns from col0 + at
                 if constexpr (F32) {
@@ -404,14 +413,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 wait(sh.acc_full[use & 1], (use >> 1) & 1);
                 tc::fence_after_sync();
             }
-            // bias, activation; residual and y 128 bytes of 32 rows at a time
-            auto finish = [&](float (&v)[32], int col) {
+            // bias, activation (32 columns from col0 + d)
+            auto finish = [&](float (&v)[32], int d) {
+                if (a.b) {
+                    const float mine = bias[d / 32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, mine, j);
+                }
+                activate32<!F32>(v, a.act);
+            };
+            auto finish_at = [&](float (&v)[32], int d) {   // (d not a constant)
+                float mine = bias[0];
+#pragma unroll
+                for (int j = 1; j < COLS / 32; ++j) mine = d == 32 * j ? bias[j] : mine;
                 if (a.b) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] += col + j < a.Cout ? __ldg(a.b + col + j) : 0.f;
+                    for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, mine, j);
                 }
-                activate32(v, a.act);
+                activate32<!F32>(v, a.act);
             };
+            bool held = !F32;   // the accumulator is not yet released
             if (active && row0 < a.rows && !*abort_flag) {
                 if (g.part) {
                     // fp32 sums of this part of Cin
@@ -434,50 +455,65 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 } else if (g.box) {
+                    // 128 bytes of 32 rows at a time; the last store's reading of the
+                    // staging, or the residual's way there, is beside the arithmetic
                     constexpr int BOX = F32 ? 32 : 64;
 #pragma unroll
                     for (int d = 0; d < COLS; d += BOX) {
                         if (col0 + d >= a.Cout) break;
-                        if (lane == 0) {
+                        if (lane == 0 && g.residual_tma) {
                             bulk_wait_read<0>();
-                            if (g.residual_tma) {
-                                mbar_arrive_expect_tx(smem_u32(&sh.residual[warp]), STG);
-                                load_3d<1>(stg, &mr, col0 + d, row0, 0, smem_u32(&sh.residual[warp]));
-                            }
+                            mbar_arrive_expect_tx(smem_u32(&sh.residual[warp]), STG);
+                            load_3d<1>(stg, &mr, col0 + d, row0, 0, smem_u32(&sh.residual[warp]));
                         }
+                        float v[BOX / 32][32];
+                        if constexpr (F32) {
+                            columns(d, v[0]);
+                        } else {
+                            uint32_t o[2][32];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) tc::tmem_ld<32>(tmem + (use & 1) * BN + col_part + d + 32 * e + lanes, o[e]);
+                            tc::tmem_wait_ld();
+                            if (d + BOX >= COLS) {   // the last of the accumulator
+                                release();
+                                held = false;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[BOX / 32 - 1 ? e : 0][j] = __uint_as_float(o[e][j]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < BOX / 32; ++e) finish(v[e], d + 32 * e);
+                        if (lane == 0 && !g.residual_tma) bulk_wait_read<0>();
                         __syncwarp();
                         if (g.residual_tma) wait(sh.residual[warp], loads++ & 1);
 #pragma unroll
-                        for (int e = 0; e < BOX; e += 32) {
-                            float v[32];
-                            columns(d + e, v);
-                            finish(v, col0 + d + e);
-#pragma unroll
-                            for (int j = 0; j < (F32 ? 8 : 4); ++j) {   // 16-byte chunks of the row
-                                const uint32_t at = stg_row + (((F32 ? j : e / 8 + j) ^ (lane & 7)) << 4);
-                                if constexpr (F32) {
-                                    if (g.residual_tma) {
-                                        const uint4 r = ld_shared_v4(at);
-                                        v[4 * j] += __uint_as_float(r.x);
-                                        v[4 * j + 1] += __uint_as_float(r.y);
-                                        v[4 * j + 2] += __uint_as_float(r.z);
-                                        v[4 * j + 3] += __uint_as_float(r.w);
-                                    }
-                                    tc::st_shared_v4(at, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                                     __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
-                                } else {
-                                    if (g.residual_tma) {
-                                        const uint4 r = ld_shared_v4(at);
-                                        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                                        for (int k = 0; k < 4; ++k) {
-                                            v[8 * j + 2 * k] += __uint_as_float(w[k] << 16);
-                                            v[8 * j + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
-                                        }
-                                    }
-                                    tc::st_shared_v4(at, tc::pack_bf16(v[8 * j], v[8 * j + 1]), tc::pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                                                     tc::pack_bf16(v[8 * j + 4], v[8 * j + 5]), tc::pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+                        for (int j = 0; j < 8; ++j) {   // 16-byte chunks of the row
+                            const uint32_t at = stg_row + ((j ^ (lane & 7)) << 4);
+                            if constexpr (F32) {
+                                float *y = v[0] + 4 * j;
+                                if (g.residual_tma) {
+                                    const uint4 r = ld_shared_v4(at);
+                                    y[0] += __uint_as_float(r.x);
+                                    y[1] += __uint_as_float(r.y);
+                                    y[2] += __uint_as_float(r.z);
+                                    y[3] += __uint_as_float(r.w);
                                 }
+                                tc::st_shared_v4(at, __float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+                            } else {
+                                float *y = v[BOX / 32 - 1 ? j / 4 : 0] + j % 4 * 8;
+                                if (g.residual_tma) {
+                                    const uint4 r = ld_shared_v4(at);
+                                    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        y[2 * k] += __uint_as_float(w[k] << 16);
+                                        y[2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
+                                    }
+                                }
+                                tc::st_shared_v4(at, tc::pack_bf16(y[0], y[1]), tc::pack_bf16(y[2], y[3]), tc::pack_bf16(y[4], y[5]),
+                                                 tc::pack_bf16(y[6], y[7]));
                             }
                         }
                         fence_proxy_async_smem();
@@ -501,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         } else {
                             columns(d, v);
                         }
-                        finish(v, col0 + d);
+                        finish_at(v, d);
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -522,7 +558,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            if constexpr (!F32) release();
+            if (held) release();
         }
         if (lane == 0) bulk_wait_read<0>();
         tc::fence_before_sync();
@@ -567,7 +603,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, co
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (col + j >= a.Cout) break;
-        float x = activate(v[j] + (a.b ? a.b[col + j] : 0.f), a.act);
+        float x = activate<sizeof(T) == 2>(v[j] + (a.b ? a.b[col + j] : 0.f), a.act);
         if (a.residual) x += to_float(static_cast<const T *>(a.residual)[row * a.rs + col + j]);
         store_as(static_cast<T *>(a.y) + row * a.ys + col + j, x);
     }
@@ -664,7 +700,7 @@ cudaError_t launch(const LinearArgs &a, const Geom &g, const Maps &m, cudaStream
     if (regs != REGS_LAUNCH) return cudaErrorNotSupported;
     int *status = device_status_ptr();
     if (!status) return cudaErrorInvalidDevice;
-    const long long slots = device_sm_count() / CG;
+    const int slots = device_sm_count() / CG;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(CG * (g.items < slots ? g.items : slots)));
     cfg.blockDim = dim3(THREADS);
@@ -721,10 +757,14 @@ cudaError_t launch_linear_tc(const LinearArgs &a, bool bf16, cudaStream_t st, co
     const int cg = shape[best].cg, bn = shape[best].bn;
     g.splits = splits;
     const long long tm = (a.rows + 128LL * cg - 1) / (128 * cg), tn = (a.Cout + (long long)bn - 1) / bn;
-    if (tm * tn > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+    if (tm * tn * splits > 0x3fffffffLL || tn > 0x3fffffffLL / lt::GROUP_M) return cudaErrorInvalidConfiguration;
     g.tiles_m = (int)tm;
     g.tiles_n = (int)tn;
-    g.items = tm * tn * splits;
+    g.items = (int)(tm * tn * splits);
+    g.per_split = make_divisor((int)(tm * tn));
+    g.per_group = make_divisor((int)(tn * lt::GROUP_M));
+    g.tail_rows = make_divisor(g.tiles_m % lt::GROUP_M ? g.tiles_m % lt::GROUP_M : lt::GROUP_M);
+    g.parts = make_divisor(splits);
 
     auto pad = [](size_t b) { return (b + 255) & ~(size_t)255; };
     g.part_ld = (a.Cout + 3) / 4 * 4;
