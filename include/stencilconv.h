@@ -389,11 +389,10 @@ typedef struct {
  *   row that all share.  y may be residual (with the same stride), else it
  *   overlaps no input.
  * Products and sums are fp32, and so is everything up to y, which is rounded
- * once (to nearest even).  Up to 16 rows are multiplied in fp32 or, in bf16, on
- * warp-wide MMAs; more go to the tensor cores, fp32 tensors in three bf16
- * planes of 24 bits in all, where an infinity times another may be NaN and an
- * element below 2^-110 keeps 2^-134.
- * Supported: rows, Cin and Cout up to 2^30.  A call may take a stream-ordered
+ * once (to nearest even).  fp32 tensors of more than 4 rows are multiplied in
+ * three bf16 planes of 24 bits in all: there an infinity times another, or times
+ * an element above 256, may be NaN, and an element below 2^-110 keeps 2^-134.
+ * Supported: rows, Cin and Cout up to 2^30, strides below 2^40 bytes.  A call may take a stream-ordered
  * temporary buffer (see sc_release_workspace).  Returns SC_OK or a negative
  * sc_status.
  */
@@ -499,8 +498,8 @@ int kv_quantize_fwd(const sc_quant_states *k, const sc_quant_states *v, const in
  * More rows: as in cross_attention_fwd, but that it is a weight times its state's
  * scale that is rounded to bf16, or taken in three planes.
  * The output is rounded once (to nearest even).
- * Supported: D % 16 == 0, D <= 128; block 16, 32, 64 or 128; otherwise as
- * cross_attention_fwd.  Returns SC_OK or a negative sc_status.
+ * Supported: D % 16 == 0, D <= 128; block 16, 32, 64 or 128; strides of k and v
+ * below 2^40 bytes; otherwise as cross_attention_fwd.  Returns SC_OK or a negative sc_status.
  */
 int cross_attention_q8_fwd(const void *q, const void *k, const float *k_scale, const void *v, const float *v_scale,
                            void *out, float *lse, const int *k_len, const unsigned char *key_mask, int N, int Tq, int Tk,
@@ -575,7 +574,8 @@ int sc_version(void);
 /*
  * sc_release_workspace: hand the memory of the library's temporary buffers
  * back to the driver.  Those buffers (the NCHW repack of conv2d_fwd,
- * the partial results and split operands of cross_attention_fwd) come from a
+ * the partial results and split operands of cross_attention_fwd, and of
+ * linear_fwd, the expanded codes of cross_attention_q8_fwd) come from a
  * library-private stream-ordered memory pool per device that otherwise keeps freed memory
  * for the next call.  Memory still in use by queued work is not affected.
  * Returns SC_OK.
@@ -674,6 +674,19 @@ int sc_test_attn_wait_expiry(const void *q, const void *k, const void *v, void *
 int sc_test_attn_slow_clear(const void *q, const void *k, const void *v, void *out, const int *k_len,
                             const unsigned char *key_mask, int N, int Tq, int Tk, int Hq, int Hkv, int D, int dtype,
                             int delay_us, sc_stream_t stream);
+
+/*
+ * sc_test_linear_wait_expiry: test hook for the device-status path, not part
+ * of the operation.  Runs linear_fwd's tensor-core kernel (packed, no bias,
+ * activation or residual, whatever the number of rows) with the copies of
+ * stage `drop_copy` (0-based, in each CTA's issue order) never issued, so the
+ * time-bounded waits for them expire after `timeout_us` microseconds.  The
+ * kernel then records SC_ERR_DEVICE_TIMEOUT (read and cleared by
+ * sc_last_device_status), waits for its other copies and products and returns;
+ * the context stays usable.  `y` is left with no defined values.
+ */
+int sc_test_linear_wait_expiry(const void *x, const void *w, void *y, int rows, int Cin, int Cout, int dtype, int drop_copy,
+                               int timeout_us, sc_stream_t stream);
 
 /*
  * sc_test_workspace_allocs: test hook, not part of the operation.  The

@@ -85,6 +85,7 @@ SIGNATURES = {
     "rotary_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "qk_norm_rotary_fwd": (_I, [_P, _P, _P, _I, _I, _I, _F, _I, _I, _I, _P]),
     "linear_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "sc_test_linear_wait_expiry": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "residual_norm_fwd": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _I, _F, _I, _P, _P]),
     "kv_quantize_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "cross_attention_q8_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P, _P]),
@@ -432,6 +433,12 @@ def sc_test_attn_slow_clear(q, k, v, out, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D
     """Test hook: cross_attention_fwd's tensor-core kernel with its clearing warps held up (see the header)."""
     return load().sc_test_attn_slow_clear(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(k_len), _ptr(key_mask), N, Tq, Tk,
                                           Hq, Hkv, D, dtype, delay_us, _stream(stream))
+
+
+def sc_test_linear_wait_expiry(x, w, y, rows, Cin, Cout, dtype, drop_copy, timeout_us, stream=None) -> int:
+    """Test hook: linear_fwd's tensor-core kernel with one stage's copies never issued (see the header)."""
+    return load().sc_test_linear_wait_expiry(_ptr(x), _ptr(w), _ptr(y), rows, Cin, Cout, dtype, drop_copy, timeout_us,
+                                             _stream(stream))
 
 
 def sc_test_stencil_wait_expiry(inp, out, H, W, drop_copy, timeout_us, stream=None) -> int:

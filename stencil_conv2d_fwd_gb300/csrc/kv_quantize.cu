@@ -3,14 +3,16 @@
 //   a = max |x| over the block's valid states,  scale = a / top,  code = nearest(top x / a)
 //
 // Bound by memory: 2 or 4 bytes read and one written an element.  A block is
-// read once into registers, 16 elements a thread, its largest value
+// read once into registers, 16 or 32 elements a thread, its largest value
 // found as the largest of the magnitudes' bits (so that an infinity or NaN is
 // above every number), and the codes written from the registers.
 // The quotient is x times top / a in fp32, off by less than 2^-22 of itself; where
 // that leaves the code open (a value next to a border between two codes, every
 // 2^13th or so of fp32 values, and many bf16 ones, which lie on borders), top x is
-// compared with border times a in exact arithmetic made of fp32 FMAs.  (In 64 bits,
-// whose rate is 1/64 here, bf16 states took 794 us where they now take @@.)
+// compared with border times a in exact arithmetic made of fp32 FMAs (in 64 bits,
+// whose rate is 1/64 here, bf16 states took 794 us where they now take 90).
+// 32 x 3136 states, 8 heads of 64, keys and values: fp32 89 us (5.8 TB/s), bf16 90 (3.4
+// TB/s: some 27 instructions an element of both, issued 82% of the time).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -25,8 +27,6 @@ namespace {
 constexpr int kQuantThreads = 256;
 template <class T>
 constexpr int E = 16 / (int)sizeof(T);           // elements of a 16-byte chunk
-template <class T>
-constexpr int kChunks = 16 / E<T>;               // a thread's: 16 elements
 
 // (a warp's access is 512 bytes in a row whatever the type)
 __device__ __forceinline__ uint4 ld16(const void *p)
@@ -115,41 +115,47 @@ __device__ __forceinline__ uint2 codes(const float (&x)[N], float a, float inv)
             v[j / 4] = __byte_perm(__byte_perm(k[0], k[1], 0x0040), __byte_perm(k[2], k[3], 0x0040), 0x5410);
         }
     }
-    if ((w[0] ^ v[0]) | (w[1] ^ v[1])) {
+    uint32_t open[2] = {w[0] ^ v[0], w[1] ^ v[1]};
+    if (open[0] | open[1]) {
         const float unit = __uint_as_float((254u << 23) - (__float_as_uint(a) & 0x7f800000u)), an = a * unit;
+        // one open code after the other: there is mostly one
+        do {
+            const int half = open[0] ? 0 : 1;
+            const uint32_t shift = (uint32_t)(__ffs((int)(half ? open[1] : open[0])) - 1) & ~7u;
+            const int j = half * 4 + (int)(shift >> 3);
+            float xj = x[0];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const uint32_t shift = 8 * (j & 3);
-            if (!((w[j / 4] ^ v[j / 4]) >> shift & 0xffu)) continue;
+            for (int i = 1; i < N; ++i) xj = i == j ? x[i] : xj;
+            uint32_t &word = half ? w[1] : w[0];
+            const uint32_t code = word >> shift & 0xffu, up = (half ? v[1] : v[0]) >> shift & 0xffu;
             // w's code is the one nearer to zero, c of the magnitude; the border to the
             // next one is half the sum of the two
-            if constexpr (E4M3) {
-                const uint32_t c = w[j / 4] >> shift & 0x7fu;
-                const float d = exact_difference(896.f, fabsf(x[j]) * unit, e4m3_sum(c, c + 1), an);
-                if (d > 0.f || (d == 0.f && (c & 1u))) w[j / 4] += 1u << shift;
-            } else {
-                const int c = abs((int)(signed char)(w[j / 4] >> shift & 0xffu));
-                const float d = exact_difference(254.f, fabsf(x[j]) * unit, 2.f * (float)c + 1.f, an);
-                if (d > 0.f || (d == 0.f && (c & 1))) w[j / 4] = (w[j / 4] & ~(0xffu << shift)) | (v[j / 4] & 0xffu << shift);
-            }
-        }
+            const int c = E4M3 ? (int)(code & 0x7fu) : abs((int)(signed char)code);
+            const float sum = E4M3 ? e4m3_sum(c, c + 1) : 2.f * (float)c + 1.f;
+            const float d = exact_difference(E4M3 ? 896.f : 254.f, fabsf(xj) * unit, sum, an);
+            if (d > 0.f || (d == 0.f && (c & 1))) word = (word & ~(0xffu << shift)) | up << shift;
+            open[0] &= half ? ~0u : ~(0xffu << shift);
+            open[1] &= half ? ~(0xffu << shift) : ~0u;
+        } while (open[0] | open[1]);
     }
     return make_uint2(w[0], w[1]);
 }
 
 // A unit: one block of one (sequence, head), `threads` of the CTA's.
 struct QuantGeom {
-    int threads;        // of a unit: 32 to 1024
+    int threads;        // of a unit: 32 to 512
     int log2_threads;
     int per_cta;        // units
     uint32_t units;     // of a tensor
     Divisor heads, blocks, row_chunks;
+    int row_step, col_step;   // rows and chunks from one of a thread's chunks to the next
 };
 
-template <class T, bool E4M3>
-__global__ void __launch_bounds__(1024) kv_quantize_kernel(const QuantArgs a, const QuantGeom g)
+// PER elements a thread.
+template <class T, bool E4M3, int PER>
+__global__ void __launch_bounds__(512) kv_quantize_kernel(const QuantArgs a, const QuantGeom g)
 {
-    __shared__ uint32_t largest[32];   // of each warp
+    __shared__ uint32_t largest[16];   // of each warp
     const QuantPart &p = a.part[blockIdx.y];
     const int tid = threadIdx.x & (g.threads - 1), slot = threadIdx.x >> g.log2_threads;
     const uint32_t unit = blockIdx.x * g.per_cta + slot;
@@ -163,30 +169,36 @@ __global__ void __launch_bounds__(1024) kv_quantize_kernel(const QuantArgs a, co
     const int rows = on ? max(0, min(a.block, len - t0)) : 0;
     const unsigned char *mb = a.key_mask ? a.key_mask + (long long)n * a.T + t0 : nullptr;
     // this thread's chunks: `col` and `row` step by g.threads chunks
-    float x[kChunks<T>][E<T>];
-    const int dr = (int)g.row_chunks.quotient(g.threads), dc = g.threads - dr * row_chunks;
-    const T *xb = static_cast<const T *>(p.x) + n * p.xs.n + (long long)t0 * p.xs.t + h * p.xs.h;
-    unsigned char *cb = p.codes + n * p.cs.n + (long long)t0 * p.cs.t + h * p.cs.h;
+    float x[PER / E<T>][E<T>];
+    const int dr = g.row_step, dc = g.col_step;
     const int row0 = (int)g.row_chunks.quotient(tid), col0 = tid - row0 * row_chunks;
-    auto next = [&](int &row, int &col) {
+    const T *xp = static_cast<const T *>(p.x) + n * p.xs.n + (long long)(t0 + row0) * p.xs.t + h * p.xs.h + col0 * E<T>;
+    unsigned char *cp = p.codes + n * p.cs.n + (long long)(t0 + row0) * p.cs.t + h * p.cs.h + col0 * E<T>;
+    // from a chunk to the next; a turn goes to the next row's start
+    const long long xs = dr * p.xs.t + dc * E<T>, xturn = p.xs.t - a.D, cs = dr * p.cs.t + dc * E<T>, cturn = p.cs.t - a.D;
+    auto next = [&](int &row, int &col, auto *&at, long long step, long long turn) {
         row += dr;
-        col += dc;
-        if (col >= row_chunks) {
-            col -= row_chunks;
-            ++row;
+        at += step;
+        if (dc != 0) {   // (heads whose chunks do not divide the threads)
+            col += dc;
+            if (col >= row_chunks) {
+                col -= row_chunks;
+                ++row;
+                at += turn;
+            }
         }
     };
     float top = 0.f;   // a NaN stays
     uint32_t on_bits = 0;
     int row = row0, col = col0;
 #pragma unroll
-    for (int i = 0; i < kChunks<T>; ++i, next(row, col))
+    for (int i = 0; i < PER / E<T>; ++i, next(row, col, xp, xs, xturn))
         if (row < rows && !(mb && mb[row] == 0)) {
             on_bits |= 1u << i;
-            load_chunk(xb + row * p.xs.t + col * E<T>, x[i]);
+            load_chunk(xp, x[i]);
         }
 #pragma unroll
-    for (int i = 0; i < kChunks<T>; ++i)
+    for (int i = 0; i < PER / E<T>; ++i)
         if (on_bits >> i & 1u) {
 #pragma unroll
             for (int j = 0; j < E<T>; j += 2) top = max_nan(top, x[i][j], x[i][j + 1]);
@@ -196,9 +208,8 @@ __global__ void __launch_bounds__(1024) kv_quantize_kernel(const QuantArgs a, co
     if (g.threads > 32) {
         if ((threadIdx.x & 31) == 0) largest[threadIdx.x >> 5] = m;
         __syncthreads();
-        const int w0 = slot * (g.threads >> 5);
-        m = 0;
-        for (int w = 0; w < g.threads >> 5; ++w) m = max(m, largest[w0 + w]);
+        const int warps = g.threads >> 5, lane = threadIdx.x & 31;
+        m = __reduce_max_sync(0xffffffffu, lane < warps ? largest[slot * warps + lane] : 0u);
     }
     if (!(m >> 31)) return;
     m &= 0x7fffffffu;
@@ -211,21 +222,22 @@ __global__ void __launch_bounds__(1024) kv_quantize_kernel(const QuantArgs a, co
     // far from 1 in size, top / a or top x may not be finite: all times a power of two
     const float move = amax < 0x1p-100f ? 0x1p100f : (amax > 0x1p100f ? 0x1p-60f : 1.f);
     amax *= move;
-    const float inv = zero ? 0.f : __fdiv_rn(largest_code, amax);
+    float inv;   // top / a, to 2^-22
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(amax));
+    inv = zero ? 0.f : inv * largest_code;
     row = row0, col = col0;
 #pragma unroll
-    for (int i = 0; i < kChunks<T>; ++i, next(row, col)) {
+    for (int i = 0; i < PER / E<T>; ++i, next(row, col, cp, cs, cturn)) {
         if (!(on_bits >> i & 1u)) continue;
         if (move != 1.f) {
 #pragma unroll
             for (int j = 0; j < E<T>; ++j) x[i][j] *= move;
         }
         const uint2 w = zero ? make_uint2(0u, 0u) : codes<E4M3>(x[i], amax, inv);
-        unsigned char *to = cb + row * p.cs.t + col * E<T>;
         if constexpr (E<T> == 8)
-            *reinterpret_cast<uint2 *>(to) = w;
+            *reinterpret_cast<uint2 *>(cp) = w;
         else
-            *reinterpret_cast<uint32_t *>(to) = w.x;
+            *reinterpret_cast<uint32_t *>(cp) = w.x;
     }
 }
 
@@ -235,7 +247,10 @@ cudaError_t launch_kv_quantize(const QuantArgs &a, bool bf16, bool e4m3, cudaStr
 {
     QuantGeom g;
     g.threads = 32;
-    while (g.threads * 16 < a.block * a.D) g.threads *= 2;   // at most 1024: 128 states of 128
+    // 32 elements a thread where 16 would be more than 256 threads to wait for one
+    // another
+    const int per = a.block * a.D > 4096 ? 32 : 16;
+    while (g.threads * per < a.block * a.D) g.threads *= 2;   // at most 512: 128 states of 128
     g.per_cta = g.threads < kQuantThreads ? kQuantThreads / g.threads : 1;
     // (2^31 units are 512 GB of codes)
     const long long units = (long long)a.N * a.blocks * a.H;
@@ -245,20 +260,26 @@ cudaError_t launch_kv_quantize(const QuantArgs &a, bool bf16, bool e4m3, cudaStr
     while (1 << g.log2_threads < g.threads) ++g.log2_threads;
     g.heads = make_divisor(a.H);
     g.blocks = make_divisor(a.blocks);
-    g.row_chunks = make_divisor(a.D / (bf16 ? 8 : 4));
+    const int row_chunks = a.D / (bf16 ? 8 : 4);
+    g.row_chunks = make_divisor(row_chunks);
+    g.row_step = g.threads / row_chunks;
+    g.col_step = g.threads % row_chunks;
     const long long ctas = (units + g.per_cta - 1) / g.per_cta;
     const dim3 grid((unsigned)ctas, a.parts), block(g.threads * g.per_cta);
-    if (bf16) {
-        if (e4m3)
-            kv_quantize_kernel<__nv_bfloat16, true><<<grid, block, 0, st>>>(a, g);
+    auto go = [&](auto small, auto large) {
+        if (per == 16)
+            small<<<grid, block, 0, st>>>(a, g);
         else
-            kv_quantize_kernel<__nv_bfloat16, false><<<grid, block, 0, st>>>(a, g);
-    } else {
-        if (e4m3)
-            kv_quantize_kernel<float, true><<<grid, block, 0, st>>>(a, g);
-        else
-            kv_quantize_kernel<float, false><<<grid, block, 0, st>>>(a, g);
-    }
+            large<<<grid, block, 0, st>>>(a, g);
+    };
+    if (bf16 && e4m3)
+        go(kv_quantize_kernel<__nv_bfloat16, true, 16>, kv_quantize_kernel<__nv_bfloat16, true, 32>);
+    else if (bf16)
+        go(kv_quantize_kernel<__nv_bfloat16, false, 16>, kv_quantize_kernel<__nv_bfloat16, false, 32>);
+    else if (e4m3)
+        go(kv_quantize_kernel<float, true, 16>, kv_quantize_kernel<float, true, 32>);
+    else
+        go(kv_quantize_kernel<float, false, 16>, kv_quantize_kernel<float, false, 32>);
     return cudaGetLastError();
 }
 

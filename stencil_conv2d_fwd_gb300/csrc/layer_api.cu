@@ -11,7 +11,10 @@ namespace {
 using sc::Region;
 
 constexpr int kMaxRows = 1 << 30;
-constexpr int kFewRowsF32 = 64;
+// Rows that stream w through registers (linear_rows.cu) rather than go to the tensor
+// cores (linear_tc.cu), which in fp32 first split all of w.  w of 8192 x 2048:
+//   bf16: 16 rows 11.6 us, 17 there 16.0;  fp32: 32 rows 38.4, there 59.3; 48 rows 68.3, there 59.5
+constexpr int kFewRowsBf16 = 16, kFewRowsF32 = 32;
 constexpr long long kMaxMapStride = 1LL << 40;   // bytes
 
 // [rows][cols] with a row stride in elements.
@@ -45,12 +48,9 @@ int take_norm(const sc_norm *n, sc::NormArgs &out)
     return SC_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int linear_fwd(const void *x, const void *w, const float *b, const void *residual, void *y, int rows, int Cin, int Cout,
-               int act, int dtype, const sc_linear_strides *strides, sc_stream_t stream)
+// linear_fwd's argument checks; SC_OK with `a` filled in when the call may launch.
+int take_linear(const void *x, const void *w, const float *b, const void *residual, void *y, int rows, int Cin, int Cout, int act,
+                int dtype, const sc_linear_strides *strides, sc::LinearArgs &a)
 {
     if (!x || !w || !y) return SC_ERR_NULL;
     if (rows < 1 || Cin < 1 || Cout < 1 || rows > kMaxRows || Cin > kMaxRows || Cout > kMaxRows) return SC_ERR_SHAPE;
@@ -59,7 +59,7 @@ int linear_fwd(const void *x, const void *w, const float *b, const void *residua
     if (act < SC_ACT_NONE || act > SC_ACT_SILU) return SC_ERR_UNSUPPORTED;
     if (Cin % 8 != 0) return SC_ERR_UNSUPPORTED;
     const int es = dtype == SC_BF16 ? 2 : 4;
-    sc::LinearArgs a{x, w, b, residual, y, rows, Cin, Cout, act, Cin, Cin, Cout, Cout};
+    a = sc::LinearArgs{x, w, b, residual, y, rows, Cin, Cout, act, Cin, Cin, Cout, Cout};
     if (strides) {
         a.xs = strides->x;
         a.ws = strides->w;
@@ -88,9 +88,36 @@ int linear_fwd(const void *x, const void *w, const float *b, const void *residua
         const Region rr = rows_region(residual, rows, Cout, a.rs, es);
         if (!same_rows(ry, rr) && sc::may_overlap(ry, rr)) return SC_ERR_ALIAS;
     }
+    return SC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int linear_fwd(const void *x, const void *w, const float *b, const void *residual, void *y, int rows, int Cin, int Cout,
+               int act, int dtype, const sc_linear_strides *strides, sc_stream_t stream)
+{
+    sc::LinearArgs a;
+    const int rc = take_linear(x, w, b, residual, y, rows, Cin, Cout, act, dtype, strides, a);
+    if (rc != SC_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SC_BF16;
-    return sc::from_cuda(rows <= (bf16 ? 16 : kFewRowsF32) ? sc::launch_linear_rows(a, bf16, st) : sc::launch_linear_tc(a, bf16, st));
+    return sc::from_cuda(rows <= (bf16 ? kFewRowsBf16 : kFewRowsF32) ? sc::launch_linear_rows(a, bf16, st)
+                                                                    : sc::launch_linear_tc(a, bf16, st));
+}
+
+int sc_test_linear_wait_expiry(const void *x, const void *w, void *y, int rows, int Cin, int Cout, int dtype, int drop_copy,
+                               int timeout_us, sc_stream_t stream)
+{
+    sc::LinearArgs a;
+    const int rc = take_linear(x, w, nullptr, nullptr, y, rows, Cin, Cout, SC_ACT_NONE, dtype, nullptr, a);
+    if (rc != SC_OK) return rc;
+    if (drop_copy < 0 || timeout_us < 1) return SC_ERR_SHAPE;
+    sc::LinearTest test;
+    test.drop_copy = drop_copy;
+    test.timeout_ns = 1000ull * (unsigned long long)timeout_us;
+    return sc::from_cuda(sc::launch_linear_tc(a, dtype == SC_BF16, reinterpret_cast<cudaStream_t>(stream), test));
 }
 
 int residual_norm_fwd(const void *x, const void *residual, void *sum, void *y, int rows, int C, const sc_norm *post,

@@ -1,15 +1,19 @@
-// y = act(x w^T + b) + residual of up to 16 rows: a decoder's step.  Bound by
-// reading w once, so a warp streams rows of w through registers and keeps all
-// rows' sums; 1 to 8 warps of a CTA share an output's Cin (more where there are
-// few outputs) and add their parts in order through shared memory.
+// y = act(x w^T + b) + residual of few rows: a decoder's step.  Bound by reading w
+// once, so a warp streams rows of w through registers and keeps all rows' sums; 1 to
+// 8 warps of a CTA, and where that is not enough 2 to 8 CTAs of a cluster, share an
+// output's Cin and add their parts in order through (distributed) shared memory:
+// 16 rows of 4096, 512 outputs in bf16 4.4 us, without clusters 8.7.
 //
-// bf16: warp-wide m16n8k16 MMAs with w as the 16-row operand.  The order of
-// summation is free, so lane (g, t) takes whole 16-byte chunks of w's rows g and
-// g + 8 and the same chunks of x's row g, with no transposition.
-// fp32, 5 rows and more: the same, both operands in three bf16 planes.
-// fp32, up to 4 rows: FMA.  A lane takes four elements of Cin of four outputs and every row of
-// x (from L1), and the 32 lanes' sums are added by halves: each exchange leaves a
-// lane half as many sums.
+// bf16, up to 16 rows: warp-wide m16n8k16 MMAs with w as the 16-row operand.  The
+// order of summation is free, so lane (g, t) takes whole 16-byte chunks of w's rows g
+// and g + 8 and the same chunks of x's row g, with no transposition.  (8 rows, w of
+// 8192 x 2048: 7.8 us, 4.3 TB/s.)
+// fp32, 5 rows to 32: the same, both operands in three bf16 planes, blocks of 16 rows
+// that read w from L2 but for one.
+// fp32, up to 4 rows: FMA.  A lane takes four elements of Cin of four outputs and
+// every row of x (from L1), and the 32 lanes' sums are added by halves: each exchange
+// leaves a lane half as many sums.  (1 row, w of 32000 x 512: 13.1 us, 5.0 TB/s; 3
+// rows 16.1.)
 #include <cuda_bf16.h>
 
 #include "attn_rows.cuh"
@@ -105,7 +109,7 @@ __device__ __forceinline__ void finish_tiles(const LinearArgs &a, const float *s
 
 // NT: 8 or 16 rows of x.
 template <int NT>
-__global__ void __launch_bounds__(kWarps * 32) linear_rows_mma_kernel(const LinearArgs a, const RowsShare share)
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) linear_rows_mma_kernel(const LinearArgs a, const RowsShare share)
 {
     constexpr int R = 8 * NT, U = 4;
     __shared__ float sums[kWarps * R * 16];
@@ -171,56 +175,49 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3])
 }
 
 // fp32 rows on the same MMAs: both operands split in registers, a product the six
-// of planes i + j <= 2.  A warp takes 32 outputs, so that x is split half as often.
-// The MMAs cut sums short, so large and small products have accumulators of their
-// own, which are moved to sums every FLUSH steps.
+// of planes i + j <= 2.  The MMAs cut sums short, so large and small products have
+// accumulators of their own, which are moved to sums every FLUSH steps.
+// 16 rows, w of 8192 x 2048: 22.0 us (67 MB; steps in twos, the next two on their way:
+// one at a time 25.1, two blocks of 16 outputs a warp 33.4, FMA 78.9); 8 rows 19.9 (FMA
+// 26.3).
 template <int NT>
 __global__ void __launch_bounds__(kWarps * 32) linear_rows_split_kernel(const LinearArgs a, const RowsShare share)
 {
     constexpr int R = 8 * NT, U = 2, FLUSH = 8;
-    __shared__ float sums[kWarps * R * 32];
+    __shared__ float sums[kWarps * R * 16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, row0 = blockIdx.y * R;
     if (share.cluster > 1) cluster_arrive();
     const RowsWork work(share, (a.Cin + 15) / 16, warp);   // steps of 16 elements: a chunk of 4 for each t
     const int s0 = work.s0, s1 = work.s1;
-    const float *wp[4], *xp[NT];
+    const float *wp[2], *xp[NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const long long o = work.tile * 32 + g + 8 * i;
+    for (int i = 0; i < 2; ++i) {
+        const long long o = work.tile * 16 + g + 8 * i;
         wp[i] = static_cast<const float *>(a.w) + (o < a.Cout ? o : a.Cout - 1LL) * a.ws + t * 4;
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) xp[i] = static_cast<const float *>(a.x) + min(row0 + g + 8 * i, a.rows - 1) * a.xs + t * 4;
-    float total[2][NT][4], big[2][NT][4], small[2][NT][4];
-    auto clear = [](float (&v)[2][NT][4]) {
+    float total[NT][4], big[NT][4], small[NT][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[m][i][j] = 0.f;
-    };
+        for (int j = 0; j < 4; ++j) total[i][j] = big[i][j] = small[i][j] = 0.f;
     auto flush = [&]() {
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) total[m][i][j] += big[m][i][j] + small[m][i][j];
-        clear(big);
-        clear(small);
+            for (int j = 0; j < 4; ++j) {
+                total[i][j] += big[i][j] + small[i][j];
+                big[i][j] = small[i][j] = 0.f;
+            }
     };
-    clear(total);
-    clear(big);
-    clear(small);
-    // the next U steps' rows are on their way while these are multiplied
-    uint4 w[U][4], x[U][NT];
+    uint4 w[U][2], x[U][NT];
     auto load = [&](int s) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool on = s + u < s1 && (s + u) * 16 + t * 4 < a.Cin;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[u][i] = on ? ld_once16(wp[i] + (s + u) * 16LL) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 2; ++i) w[u][i] = on ? ld_once16(wp[i] + (s + u) * 16LL) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int i = 0; i < NT; ++i)
                 x[u][i] = on ? __ldg(reinterpret_cast<const uint4 *>(xp[i] + (s + u) * 16LL)) : make_uint4(0u, 0u, 0u, 0u);
@@ -229,11 +226,11 @@ __global__ void __launch_bounds__(kWarps * 32) linear_rows_split_kernel(const Li
     load(s0);
     int since = 0;
     for (int s = s0; s < s1; s += U) {
-        uint32_t wl[U][4][3], wh[U][4][3], xl[U][NT][3], xh[U][NT][3];   // the chunks' two halves in planes
+        uint32_t wl[U][2][3], wh[U][2][3], xl[U][NT][3], xh[U][NT][3];   // the chunks' two halves in planes
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 split3(__uint_as_float(w[u][i].x), __uint_as_float(w[u][i].y), wl[u][i]);
                 split3(__uint_as_float(w[u][i].z), __uint_as_float(w[u][i].w), wh[u][i]);
             }
@@ -251,25 +248,21 @@ __global__ void __launch_bounds__(kWarps * 32) linear_rows_split_kernel(const Li
 #pragma unroll
                 for (int j = 2 - k; j >= 0; --j)
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-                            mma16816(k + j == 0 ? big[m][i] : small[m][i], wl[u][2 * m][k], wl[u][2 * m + 1][k], wh[u][2 * m][k],
-                                     wh[u][2 * m + 1][k], xl[u][i][j], xh[u][i][j]);
+                    for (int i = 0; i < NT; ++i)
+                        mma16816(k + j == 0 ? big[i] : small[i], wl[u][0][k], wl[u][1][k], wh[u][0][k], wh[u][1][k], xl[u][i][j],
+                                 xh[u][i][j]);
         if (++since == FLUSH / U) {
             flush();
             since = 0;
         }
     }
     flush();
-    float *mine = sums + warp * R * 32;
+    float *mine = sums + warp * R * 16;
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mine[(i * 8 + 2 * t + (j & 1)) * 32 + 16 * m + g + 8 * (j >> 1)] = total[m][i][j];
-    finish_tiles<float, 32, R>(a, sums, share);
+        for (int j = 0; j < 4; ++j) mine[(i * 8 + 2 * t + (j & 1)) * 16 + g + 8 * (j >> 1)] = total[i][j];
+    finish_tiles<float, 16, R>(a, sums, share);
 }
 
 // R rows of x, four outputs a warp.
@@ -383,8 +376,8 @@ cudaError_t launch_linear_rows(const LinearArgs &a, bool bf16, cudaStream_t st)
     if (a.rows <= 1) return launch<4>(linear_rows_fma_kernel<1>, a, steps, st, 1);
     if (a.rows <= 2) return launch<4>(linear_rows_fma_kernel<2>, a, steps, st, 2);
     if (a.rows <= 4) return launch<4>(linear_rows_fma_kernel<4>, a, steps, st, 4);
-    if (a.rows <= 8) return launch<32>(linear_rows_split_kernel<1>, a, steps16, st, 8);
-    return launch<32>(linear_rows_split_kernel<2>, a, steps16, st, 16);
+    if (a.rows <= 8) return launch<16>(linear_rows_split_kernel<1>, a, steps16, st, 8);
+    return launch<16>(linear_rows_split_kernel<2>, a, steps16, st, 16);
 }
 
 }  // namespace sc

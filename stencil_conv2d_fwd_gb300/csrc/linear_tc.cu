@@ -19,8 +19,8 @@
 // cut each sum short instead of rounding it, so an accumulator takes no more than
 // KCHUNK elements of Cin; the epilogue's threads add those up in registers.
 //
-// Few tiles are split along Cin (`splits`): each part writes fp32 sums, which a
-// second kernel adds in order and finishes.
+// The tiles after the last full turn of the SMs may be split along Cin (`splits`):
+// each part writes fp32 sums, which a second kernel adds in order and finishes.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -67,15 +67,25 @@ template <int CG, int BN>
 constexpr int smem_bytes() { return stages<CG, BN>() * stage_bytes<CG, BN>() + EPI_WARPS * STG + (int)sizeof(Shared); }
 
 struct Geom {
-    int tiles_m, tiles_n, splits;
+    int tiles_m, tiles_n;
+    int whole, splits;  // tiles before the first one that is split along Cin; parts of those from there on
     int steps;          // stages of Cin: ceil(Cin / 64)
-    int items;          // tiles_m * tiles_n * splits
-    Divisor per_split, per_group, tail_rows, parts;   // tiles; tiles of a group; row tiles of the last group; splits
+    int items;          // whole + (tiles - whole) * splits
+    Divisor per_group, tail_rows, parts;   // tiles of a group; row tiles of the last group; splits
     int box;            // columns of y that a TMA store takes: 64 (bf16) or 32; 0: rows by the warp
     bool residual_tma;
-    float *part;        // splits > 1: [splits][rows][part_ld]
-    int part_ld;
+    float *part;        // splits > 1: [splits][split tile][row][BN]
 };
+
+// The place of tile t: row tiles in groups that go over w together.  (By
+// multiplications: with divisions the products waited 3 us for each tile.)
+__device__ __forceinline__ void tile_at(const Geom &g, int t, int &m, int &n)
+{
+    const int grp = (int)g.per_group.quotient(t), in = t - grp * (int)g.per_group.d;
+    const bool tail = (grp + 1) * GROUP_M > g.tiles_m;
+    n = tail ? (int)g.tail_rows.quotient(in) : in / GROUP_M;
+    m = grp * GROUP_M + in - n * (tail ? (int)g.tail_rows.d : GROUP_M);
+}
 
 __device__ __forceinline__ uint32_t elect_one()
 {
@@ -220,8 +230,8 @@ constexpr uint32_t idesc()   // D fp32, A and B bf16, both K-major
 template <int CG, int BN, bool F32>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-                     const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mr, const LinearArgs a,
-                     const Geom g, int *status, const LinearTest test)
+                     const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mr,
+                     const __grid_constant__ CUtensorMap mp, const LinearArgs a, const Geom g, int *status, const LinearTest test)
 {
     constexpr int STAGES = stages<CG, BN>(), STAGE = stage_bytes<CG, BN>();
     constexpr int COLS = BN >= 128 ? BN / 2 : BN;      // columns of an epilogue warp
@@ -250,21 +260,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
     };
-    // Work item: a tile and a part of Cin.  Row tiles in groups that go over w together.
+    // Work item: a tile, or a part of Cin of one of the last tiles.
     struct Item {
-        int m, n, k0, k1, split;
+        int m, n, k0, k1, split, part;   // part: the split tile's number, -1: a whole one
     };
-    // (by multiplications: with divisions the products waited 3 us for each tile)
     auto item = [&](int i) {
         Item r;
-        r.split = g.splits == 1 ? 0 : (int)g.per_split.quotient(i);
-        const int t = i - r.split * (int)g.per_split.d;
-        const int grp = (int)g.per_group.quotient(t), in = t - grp * (int)g.per_group.d;
-        const bool tail = (grp + 1) * GROUP_M > g.tiles_m;
-        r.n = tail ? (int)g.tail_rows.quotient(in) : in / GROUP_M;
-        r.m = grp * GROUP_M + in - r.n * (tail ? (int)g.tail_rows.d : GROUP_M);
-        r.k0 = g.splits == 1 ? 0 : (int)g.parts.quotient(g.steps * r.split);
-        r.k1 = g.splits == 1 ? g.steps : (int)g.parts.quotient(g.steps * (r.split + 1));
+        r.part = -1;
+        r.split = 0;
+        int t = i;
+        if (i >= g.whole && g.splits > 1) {
+            r.part = (int)g.parts.quotient(i - g.whole);
+            r.split = i - g.whole - r.part * g.splits;
+            t = g.whole + r.part;
+        }
+        tile_at(g, t, r.m, r.n);
+        r.k0 = r.part < 0 ? 0 : (int)g.parts.quotient(g.steps * r.split);
+        r.k1 = r.part < 0 ? g.steps : (int)g.parts.quotient(g.steps * (r.split + 1));
         return r;
     };
     constexpr int PRODUCTS = F32 ? 6 : 1;
@@ -434,11 +446,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             bool held = !F32;   // the accumulator is not yet released
             if (active && row0 < a.rows && !*abort_flag) {
-                if (g.part) {
+                if (it.part >= 0) {
                     // fp32 sums of this part of Cin
 #pragma unroll
                     for (int d = 0; d < COLS; d += 32) {
-                        if (col0 + d >= a.Cout) break;
                         float v[32];
                         columns(d, v);
                         if (lane == 0) bulk_wait_read<0>();
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            store_3d(&my, stg, col0 + d, row0, it.split);
+                            store_3d(&mp, stg, col_part + d, (it.part * CG + rank) * TILE + quad * 32, it.split);
                             bulk_commit();
                         }
                     }
@@ -578,34 +589,51 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncthreads();
     }
-    if constexpr (CG == 2) cluster_sync();   // neither leaves while the other's copies and products use its memory
+    if constexpr (CG == 2) {
+        // neither leaves while the other's copies and products use its memory; after
+        // an expired wait the second CTA's last copies may have no one who waits for
+        // them, so both stay for a thousand times as long as a copy takes
+        if (tid == 0 && sh.abort) {
+            uint32_t there;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(there) : "r"(smem_u32(&sh.abort)), "r"(rank ^ 1));
+            asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(there), "r"(1) : "memory");
+        }
+        cluster_sync();
+        if (*abort_flag) {
+            for (const unsigned long long t0 = global_ns(); global_ns() - t0 < 1000000ull;) __nanosleep(1000);
+            cluster_sync();
+        }
+    }
     if (warp == 9) dealloc<CG>(tmem, TMEM_COLS);
 }
 
-// Adds the parts of Cin in order and finishes: y = act(sum + b) + residual.
+// Adds the parts of Cin of the split tiles in order and finishes: y = act(sum + b) +
+// residual.  Tiles of rows x BN elements; a thread has four columns of a row.
 template <class T>
-__global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, const float *part, int splits, int ld)
+__global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, const Geom g, int rows, int bn)
 {
     pdl_wait();
-    const int quads = (a.Cout + 3) / 4;
-    const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (e >= (long long)a.rows * quads) return;
-    const long long row = e / quads;
-    const int col = (int)(e - row * quads) * 4;
+    const int e = blockIdx.x * 256 + threadIdx.x, quads = bn / 4;   // of the tile blockIdx.y
+    const int row = e / quads, c = (e - row * quads) * 4;
+    int m, n;
+    tile_at(g, g.whole + blockIdx.y, m, n);
+    const long long r = (long long)m * rows + row;
+    const int col = n * bn + c;
+    if (row >= rows || r >= a.rows || col >= a.Cout) return;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float *p = part + row * ld + col;
+    const float *p = g.part + ((long long)blockIdx.y * rows + row) * bn + c;
 #pragma unroll 4
-    for (int i = 0; i < splits; ++i, p += (long long)a.rows * ld) {
+    for (int i = 0; i < g.splits; ++i, p += (long long)gridDim.y * rows * bn) {
         const float4 v = *reinterpret_cast<const float4 *>(p);
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-    float v[4] = {s.x, s.y, s.z, s.w};
+    const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (col + j >= a.Cout) break;
         float x = activate<sizeof(T) == 2>(v[j] + (a.b ? a.b[col + j] : 0.f), a.act);
-        if (a.residual) x += to_float(static_cast<const T *>(a.residual)[row * a.rs + col + j]);
-        store_as(static_cast<T *>(a.y) + row * a.ys + col + j, x);
+        if (a.residual) x += to_float(static_cast<const T *>(a.residual)[r * a.rs + col + j]);
+        store_as(static_cast<T *>(a.y) + r * a.ys + col + j, x);
     }
 }
 
@@ -677,7 +705,7 @@ bool encode_map(CUtensorMap *m, bool bf16, const void *base, long long cols, lon
 }
 
 struct Maps {
-    CUtensorMap x, w, y, r;
+    CUtensorMap x, w, y, r, part;
 };
 
 template <int CG, int BN, bool F32>
@@ -721,7 +749,7 @@ cudaError_t launch(const LinearArgs &a, const Geom &g, const Maps &m, cudaStream
     }
     cfg.attrs = at;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, BN, F32>, m.x, m.w, m.y, m.r, a, g, status, test);
+    return cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, BN, F32>, m.x, m.w, m.y, m.r, m.part, a, g, status, test);
 }
 
 }  // namespace lt
@@ -733,49 +761,64 @@ cudaError_t launch_linear_tc(const LinearArgs &a, bool bf16, cudaStream_t st, co
     lt::Geom g = {};
     g.steps = (a.Cin + lt::KB - 1) / lt::KB;
     const int sms = device_sm_count();
-    // Tile and split: see the table
+    // Tile and parts.  Estimated clocks: a tile's stages (of which one in four more
+    // waits for copies where a CTA is alone, or the pair's tile narrow), 1500 for a tile's
+    // turn, 4000 for the start and the last epilogue.  The tiles after the last full turn
+    // of the SMs, or all where there are few, are split along Cin into as many parts as
+    // fill a turn, for a second launch (6000) that reads them.  2464 x 2048 x 2048 bf16
+    // (80 tiles on 76 pairs): 28.2 us with whole tiles, 23.4 with the last four split.
     static const struct {
         int cg, bn;
         double step;    // clocks of a stage
     } shape[4] = {{2, 256, 540.}, {2, 128, 400.}, {1, 128, 520.}, {1, 64, 420.}};
     int best = 0, splits = 1;
+    long long whole = 0;
     double least = 1e300;
     for (int i = 0; i < 4; ++i) {
         const long long tm = (a.rows + 128LL * shape[i].cg - 1) / (128 * shape[i].cg), tn = (a.Cout + (long long)shape[i].bn - 1) / shape[i].bn;
-        const long long slots = sms / shape[i].cg;
-        for (int s = 1; s <= 16 && s <= (g.steps + 3) / 4; ++s) {
-            const double waves = (double)((tm * tn * s + slots - 1) / slots);
-            const double join = s > 1 ? 6000. + (double)a.rows * a.Cout * 4 * (s + 1) / 3000. : 0.;
-            const double t = waves * ((double)(g.steps * products) / s * shape[i].step + 1500.) + 4000. + join;
-            if (t < least) {
+        const long long slots = sms / shape[i].cg, tiles = tm * tn, rest = tiles % slots;
+        const double tile = (double)g.steps * products * shape[i].step;
+        const double t1 = (double)((tiles + slots - 1) / slots) * (tile + 1500.);
+        if (t1 + 4000. < least) {
+            least = t1 + 4000.;
+            best = i;
+            splits = 1;
+            whole = tiles;
+        }
+        for (int s = 2; s <= 16 && s <= (g.steps + 3) / 4 && rest * s <= slots; ++s) {
+            const double join = 6000. + (double)rest * 128 * shape[i].cg * shape[i].bn * 4 * (s + 1) / 3000.;
+            const double t = (double)(tiles / slots) * (tile + 1500.) + tile / s + 1500. + 4000. + join;
+            if (rest > 0 && t < least) {
                 least = t;
                 best = i;
                 splits = s;
+                whole = tiles - rest;
             }
         }
     }
     const int cg = shape[best].cg, bn = shape[best].bn;
-    g.splits = splits;
     const long long tm = (a.rows + 128LL * cg - 1) / (128 * cg), tn = (a.Cout + (long long)bn - 1) / bn;
-    if (tm * tn * splits > 0x3fffffffLL || tn > 0x3fffffffLL / lt::GROUP_M) return cudaErrorInvalidConfiguration;
+    if (tm * tn > 0x3fffffffLL || tn > 0x3fffffffLL / lt::GROUP_M) return cudaErrorInvalidConfiguration;
     g.tiles_m = (int)tm;
     g.tiles_n = (int)tn;
-    g.items = (int)(tm * tn * splits);
-    g.per_split = make_divisor((int)(tm * tn));
+    g.splits = splits;
+    g.whole = (int)whole;
+    const int split_tiles = (int)(tm * tn - whole);
+    g.items = g.whole + split_tiles * splits;
     g.per_group = make_divisor((int)(tn * lt::GROUP_M));
     g.tail_rows = make_divisor(g.tiles_m % lt::GROUP_M ? g.tiles_m % lt::GROUP_M : lt::GROUP_M);
     g.parts = make_divisor(splits);
 
     auto pad = [](size_t b) { return (b + 255) & ~(size_t)255; };
-    g.part_ld = (a.Cout + 3) / 4 * 4;
-    const size_t pp = splits > 1 ? pad((size_t)splits * a.rows * g.part_ld * 4) : 0;
+    const int tile_rows = lt::TILE * cg;
+    const size_t pp = pad((size_t)splits * split_tiles * tile_rows * bn * 4);
     const size_t px = bf16 ? 0 : pad((size_t)a.rows * a.Cin * 6), pw = bf16 ? 0 : pad((size_t)a.Cout * a.Cin * 6);
     char *ws = nullptr;
     if (pp + px + pw > 0) {
         const cudaError_t e = workspace_alloc(reinterpret_cast<void **>(&ws), pp + px + pw, st);
         if (e != cudaSuccess) return e;
     }
-    g.part = splits > 1 ? reinterpret_cast<float *>(ws) : nullptr;
+    g.part = split_tiles > 0 ? reinterpret_cast<float *>(ws) : nullptr;
     auto tma_rows = [&](const void *p, long long stride) {
         return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * es % 16 == 0 && stride > 0;
     };
@@ -793,11 +836,12 @@ cudaError_t launch_linear_tc(const LinearArgs &a, bool bf16, cudaStream_t st, co
         ok = lt::encode_map(&m.x, true, ws + pp, a.Cin, a.rows, 3, a.Cin, (long long)a.rows * a.Cin, lt::TILE) &&
              lt::encode_map(&m.w, true, ws + pp + px, a.Cin, a.Cout, 3, a.Cin, (long long)a.Cout * a.Cin, bn / cg);
     }
-    if (g.part)
-        ok = ok && lt::encode_map(&m.y, false, g.part, a.Cout, a.rows, splits, g.part_ld, (long long)a.rows * g.part_ld, 32);
-    else if (g.box)
-        ok = ok && lt::encode_map(&m.y, bf16, a.y, a.Cout, a.rows, 1, a.ys, 0, 32);
-    if (g.residual_tma && !g.part) ok = ok && lt::encode_map(&m.r, bf16, a.residual, a.Cout, a.rows, 1, a.rs, 0, 32);
+    if (g.part) {
+        const long long rows = (long long)split_tiles * tile_rows;
+        ok = ok && lt::encode_map(&m.part, false, g.part, bn, rows, splits, bn, rows * bn, 32);
+    }
+    if (g.box) ok = ok && lt::encode_map(&m.y, bf16, a.y, a.Cout, a.rows, 1, a.ys, 0, 32);
+    if (g.residual_tma) ok = ok && lt::encode_map(&m.r, bf16, a.residual, a.Cout, a.rows, 1, a.rs, 0, 32);
     cudaError_t e = ok ? cudaSuccess : cudaErrorInvalidValue;
     if (e == cudaSuccess && !bf16) {
         const lt::SplitPart p0{static_cast<const float *>(a.x), reinterpret_cast<__nv_bfloat16 *>(ws + pp), a.rows, a.xs};
@@ -821,9 +865,8 @@ cudaError_t launch_linear_tc(const LinearArgs &a, bool bf16, cudaStream_t st, co
         }
     }
     if (e == cudaSuccess && g.part) {
-        const long long quads = (a.Cout + 3LL) / 4 * a.rows;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((quads + 255) / 256));
+        cfg.gridDim = dim3((unsigned)(tile_rows * (bn / 4) / 256), (unsigned)split_tiles);
         cfg.blockDim = dim3(256);
         cfg.stream = st;
         cudaLaunchAttribute at[1];
@@ -831,8 +874,8 @@ cudaError_t launch_linear_tc(const LinearArgs &a, bool bf16, cudaStream_t st, co
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        e = bf16 ? cudaLaunchKernelEx(&cfg, lt::linear_join_kernel<__nv_bfloat16>, a, (const float *)g.part, splits, g.part_ld)
-                 : cudaLaunchKernelEx(&cfg, lt::linear_join_kernel<float>, a, (const float *)g.part, splits, g.part_ld);
+        e = bf16 ? cudaLaunchKernelEx(&cfg, lt::linear_join_kernel<__nv_bfloat16>, a, g, tile_rows, bn)
+                 : cudaLaunchKernelEx(&cfg, lt::linear_join_kernel<float>, a, g, tile_rows, bn);
     }
     if (ws) {
         const cudaError_t ef = workspace_free(ws, st);

@@ -1,0 +1,129 @@
+"""The decoder layer's operators one after the other, as a layer over a feature map uses them, against the plain
+64-bit forms: each operator's result within its own bound for the inputs that it was given, and the layer's result
+near the layer computed in 64 bits throughout; then the same layer captured into a graph, for one new token."""
+import math
+
+import pytest
+
+import layer_ref as ref
+import stencil_conv2d_fwd_gb300 as scl
+
+HEADS, KEY_HEADS, D, WIDTH, MLP, BLOCK = 8, 2, 64, 512, 1536, 32
+
+
+def make_weights(torch, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    t = torch.bfloat16 if dtype == scl.SC_BF16 else torch.float32
+
+    def matrix(cout, cin):
+        return (torch.randn(cout, cin, generator=g) * cin ** -0.5).to(t).cuda()
+
+    def vector(n, gain=0.2, one=1.0):
+        return (one + gain * torch.randn(n, generator=g)).cuda()
+
+    return {"q": matrix(HEADS * D, WIDTH), "out": matrix(WIDTH, HEADS * D), "up": matrix(MLP, WIDTH), "down": matrix(WIDTH, MLP),
+            "up_b": vector(MLP, 0.1, 0.0), "down_b": vector(WIDTH, 0.1, 0.0), "norm_in": vector(WIDTH), "norm_post": vector(WIDTH),
+            "norm_mlp": vector(WIDTH)}
+
+
+class Layer:
+    """Buffers of a layer for N x T tokens, run in place on the residual stream."""
+
+    def __init__(self, torch, sc, w, N, T, dtype, code):
+        t = torch.bfloat16 if dtype == scl.SC_BF16 else torch.float32
+        self.sc, self.w, self.N, self.T, self.dtype, self.code = sc, w, N, T, dtype, code
+        n = N * T
+        self.h, self.q, self.a, self.o, self.s, self.m, self.u = (torch.empty(n, c, dtype=t, device="cuda") for c in
+                                                                 (WIDTH, HEADS * D, HEADS * D, WIDTH, WIDTH, WIDTH, MLP))
+
+    def run(self, x, cache, gate, k_len):
+        sc, w, N, T, dt = self.sc, self.w, self.N, self.T, self.dtype
+        n, Tk = N * T, cache["k"].shape[1]
+        rms = lambda v: (sc.SC_NORM_RMS, v, None, 1e-6)  # noqa: E731
+        sc.check(sc.residual_norm_fwd(x, None, None, self.h, n, WIDTH, pre=rms(w["norm_in"]), dtype=dt))
+        sc.check(sc.linear_fwd(self.h, w["q"], None, self.q, n, WIDTH, HEADS * D, dtype=dt))
+        sc.check(sc.cross_attention_q8_fwd(self.q, cache["k"], cache["ks"], cache["v"], cache["vs"], self.a, N, T, Tk, HEADS,
+                                           KEY_HEADS, D, D ** -0.5, BLOCK, self.code, dt, k_len=k_len))
+        sc.check(sc.linear_fwd(self.a, w["out"], None, self.o, n, HEADS * D, WIDTH, dtype=dt))
+        sc.check(sc.residual_norm_fwd(self.o, x, self.s, self.m, n, WIDTH, post=rms(w["norm_post"]), pre=rms(w["norm_mlp"]),
+                                      gate=gate, gate_rows=T, dtype=dt))
+        sc.check(sc.linear_fwd(self.m, w["up"], w["up_b"], self.u, n, WIDTH, MLP, sc.SC_ACT_GELU, dt))
+        sc.check(sc.linear_fwd(self.u, w["down"], w["down_b"], self.s, n, MLP, WIDTH, dtype=dt, residual=self.s))
+        return self.s
+
+
+def reference(torch, w, x, k, v, gate, valid, T):
+    """The layer in 64 bits on the dequantised states."""
+    N, n = valid.shape[0], x.shape[0]
+    rms = lambda y, g: ref.normed(y, 1, g, None, 1e-6)[0]  # noqa: E731
+    q = rms(x.double(), w["norm_in"]) @ w["q"].double().t()
+    a = ref.attention(q.view(N, T, HEADS, D), k, v, D ** -0.5, valid)[0].reshape(n, HEADS * D)
+    s = x.double() + gate.double().repeat_interleave(T, dim=0) * rms(a @ w["out"].double().t(), w["norm_post"])
+    u = rms(s, w["norm_mlp"]) @ w["up"].double().t() + w["up_b"].double()
+    return s + (u * torch.special.ndtr(u)) @ w["down"].double().t() + w["down_b"].double()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("code", [scl.SC_CODE_I8, scl.SC_CODE_E4M3])
+@pytest.mark.parametrize("dtype", [scl.SC_F32, scl.SC_BF16])
+def test_layer(sc, dtype, code):
+    import torch
+    bf16, N, H, W = dtype == scl.SC_BF16, 3, 21, 17
+    Tk = H * W
+    t = torch.bfloat16 if bf16 else torch.float32
+    g = torch.Generator().manual_seed(1)
+    w = make_weights(torch, dtype)
+    k, v = (torch.randn(N, Tk, KEY_HEADS, D, generator=g).to(t).cuda() for _ in range(2))
+    lens = [Tk, 100, 0]
+    k[1, 100:], v[1, 100:] = math.nan, math.nan
+    k_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cache = {n: torch.zeros(N, Tk, KEY_HEADS, D, dtype=torch.uint8, device="cuda") for n in "kv"}
+    cache |= {n + "s": torch.zeros(N, KEY_HEADS, -(-Tk // BLOCK), device="cuda") for n in "kv"}
+    sc.check(sc.kv_quantize_fwd((k, cache["k"], cache["ks"]), (v, cache["v"], cache["vs"]), N, Tk, KEY_HEADS, D, BLOCK, code, dtype,
+                                k_len=k_len), "kv_quantize_fwd")
+    as_code = torch.float8_e4m3fn if code == scl.SC_CODE_E4M3 else torch.int8
+    kk, vv = (ref.dequantize(cache[n].view(as_code).double(), cache[n + "s"], BLOCK) for n in "kv")
+    valid = torch.arange(Tk, device="cuda")[None] < k_len[:, None]
+    # the cache is near the states: half a code's step of the block's largest value, or of the value itself
+    for x, y in ((k, kk), (v, vv)):
+        near = 2.0 ** -4 * x.double().abs() + x[valid].double().abs().max() * 2.0 ** -9 if code == scl.SC_CODE_E4M3 else \
+            x[valid].double().abs().max() / 254 * (1 + 2.0 ** -7)
+        assert ((x.double() - y).abs() <= near)[valid].all()
+    gate = (1 + 0.3 * torch.randn(N, WIDTH, generator=g)).cuda()
+    for T in (40, 1):   # a prompt, then a token
+        x = torch.randn(N * T, WIDTH, generator=g).to(t).cuda()
+        layer = Layer(torch, sc, w, N, T, dtype, code)
+        y = layer.run(x, cache, gate, k_len).clone()
+        sc.check(sc.sc_last_device_status())
+        want = reference(torch, w, x, kk, vv, gate, valid, T)
+        assert torch.isfinite(y.float()).all()
+        # eight roundings of the stream and what feeds it, bf16's or fp32's with its sums, relative to the rows' size
+        rel = ((y.double() - want).norm() / want.norm()).item()
+        assert rel <= (8 * ref.UB if bf16 else 64 * ref.U * math.sqrt(MLP)), rel
+        # each operator on the inputs that it was given
+        n = N * T
+        q = layer.q.double().view(N, T, HEADS, D)
+        o, _, wabs, mag = ref.attention(q, kk, vv, D ** -0.5, valid)
+        bound = wabs * (2 * ref.U * (6 * math.sqrt(D) + 32) * mag.transpose(1, 2)[..., None] + 2.0 ** -19 + (2 * ref.UB if bf16 else 0)) \
+            + 2.0 ** -39 * vv.abs().sum(dim=1).repeat_interleave(HEADS // KEY_HEADS, dim=1)[:, None].nan_to_num()
+        assert ((layer.a.double().view(N, T, HEADS, D) - o).abs() <= bound + 1e-30).all()
+        assert (layer.a.view(N, T, -1)[2] == 0).all()       # the sequence without a state
+        for src, wt, b, act, dst in ((layer.h, "q", None, 0, layer.q), (layer.a, "out", None, 0, layer.o),
+                                     (layer.m, "up", "up_b", ref.ACT_GELU, layer.u)):
+            want, mag, a = ref.linear(src, w[wt], None if b is None else w[b], None, act)
+            assert ((dst.double() - want).abs() <= ref.linear_bound(want, mag, a, src.shape[1], bf16)).all(), wt
+    # the token's layer in a graph, replayed on another token: the same bits as the calls
+    x2 = torch.randn(N, WIDTH, generator=g).to(t).cuda()
+    eager = layer.run(x2, cache, gate, k_len).clone()
+    xin = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.run(xin, cache, gate, k_len)
+    xin.copy_(x2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(layer.s, eager)
+    xin.copy_(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(layer.s, y)

@@ -209,7 +209,7 @@ A, B, C, D_ = 1 << 20, 1 << 24, 1 << 28, 1 << 32   # addresses, 16-byte aligned,
     (dict(strides=(66, 64, 32, 32)), scl.SC_ERR_ALIGN), (dict(strides=(64, 70, 32, 32)), scl.SC_ERR_ALIGN),
     (dict(strides=(0, 64, 32, 32)), scl.SC_ERR_UNSUPPORTED), (dict(strides=(64, 56, 32, 32)), scl.SC_ERR_UNSUPPORTED),
     (dict(strides=(-64, 64, 32, 32)), scl.SC_ERR_SHAPE), (dict(strides=(64, 64, 32, -1), residual=D_), scl.SC_ERR_SHAPE),
-    (dict(strides=(1 << 60, 64, 32, 32)), scl.SC_ERR_SHAPE),
+    (dict(strides=(1 << 60, 64, 32, 32)), scl.SC_ERR_SHAPE), (dict(strides=(1 << 38, 64, 32, 32)), scl.SC_ERR_UNSUPPORTED),
     (dict(strides=(64, 64, 31, 32)), scl.SC_ERR_ALIAS), (dict(strides=(64, 64, 0, 32)), scl.SC_ERR_ALIAS),
     (dict(y=A + 64), scl.SC_ERR_ALIAS), (dict(y=B), scl.SC_ERR_ALIAS), (dict(y=C, b=C + 16), scl.SC_ERR_ALIAS),
     (dict(residual=C + 4), scl.SC_ERR_ALIAS), (dict(residual=C, strides=(64, 64, 32, 40)), scl.SC_ERR_ALIAS),
@@ -226,3 +226,24 @@ def test_refusals(change, expect):
 @pytest.mark.parametrize("act", [scl.SC_ACT_GELU, scl.SC_ACT_SILU])
 def test_convolutions_take_no_other_activation(act):
     assert scl.conv2d_fwd(A, B, None, C, 1, 8, 8, 8, 8, 1, 1, scl.SC_NHWC, act, stream=0) == scl.SC_ERR_UNSUPPORTED
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape,drop_copy", [((40, 256, 300), 0), ((300, 1024, 700), 3), ((5000, 512, 2100), 17)])
+def test_expired_wait_is_reported(sc, shape, drop_copy, dtype):
+    """Stages whose copies are never issued: the waits run out, the status says so, and the next call is right."""
+    import torch
+    x, w, _, _ = tensors(torch, dtype, *shape, seed=8, bias=False, residual=False)
+    y = torch.empty(shape[0], shape[2], dtype=x.dtype, device="cuda")
+    sc.check(sc.sc_test_linear_wait_expiry(x, w, y, *shape, dtype, drop_copy, 2000), "sc_test_linear_wait_expiry")
+    assert sc.sc_last_device_status() == sc.SC_ERR_DEVICE_TIMEOUT
+    assert sc.sc_last_device_status() == sc.SC_OK
+    check(torch, run(torch, sc, x, w, None, None, 0, dtype), x, w, None, None, 0, dtype)
+
+
+def test_wait_expiry_hook_refusals():
+    assert scl.sc_test_linear_wait_expiry(None, B, C, 5, 64, 32, BF16, 0, 10, stream=0) == scl.SC_ERR_NULL
+    assert scl.sc_test_linear_wait_expiry(A, B, C, 5, 64, 32, BF16, -1, 10, stream=0) == scl.SC_ERR_SHAPE
+    assert scl.sc_test_linear_wait_expiry(A, B, C, 5, 64, 32, BF16, 0, 0, stream=0) == scl.SC_ERR_SHAPE
+    assert scl.sc_test_linear_wait_expiry(A, B, C, 5, 60, 32, BF16, 0, 10, stream=0) == scl.SC_ERR_UNSUPPORTED
