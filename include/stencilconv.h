@@ -499,7 +499,8 @@ int kv_quantize_fwd(const sc_quant_states *k, const sc_quant_states *v, const in
  * scale that is rounded to bf16, or taken in three planes.
  * The output is rounded once (to nearest even).
  * Supported: D % 16 == 0, D <= 128; block 16, 32, 64 or 128; strides of k and v
- * below 2^40 bytes; otherwise as cross_attention_fwd.  Returns SC_OK or a negative sc_status.
+ * below 2^40 bytes, their token strides above 0; otherwise as
+ * cross_attention_fwd.  Returns SC_OK or a negative sc_status.
  */
 int cross_attention_q8_fwd(const void *q, const void *k, const float *k_scale, const void *v, const float *v_scale,
                            void *out, float *lse, const int *k_len, const unsigned char *key_mask, int N, int Tq, int Tk,

@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitAr
 // 8-bit states for the tensor cores: codes as bf16, which holds every one exactly
 // (0 for states that are not valid), and the factor of each 16 keys, which lie in
 // one block:
-//   keys    |scale of the block| * scale * log2 e, at least fp32's smallest normal number (so that it times
-//           minus infinity, the score of a key that is not valid, is not NaN); a negative scale turns the codes
+//   keys    scale of the block * scale * log2 e, fp32's smallest normal number where it is smaller (so that
+//           it times an infinity, the score of a key that is not valid, is not NaN)
 //   values  the block's scale
 // Groups without a valid state get that smallest number and 0, whatever their scale
 // is.  Bound by memory: a byte read and two written an element.
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kSplitThreads) attn_expand_kernel(const Expand
             float kf = 0x1p-126f, vf = 0.f;
             if (any) {
                 const long long at = nh * a.blocks + (t0 >> a.log2_block);
-                kf = fabsf(a.k_scale[at]) * x.scale;
-                if (kf < 0x1p-126f) kf = 0x1p-126f;   // (a NaN stays)
+                kf = a.k_scale[at] * x.scale;
+                if (fabsf(kf) < 0x1p-126f) kf = 0x1p-126f;   // (a NaN stays)
                 vf = a.v_scale[at];
             }
             x.k_factor[e] = kf;
@@ -167,18 +167,14 @@ __global__ void __launch_bounds__(kSplitThreads) attn_expand_kernel(const Expand
         const long long row = e / chunks, nh = row / a.Tk;
         const int c = (int)(e - row * chunks), t = (int)(row - nh * a.Tk), n = (int)(nh / a.Hkv), h = (int)(nh - (long long)n * a.Hkv);
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        uint32_t sign = 0;
         const bool on = t < length(n) && (!a.key_mask || a.key_mask[(long long)n * a.Tk + t] != 0);
-        if (on) {
-            w = __ldg(reinterpret_cast<const uint4 *>(src + n * s.n + t * s.t + h * s.h + c * 16));
-            if (!value && a.k_scale[nh * a.blocks + (t >> a.log2_block)] < 0.f) sign = 0x80008000u;
-        }
+        if (on) w = __ldg(reinterpret_cast<const uint4 *>(src + n * s.n + t * s.t + h * s.h + c * 16));
         const uint32_t b[4] = {w.x, w.y, w.z, w.w};
         uint32_t y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            y[2 * i] = on ? pair_to_bf16<E4M3>(b[i] & 0xffffu) ^ sign : 0u;
-            y[2 * i + 1] = on ? pair_to_bf16<E4M3>(b[i] >> 16) ^ sign : 0u;
+            y[2 * i] = on ? pair_to_bf16<E4M3>(b[i] & 0xffffu) : 0u;
+            y[2 * i + 1] = on ? pair_to_bf16<E4M3>(b[i] >> 16) : 0u;
         }
         uint4 *out = reinterpret_cast<uint4 *>(dst + e * 8);
         out[0] = make_uint4(y[0], y[1], y[2], y[3]);
@@ -202,16 +198,21 @@ cudaError_t launch_attn_split(const AttnArgs &a, bool bf16, void *const (&planes
     const HeadStrides hs[3] = {a.qs, a.ks, a.vs};
     long long most = 0;
     for (int i = 0; i < 3; ++i) {
+        if (!planes[i]) {   // not asked for
+            s.p[i] = SplitPart{};
+            continue;
+        }
         s.p[i] = split_part_of(x[i], planes[i], hs[i], a.N, i ? a.Tk : a.Tq, i ? a.Hkv : a.Hq, i ? 1 : a.G, a.D);
         if (s.p[i].chunks > most) most = s.p[i].chunks;
     }
     long long blocks = (most + kSplitThreads - 1) / kSplitThreads;
     const long long cap = 16LL * device_sm_count();
     if (blocks > cap) blocks = cap;
+    const dim3 grid((unsigned)blocks, planes[1] ? 3 : 1);
     if (bf16)
-        attn_split_kernel<true><<<dim3((unsigned)blocks, 3), kSplitThreads, 0, st>>>(s);
+        attn_split_kernel<true><<<grid, kSplitThreads, 0, st>>>(s);
     else
-        attn_split_kernel<false><<<dim3((unsigned)blocks, 3), kSplitThreads, 0, st>>>(s);
+        attn_split_kernel<false><<<grid, kSplitThreads, 0, st>>>(s);
     return cudaGetLastError();
 }
 

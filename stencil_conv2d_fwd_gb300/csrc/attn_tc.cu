@@ -89,6 +89,7 @@ constexpr int key_tile() { return PL == 3 && DP == 128 ? 64 : 128; }
 constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 216, REGS_OTHER = 72;
 constexpr int THREADS = 384;
 constexpr int MAX_SLOTS = 12;
+constexpr int CODE_RING = 32768;       // bytes of the ring of codes: 2 or 4 key tiles
 constexpr int VC = 8;                  // barriers of cleared value tiles: more than the ring holds
 constexpr int LIST = 512;              // key tiles of a share that are looked through; a longer share keeps all
 constexpr int GRID_Y = 32768;          // (sequence, key head) pairs of a grid's y axis
@@ -102,9 +103,12 @@ struct Geom {
     int splits;           // CTAs that share a row unit's keys
     bool packed;          // q is the workspace's copy (attn_split.cu)
     bool behind;          // k and v, or q, are written by the launch before
-    // 8-bit states: factors of 16 keys each, [N * Hkv][groups] (attn_split.cu)
+    // 8-bit states: scales of 2^log2_group keys each, [N * Hkv][groups], of which the
+    // keys' times k_times are the scores' factors
     const float *k_factor, *v_factor;
-    int groups;
+    int groups, log2_group;
+    float k_times;
+    bool e4m3;
     int k_axes[2], v_axes[2];        // whether the maps' (h, n) are axes (1), or shared by all (0)
 };
 
@@ -198,6 +202,27 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+// Two int8 codes, each the low byte of a half, as bf16: 128 + (x mod 128) and 128, or
+// 256 for a negative x, are exact, and so is their difference.
+__device__ __forceinline__ uint32_t i8_pair_to_bf16(uint32_t x)
+{
+    uint32_t a, b, y;
+    asm("lop3.b32 %0, %1, 0x007f007f, %2, 0xea;" : "=r"(a) : "r"(x), "r"(0x43004300u));
+    asm("lop3.b32 %0, %1, 0x00800080, %2, 0xea;" : "=r"(b) : "r"(x), "r"(0x43004300u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+// The two e4m3 codes in the low half, as bf16.
+__device__ __forceinline__ uint32_t e4m3_pair_to_bf16(uint32_t x)
+{
+    float lo, hi;
+    asm("{\n.reg .b16 l, h;\n.reg .b32 p;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 p, l;\nmov.b32 {l, h}, p;\n"
+        "cvt.f32.f16 %0, l;\ncvt.f32.f16 %1, h;\n}\n"
+        : "=f"(lo), "=f"(hi)
+        : "r"(x));
+    return tc::pack_bf16(lo, hi);
+}
+
 // The largest of three, one instruction at the rate of a maximum of two.
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -237,6 +262,7 @@ struct Shared {
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], q_full, s_full[2], o_full[2], drain;
     uint64_t vclean[VC];
     uint64_t p_full[2][2];
+    uint64_t code_full[4], code_empty[4];   // 8-bit states
     uint32_t words[2][2][4];           // valid bits of a key tile, per stream, two tiles deep
     float factors[Q8 ? 2 : 1][Q8 ? 2 : 1][Q8 ? 16 : 1];   // 8-bit states: a key tile's factors of keys, then of values
     float m[PAIR ? 1 : TILE], l[PAIR ? 1 : TILE];   // stream 1's, at the end
@@ -259,7 +285,8 @@ constexpr int q_region()
 template <int DP, int PL, bool PAIR, bool Q8>
 constexpr int ring_slots()
 {
-    const int n = ((int)SMEM_CAP - q_region<DP, PL, PAIR>() - (int)sizeof(Shared<PAIR, Q8>)) / (DP / 64 * key_tile<DP, PL>() * 128);
+    const int n = ((int)SMEM_CAP - q_region<DP, PL, PAIR>() - (Q8 && !PAIR ? CODE_RING : 0) - (int)sizeof(Shared<PAIR, Q8>)) /
+                  (DP / 64 * key_tile<DP, PL>() * 128);
     return n < MAX_SLOTS ? n : MAX_SLOTS;
 }
 
@@ -270,9 +297,14 @@ struct Bool {
 
 // PL operand planes: 1 (bf16 tensors), or 3 (fp32 tensors split into three
 // bf16 planes, see attn_split.cu).
-// Q8: 8-bit states.  Keys and values are one plane of codes, exact in bf16
-// (attn_split.cu), and the scales enter the scores and the weights in fp32, 16
-// keys at a time.
+// Q8: 8-bit states.  Keys and values are one plane of codes, exact in bf16, and the
+// scales enter the scores and the weights in fp32, 16 keys at a time.  With one row
+// tile a CTA (CODES) the tiles are copied as codes and warps 10 and 11 write them to
+// the ring as bf16: 32 x 77 queries over 3136 states, 8 heads of 64, 84 us, where
+// codes expanded in memory first took 105 (bf16 states take 46: the two warps are the
+// bound).  Two row tiles, whose ring the two
+// warps would not keep up with and whose arithmetic hides the expansion's cost, get
+// them from attn_split.cu.
 template <int DP, int PL, bool PAIR, bool Q8>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -287,8 +319,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int KBLK = KT * 128;              // bytes of a key tile's rows of 64 bf16
     constexpr int SLOT = DB * KBLK;
     constexpr int SLOTS = ring_slots<DP, PL, PAIR, Q8>();
+    constexpr bool CODES = Q8 && !PAIR;
+    constexpr int CSLOT = KT * DP, CSLOTS = CODES ? CODE_RING / CSLOT : 1;   // the ring of codes
     extern __shared__ __align__(1024) unsigned char dyn[];
-    Shared<PAIR, Q8> &sh = *reinterpret_cast<Shared<PAIR, Q8> *>(dyn + q_region<DP, PL, PAIR>() + SLOTS * SLOT);
+    constexpr int CODE_AT = q_region<DP, PL, PAIR>() + SLOTS * SLOT;
+    Shared<PAIR, Q8> &sh = *reinterpret_cast<Shared<PAIR, Q8> *>(dyn + CODE_AT + (CODES ? CODE_RING : 0));
 
     // (the shuffle makes the warp's number, and all that follows from it, uniform)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -343,6 +378,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int tile = seq < l0 ? seq : (s >= both ? nt - l0 + s - both : (value ? s / 2 : l0 + s / 2));
         const int *ax = value ? g.v_axes : g.k_axes;
         const int key0 = tile_key(tile);
+        if constexpr (CODES) {
+            const uint32_t slot = issued % CSLOTS, round = issued / CSLOTS, bar = smem_u32(&sh.code_full[slot]);
+            if (round > 0) wait(sh.code_empty[slot], (round - 1) & 1);
+            if (*abort_flag) return;
+            if ((int)issued++ == test.drop_copy) return;
+            mbar_arrive_expect_tx(bar, CSLOT);
+            tma_load_5d(q_smem + CODE_AT + slot * CSLOT, value ? &mv : &mk, 0, key0, h * ax[0], n * ax[1], 0, bar);
+            return;
+        }
         for (int p = KPL - 1; p >= 0; --p, ++issued) {   // the smallest plane first
             const uint32_t slot = issued % SLOTS, round = issued / SLOTS;
             const uint32_t bar = smem_u32(&sh.full[slot]);
@@ -359,7 +403,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int release = !Q8 && (mb || len < a.Tk) ? 3 : 1;   // arrivals of `empty`: 3 where value rows are cleared (`ragged` below)
         for (int i = lane; i < BARS; i += 32)
             mbar_init(smem_u32(&sh.full[0]) + 8 * i,
-                      i < BARS_ONE ? (i >= MAX_SLOTS && i < 2 * MAX_SLOTS ? release : 1) : (i < BARS_TWO ? 2 : 4));
+                      i < BARS_ONE ? (i >= MAX_SLOTS && i < 2 * MAX_SLOTS ? release : (CODES && i < MAX_SLOTS ? 2 : 1))
+                                   : (i < BARS_TWO ? 2 : 4));
+        if (CODES && lane < 8) mbar_init(smem_u32(&sh.code_full[0]) + 8 * lane, lane < 4 ? 1 : 2);
         if (lane == 0) sh.abort = 0;
         fence_mbar_init();
         __syncwarp();
@@ -513,6 +559,84 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             __syncwarp();
+        } else if constexpr (CODES) {
+            // codes to bf16, each warp half of a tile's rows, in the order of the copies
+            constexpr int CH = DP / 16, HALF = KT / 2, WORDS = HALF / 32;   // 16-byte chunks of a row; rows; their bits
+            const int r0 = (warp - 10) * HALF;
+            const uint32_t chunk = lane % CH;
+            auto convert = [&](uint32_t e, bool value, int key0) {
+                // values that are not valid are 0: bits of the warp's rows, whose mask is
+                // on its way while the copy is waited for
+                const bool plain = !value || (!mb && key0 + KT <= len);
+                bool on[WORDS];
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) {
+                    const int key = key0 + r0 + 32 * i + lane;
+                    on[i] = plain || (key < len && (!mb || mb[key] != 0));
+                }
+                const uint32_t cs = e % CSLOTS, slot = e % SLOTS;
+                wait(sh.code_full[cs], (e / CSLOTS) & 1);
+                if (e >= (uint32_t)SLOTS) wait(sh.empty[slot], (e / SLOTS - 1) & 1);
+                uint32_t bits[WORDS];
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) bits[i] = plain ? ~0u : __ballot_sync(0xffffffffu, on[i]);
+                const uint32_t from = q_smem + CODE_AT + cs * CSLOT + (r0 * CH + lane) * 16, to = ring + slot * SLOT;
+                // four chunks at a time, so that their instructions overlap
+#pragma unroll 1
+                for (int i0 = 0; i0 < HALF * CH / 32; i0 += 4) {
+                    uint32_t c[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                                     : "=r"(c[i][0]), "=r"(c[i][1]), "=r"(c[i][2]), "=r"(c[i][3])
+                                     : "r"(from + (i0 + i) * 512));
+                    uint32_t y[4][8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (g.e4m3) {
+                                y[i][2 * k] = e4m3_pair_to_bf16(c[i][k]);
+                                y[i][2 * k + 1] = e4m3_pair_to_bf16(c[i][k] >> 16);
+                            } else {
+                                y[i][2 * k] = i8_pair_to_bf16(__byte_perm(c[i][k], 0u, 0x4140));
+                                y[i][2 * k + 1] = i8_pair_to_bf16(__byte_perm(c[i][k], 0u, 0x4342));
+                            }
+                        }
+                    if (!plain) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = (i0 + i) * (32 / CH) + lane / CH;   // of the warp's
+                            uint32_t word = bits[0];
+#pragma unroll
+                            for (int k = 1; k < WORDS; ++k) word = row / 32 == k ? bits[k] : word;
+                            const bool bit = word >> (row & 31) & 1u;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) y[i][k] = bit ? y[i][k] : 0u;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = r0 + (i0 + i) * (32 / CH) + lane / CH;
+                        const uint32_t at = to + (chunk / 4) * KBLK + row * 128, q = chunk % 4 * 2;
+                        tc::st_shared_v4(at + ((q ^ (row & 7)) << 4), y[i][0], y[i][1], y[i][2], y[i][3]);
+                        tc::st_shared_v4(at + (((q + 1) ^ (row & 7)) << 4), y[i][4], y[i][5], y[i][6], y[i][7]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh.code_empty[cs]));
+                    mbar_arrive(smem_u32(&sh.full[slot]));
+                }
+            };
+            uint32_t e = 0;
+            for (int j = 0; j < LAG && j < nt; ++j) convert(e++, false, tile_key(j));
+#pragma unroll 1
+            for (int j = 0; j < nt; ++j) {
+                convert(e++, true, tile_key(j));
+                if (j + LAG < nt) convert(e++, false, tile_key(j + LAG));
+            }
         } else if (ragged) {
             // value rows that are not valid: zero, in every plane and block.
             // A barrier's parity tells a round only from its neighbours, so these
@@ -595,7 +719,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto factor = [&](int j) {
             if (j >= nt || row >= 2 * KG) return 0.f;
             const float *f = row < KG ? g.k_factor : g.v_factor;
-            return __ldg(f + (long long)nh * g.groups + tile_key(j) / 16 + row % KG);
+            const float x = __ldg(f + (long long)nh * g.groups + (min(tile_key(j) + 16 * (row % KG), len - 1) >> g.log2_group));
+            if (row >= KG) return x;
+            const float y = x * g.k_times;
+            return fabsf(y) < 0x1p-126f ? 0x1p-126f : y;   // (times an infinity it is not NaN; a NaN stays)
         };
         if (Q8 && g.behind) pdl_wait();   // the factors are the launch before's
         float next_factor = Q8 ? factor(PAIR ? 0 : i) : 0.f;
@@ -606,14 +733,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[i][part]));
         };
-        // 32 scores from column 32 e; those that are not valid become -infinity
-        auto load_scores = [&](int e, uint32_t (&s)[32], uint32_t w, bool masked) {
+        // 32 scores from column 32 e; those that are not valid become -infinity times the
+        // sign of their factor (f0 of the first 16, f1 of the others)
+        auto load_scores = [&](int e, uint32_t (&s)[32], uint32_t w, bool masked, float f0, float f1) {
             tc::tmem_ld<32>(ts + e * 32, s);
             tc::tmem_wait_ld();
             if (masked) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                    if (!((w >> k) & 1u)) s[k] = 0xff800000u;
+                    if (!((w >> k) & 1u)) s[k] = Q8 && (k < 16 ? f0 : f1) < 0.f ? 0x7f800000u : 0xff800000u;
             }
         };
         for (int j = PAIR ? 0 : i; j < nt; j += step, ++use) {
@@ -660,6 +788,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                     kf[e] = sh.factors[i][use & 1][e];
                     vf[e] = sh.factors[i][use & 1][KG + e];
                 }
+                if (masked) {   // the scale of keys none of which is valid may be anything
+#pragma unroll
+                    for (int e = 0; e < KG; ++e)
+                        if ((w[e / 2] >> (16 * (e & 1)) & 0xffffu) == 0) {
+                            kf[e] = 0x1p-126f;
+                            vf[e] = 0.f;
+                        }
+                }
+            }
+            // negative scales: a group's largest product is not its largest score
+            bool negative = false;
+            if constexpr (Q8) {
+                float least = kf[0];
+#pragma unroll
+                for (int e = 1; e < KG; ++e) least = fminf(least, kf[Q8 ? e : 0]);
+                negative = least < 0.f;
             }
             auto key_factor = [&](int k) { return Q8 ? kf[Q8 ? k / 16 : 0] : c; };   // of key k of the tile
             wait(sh.s_full[i], use & 1);
@@ -674,7 +818,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            if (!((w[e] >> k) & 1u)) s[e][k] = 0xff800000u;
+                            if (!((w[e] >> k) & 1u)) s[e][k] = Q8 && key_factor(32 * e + k) < 0.f ? 0x7f800000u : 0xff800000u;
                 }
                 float mx[4];
 #pragma unroll
@@ -696,6 +840,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int k = 3; k < 15; k += 2)
                             z = max3(z, __uint_as_float(s[e / 2][e % 2 * 16 + k]), __uint_as_float(s[e / 2][e % 2 * 16 + k + 1]));
                         top = fmaxf(top, fmaxf(z, __uint_as_float(s[e / 2][e % 2 * 16 + 15])) * kf[Q8 ? e : 0]);
+                    }
+                    if (negative) {
+                        top = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(s[e][k]) * key_factor(32 * e + k));
                     }
                 }
                 const bool grow = top - m > GROW;   // false where both are -infinity
@@ -748,12 +899,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < KW; ++e) {
                     uint32_t s[32];
-                    load_scores(e, s, w[e], masked);
+                    load_scores(e, s, w[e], masked, key_factor(32 * e), key_factor(32 * e + 16));
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
                         if (Q8 && k % 16 == 0) mx[0] = mx[1] = -INFINITY;
                         mx[k / 2 & 1] = max3(mx[k / 2 & 1], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
                         if (Q8 && k % 16 == 14) top8 = fmaxf(top8, fmaxf(mx[0], mx[1]) * key_factor(32 * e + k));
+                        if (Q8 && negative)
+                            top8 = fmaxf(top8, fmaxf(__uint_as_float(s[k]) * key_factor(32 * e + k), __uint_as_float(s[k + 1]) * key_factor(32 * e + k)));
                         if (e >= KW - HOLD) {
                             hold[e - (KW - HOLD)][k] = s[k];
                             hold[e - (KW - HOLD)][k + 1] = s[k + 1];
@@ -782,7 +935,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int e = 0; e < KW; ++e) {
                     uint32_t s[32];
                     if (e < KW - HOLD) {
-                        load_scores(e, s, w[e], masked);
+                        load_scores(e, s, w[e], masked, key_factor(32 * e), key_factor(32 * e + 16));
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) s[k] = hold[HOLD > 0 ? e - (KW - HOLD) : 0][k];
@@ -953,8 +1106,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (tid == 0) atomicExch(status, kDeviceTimeout);
         if (warp == 8 && lane == 0) {
             if (q_tiles > 0) (void)mbar_wait_bounded(smem_u32(&sh.q_full), 0, test.timeout_ns);
-            for (uint32_t e = issued > (uint32_t)SLOTS ? issued - SLOTS : 0; e < issued; ++e)
-                (void)mbar_wait_bounded(smem_u32(&sh.full[e % SLOTS]), (e / SLOTS) & 1, test.timeout_ns);
+            if constexpr (CODES) {
+                for (uint32_t e = issued > (uint32_t)CSLOTS ? issued - CSLOTS : 0; e < issued; ++e)
+                    (void)mbar_wait_bounded(smem_u32(&sh.code_full[e % CSLOTS]), (e / CSLOTS) & 1, test.timeout_ns);
+            } else {
+                for (uint32_t e = issued > (uint32_t)SLOTS ? issued - SLOTS : 0; e < issued; ++e)
+                    (void)mbar_wait_bounded(smem_u32(&sh.full[e % SLOTS]), (e / SLOTS) & 1, test.timeout_ns);
+            }
         }
         if (warp == 9) {
             mma_commit(elect_one(), smem_u32(&sh.drain));   // by the thread that issued the products
@@ -983,6 +1141,20 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
 
 // A map of rows of D elements with four outer axes (strides in bytes), boxes of
 // 128 bytes of box1 x box2 rows.
+bool encode_codes(CUtensorMap *m, const void *base, int D, int DP, const long long (&size)[4], const long long (&stride)[4], int box1)
+{
+    cuuint64_t dims[5] = {(cuuint64_t)D}, strides[4];
+    for (int i = 0; i < 4; ++i) {
+        dims[i + 1] = (cuuint64_t)size[i];
+        strides[i] = size[i] == 1 ? 16 : (cuuint64_t)stride[i];
+    }
+    const cuuint32_t box[5] = {(cuuint32_t)DP, (cuuint32_t)box1, 1, 1, 1};   // whole heads, as they lie
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(base), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_map(CUtensorMap *m, bool bf16, const void *base, int D, const long long (&size)[4], const long long (&stride)[4],
                 int box1, int box2)
 {
@@ -1010,7 +1182,8 @@ cudaError_t launch(const AttnArgs &a, const Geom &g, const Maps &m, const AttnPa
                    const TcTest &test)
 {
     constexpr int SMEM = q_region<DP, PL, PAIR>() + ring_slots<DP, PL, PAIR, Q8>() * (DP / 64 * key_tile<DP, PL>() * 128) +
-                         (int)sizeof(Shared<PAIR, Q8>);
+                         (Q8 && !PAIR ? CODE_RING : 0) + (int)sizeof(Shared<PAIR, Q8>);
+    static_assert(SMEM <= (int)SMEM_CAP, "shared memory");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1091,9 +1264,9 @@ static cudaError_t attn_tc(const AttnArgs &a, const AttnQ8Args *q8, bool e4m3, b
     // not shared
     g.packed = !bf16 || (a.G > 1 && a.qs.h == 0) || (a.Tq > 1 && a.qs.t == 0) || (a.Hkv > 1 && a.qs.h == 0) ||
                (a.N > 1 && a.qs.n == 0) || (!q8 && a.Tk > 1 && (a.ks.t == 0 || a.vs.t == 0));
-    // 8-bit states are expanded to one plane of bf16 codes
-    const bool kv_packed = g.packed || q8;
-    g.behind = kv_packed;
+    // 8-bit states: tiles of codes (one row tile a CTA), or expanded to one plane of bf16
+    const bool codes = q8 && !pair, kv_packed = q8 ? !codes : g.packed;
+    g.behind = g.packed || kv_packed;
     const int planes = bf16 ? 1 : 3, kv_planes = q8 ? 1 : planes;
     const long long rows = (long long)a.N * a.Hq * a.Tq, keys = (long long)a.N * a.Hkv * a.Tk;
     g.k_axes[0] = kv_packed || a.ks.h != 0;
@@ -1108,8 +1281,8 @@ static cudaError_t attn_tc(const AttnArgs &a, const AttnQ8Args *q8, bool e4m3, b
     const size_t pq = g.packed ? pad((size_t)rows * a.D * 2 * planes) : 0;
     const size_t pk = kv_packed ? pad((size_t)keys * a.D * 2 * kv_planes) : 0;
     // a key tile's groups, whole
-    g.groups = (int)((a.Tk + 127LL) / 128 * 8);
-    const size_t pf = q8 ? pad((size_t)a.N * a.Hkv * g.groups * 4) : 0;
+    g.groups = codes ? q8->blocks : (int)((a.Tk + 127LL) / 128 * 8);
+    const size_t pf = q8 && !codes ? pad((size_t)a.N * a.Hkv * g.groups * 4) : 0;
     char *ws = nullptr;
     if (po + pml + pq + pk > 0) {
         const cudaError_t e = workspace_alloc(reinterpret_cast<void **>(&ws), po + pml + pq + 2 * pk + 2 * pf, st);
@@ -1120,8 +1293,11 @@ static cudaError_t attn_tc(const AttnArgs &a, const AttnQ8Args *q8, bool e4m3, b
     void *const plane[3] = {ws + po + pml, ws + po + pml + pq, ws + po + pml + pq + pk};
     float *const factor[2] = {reinterpret_cast<float *>(ws + po + pml + pq + 2 * pk),
                               reinterpret_cast<float *>(ws + po + pml + pq + 2 * pk + pf)};
-    g.k_factor = factor[0];
-    g.v_factor = factor[1];
+    g.k_factor = codes ? q8->k_scale : factor[0];
+    g.v_factor = codes ? q8->v_scale : factor[1];
+    g.log2_group = codes ? q8->log2_block : 4;
+    g.k_times = codes ? a.scale * kLog2e : 1.f;
+    g.e4m3 = e4m3;
 
     at::Maps m;
     std::memset(&m, 0, sizeof(m));
@@ -1143,6 +1319,11 @@ static cudaError_t attn_tc(const AttnArgs &a, const AttnQ8Args *q8, bool e4m3, b
         const long long lying[2][4] = {{a.Tk, s.h ? a.Hkv : 1, s.n ? a.N : 1, 1}, {s.t * 2, s.h * 2, s.n * 2, 16}};
         const void *p = kv_packed ? plane[1 + i] : (i ? a.v : a.k);
         const auto &map = kv_packed ? packed : lying;
+        if (codes) {
+            const long long bytes[4] = {s.t, s.h, s.n, 16};
+            ok = ok && at::encode_codes(i ? &m.v : &m.k, p, a.D, a.D <= 64 ? 64 : 128, lying[0], bytes, kt);
+            continue;
+        }
         ok = ok && at::encode_map(i ? &m.v : &m.k, true, p, a.D, map[0], map[1], kt, 1);
     }
     if (part.parts > 0) {
@@ -1156,10 +1337,12 @@ static cudaError_t attn_tc(const AttnArgs &a, const AttnQ8Args *q8, bool e4m3, b
         ok = ok && at::encode_map(&m.out, bf16, a.out, a.D, size, stride, g.gb, g.tb);
     }
     cudaError_t e = ok ? cudaSuccess : cudaErrorInvalidValue;
-    if (e == cudaSuccess && q8)
+    if (e == cudaSuccess && q8 && !codes)
         e = launch_attn_expand(*q8, bf16, e4m3, g.packed ? plane[0] : nullptr, plane[1], plane[2], factor[0], factor[1], g.groups, st);
-    else if (e == cudaSuccess && g.packed)
-        e = launch_attn_split(a, bf16, plane, st);
+    else if (e == cudaSuccess && g.packed) {
+        void *const only_q[3] = {plane[0], nullptr, nullptr};
+        e = codes ? launch_attn_split(a, bf16, only_q, st) : launch_attn_split(a, bf16, plane, st);
+    }
     if (e == cudaSuccess)
         e = q8 ? at::dispatch<true>(a, g, m, part, bf16, pair, st, test) : at::dispatch<false>(a, g, m, part, bf16, pair, st, test);
     if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st);

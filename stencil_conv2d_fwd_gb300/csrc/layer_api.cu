@@ -234,7 +234,8 @@ int cross_attention_q8_fwd(const void *q, const void *k, const float *k_scale, c
     rc = sc::take_attention(q, k, v, out, lse, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, scale, dtype, 1, strides, a);
     if (rc != SC_OK) return rc;
     if (!sc::aligned(k_scale, 4) || !sc::aligned(v_scale, 4)) return SC_ERR_ALIGN;
-    // a tensor map's strides
+    // a tensor map's strides; states of one stride 0 would be one state
+    if (Tk > 1 && (a.ks.t == 0 || a.vs.t == 0)) return SC_ERR_UNSUPPORTED;
     if (a.ks.n >= kMaxMapStride || a.ks.t >= kMaxMapStride || a.ks.h >= kMaxMapStride || a.vs.n >= kMaxMapStride ||
         a.vs.t >= kMaxMapStride || a.vs.h >= kMaxMapStride)
         return SC_ERR_UNSUPPORTED;
@@ -254,9 +255,7 @@ int cross_attention_q8_fwd(const void *q, const void *k, const float *k_scale, c
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SC_BF16, e4m3 = code == SC_CODE_E4M3;
     const long long rows = (long long)Tq * a.G;
-    // (states that share one row by a stride of 0 cannot be copied tile by tile)
-    const bool few = rows <= 16 && (Tk == 1 || (a.ks.t > 0 && a.vs.t > 0));
-    return sc::from_cuda(few ? sc::launch_attn_q8(a, bf16, e4m3, st) : sc::launch_attn_tc_q8(a, bf16, e4m3, st));
+    return sc::from_cuda(rows > 16 ? sc::launch_attn_tc_q8(a, bf16, e4m3, st) : sc::launch_attn_q8(a, bf16, e4m3, st));
 }
 
 }  // extern "C"

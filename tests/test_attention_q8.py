@@ -208,10 +208,26 @@ def test_scales_and_queries_far_apart(sc, dtype, Tq):
     e = torch.arange(vs.shape[2], device="cuda") % 41
     vs *= 2.0 ** (e - 20.0)
     vs[..., 3], ks[..., 5] = 0.0, 0.0
+    ks[..., 8::7] *= -1   # no call writes such scales, but they have a meaning
     for t in range(Tq):
         f = [1.0, 2.0 ** -60, 2.0 ** 20, 0.0][t % 4]
         q[:, t] *= f
     run_and_check(torch, sc, (q, k, ks, v, vs), dtype, I8, block, scale=2.0 ** -18 / 8 if Tq > 2 else 0.125)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tq,H,D", [(3, 2, 64), (90, 2, 64), (300, 80, 64), (300, 80, 128)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_negative_scales(sc, dtype, Tq, H, D, masked):
+    """Every other block of keys turned by its scale, under a mask and a length; one and two row tiles a CTA."""
+    import torch
+    N, Tk, block = 1, 400, 16
+    q, k, ks, v, vs = make(torch, dtype, E4M3, N, Tq, Tk, H, H, D, block, seed=11)
+    ks[..., 1::2] *= -1
+    vs[..., ::3] *= -1
+    mask = (np.random.default_rng(1).random((N, Tk)) < 0.7).astype(np.uint8) if masked else None
+    run_and_check(torch, sc, (q, k, ks, v, vs), dtype, E4M3, block, key_mask=mask, k_len=[390] if masked else None)
 
 
 @pytest.mark.gpu
@@ -330,6 +346,8 @@ A, B, C, D_, E, G = (1 << k for k in (20, 24, 28, 32, 34, 36))
     (dict(ks=C + 2), scl.SC_ERR_ALIGN), (dict(vs=C + 1), scl.SC_ERR_ALIGN), (dict(out=G + 8), scl.SC_ERR_ALIGN),
     (dict(strides=((256, 64, 32), (1280, 40, 16), (1280, 32, 16), (256, 64, 32))), scl.SC_ERR_ALIGN),
     (dict(strides=((256, 64, 32), (1280, -32, 16), (1280, 32, 16), (256, 64, 32))), scl.SC_ERR_SHAPE),
+    (dict(strides=((256, 64, 32), (1280, 64, 32), (1280, 0, 32), (256, 64, 32))), scl.SC_ERR_UNSUPPORTED),
+    (dict(strides=((256, 64, 32), (1 << 40, 64, 32), (1280, 64, 32), (256, 64, 32)), k=1 << 50), scl.SC_ERR_UNSUPPORTED),
     (dict(strides=((256, 64, 32), (1280, 32, 16), (1280, 32, 16), (256, 32, 32))), scl.SC_ERR_ALIAS),
     (dict(out=A), scl.SC_ERR_ALIAS), (dict(out=B + 16), scl.SC_ERR_ALIAS), (dict(out=C), scl.SC_ERR_ALIAS),
     (dict(out=G, lse=G + 4), scl.SC_ERR_ALIAS), (dict(lse=C + 4), scl.SC_ERR_ALIAS), (dict(lse=B), scl.SC_ERR_ALIAS),
