@@ -7,9 +7,9 @@ they lie in memory ([N][H][W][heads * D] is [N][H * W][heads][D]).  Queries
 (tokens of a decoder, or points of interest, each with a place in the image)
 and keys are normalised per head and rotated by their row and column, and the
 queries attend to the map.  A later step with new queries keeps the map's keys
-and values.
+and values, with --states in 8 bits.
 
-    python examples/feature_map_attention.py [--dtype bf16] [--size 720x1280]
+    python examples/feature_map_attention.py [--dtype bf16] [--size 720x1280] [--states i8]
 """
 import argparse
 import os
@@ -22,6 +22,7 @@ import stencil_conv2d_fwd_gb300 as sc  # noqa: E402
 
 HEADS, KEY_HEADS, D = 8, 2, 64      # four query heads share a key head
 FEATURES = 32
+BLOCK = 64                          # states that share a scale in 8 bits
 
 
 def make_weights(seed=0, device="cuda"):
@@ -39,9 +40,11 @@ def make_weights(seed=0, device="cuda"):
 
 
 class FeatureMap:
-    """Keys and values of N images [N][H][W] (fp32), padded to one size: valid[n] = (height, width)."""
+    """Keys and values of N images [N][H][W] (fp32), padded to one size: valid[n] = (height, width).
 
-    def __init__(self, images, weights, valid=None, dtype=sc.SC_F32):
+    code (SC_CODE_I8 or SC_CODE_E4M3): from the first queries on the states are held in 8 bits."""
+
+    def __init__(self, images, weights, valid=None, dtype=sc.SC_F32, code=None):
         N, H, W = images.shape
         dev, t = images.device, torch.bfloat16 if dtype == sc.SC_BF16 else torch.float32
         self.N, self.H, self.W, self.dtype, self.weights = N, H, W, dtype, weights
@@ -72,6 +75,16 @@ class FeatureMap:
             inside = (rows < hw[:, :1, None]) & (cols < hw[:, 1:, None])
             self.mask = inside.to(torch.uint8).contiguous()
         self._keys_ready = False
+        self.code, self.cache = code, None
+
+    def _quantize(self):
+        states, dev = self.H * self.W, self.k.device
+        codes = [torch.empty(self.N, states, KEY_HEADS, D, dtype=torch.int8, device=dev) for _ in range(2)]
+        scales = [torch.empty(self.N, KEY_HEADS, -(-states // BLOCK), device=dev) for _ in range(2)]
+        sc.check(sc.kv_quantize_fwd((self.k, codes[0], scales[0]), (self.v, codes[1], scales[1]), self.N, states, KEY_HEADS, D,
+                                    BLOCK, self.code, self.dtype, key_mask=self.mask), "kv_quantize_fwd")
+        self.cache = (codes[0], scales[0], codes[1], scales[1])
+        self.k = self.v = None
 
     def attend(self, q, places):
         """q [N][T][HEADS][D] (left as it is), places [2][N * T] int32: (row, column) of each query."""
@@ -85,8 +98,14 @@ class FeatureMap:
         sc.check(sc.qk_norm_rotary_fwd(queries, keys, self.table, D, D, self.side, 1e-6, sc.SC_ROT_HALF, axes=2,
                                        dtype=self.dtype), "qk_norm_rotary_fwd")
         self._keys_ready = True
-        sc.check(sc.cross_attention_fwd(qn, self.k, self.v, out, N, T, self.H * self.W, HEADS, KEY_HEADS, D, D ** -0.5,
-                                        self.dtype, key_mask=self.mask), "cross_attention_fwd")
+        if self.code is None:
+            sc.check(sc.cross_attention_fwd(qn, self.k, self.v, out, N, T, self.H * self.W, HEADS, KEY_HEADS, D, D ** -0.5,
+                                            self.dtype, key_mask=self.mask), "cross_attention_fwd")
+            return out
+        if self.cache is None:
+            self._quantize()
+        sc.check(sc.cross_attention_q8_fwd(qn, *self.cache, out, N, T, self.H * self.W, HEADS, KEY_HEADS, D, D ** -0.5, BLOCK,
+                                           self.code, self.dtype, key_mask=self.mask), "cross_attention_q8_fwd")
         return out
 
 
@@ -96,6 +115,7 @@ def main():
     ap.add_argument("--size", default="360x640")
     ap.add_argument("--images", type=int, default=2)
     ap.add_argument("--queries", type=int, default=100)
+    ap.add_argument("--states", choices=["as they are", "i8", "e4m3"], default="as they are")
     args = ap.parse_args()
     H, W = (int(s) for s in args.size.split("x"))
     dtype = sc.SC_BF16 if args.dtype == "bf16" else sc.SC_F32
@@ -103,7 +123,8 @@ def main():
     g = torch.Generator(device="cuda").manual_seed(1)
     images = torch.rand(args.images, H, W, device="cuda", generator=g)
     valid = [(H - 8 * i, W - 16 * i) for i in range(args.images)]
-    fmap = FeatureMap(images, make_weights(), valid, dtype)
+    code = {"i8": sc.SC_CODE_I8, "e4m3": sc.SC_CODE_E4M3}.get(args.states)
+    fmap = FeatureMap(images, make_weights(), valid, dtype, code)
     for T in (args.queries, 1, 1):      # points of interest, then single tokens
         q = torch.randn(args.images, T, HEADS, D, device="cuda", generator=g).to(t)
         places = torch.stack([torch.randint(0, s, (args.images * T,), device="cuda", generator=g, dtype=torch.int32)

@@ -470,8 +470,8 @@ typedef struct {
  * (NULL: all).  Others are not read; their codes, and the scales of blocks
  * without a valid state, are left as they were.
  * x : [N][Tk][Hkv][D] of `dtype`; k or v may be NULL (not both).  x, codes and
- *   scale do not overlap.  To append blocks of states to a cache, pass the
- *   addresses of the first new block.
+ *   scale do not overlap.  To append whole blocks of states to a cache of Tk
+ *   places, mask the others out.
  * Supported: D % 16 == 0, D <= 128; block 16, 32, 64 or 128; rows of x and of
  *   codes 16-byte aligned.  Returns SC_OK or a negative sc_status.
  */
@@ -496,7 +496,9 @@ int kv_quantize_fwd(const sc_quant_states *k, const sc_quant_states *v, const in
  * weight below 2^-28 of the largest one among its 16 or 32 neighbours keeps 2^-39
  * of that.
  * More rows: as in cross_attention_fwd, but that it is a weight times its state's
- * scale that is rounded to bf16, or taken in three planes.
+ * scale that is taken in three planes, or with bf16 tensors rounded to fp16 (one
+ * below 2^-20 of the row's largest keeps 2^-31 of that; v_scale 0, or between 2^-80
+ * and 2^80 in size).
  * The output is rounded once (to nearest even).
  * Supported: D % 16 == 0, D <= 128; block 16, 32, 64 or 128; strides of k and v
  * below 2^40 bytes, their token strides above 0; otherwise as

@@ -160,6 +160,8 @@ struct Q8Ring {
         ring = memory;
         bars = barriers;
         lane = threadIdx.x & 31;
+        if (lane < 2)   // the maps come beside the length
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<unsigned long long>(lane ? &m.v : &m.k)) : "memory");
         len = a.Tk;
         if (a.k_len) len = max(0, min(len, a.k_len[n]));
         const int pieces = (len + KP - 1) / KP;

@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitAr
     split_part<BF16>(a.p[blockIdx.y], a.D8);
 }
 
-// 8-bit states for the tensor cores: codes as bf16, which holds every one exactly
-// (0 for states that are not valid), and the factor of each 16 keys, which lie in
+// 8-bit states for the tensor cores: codes as bf16, or fp16 (the values of bf16
+// tensors), which hold every one exactly (0 for states that are not valid), and the factor of each 16 keys, which lie in
 // one block:
 //   keys    scale of the block * scale * log2 e, fp32's smallest normal number where it is smaller (so that
 //           it times an infinity, the score of a key that is not valid, is not NaN)
@@ -121,6 +121,20 @@ __device__ __forceinline__ uint32_t pair_to_bf16(uint32_t two)   // the two low 
         const float hi = __uint_as_float(0x4b000000u | (u >> 8 & 0xffu)) - 8388736.f;
         return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
     }
+}
+
+template <bool E4M3>
+__device__ __forceinline__ uint32_t pair_to_f16(uint32_t two)
+{
+    uint32_t h;
+    if constexpr (E4M3) {
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(h) : "r"(two));
+    } else {
+        // 1024 + (x + 128) in fp16, less 1152
+        const uint32_t u = __byte_perm(two ^ 0x8080u, 0x64646464u, 0x4140);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(u), "r"(0x64806480u));
+    }
+    return h;
 }
 
 template <bool BF16, bool E4M3>
@@ -173,8 +187,9 @@ __global__ void __launch_bounds__(kSplitThreads) attn_expand_kernel(const Expand
         uint32_t y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            y[2 * i] = on ? pair_to_bf16<E4M3>(b[i] & 0xffffu) : 0u;
-            y[2 * i + 1] = on ? pair_to_bf16<E4M3>(b[i] >> 16) : 0u;
+            // the values of bf16 tensors meet weights in fp16
+            y[2 * i] = !on ? 0u : (BF16 && value ? pair_to_f16<E4M3>(b[i] & 0xffffu) : pair_to_bf16<E4M3>(b[i] & 0xffffu));
+            y[2 * i + 1] = !on ? 0u : (BF16 && value ? pair_to_f16<E4M3>(b[i] >> 16) : pair_to_bf16<E4M3>(b[i] >> 16));
         }
         uint4 *out = reinterpret_cast<uint4 *>(dst + e * 8);
         out[0] = make_uint4(y[0], y[1], y[2], y[3]);

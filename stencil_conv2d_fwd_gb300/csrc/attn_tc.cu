@@ -212,6 +212,28 @@ __device__ __forceinline__ uint32_t i8_pair_to_bf16(uint32_t x)
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
     return y;
 }
+// Four codes as fp16, in order: an int8 x with its sign bit turned is the low byte
+// of 1024 + 128 + x.
+__device__ __forceinline__ void codes_to_f16(uint32_t x, bool e4m3, uint32_t &lo, uint32_t &hi)
+{
+    if (e4m3) {
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+            : "=r"(lo), "=r"(hi)
+            : "r"(x));
+    } else {
+        const uint32_t y = x ^ 0x80808080u, magic = 0x64646464u, bias = 0x64806480u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(y, magic, 0x4140)), "r"(bias));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(y, magic, 0x4342)), "r"(bias));
+    }
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+constexpr float WEIGHT = 64.f;   // fp16 weights are 64 P: up to 2^14 where a maximum has grown by 2^GROW
+
 // The two e4m3 codes in the low half, as bf16.
 __device__ __forceinline__ uint32_t e4m3_pair_to_bf16(uint32_t x)
 {
@@ -264,7 +286,7 @@ struct Shared {
     uint64_t p_full[2][2];
     uint64_t code_full[4], code_empty[4];   // 8-bit states
     uint32_t words[2][2][4];           // valid bits of a key tile, per stream, two tiles deep
-    float factors[Q8 ? 2 : 1][Q8 ? 2 : 1][Q8 ? 16 : 1];   // 8-bit states: a key tile's factors of keys, then of values
+    float factors[Q8 ? 2 : 1][Q8 ? 2 : 1][Q8 ? 24 : 1];   // 8-bit states: a key tile's factors of keys and of values, and the latter's sizes
     float m[PAIR ? 1 : TILE], l[PAIR ? 1 : TILE];   // stream 1's, at the end
     uint16_t tiles[LIST];              // the share's key tiles that have a valid state
     uint8_t any[LIST];                 // whether a tile has one
@@ -298,13 +320,16 @@ struct Bool {
 // PL operand planes: 1 (bf16 tensors), or 3 (fp32 tensors split into three
 // bf16 planes, see attn_split.cu).
 // Q8: 8-bit states.  Keys and values are one plane of codes, exact in bf16, and the
-// scales enter the scores and the weights in fp32, 16 keys at a time.  With one row
-// tile a CTA (CODES) the tiles are copied as codes and warps 10 and 11 write them to
-// the ring as bf16: 32 x 77 queries over 3136 states, 8 heads of 64, 84 us, where
+// scales enter the scores and the weights in fp32, 16 keys at a time.  With bf16
+// queries a weight times its scale and the values' codes are fp16 (2^-11; with bf16's
+// 2^-8 the error was half as large again as the output's rounding); the running
+// maximum is that of score + log2 |scale|, so that they stay within fp16's range
+// whatever the scales.
+// With one row tile a CTA (CODES) the tiles are copied as codes and warps 10 and 11
+// write them to the ring: 32 x 77 queries over 3136 states, 8 heads of 64, 79 us, where
 // codes expanded in memory first took 105 (bf16 states take 46: the two warps are the
-// bound).  Two row tiles, whose ring the two
-// warps would not keep up with and whose arithmetic hides the expansion's cost, get
-// them from attn_split.cu.
+// bound).  Two row tiles, whose ring the two warps would not keep up with and whose
+// arithmetic hides the expansion's cost, get them from attn_split.cu.
 template <int DP, int PL, bool PAIR, bool Q8>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -316,6 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int KT = key_tile<DP, PL>();
     constexpr int KPL = Q8 ? 1 : PL;            // planes of keys and values
     constexpr int KG = KT / 16;                 // groups of keys with one scale
+    constexpr bool HALF_V = Q8 && PL == 1;      // weights and values in fp16
     constexpr int KBLK = KT * 128;              // bytes of a key tile's rows of 64 bf16
     constexpr int SLOT = DB * KBLK;
     constexpr int SLOTS = ring_slots<DP, PL, PAIR, Q8>();
@@ -479,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp == 9) {
             if (nt > 0) {
                 const uint32_t one = elect_one();
-                const uint32_t idesc_s = tc::idesc_mma(1, KT), idesc_v = tc::idesc_mma(1, (a.D + 15) / 16 * 16) | (1u << 16);
+                const uint32_t idesc_s = tc::idesc_mma(1, KT), idesc_v = tc::idesc_mma(HALF_V ? 0 : 1, (a.D + 15) / 16 * 16) | (1u << 16);
                 wait(sh.q_full, 0);
                 // S of stream i from the key tile whose first plane is ring entry c
                 auto mma_s = [&](int i, uint32_t c, bool release) {
@@ -595,7 +621,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            if (g.e4m3) {
+                            if (HALF_V && value) {
+                                codes_to_f16(c[i][k], g.e4m3, y[i][2 * k], y[i][2 * k + 1]);
+                            } else if (g.e4m3) {
                                 y[i][2 * k] = e4m3_pair_to_bf16(c[i][k]);
                                 y[i][2 * k + 1] = e4m3_pair_to_bf16(c[i][k] >> 16);
                             } else {
@@ -717,10 +745,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         int next = mb ? mask_byte(PAIR ? 0 : i) : 0;
         // 8-bit states: this thread's factor of key tile j
         auto factor = [&](int j) {
-            if (j >= nt || row >= 2 * KG) return 0.f;
+            if (j >= nt || row >= 3 * KG) return 0.f;
             const float *f = row < KG ? g.k_factor : g.v_factor;
             const float x = __ldg(f + (long long)nh * g.groups + (min(tile_key(j) + 16 * (row % KG), len - 1) >> g.log2_group));
-            if (row >= KG) return x;
+            // (beyond 2^80 either way a size is taken as that: a sum of unscaled weights
+            // stays within fp32's range)
+            if (row >= 2 * KG) return fminf(fmaxf(__log2f(fabsf(x)), -80.f), 80.f);
+            if (row >= KG) return HALF_V ? x * WEIGHT : x;
             const float y = x * g.k_times;
             return fabsf(y) < 0x1p-126f ? 0x1p-126f : y;   // (times an infinity it is not NaN; a NaN stays)
         };
@@ -749,7 +780,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t w[KW];
             bool masked = key0 + KT > len;
             if constexpr (Q8) {
-                if (row < 2 * KG) sh.factors[i][use & 1][row] = next_factor;
+                if (row < 3 * KG) sh.factors[i][use & 1][row] = next_factor;
                 next_factor = factor(j + step);
             }
             if (mb) {
@@ -805,6 +836,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int e = 1; e < KG; ++e) least = fminf(least, kf[Q8 ? e : 0]);
                 negative = least < 0.f;
             }
+            auto size_of = [&](int e) { return sh.factors[i][use & 1][Q8 ? 2 * KG + e : 0]; };   // log2 of group e's value scale
             auto key_factor = [&](int k) { return Q8 ? kf[Q8 ? k / 16 : 0] : c; };   // of key k of the tile
             wait(sh.s_full[i], use & 1);
             tc::fence_after_sync();
@@ -839,14 +871,15 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int k = 3; k < 15; k += 2)
                             z = max3(z, __uint_as_float(s[e / 2][e % 2 * 16 + k]), __uint_as_float(s[e / 2][e % 2 * 16 + k + 1]));
-                        top = fmaxf(top, fmaxf(z, __uint_as_float(s[e / 2][e % 2 * 16 + 15])) * kf[Q8 ? e : 0]);
+                        top = fmaxf(top, fmaf(fmaxf(z, __uint_as_float(s[e / 2][e % 2 * 16 + 15])), kf[Q8 ? e : 0], size_of(e)));
                     }
                     if (negative) {
                         top = -INFINITY;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(s[e][k]) * key_factor(32 * e + k));
+                            for (int k = 0; k < 32; ++k)
+                                top = fmaxf(top, fmaf(__uint_as_float(s[e][k]), key_factor(32 * e + k), size_of(2 * e + k / 16)));
                     }
                 }
                 const bool grow = top - m > GROW;   // false where both are -infinity
@@ -884,7 +917,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             x *= vf[Q8 ? (e * 32 + k) / 16 : 0];
                             y *= vf[Q8 ? (e * 32 + k) / 16 : 0];
                         }
-                        p[k / 2] = tc::pack_bf16(x, y);
+                        p[k / 2] = HALF_V ? pack_f16(x, y) : tc::pack_bf16(x, y);
                     }
                     tmem_st32(ts + e * 16, p);
                     hand_over(e / 2);
@@ -981,7 +1014,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tmem_ld<32>(to + d, o);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) + (PL == 3 ? acc[PL == 3 ? d + k : 0] : 0.f);
+            for (int k = 0; k < 32; ++k)
+                y[k] = HALF_V ? __uint_as_float(o[k]) * (1.f / WEIGHT) : __uint_as_float(o[k]) + (PL == 3 ? acc[PL == 3 ? d + k : 0] : 0.f);
         };
         // this thread's row
         const int rt = PAIR ? unit * 2 + i : unit;

@@ -2,14 +2,16 @@
 
 The bound: codes are exact, so a score has the error of an fp32 dot product of D
 terms (fp32 queries in two planes of fp16: 2^-22 of each product more), the
-scales' and the exponential's; bf16 tensors round a weight to fp16 (2^-11), with more
-than 16 rows a key head a weight times its scale to bf16 (2^-8), and the output once;
-fp32 weights have two planes of fp16 (2^-22) or three of bf16 (2^-24).  A weight enters the MMAs as a
+scales' and the exponential's; bf16 tensors round a weight (with more than 16 rows a
+key head, a weight times its scale) to fp16 (2^-11), and the output once; fp32 weights
+have two planes of fp16 (2^-22) or three of bf16 (2^-24).  A weight enters the MMAs as a
 fp16 number in which the largest of its group of 16 or 32 states is 2^14; fp16's
 spacing is never under 2^-24, so a weight that is small in its group is off by up to
 2^-25 / 2^14 = 2^-39 of that largest, whatever its own size.  That is seen where
 the group's larger weights meet codes of 0: the bound has 2^-39 of the row's largest
-weight times sum_j |v_j|."""
+weight times sum_j |v_j|.  With more than 16 rows and bf16 tensors it is a weight times
+its scale, of which the row's largest is 2^6 or more: the bound has 2^-25 / 2^6 = 2^-31 of
+that largest times the sum of the codes' sizes."""
 import math
 
 import numpy as np
@@ -39,12 +41,12 @@ def values(torch, c, code):
     return c.view(torch.float8_e4m3fn if code == E4M3 else torch.int8).double()
 
 
-def bounds(out, lse, wabs, mag, D, Tk, bf16, largest, many):
-    """largest: the row's largest weight times sum_j |v_j|, [N][Tq][Hq][D]; many: more than 16 rows a key head."""
+def bounds(out, lse, wabs, mag, D, Tk, bf16, largest):
+    """largest: what a spacing of fp16 leaves, relative to a row's largest weight, [N][Tq][Hq][D]."""
     ds = ref.U * (6 * math.sqrt(D) + 16) * mag + 2.0 ** -21 + (0.0 if bf16 else 2.0 ** -22 * mag)
     # |lse| log2 e and m are rounded where they are subtracted: part of the score's own size
-    b = wabs * (2 * ds.transpose(1, 2)[..., None] + (6 * math.sqrt(Tk) + 16) * ref.U + ((ref.UB if many else 2.0 ** -11) if bf16 else 2.0 ** -22)) + 1e-30
-    b = b + 2.0 ** -39 * largest
+    b = wabs * (2 * ds.transpose(1, 2)[..., None] + (6 * math.sqrt(Tk) + 16) * ref.U + (2.0 ** -11 if bf16 else 2.0 ** -22)) + 1e-30
+    b = b + largest
     if bf16:
         b = b + ref.UB * out.abs()
     z = ds + (6 * math.sqrt(Tk) + 16) * ref.U + 4 * ref.U * lse.abs().nan_to_num(posinf=0.0)
@@ -75,9 +77,19 @@ def run_and_check(torch, sc, data, dtype, code, block, k_len=None, key_mask=None
         valid &= km != 0
     kk, vv = (ref.dequantize(values(torch, c, code), s, block) for c, s in ((pk, ks), (pv, vs)))
     o, z, wabs, mag = ref.attention(q.double(), kk, vv, scale, valid)
-    # the weights sum to 1: none is above it
-    vsum = torch.where(valid[:, :, None, None], vv.abs(), torch.zeros_like(vv)).sum(dim=1).repeat_interleave(Hq // Hkv, dim=1)
-    b, zb = bounds(o, z, wabs, mag, D, Tk, dtype == BF16, vsum[:, None], Tq * Hq // Hkv > 16)
+    G = Hq // Hkv
+    zero = torch.zeros((), dtype=torch.float64, device="cuda")
+    ok = valid[:, :, None, None]
+    if dtype == BF16 and Tq * G > 16:
+        s = scale * (q.double().transpose(1, 2) @ torch.where(ok, kk, zero).repeat_interleave(G, dim=2).permute(0, 2, 3, 1))
+        p = torch.exp(s - torch.where(z.isinf(), zero, z)[..., None]) * valid[:, None, None, :]
+        size = torch.where(ok[..., 0], vs.double().abs().transpose(1, 2).repeat_interleave(block, dim=1)[:, :Tk], zero)
+        most = (p * size.repeat_interleave(G, dim=2).transpose(1, 2)[:, :, None, :]).amax(dim=-1)            # [N][Hq][Tq]
+        codes = torch.where(ok, values(torch, pv, code).abs(), zero).sum(dim=1).repeat_interleave(G, dim=1)     # [N][Hq][D]
+        small = 2.0 ** -31 * (most[..., None] * codes[:, :, None, :]).transpose(1, 2)
+    else:   # the weights sum to 1: none is above it
+        small = 2.0 ** -39 * torch.where(ok, vv.abs(), zero).sum(dim=1).repeat_interleave(G, dim=1)[:, None]
+    b, zb = bounds(o, z, wabs, mag, D, Tk, dtype == BF16, small)
     assert torch.isfinite(out.float()).all()
     err = (out.double() - o).abs()
     assert (err <= b).all(), f"out: worst {(err / b).max().item():.2f} of its bound"

@@ -2,6 +2,8 @@
 64-bit forms: each operator's result within its own bound for the inputs that it was given, and the layer's result
 near the layer computed in 64 bits throughout; then the same layer captured into a graph, for one new token."""
 import math
+import os
+import sys
 
 import pytest
 
@@ -127,3 +129,31 @@ def test_layer(sc, dtype, code):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(layer.s, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("code,near", [(scl.SC_CODE_I8, 127.0), (scl.SC_CODE_E4M3, 16.0)])
+@pytest.mark.parametrize("dtype", [scl.SC_F32, scl.SC_BF16])
+def test_example_with_states_in_8_bits(sc, dtype, code, near):
+    """The feature-map example runs with its states in 8 bits, for points of interest and for a token, and gives what it
+    gives without, but for the states' rounding: half a step of 1 / 127, or 1 / 16, of a block's largest value."""
+    import torch
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import feature_map_attention as ex
+    N, H, W = 2, 24, 40
+    g = torch.Generator().manual_seed(3)
+    images, w = torch.rand(N, H, W, generator=g).cuda(), ex.make_weights()
+    valid = [(24, 31), (17, 40)]
+    plain, held = ex.FeatureMap(images, w, valid, dtype), ex.FeatureMap(images, w, valid, dtype, code)
+    t = torch.bfloat16 if dtype == scl.SC_BF16 else torch.float32
+    for T in (9, 1):
+        q = torch.randn(N, T, ex.HEADS, ex.D, generator=g).to(t).cuda()
+        places = torch.stack([torch.randint(0, s, (N * T,), generator=g, dtype=torch.int32) for s in (H, W)]).cuda()
+        a, b = plain.attend(q, places), held.attend(q, places)
+        sc.check(sc.sc_last_device_status())
+        assert held.k is None and held.cache is not None
+        # a normalised key's element is off by at most 8 / (2 near), in length sqrt(64) times that, so a score by 1.5 * 8 of
+        # it times 1 / 8 (|q| is 1.5 sqrt(64), the scale 1 / 8), weights by twice that, values by their own half step
+        ds = 1.5 * 8 * 8 / (2 * near)
+        size = plain.v.float().abs().amax()
+        assert ((a.float() - b.float()).abs() <= size * (2 * min(1.0, ds) + 1 / (2 * near) + 2.0 ** -6)).all()

@@ -166,6 +166,29 @@ def test_strides_streams_and_appending(sc, code, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("code", [I8, E4M3])
+def test_keys_and_values_in_one_cache(sc, code):
+    """Codes of keys and values side by side in one [N][T][2][H][D] cache, which grows by whole blocks under masks."""
+    import torch
+    N, T, H, D, block = 3, 256, 2, 48, 64
+    k, v = states(torch, BF16, N, T, H, D, seed=8), states(torch, BF16, N, T, H, D, seed=9)
+    both = torch.full((N, T, 2, H, D), 0x55, dtype=torch.uint8, device="cuda")
+    ks, vs = (torch.full((N, H, T // block), -7.0, device="cuda") for _ in range(2))
+    cs = (T * 2 * H * D, 2 * H * D, D)
+    for b0, b1 in ((0, 1), (1, 3), (3, 4)):
+        mask = torch.zeros(N, T, dtype=torch.uint8, device="cuda")
+        mask[:, b0 * block:b1 * block] = 1
+        old = both.clone(), ks.clone(), vs.clone()
+        sc.check(sc.kv_quantize_fwd((k, both, ks, None, cs), (v, both[0, 0, 1], vs, None, cs), N, T, H, D, block, code, BF16,
+                                    key_mask=mask), "kv_quantize_fwd")
+        sc.check(sc.sc_last_device_status())
+        assert torch.equal(both[:, :b0 * block], old[0][:, :b0 * block]) and (both[:, b1 * block:] == 0x55).all()
+        assert torch.equal(ks[..., :b0], old[1][..., :b0]) and (vs[..., b1:] == -7.0).all()
+    for x, i, s in ((k, 0, ks), (v, 1, vs)):
+        check(torch, x, both[:, :, i].contiguous(), s, valid_of(torch, N, T), block, code)
+
+
+@pytest.mark.gpu
 def test_offsets_beyond_32_bits(sc):
     import torch
     T, D, pitch = 48, 16, 1 << 26   # states 2^26 elements apart: the last at 47 * 2^26
