@@ -679,6 +679,15 @@ int sc_test_attn_slow_clear(const void *q, const void *k, const void *v, void *o
                             int delay_us, sc_stream_t stream);
 
 /*
+ * sc_test_attn_q8_wait_expiry: sc_test_attn_wait_expiry for
+ * cross_attention_q8_fwd's tensor-core kernel (packed, scale 1, whatever the
+ * number of rows).
+ */
+int sc_test_attn_q8_wait_expiry(const void *q, const void *k, const float *k_scale, const void *v, const float *v_scale,
+                                void *out, int N, int Tq, int Tk, int Hq, int Hkv, int D, int block, int code, int dtype,
+                                int drop_copy, int timeout_us, sc_stream_t stream);
+
+/*
  * sc_test_linear_wait_expiry: test hook for the device-status path, not part
  * of the operation.  Runs linear_fwd's tensor-core kernel (packed, no bias,
  * activation or residual, whatever the number of rows) with the copies of

@@ -88,6 +88,7 @@ SIGNATURES = {
     "sc_test_linear_wait_expiry": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "residual_norm_fwd": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _I, _F, _I, _P, _P]),
     "kv_quantize_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "sc_test_attn_q8_wait_expiry": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "cross_attention_q8_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P, _P]),
 }
 SC_CHAIN_MAX_LAYERS = 64
@@ -358,10 +359,9 @@ _NORM = struct.Struct("@ifPP")
 
 
 def _norm_of(t):
-    if t is None:
+    if t is None or t[0] == SC_NORM_NONE:
         return None
-    kind, weight, bias, eps = t
-    return _NORM.pack(kind, eps, _ptr(weight) or 0, _ptr(bias) or 0)
+    return _NORM.pack(t[0], t[3], _ptr(t[1]) or 0, _ptr(t[2]) or 0)
 
 
 def residual_norm_fwd(x, residual, sum, y, rows, C, post=None, pre=None, gate=None, gate_rows=1, scale=1.0, dtype=SC_F32,
@@ -375,17 +375,20 @@ def residual_norm_fwd(x, residual, sum, y, rows, C, post=None, pre=None, gate=No
                                     None if strides is None else _FOUR_STRIDES.pack(*strides), _stream(stream))
 
 
-# sc_quant_states as bytes
-_QUANT_STATES = struct.Struct("@PPPiiqqqqqq")
+# sc_quant_states as bytes: addresses, then what says that both tensors are packed, or strides
+_THREE_POINTERS = struct.Struct("@PPP")
+_QUANT_STRIDES = struct.Struct("@iiqqqqqq")
+_QUANT_PACKED = _QUANT_STRIDES.pack(1, 1, 0, 0, 0, 0, 0, 0)
 
 
 def _quant_states(t):
     if t is None:
         return None
-    x, codes, scale, *strides = t
-    xs, cs = strides or (None, None)
-    return _QUANT_STATES.pack(_ptr(x) or 0, _ptr(codes) or 0, _ptr(scale) or 0, xs is None, cs is None,
-                              *(xs or (0, 0, 0)), *(cs or (0, 0, 0)))
+    head = _THREE_POINTERS.pack(_ptr(t[0]) or 0, _ptr(t[1]) or 0, _ptr(t[2]) or 0)
+    if len(t) == 3:
+        return head + _QUANT_PACKED
+    xs, cs = t[3:]
+    return head + _QUANT_STRIDES.pack(xs is None, cs is None, *(xs or (0, 0, 0)), *(cs or (0, 0, 0)))
 
 
 def kv_quantize_fwd(k, v, N, Tk, Hkv, D, block, code=SC_CODE_I8, dtype=SC_F32, k_len=None, key_mask=None,
@@ -433,6 +436,13 @@ def sc_test_attn_slow_clear(q, k, v, out, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D
     """Test hook: cross_attention_fwd's tensor-core kernel with its clearing warps held up (see the header)."""
     return load().sc_test_attn_slow_clear(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(k_len), _ptr(key_mask), N, Tq, Tk,
                                           Hq, Hkv, D, dtype, delay_us, _stream(stream))
+
+
+def sc_test_attn_q8_wait_expiry(q, k, k_scale, v, v_scale, out, N, Tq, Tk, Hq, Hkv, D, block, code, dtype, drop_copy,
+                                timeout_us, stream=None) -> int:
+    """Test hook: cross_attention_q8_fwd's tensor-core kernel with one copy never issued (see the header)."""
+    return load().sc_test_attn_q8_wait_expiry(_ptr(q), _ptr(k), _ptr(k_scale), _ptr(v), _ptr(v_scale), _ptr(out), N, Tq, Tk, Hq,
+                                              Hkv, D, block, code, dtype, drop_copy, timeout_us, _stream(stream))
 
 
 def sc_test_linear_wait_expiry(x, w, y, rows, Cin, Cout, dtype, drop_copy, timeout_us, stream=None) -> int:

@@ -1392,9 +1392,9 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, const 
     return attn_tc(a, nullptr, false, bf16, st, test);
 }
 
-cudaError_t launch_attn_tc_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st)
+cudaError_t launch_attn_tc_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st, const TcTest &test)
 {
-    return attn_tc(a, &a, e4m3, bf16, st, TcTest());
+    return attn_tc(a, &a, e4m3, bf16, st, test);
 }
 
 }  // namespace sc

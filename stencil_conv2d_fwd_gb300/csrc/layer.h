@@ -74,7 +74,7 @@ cudaError_t launch_attn_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream
 
 // Many rows per key head: the codes as bf16 in a workspace, and the tensor cores
 // (attn_split.cu, attn_tc.cu).
-cudaError_t launch_attn_tc_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st);
+cudaError_t launch_attn_tc_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st, const TcTest &test = TcTest());
 // q ([plane][N][Hkv][Tq][G][D], as attn_split; nullptr: used as it lies), codes
 // as bf16, the values of bf16 tensors as fp16 ([N][Hkv][Tk][D]), and the factors of 16 keys each ([N * Hkv][groups]).
 cudaError_t launch_attn_expand(const AttnQ8Args &a, bool bf16, bool e4m3, void *q, void *k, void *v, float *k_factor, float *v_factor,

@@ -91,6 +91,38 @@ int take_linear(const void *x, const void *w, const float *b, const void *residu
     return SC_OK;
 }
 
+// cross_attention_q8_fwd's argument checks, as take_linear.
+int take_q8(const void *q, const void *k, const float *k_scale, const void *v, const float *v_scale, void *out, float *lse,
+            const int *k_len, const unsigned char *key_mask, int N, int Tq, int Tk, int Hq, int Hkv, int D, float scale, int block,
+            int code, int dtype, const sc_attn_strides *strides, sc::AttnQ8Args &a)
+{
+    if (!k_scale || !v_scale) return SC_ERR_NULL;
+    int rc = check_block(D, block, code);
+    if (rc != SC_OK) return rc;
+    rc = sc::take_attention(q, k, v, out, lse, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, scale, dtype, 1, strides, a);
+    if (rc != SC_OK) return rc;
+    if (!sc::aligned(k_scale, 4) || !sc::aligned(v_scale, 4)) return SC_ERR_ALIGN;
+    // a tensor map's strides; states of one stride 0 would be one state
+    if (Tk > 1 && (a.ks.t == 0 || a.vs.t == 0)) return SC_ERR_UNSUPPORTED;
+    if (a.ks.n >= kMaxMapStride || a.ks.t >= kMaxMapStride || a.ks.h >= kMaxMapStride || a.vs.n >= kMaxMapStride ||
+        a.vs.t >= kMaxMapStride || a.vs.h >= kMaxMapStride)
+        return SC_ERR_UNSUPPORTED;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block = block;
+    a.log2_block = block == 16 ? 4 : (block == 32 ? 5 : (block == 64 ? 6 : 7));
+    a.blocks = (Tk + block - 1) / block;
+    const Region ro = sc::region(out, N, Tq, Hq, D, a.os, dtype == SC_BF16 ? 2 : 4);
+    const long long bytes = 4LL * N * Hkv * a.blocks;
+    if (sc::flat_overlap(ro, k_scale, bytes) || sc::flat_overlap(ro, v_scale, bytes)) return SC_ERR_ALIAS;
+    if (lse) {
+        const long long lse_bytes = 4LL * N * Hq * Tq;
+        const Region rl{reinterpret_cast<uintptr_t>(lse), 1, 1, 1, lse_bytes, 0, lse_bytes, 0};
+        if (sc::flat_overlap(rl, k_scale, bytes) || sc::flat_overlap(rl, v_scale, bytes)) return SC_ERR_ALIAS;
+    }
+    return SC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -227,35 +259,29 @@ int cross_attention_q8_fwd(const void *q, const void *k, const float *k_scale, c
                            int Hq, int Hkv, int D, float scale, int block, int code, int dtype,
                            const sc_attn_strides *strides, sc_stream_t stream)
 {
-    if (!k_scale || !v_scale) return SC_ERR_NULL;
-    int rc = check_block(D, block, code);
-    if (rc != SC_OK) return rc;
     sc::AttnQ8Args a;
-    rc = sc::take_attention(q, k, v, out, lse, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, scale, dtype, 1, strides, a);
+    const int rc = take_q8(q, k, k_scale, v, v_scale, out, lse, k_len, key_mask, N, Tq, Tk, Hq, Hkv, D, scale, block, code, dtype,
+                           strides, a);
     if (rc != SC_OK) return rc;
-    if (!sc::aligned(k_scale, 4) || !sc::aligned(v_scale, 4)) return SC_ERR_ALIGN;
-    // a tensor map's strides; states of one stride 0 would be one state
-    if (Tk > 1 && (a.ks.t == 0 || a.vs.t == 0)) return SC_ERR_UNSUPPORTED;
-    if (a.ks.n >= kMaxMapStride || a.ks.t >= kMaxMapStride || a.ks.h >= kMaxMapStride || a.vs.n >= kMaxMapStride ||
-        a.vs.t >= kMaxMapStride || a.vs.h >= kMaxMapStride)
-        return SC_ERR_UNSUPPORTED;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
-    a.block = block;
-    a.log2_block = block == 16 ? 4 : (block == 32 ? 5 : (block == 64 ? 6 : 7));
-    a.blocks = (Tk + block - 1) / block;
-    const Region ro = sc::region(out, N, Tq, Hq, D, a.os, dtype == SC_BF16 ? 2 : 4);
-    const long long bytes = 4LL * N * Hkv * a.blocks;
-    if (sc::flat_overlap(ro, k_scale, bytes) || sc::flat_overlap(ro, v_scale, bytes)) return SC_ERR_ALIAS;
-    if (lse) {
-        const long long lse_bytes = 4LL * N * Hq * Tq;
-        const Region rl{reinterpret_cast<uintptr_t>(lse), 1, 1, 1, lse_bytes, 0, lse_bytes, 0};
-        if (sc::flat_overlap(rl, k_scale, bytes) || sc::flat_overlap(rl, v_scale, bytes)) return SC_ERR_ALIAS;
-    }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SC_BF16, e4m3 = code == SC_CODE_E4M3;
     const long long rows = (long long)Tq * a.G;
     return sc::from_cuda(rows > 16 ? sc::launch_attn_tc_q8(a, bf16, e4m3, st) : sc::launch_attn_q8(a, bf16, e4m3, st));
+}
+
+int sc_test_attn_q8_wait_expiry(const void *q, const void *k, const float *k_scale, const void *v, const float *v_scale,
+                                void *out, int N, int Tq, int Tk, int Hq, int Hkv, int D, int block, int code, int dtype,
+                                int drop_copy, int timeout_us, sc_stream_t stream)
+{
+    sc::AttnQ8Args a;
+    const int rc = take_q8(q, k, k_scale, v, v_scale, out, nullptr, nullptr, nullptr, N, Tq, Tk, Hq, Hkv, D, 1.f, block, code, dtype,
+                           nullptr, a);
+    if (rc != SC_OK) return rc;
+    if (drop_copy < 0 || timeout_us < 1) return SC_ERR_SHAPE;
+    sc::TcTest test;
+    test.drop_copy = drop_copy;
+    test.timeout_ns = 1000ull * (unsigned long long)timeout_us;
+    return sc::from_cuda(sc::launch_attn_tc_q8(a, dtype == SC_BF16, code == SC_CODE_E4M3, reinterpret_cast<cudaStream_t>(stream), test));
 }
 
 }  // extern "C"

@@ -228,6 +228,20 @@ def test_scales_and_queries_far_apart(sc, dtype, Tq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,H,Tq", [(BF16, 160, 20), (F32, 160, 20), (BF16, 80, 260)])
+def test_long_masked_share(sc, dtype, H, Tq):
+    """More key tiles in a CTA's share than it lists (512 of 128 keys), most of them empty; one and two row tiles."""
+    import torch
+    Tk, D, block = 70000, 16, 128
+    data = make(torch, dtype, E4M3, 1, Tq, Tk, H, H, D, block, seed=12)
+    mask = np.zeros((1, Tk), np.uint8)
+    mask[0, 3:40], mask[0, 40000:40300:3], mask[0, 69990:] = 1, 1, 1
+    on = torch.as_tensor(mask).cuda() != 0
+    data[1][~on], data[3][~on] = 0x7f, 0xff   # NaN codes where the mask is 0
+    run_and_check(torch, sc, data, dtype, E4M3, block, key_mask=mask)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("Tq,H,D", [(3, 2, 64), (90, 2, 64), (300, 80, 64), (300, 80, 128)])
 @pytest.mark.parametrize("masked", [False, True])
@@ -342,6 +356,31 @@ def test_offsets_beyond_32_bits(sc, dtype, Tq):
     buf.as_strided((Tk, D), (pitch, 1), D).copy_(v[0, :, 0])
     st, packed = (0, pitch, D), (Tq * H * D, H * D, D)
     run_and_check(torch, sc, (q, buf, ks, buf[D:], vs), dtype, I8, block, strides=(packed, st, st, packed), plain=(k, v))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("code", [I8, E4M3])
+@pytest.mark.parametrize("shape", [(1, 140, 1000, 2, 2, 64, 32), (11, 300, 700, 6, 6, 64, 64), (1, 40, 20000, 2, 2, 128, 128)])
+@pytest.mark.parametrize("drop_copy", [0, 1, 5])
+def test_expired_wait_is_reported(sc, shape, drop_copy, code, dtype):
+    """A copy that never comes: its waits run out, the status says so, and the next call is right."""
+    import torch
+    data = make(torch, dtype, code, *shape, seed=13)
+    q, k, ks, v, vs = data
+    sc.check(sc.sc_last_device_status())
+    sc.check(sc.sc_test_attn_q8_wait_expiry(q, k, ks, v, vs, torch.empty_like(q), *shape, code, dtype, drop_copy, 300))
+    assert sc.sc_last_device_status() == scl.SC_ERR_DEVICE_TIMEOUT
+    assert sc.sc_last_device_status() == scl.SC_OK
+    run_and_check(torch, sc, data, dtype, code, shape[-1])
+
+
+def test_wait_expiry_hook_refusals():
+    args = (A, B, C, D_, E, G, 2, 4, 40, 2, 2, 32)
+    assert scl.sc_test_attn_q8_wait_expiry(None, *args[1:], 16, I8, F32, 0, 10, stream=0) == scl.SC_ERR_NULL
+    assert scl.sc_test_attn_q8_wait_expiry(*args, 20, I8, F32, 0, 10, stream=0) == scl.SC_ERR_UNSUPPORTED
+    assert scl.sc_test_attn_q8_wait_expiry(*args, 16, I8, F32, -1, 10, stream=0) == scl.SC_ERR_SHAPE
+    assert scl.sc_test_attn_q8_wait_expiry(*args, 16, I8, F32, 0, 0, stream=0) == scl.SC_ERR_SHAPE
 
 
 A, B, C, D_, E, G = (1 << k for k in (20, 24, 28, 32, 34, 36))
