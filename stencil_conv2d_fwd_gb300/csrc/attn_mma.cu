@@ -317,7 +317,7 @@ cudaError_t launch_mma(const AttnArgs &a, cudaStream_t st)
 {
     static KernelCache cache;
     return launch_rows_kernel(attn_mma_kernel<T, DP, RH>, cache, a, sizeof(T) == 2, 8 * RH,
-                              (int)sizeof(MmaShared<T, DP, RH>), st, 1);
+                              (int)sizeof(MmaShared<T, DP, RH>), st, false);
 }
 
 }  // namespace

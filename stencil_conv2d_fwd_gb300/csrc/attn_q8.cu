@@ -162,6 +162,7 @@ struct Q8Ring {
         lane = threadIdx.x & 31;
         if (lane < 2)   // the maps come beside the length
             asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<unsigned long long>(lane ? &m.v : &m.k)) : "memory");
+        pdl_wait();
         len = a.Tk;
         if (a.k_len) len = max(0, min(len, a.k_len[n]));
         const int pieces = (len + KP - 1) / KP;
@@ -214,7 +215,6 @@ struct Q8Shared {
     uint64_t bars[kRowWarps][Q8Ring<DP>::STAGES];
 };
 
-constexpr int kCtasPerSm = 1;
 constexpr float kWeightLog2 = 14.f;   // weights are 2^14 P
 
 // T: float or bf16 queries; R: 8 rows, or with bf16 16.
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
         if (threadIdx.x == 0) atomicExch(axes.status, kDeviceTimeout);
         return;
     }
-    pdl_trigger();   // the join kernel may be set up; it waits for this grid's end
+    pdl_trigger();   // the join kernel, or the next, may be set up; it waits for this grid's end
     if (g.cluster > 1) cluster_arrive();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % g.splits;
@@ -542,8 +542,7 @@ cudaError_t launch_q8(const AttnQ8Args &a, cudaStream_t st)
     Q8Maps m;
     std::memset(&m, 0, sizeof(m));
     if (!encode_map<DP>(&m.k, a.k, a.ks, a) || !encode_map<DP>(&m.v, a.v, a.vs, a)) return cudaErrorInvalidValue;
-    return launch_rows_kernel(attn_q8_kernel<T, DP, E4M3, R>, cache, a, sizeof(T) == 2, R, (int)sizeof(Q8Shared<DP, R>), st, kCtasPerSm, m,
-                              ax);
+    return launch_rows_kernel(attn_q8_kernel<T, DP, E4M3, R>, cache, a, sizeof(T) == 2, R, (int)sizeof(Q8Shared<DP, R>), st, true, m, ax);
 }
 
 template <class T, bool E4M3>

@@ -228,7 +228,7 @@ template <int LPK, int R, int U>
 cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
 {
     static KernelCache cache;
-    return launch_rows_kernel(attn_rows_kernel<LPK, R, U>, cache, a, false, R, 0, st, 1);
+    return launch_rows_kernel(attn_rows_kernel<LPK, R, U>, cache, a, false, R, 0, st, false);
 }
 
 template <int LPK, int U>

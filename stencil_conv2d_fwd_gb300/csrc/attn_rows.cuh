@@ -295,10 +295,9 @@ __device__ __forceinline__ void finish_rows(const WarpSums<R, DP> &sm, CtaSums<R
 //   32 x 4 of 64, four bf16 rows over 3136: 23.7 and 26.3; two CTAs for every SM 27.2, four 33.3
 //   (a CTA's start and end cost what it reads in 1 us)
 //   one of 64, four bf16 rows over 921600: 45.0, two CTAs for every SM 48.1, four 54.9
-// per_sm: CTAs for every SM (8-bit states, whose conversion needs more warps than
-// their reading, take two: see attn_q8.cu).
+// behind: the kernel calls pdl_wait before it touches global memory.
 template <class K, class A, class... More>
-cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const A &a, bool bf16, int R, int smem, cudaStream_t st, int per_sm,
+cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const A &a, bool bf16, int R, int smem, cudaStream_t st, bool behind,
                                const More &...more)
 {
     int dev = 0;
@@ -312,7 +311,7 @@ cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const A &a, bool bf
     RowsGeom g;
     g.row_blocks = (int)((rows + R - 1) / R);
     const long long blocks = (long long)a.N * a.Hkv * g.row_blocks;
-    const long long want = ((long long)per_sm * device_sm_count() + blocks - 1) / blocks;
+    const long long want = (device_sm_count() + blocks - 1) / blocks;
     const long long most = ((long long)a.Tk + step - 1) / step;
     const long long s = want < most ? want : most;
     if (s <= kMaxCluster || most <= kMaxCluster * 4) {
@@ -339,12 +338,21 @@ cudaError_t launch_rows_kernel(K kernel, KernelCache &cache, const A &a, bool bf
     cfg.blockDim = dim3(kRowThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = g.cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    int attrs = 0;
+    if (g.cluster > 1) {
+        at[attrs].id = cudaLaunchAttributeClusterDimension;
+        at[attrs].val.clusterDim.x = g.cluster;
+        at[attrs].val.clusterDim.y = at[attrs].val.clusterDim.z = 1;
+        ++attrs;
+    }
+    if (behind) {
+        at[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[attrs].val.programmaticStreamSerializationAllowed = 1;
+        ++attrs;
+    }
     cfg.attrs = at;
-    cfg.numAttrs = g.cluster > 1 ? 1 : 0;
+    cfg.numAttrs = attrs;
     e = cudaLaunchKernelEx(&cfg, kernel, a, g, part, more...);
     if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st);
     if (ws) {

@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(512) kv_quantize_kernel(const QuantArgs a, con
     const uint32_t nb = on ? g.heads.quotient(unit) : 0u;
     const int h = on ? (int)(unit - nb * a.H) : 0;
     const int n = (int)g.blocks.quotient(nb), b = (int)nb - n * a.blocks;
+    pdl_trigger();   // the next kernel may be set up; it waits for this grid's end
+    pdl_wait();
     int len = a.T;
     if (a.k_len) len = max(0, min(len, a.k_len[n]));
     const int row_chunks = a.D / E<T>, t0 = b * a.block;
@@ -266,21 +268,11 @@ cudaError_t launch_kv_quantize(const QuantArgs &a, bool bf16, bool e4m3, cudaStr
     g.col_step = g.threads % row_chunks;
     const long long ctas = (units + g.per_cta - 1) / g.per_cta;
     const dim3 grid((unsigned)ctas, a.parts), block(g.threads * g.per_cta);
-    auto go = [&](auto small, auto large) {
-        if (per == 16)
-            small<<<grid, block, 0, st>>>(a, g);
-        else
-            large<<<grid, block, 0, st>>>(a, g);
-    };
-    if (bf16 && e4m3)
-        go(kv_quantize_kernel<__nv_bfloat16, true, 16>, kv_quantize_kernel<__nv_bfloat16, true, 32>);
-    else if (bf16)
-        go(kv_quantize_kernel<__nv_bfloat16, false, 16>, kv_quantize_kernel<__nv_bfloat16, false, 32>);
-    else if (e4m3)
-        go(kv_quantize_kernel<float, true, 16>, kv_quantize_kernel<float, true, 32>);
-    else
-        go(kv_quantize_kernel<float, false, 16>, kv_quantize_kernel<float, false, 32>);
-    return cudaGetLastError();
+    auto go = [&](auto small, auto large) { return launch_behind(per == 16 ? small : large, grid, block, st, 1, a, g); };
+    if (bf16 && e4m3) return go(kv_quantize_kernel<__nv_bfloat16, true, 16>, kv_quantize_kernel<__nv_bfloat16, true, 32>);
+    if (bf16) return go(kv_quantize_kernel<__nv_bfloat16, false, 16>, kv_quantize_kernel<__nv_bfloat16, false, 32>);
+    if (e4m3) return go(kv_quantize_kernel<float, true, 16>, kv_quantize_kernel<float, true, 32>);
+    return go(kv_quantize_kernel<float, false, 16>, kv_quantize_kernel<float, false, 32>);
 }
 
 }  // namespace sc

@@ -80,4 +80,24 @@ cudaError_t launch_attn_tc_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStr
 cudaError_t launch_attn_expand(const AttnQ8Args &a, bool bf16, bool e4m3, void *q, void *k, void *v, float *k_factor, float *v_factor,
                                int groups, cudaStream_t st);
 
+// Launches a kernel that may be set up while the stream's last one ends: it has to
+// call pdl_wait before it touches global memory.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t st, int cluster, const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace sc

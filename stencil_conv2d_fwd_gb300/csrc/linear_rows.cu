@@ -114,7 +114,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) linear_rows_mma_
     constexpr int R = 8 * NT, U = 4;
     __shared__ float sums[kWarps * R * 16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    pdl_trigger();   // the next kernel may be set up; it waits for this grid's end
     if (share.cluster > 1) cluster_arrive();
+    pdl_wait();
     const RowsWork work(share, (a.Cin + 31) / 32, warp);   // steps of 32 elements: a chunk of 8 for each t
     const long long tile = work.tile;
     const int s0 = work.s0, s1 = work.s1;
@@ -186,7 +188,9 @@ __global__ void __launch_bounds__(kWarps * 32) linear_rows_split_kernel(const Li
     constexpr int R = 8 * NT, U = 2, FLUSH = 8;
     __shared__ float sums[kWarps * R * 16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, row0 = blockIdx.y * R;
+    pdl_trigger();   // the next kernel may be set up; it waits for this grid's end
     if (share.cluster > 1) cluster_arrive();
+    pdl_wait();
     const RowsWork work(share, (a.Cin + 15) / 16, warp);   // steps of 16 elements: a chunk of 4 for each t
     const int s0 = work.s0, s1 = work.s1;
     const float *wp[2], *xp[NT];
@@ -272,7 +276,9 @@ __global__ void __launch_bounds__(kWarps * 32, R <= 2 ? 4 : 3) linear_rows_fma_k
     constexpr int O = 4, U = 2, V = O * R;
     __shared__ float sums[kWarps * R * O];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_trigger();   // the next kernel may be set up; it waits for this grid's end
     if (share.cluster > 1) cluster_arrive();
+    pdl_wait();
     const RowsWork work(share, (a.Cin + 127) / 128, warp);   // steps of 128 elements, four a lane
     const long long tile = work.tile;
     const int s0 = work.s0, s1 = work.s1;
@@ -351,17 +357,7 @@ cudaError_t launch(K kernel, const LinearArgs &a, int steps, cudaStream_t st, in
     const int per = kWarps >> g.log2_slices;
     const long long ctas = (tiles + per - 1) / per * g.cluster;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)blocks);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = g.cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = g.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a, g);
+    return launch_behind(kernel, dim3((unsigned)ctas, (unsigned)blocks), dim3(kWarps * 32), st, g.cluster, a, g);
 }
 
 }  // namespace

@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_kernel(const Res
     __shared__ float slots[ONE ? 1 : 4 * kMaxWarps];   // a row (a CTA has one): four reductions
     const int lane = threadIdx.x & 31, w = ONE ? 0 : threadIdx.x >> 5, W = ONE ? 1 : blockDim.x >> 5;
     const int row = blockIdx.x * blockDim.y + threadIdx.y;
+    pdl_trigger();   // the next kernel may be set up; it waits for this grid's end
+    pdl_wait();
     if (row >= a.rows) return;   // whole warps; with several warps a row a CTA has one row
     const int first = threadIdx.x * N, step = blockDim.x * N;
     const T *xp = static_cast<const T *>(a.x) + row * a.xs;
@@ -186,11 +188,8 @@ cudaError_t launch(const ResidualNormArgs &a, int warps, cudaStream_t st)
     // a warp a row: four rows a CTA, unless the rows are few
     const int per = warps == 1 && a.rows > 4 * device_sm_count() ? 4 : 1;
     const dim3 block(32 * warps, per), grid((unsigned)((a.rows + per - 1) / per));
-    if (warps == 1)
-        residual_norm_kernel<T, NV, true><<<grid, block, 0, st>>>(a);
-    else
-        residual_norm_kernel<T, NV, false><<<grid, block, 0, st>>>(a);
-    return cudaGetLastError();
+    return warps == 1 ? launch_behind(residual_norm_kernel<T, NV, true>, grid, block, st, 1, a)
+                      : launch_behind(residual_norm_kernel<T, NV, false>, grid, block, st, 1, a);
 }
 
 template <class T>
