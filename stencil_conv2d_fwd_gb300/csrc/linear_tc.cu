@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 9) {
         alloc<CG>(smem_u32(&sh.tmem), TMEM_COLS);
     }
+    pdl_wait();   // what comes before touches no global memory
     tc::fence_before_sync();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
@@ -313,7 +314,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_OTHER));
         if (warp == 8) {
-            if (F32) pdl_wait();   // the planes are the launch before's
             if (lane == 0) {
                 for (int i = first; i < g.items; i += stride) {
                     const Item it = item(i);
@@ -648,6 +648,7 @@ struct SplitPart {
 __global__ void __launch_bounds__(256) linear_split_kernel(const SplitPart p0, const SplitPart p1, int cols8)
 {
     pdl_trigger();   // the product's kernel may be set up; its copies wait for this grid's end
+    pdl_wait();
     const SplitPart &p = blockIdx.y ? p1 : p0;
     const long long chunks = p.rows * cols8, plane = chunks * 8;
     for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < chunks; e += (long long)gridDim.x * 256) {
@@ -742,11 +743,9 @@ cudaError_t launch(const LinearArgs &a, const Geom &g, const Maps &m, cudaStream
         at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
         ++n;
     }
-    if (F32) {   // behind linear_split_kernel
-        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
     cfg.attrs = at;
     cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, BN, F32>, m.x, m.w, m.y, m.r, m.part, a, g, status, test);
@@ -849,8 +848,7 @@ cudaError_t launch_linear_tc(const LinearArgs &a, bool bf16, cudaStream_t st, co
         const long long most = (a.rows > a.Cout ? a.rows : a.Cout) * (a.Cin / 8LL);
         long long blocks = (most + 255) / 256;
         if (blocks > 16LL * sms) blocks = 16LL * sms;
-        lt::linear_split_kernel<<<dim3((unsigned)blocks, 2), 256, 0, st>>>(p0, p1, a.Cin / 8);
-        e = cudaGetLastError();
+        e = launch_behind(lt::linear_split_kernel, dim3((unsigned)blocks, 2), dim3(256), st, 1, p0, p1, a.Cin / 8);
     }
     if (e == cudaSuccess) {
         switch (best * 2 + (bf16 ? 0 : 1)) {
