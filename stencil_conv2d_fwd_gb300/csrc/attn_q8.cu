@@ -29,6 +29,12 @@
 // Integer codes become fp16 in 2.5 (K) or 3 (V) instructions for two: a byte
 // with its sign bit turned is the low byte of 1024 + 128 + x in fp16, from which
 // 1152 is taken.
+//
+// Measured (in a graph): one bf16 token, 4 heads on one key head of 64, over 921600
+// e4m3 states 30.6 us (118 MB; 9 us of launch, ring start and join, the rest at 5.6
+// TB/s); 32 tokens, 16 heads on 4, over up to 3136 int8 states 17.1.  A warp's chain of
+// products, maximum and weights is what a step waits for (issue slots 49% busy); two
+// CTAs an SM took as long on one sequence and a third longer on a batch.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

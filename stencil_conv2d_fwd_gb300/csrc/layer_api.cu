@@ -12,9 +12,17 @@ using sc::Region;
 
 constexpr int kMaxRows = 1 << 30;
 // Rows that stream w through registers (linear_rows.cu) rather than go to the tensor
-// cores (linear_tc.cu), which in fp32 first split all of w.  w of 8192 x 2048:
-//   bf16: 16 rows 11.6 us, 17 there 16.0;  fp32: 32 rows 38.4, there 59.3; 48 rows 68.3, there 59.5
-constexpr int kFewRowsBf16 = 16, kFewRowsF32 = 32;
+// cores (linear_tc.cu), which in fp32 first split x and w in a launch of their own.
+//   bf16, w of 8192 x 2048: 16 rows 10.2 us, 17 there 14.9
+//   fp32, w of 8192 x 2048: 32 rows 38.4, there 59.3; 48 rows 68.3, there 59.5
+//   fp32, few products: 128 rows, w of 1024 x 1024 11.8, there 14.2; 1001 rows, 256 x 256 8.2 and
+//   12.8; 64 rows, 2048 x 2048 19.7 and 19.6; 2000 rows, 256 x 128 10.2 and 9.6
+bool few_rows(const sc::LinearArgs &a, bool bf16)
+{
+    if (bf16) return a.rows <= 16;
+    return a.rows <= 32 || (a.rows <= 1024 && (double)a.rows * a.Cin * a.Cout <= 140e6);
+}
+
 constexpr long long kMaxMapStride = 1LL << 40;   // bytes
 
 // [rows][cols] with a row stride in elements.
@@ -135,8 +143,7 @@ int linear_fwd(const void *x, const void *w, const float *b, const void *residua
     if (rc != SC_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SC_BF16;
-    return sc::from_cuda(rows <= (bf16 ? kFewRowsBf16 : kFewRowsF32) ? sc::launch_linear_rows(a, bf16, st)
-                                                                    : sc::launch_linear_tc(a, bf16, st));
+    return sc::from_cuda(few_rows(a, bf16) ? sc::launch_linear_rows(a, bf16, st) : sc::launch_linear_tc(a, bf16, st));
 }
 
 int sc_test_linear_wait_expiry(const void *x, const void *w, void *y, int rows, int Cin, int Cout, int dtype, int drop_copy,

@@ -8,7 +8,7 @@
 // order of summation is free, so lane (g, t) takes whole 16-byte chunks of w's rows g
 // and g + 8 and the same chunks of x's row g, with no transposition.  (8 rows, w of
 // 8192 x 2048: 7.8 us, 4.3 TB/s.)
-// fp32, 5 rows to 32: the same, both operands in three bf16 planes, blocks of 16 rows
+// fp32, 5 rows and more: the same, both operands in three bf16 planes, blocks of 16 rows
 // that read w from L2 but for one.
 // fp32, up to 4 rows: FMA.  A lane takes four elements of Cin of four outputs and
 // every row of x (from L1), and the 32 lanes' sums are added by halves: each exchange

@@ -57,7 +57,7 @@ def test_shapes(sc, shape, dtype):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("act", [ref.ACT_NONE, ref.ACT_RELU, ref.ACT_GELU, ref.ACT_SILU])
 @pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True), (True, True)])
-@pytest.mark.parametrize("shape", [(3, 256, 130), (140, 256, 200), (700, 128, 515)])
+@pytest.mark.parametrize("shape", [(3, 256, 130), (140, 256, 200), (700, 128, 515), (1100, 264, 132), (1030, 256, 515)])
 def test_epilogues(sc, shape, bias, residual, act, dtype):
     import torch
     x, w, b, r = tensors(torch, dtype, *shape, seed=1, bias=bias, residual=residual)
@@ -68,7 +68,7 @@ def test_epilogues(sc, shape, bias, residual, act, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("shape", [(3, 128, 50), (16, 256, 100), (200, 128, 131), (513, 512, 264)])
+@pytest.mark.parametrize("shape", [(3, 128, 50), (16, 256, 100), (200, 128, 131), (513, 512, 264), (1100, 256, 264)])
 @pytest.mark.parametrize("pad", [8, 40])
 def test_strides(sc, shape, pad, dtype):
     """Rows inside wider ones (a fused projection), y at an odd address and pitch, guard bytes around y."""
@@ -93,7 +93,7 @@ def test_strides(sc, shape, pad, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("shape", [(4, 256, 512), (300, 256, 515)])
+@pytest.mark.parametrize("shape", [(4, 256, 512), (300, 256, 515), (1100, 256, 512), (2000, 1024, 2048)])
 def test_residual_in_place_and_shared(sc, shape, dtype):
     import torch
     rows, Cin, Cout = shape
@@ -109,7 +109,7 @@ def test_residual_in_place_and_shared(sc, shape, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("rows", [2, 40])
+@pytest.mark.parametrize("rows", [2, 40, 1500])
 def test_not_finite(sc, rows, dtype):
     """An infinity or NaN reaches the outputs of its row (x) or column (w), and no others."""
     import torch
@@ -130,7 +130,7 @@ def test_not_finite(sc, rows, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows", [3, 100])
+@pytest.mark.parametrize("rows", [3, 12, 100, 1500])
 @pytest.mark.parametrize("big", [3e38, 1e-30])
 def test_ends_of_fp32(sc, rows, big):
     """Values above bf16's largest, and products near fp32's smallest."""
