@@ -95,6 +95,21 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// l f of a sum of weights, f = 2^d, d <= 0.  Weights relative to a maximum that the
+// values' scales have entered (8-bit states) add up to between 2^-80 and 2^118, so an
+// f that ex2 flushes to 0 goes in two halves.
+__device__ __forceinline__ float rescale_sum(float l, float f, float d)
+{
+    if (d >= -126.f) return l * f;
+    const float h = ex2(0.5f * d);
+    return l * h * h;
+}
+// l1 2^d1 + l2 2^d2 of two such sums.
+__device__ __forceinline__ float join_sums(float l1, float f1, float d1, float l2, float f2, float d2)
+{
+    if (fminf(d1, d2) >= -126.f) return l1 * f1 + l2 * f2;
+    return rescale_sum(l1, f1, d1) + rescale_sum(l2, f2, d2);
+}
 // Two floats -> two bf16 (to nearest even, at most bf16's largest finite
 // value; NaN stays), `lo` at the lower address.
 __device__ __forceinline__ uint32_t pack_bf16_finite(float lo, float hi)

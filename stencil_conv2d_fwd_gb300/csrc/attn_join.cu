@@ -21,8 +21,8 @@ __device__ __forceinline__ void join4(float &m, float &l, float4 &o, float m2, f
 {
     const float mm = fmaxf(m, m2), ms = mm == -INFINITY ? 0.f : mm;
     const float f1 = ex2(m - ms), f2 = ex2(m2 - ms);
+    l = join_sums(l, f1, m - ms, l2, f2, m2 - ms);
     m = mm;
-    l = l * f1 + l2 * f2;
     o.x = o.x * f1 + o2.x * f2;
     o.y = o.y * f1 + o2.y * f2;
     o.z = o.z * f1 + o2.z * f2;
@@ -64,13 +64,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) mm = fmaxf(mm, ml[k].x);
             const float ms = mm == -INFINITY ? 0.f : mm, f0 = ex2(m - ms);
-            l *= f0;
+            l = rescale_sum(l, f0, m - ms);
             o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
             m = mm;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const float f = ex2(ml[k].x - ms);
-                l = fmaf(ml[k].y, f, l);
+                const float d = ml[k].x - ms, f = ex2(d);
+                l = d >= -126.f ? fmaf(ml[k].y, f, l) : l + rescale_sum(ml[k].y, f, d);
                 o.x = fmaf(q[k].x, f, o.x);
                 o.y = fmaf(q[k].y, f, o.y);
                 o.z = fmaf(q[k].z, f, o.z);

@@ -324,7 +324,8 @@ struct Bool {
 // queries a weight times its scale and the values' codes are fp16 (2^-11; with bf16's
 // 2^-8 the error was half as large again as the output's rounding); the running
 // maximum is that of score + log2 |scale|, so that they stay within fp16's range
-// whatever the scales.
+// for scales of 2^-80 to 2^80 (0 is taken as 2^-80).  The unscaled weights' sum is relative to
+// that maximum too, and so may be far from 1 (rescale_sum).
 // With one row tile a CTA (CODES) the tiles are copied as codes and warps 10 and 11
 // write them to the ring: 32 x 77 queries over 3136 states, 8 heads of 64, 79 us, where
 // codes expanded in memory first took 105 (bf16 states take 46: the two warps are the
@@ -886,8 +887,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float f = 1.f;
                 if (grow) {
                     f = ex2(m - top);
+                    l = Q8 ? rescale_sum(l, f, m - top) : l * f;
                     m = top;
-                    l *= f;
                 }
                 if (use > 0 && __any_sync(0xffffffffu, grow)) {
                     // the stream's last product is complete: it was issued before this S
@@ -1050,7 +1051,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float mm = fmaxf(m, m1), ms = mm == -INFINITY ? 0.f : mm;
                 f0 = ex2(m - ms);
                 f1 = ex2(m1 - ms);
-                l = l * f0 + l1 * f1;
+                l = HALF_V ? join_sums(l, f0, m - ms, l1, f1, m1 - ms) : l * f0 + l1 * f1;
                 m = mm;
             }
         }

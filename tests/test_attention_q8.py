@@ -228,6 +228,28 @@ def test_scales_and_queries_far_apart(sc, dtype, Tq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,code", [(BF16, I8), (BF16, E4M3), (F32, I8)])
+@pytest.mark.parametrize("shape", [(3, 2, 64, 1500), (90, 2, 64, 700), (90, 2, 64, 9000), (40, 2, 128, 2000), (300, 80, 64, 700),
+                                   (300, 80, 128, 700)])
+@pytest.mark.parametrize("low,high", [(0.0, 2.0 ** 50), (0.0, 2.0 ** 80), (2.0 ** -80, 2.0 ** 60), (2.0 ** -70, 2.0 ** 80)])
+def test_value_scales_over_the_documented_range(sc, shape, low, high, dtype, code):
+    """Equal scores, value scales from the least (or 0) to the largest: in the first states or the last, in every other
+    tile of 128 and in every third (so that each stream of a CTA has both), on few rows, one and two row tiles and split
+    keys.  Equal scores make every weight a power of two and their sum exact, so that what is left of lse's error is m ln 2's
+    and the logarithm's, numbers below 64: at most 2 ulp, 2^-17, where the bound has (6 sqrt(700) + 16) 2^-24, 1.3 * 2^-17."""
+    import torch
+    Tq, H, D, Tk = shape
+    N, block = 1, 128
+    q, k, ks, v, vs = make(torch, dtype, code, N, Tq, Tk, H, H, D, block, seed=14)
+    q.zero_()
+    b = torch.arange(vs.shape[2], device="cuda")
+    n = vs.shape[2]
+    for first in (b < n // 2, b >= n // 2, b % 2 == 0, b % 2 == 1, b % 3 == 0, b == n - 1):
+        vs[:] = torch.where(first, low, high)
+        run_and_check(torch, sc, (q, k, ks, v, vs), dtype, code, block)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,H,Tq", [(BF16, 160, 20), (F32, 160, 20), (BF16, 80, 260)])
 def test_long_masked_share(sc, dtype, H, Tq):
     """More key tiles in a CTA's share than it lists (512 of 128 keys), most of them empty; one and two row tiles."""
