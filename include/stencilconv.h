@@ -695,7 +695,9 @@ int sc_test_attn_q8_wait_expiry(const void *q, const void *k, const float *k_sca
  * time-bounded waits for them expire after `timeout_us` microseconds.  The
  * kernel then records SC_ERR_DEVICE_TIMEOUT (read and cleared by
  * sc_last_device_status), waits for its other copies and products and returns;
- * the context stays usable.  `y` is left with no defined values.
+ * the context stays usable.  `y` is left with no defined values.  With a drop_copy
+ * that no CTA reaches the waits that happen to take longer than timeout_us expire,
+ * if any.
  */
 int sc_test_linear_wait_expiry(const void *x, const void *w, void *y, int rows, int Cin, int Cout, int dtype, int drop_copy,
                                int timeout_us, sc_stream_t stream);

@@ -61,7 +61,8 @@ constexpr int stage_bytes() { return TILE * 128 + BN / CG * 128; }
 struct Shared {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], residual[EPI_WARPS], drain;
     uint32_t tmem;
-    int abort;
+    int abort;         // a wait of this CTA has expired
+    int other_abort;   // one of the pair's other CTA, which writes it before the last barrier of the two
 };
 template <int CG, int BN>
 constexpr int stages()
@@ -232,7 +233,7 @@ constexpr uint32_t idesc()   // D fp32, A and B bf16, both K-major
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(TILE * CG >> 4) << 24);
 }
 
-// F32: planes of fp32 tensors; else bf16 tensors.  SPLIT: fp32 sums to g.part.
+// F32: planes of fp32 tensors; else bf16 tensors.
 template <int CG, int BN, bool F32>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
@@ -253,18 +254,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;
     const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
+    // Whether the barrier's phase is complete: not if it took too long, or if another
+    // wait of this CTA did (the lanes of a warp may see that flag at different times).
     volatile int *abort_flag = &sh.abort;
     auto wait = [&](uint64_t &bar, uint32_t parity) {
         const uint32_t b = smem_u32(&bar);
-        if (mbar_try_wait(b, parity)) return;
+        if (mbar_try_wait(b, parity)) return true;
         const unsigned long long t0 = global_ns();
         while (!mbar_try_wait(b, parity)) {
-            if (*abort_flag) return;
+            if (*abort_flag) return false;
             if (global_ns() - t0 > test.timeout_ns) {
                 *abort_flag = 1;
-                return;
+                return false;
             }
         }
+        return true;
     };
     // Work item: a tile, or a part of Cin of one of the last tiles.
     struct Item {
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             for (int i = 0; i < EPI_WARPS; ++i) mbar_init(smem_u32(&sh.residual[i]), 1);
             mbar_init(smem_u32(&sh.drain), 1);
-            sh.abort = 0;
+            sh.abort = sh.other_abort = 0;
             fence_mbar_init();
         }
         __syncwarp();
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_OTHER));
         if (warp == 8) {
             if (lane == 0) {
-                for (int i = first; i < g.items; i += stride) {
+                for (int i = first; i < g.items && !*abort_flag; i += stride) {
                     const Item it = item(i);
                     const int row = (it.m * CG + rank) * TILE, col = it.n * BN + rank * (BN / CG);
                     for (int c0 = it.k0; c0 < it.k1; c0 += F32 ? KCHUNK : it.k1) {
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             for (int k = c0; k < c1; ++k, ++issued) {
                                 const uint32_t slot = issued % STAGES, round = issued / STAGES;
                                 const uint32_t bar = CG == 2 ? in_leader(smem_u32(&sh.full[slot])) : smem_u32(&sh.full[slot]);
-                                if (round > 0) wait(sh.empty[slot], (round - 1) & 1);
+                                if (round > 0) (void)wait(sh.empty[slot], (round - 1) & 1);
                                 if (*abort_flag) break;
                                 if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[slot]), CG * STAGE);
                                 const uint32_t at = base + slot * STAGE;
@@ -345,16 +349,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp == 9 && rank == 0) {
             const uint32_t one = elect_one();
             uint32_t c = 0, use = 0;   // stages and accumulators used
-            for (int i = first; i < g.items; i += stride) {
+            // An expired wait ends the products, for the whole warp: each one more would
+            // give stages back that the pair's second CTA would fill, with no one to expect
+            // the bytes.
+            bool on = true;
+            for (int i = first; i < g.items && on; i += stride) {
                 const Item it = item(i);
-                for (int c0 = it.k0; c0 < it.k1; c0 += F32 ? KCHUNK : it.k1, ++use) {
+                for (int c0 = it.k0; c0 < it.k1 && on; c0 += F32 ? KCHUNK : it.k1, ++use) {
                     const int n = (F32 ? min(c0 + KCHUNK, it.k1) - c0 : it.k1 - c0) * PRODUCTS;
                     const uint32_t buf = use & 1;
-                    if (use > 1) wait(sh.acc_empty[buf], ((use >> 1) - 1) & 1);
+                    if (use > 1) on = __all_sync(0xffffffffu, wait(sh.acc_empty[buf], ((use >> 1) - 1) & 1));
                     tc::fence_after_sync();
-                    for (int k = 0; k < n; ++k, ++c) {
+                    for (int k = 0; k < n && on; ++k, ++c) {
                         const uint32_t slot = c % STAGES;
-                        wait(sh.full[slot], (c / STAGES) & 1);
+                        on = __all_sync(0xffffffffu, wait(sh.full[slot], (c / STAGES) & 1));
+                        if (!on) break;
                         tc::fence_after_sync();
                         const uint32_t xa = ((base + slot * STAGE) >> 4) | DESC_LO;
                         const uint32_t wa = ((base + slot * STAGE + TILE * 128) >> 4) | DESC_LO;
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             mma<CG>(one, tmem + buf * BN, xa + 2 * j, wa + 2 * j, DESC_HI, idesc<CG, BN>(), k > 0 || j > 0);
                         commit<CG>(one, smem_u32(&sh.empty[slot]));
                     }
-                    commit<CG>(one, smem_u32(&sh.acc_full[buf]));
+                    if (on) commit<CG>(one, smem_u32(&sh.acc_full[buf]));
                 }
             }
             __syncwarp();
@@ -413,7 +422,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             if constexpr (F32) {
                 for (int c0 = it.k0; c0 < it.k1; c0 += KCHUNK) {
-                    wait(sh.acc_full[use & 1], (use >> 1) & 1);
+                    (void)wait(sh.acc_full[use & 1], (use >> 1) & 1);
+                    __syncwarp();
                     tc::fence_after_sync();
                     if (active) {
 #pragma unroll
@@ -428,7 +438,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     release();
                 }
             } else {
-                wait(sh.acc_full[use & 1], (use >> 1) & 1);
+                (void)wait(sh.acc_full[use & 1], (use >> 1) & 1);
+                __syncwarp();
                 tc::fence_after_sync();
             }
             // bias, activation (32 columns from col0 + d)
@@ -451,7 +462,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 activate32<!F32>(v, a.act);
             };
             bool held = !F32;   // the accumulator is not yet released
-            if (active && row0 < a.rows && !*abort_flag) {
+            // (one answer for the warp: what follows is for all of its lanes)
+            if (active && row0 < a.rows && !__any_sync(0xffffffffu, *abort_flag)) {
                 if (it.part >= 0) {
                     // fp32 sums of this part of Cin
 #pragma unroll
@@ -504,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int e = 0; e < BOX / 32; ++e) finish(v[e], d + 32 * e);
                         if (lane == 0 && !g.residual_tma) bulk_wait_read<0>();
                         __syncwarp();
-                        if (g.residual_tma) wait(sh.residual[warp], loads++ & 1);
+                        if (g.residual_tma) (void)wait(sh.residual[warp], loads++ & 1);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {   // 16-byte chunks of the row
                             const uint32_t at = stg_row + ((j ^ (lane & 7)) << 4);
@@ -580,17 +592,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) bulk_wait_read<0>();
         tc::fence_before_sync();
     }
-    __syncthreads();
-    if (sh.abort) {
-        // give the copies and products in flight their time to end before the
-        // shared and tensor memory are given back
+    // One answer for the CTA: its threads part ways below, and meet at barriers.
+    const bool expired = __syncthreads_or(*abort_flag);
+    if (expired) {
+        // give the copies and products in flight their time to end before the shared
+        // and tensor memory are given back: a thousand times what they take, however short
+        // the limit of the waits is
+        const unsigned long long limit = test.timeout_ns > 1000000ull ? test.timeout_ns : 1000000ull;
         if (tid == 0) atomicExch(status, kDeviceTimeout);
         if (warp == 8 && lane == 0 && rank == 0)
             for (uint32_t e = issued > (uint32_t)STAGES ? issued - STAGES : 0; e < issued; ++e)
-                (void)mbar_wait_bounded(smem_u32(&sh.full[e % STAGES]), (e / STAGES) & 1, test.timeout_ns);
+                (void)mbar_wait_bounded(smem_u32(&sh.full[e % STAGES]), (e / STAGES) & 1, limit);
         if (warp == 9 && rank == 0) {
             commit<CG>(elect_one(), smem_u32(&sh.drain));
-            (void)mbar_wait_bounded(smem_u32(&sh.drain), 0, test.timeout_ns);
+            (void)mbar_wait_bounded(smem_u32(&sh.drain), 0, limit);
             __syncwarp();
         }
         __syncthreads();
@@ -598,15 +613,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     if constexpr (CG == 2) {
         // neither leaves while the other's copies and products use its memory; after
         // an expired wait the second CTA's last copies may have no one who waits for
-        // them, so both stay for a thousand times as long as a copy takes
-        if (tid == 0 && sh.abort) {
+        // them, so both stay for a thousand times as long as a copy takes.  Each tells the
+        // other in a word of its own, which is read behind the barrier that orders it.
+        if (tid == 0 && expired) {
             uint32_t there;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(there) : "r"(smem_u32(&sh.abort)), "r"(rank ^ 1));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(there) : "r"(smem_u32(&sh.other_abort)), "r"(rank ^ 1));
             asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(there), "r"(1) : "memory");
         }
+        __syncwarp();
         cluster_sync();
-        if (*abort_flag) {
+        if (expired || *static_cast<volatile int *>(&sh.other_abort)) {
             for (const unsigned long long t0 = global_ns(); global_ns() - t0 < 1000000ull;) __nanosleep(1000);
+            __syncwarp();
             cluster_sync();
         }
     }

@@ -242,6 +242,25 @@ def test_expired_wait_is_reported(sc, shape, drop_copy, dtype):
     check(torch, run(torch, sc, x, w, None, None, 0, dtype), x, w, None, None, 0, dtype)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(40, 256, 300), (1030, 1024, 700), (5000, 1024, 2100)])
+def test_waits_that_expire_anywhere(sc, shape, dtype):
+    """No copy is left out, but the waits' limit is as short as the waits themselves, so that they run out in one warp or
+    another, in one CTA of a pair or in both, at the start or in the middle: each call ends, says so or not, and the next
+    ordinary one is right.  Then a stage left out early in a long product, where the pair's second CTA is left waiting."""
+    import torch
+    x, w, _, _ = tensors(torch, dtype, *shape, seed=9, bias=False, residual=False)
+    y = torch.empty(shape[0], shape[2], dtype=x.dtype, device="cuda")
+    seen = set()
+    for drop_copy, limit in [(1 << 30, t) for t in (1, 2, 3, 5, 8, 13, 20, 30) for _ in range(8)] + [(1, 100), (9, 100)]:
+        sc.check(sc.sc_test_linear_wait_expiry(x, w, y, *shape, dtype, drop_copy, limit), "sc_test_linear_wait_expiry")
+        torch.cuda.synchronize()
+        seen.add(sc.sc_last_device_status())
+    assert seen <= {sc.SC_OK, sc.SC_ERR_DEVICE_TIMEOUT} and sc.SC_ERR_DEVICE_TIMEOUT in seen
+    check(torch, run(torch, sc, x, w, None, None, 0, dtype), x, w, None, None, 0, dtype)
+
+
 def test_wait_expiry_hook_refusals():
     assert scl.sc_test_linear_wait_expiry(None, B, C, 5, 64, 32, BF16, 0, 10, stream=0) == scl.SC_ERR_NULL
     assert scl.sc_test_linear_wait_expiry(A, B, C, 5, 64, 32, BF16, -1, 10, stream=0) == scl.SC_ERR_SHAPE
