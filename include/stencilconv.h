@@ -689,8 +689,8 @@ int sc_test_attn_q8_wait_expiry(const void *q, const void *k, const float *k_sca
 
 /*
  * sc_test_linear_wait_expiry: test hook for the device-status path, not part
- * of the operation.  Runs linear_fwd's tensor-core kernel (packed, no bias,
- * activation or residual, whatever the number of rows) with the copies of
+ * of the operation.  Runs linear_fwd's tensor-core kernel (packed, no bias or
+ * activation, residual or NULL, whatever the number of rows) with the copies of
  * stage `drop_copy` (0-based, in each CTA's issue order) never issued, so the
  * time-bounded waits for them expire after `timeout_us` microseconds.  The
  * kernel then records SC_ERR_DEVICE_TIMEOUT (read and cleared by
@@ -699,8 +699,8 @@ int sc_test_attn_q8_wait_expiry(const void *q, const void *k, const float *k_sca
  * that no CTA reaches the waits that happen to take longer than timeout_us expire,
  * if any.
  */
-int sc_test_linear_wait_expiry(const void *x, const void *w, void *y, int rows, int Cin, int Cout, int dtype, int drop_copy,
-                               int timeout_us, sc_stream_t stream);
+int sc_test_linear_wait_expiry(const void *x, const void *w, const void *residual, void *y, int rows, int Cin, int Cout,
+                               int dtype, int drop_copy, int timeout_us, sc_stream_t stream);
 
 /*
  * sc_test_workspace_allocs: test hook, not part of the operation.  The

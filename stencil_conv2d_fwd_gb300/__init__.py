@@ -85,7 +85,7 @@ SIGNATURES = {
     "rotary_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "qk_norm_rotary_fwd": (_I, [_P, _P, _P, _I, _I, _I, _F, _I, _I, _I, _P]),
     "linear_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
-    "sc_test_linear_wait_expiry": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "sc_test_linear_wait_expiry": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "residual_norm_fwd": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _I, _F, _I, _P, _P]),
     "kv_quantize_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "sc_test_attn_q8_wait_expiry": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
@@ -445,10 +445,10 @@ def sc_test_attn_q8_wait_expiry(q, k, k_scale, v, v_scale, out, N, Tq, Tk, Hq, H
                                               Hkv, D, block, code, dtype, drop_copy, timeout_us, _stream(stream))
 
 
-def sc_test_linear_wait_expiry(x, w, y, rows, Cin, Cout, dtype, drop_copy, timeout_us, stream=None) -> int:
+def sc_test_linear_wait_expiry(x, w, y, rows, Cin, Cout, dtype, drop_copy, timeout_us, residual=None, stream=None) -> int:
     """Test hook: linear_fwd's tensor-core kernel with one stage's copies never issued (see the header)."""
-    return load().sc_test_linear_wait_expiry(_ptr(x), _ptr(w), _ptr(y), rows, Cin, Cout, dtype, drop_copy, timeout_us,
-                                             _stream(stream))
+    return load().sc_test_linear_wait_expiry(_ptr(x), _ptr(w), _ptr(residual), _ptr(y), rows, Cin, Cout, dtype, drop_copy,
+                                             timeout_us, _stream(stream))
 
 
 def sc_test_stencil_wait_expiry(inp, out, H, W, drop_copy, timeout_us, stream=None) -> int:

@@ -146,11 +146,11 @@ int linear_fwd(const void *x, const void *w, const float *b, const void *residua
     return sc::from_cuda(few_rows(a, bf16) ? sc::launch_linear_rows(a, bf16, st) : sc::launch_linear_tc(a, bf16, st));
 }
 
-int sc_test_linear_wait_expiry(const void *x, const void *w, void *y, int rows, int Cin, int Cout, int dtype, int drop_copy,
-                               int timeout_us, sc_stream_t stream)
+int sc_test_linear_wait_expiry(const void *x, const void *w, const void *residual, void *y, int rows, int Cin, int Cout,
+                               int dtype, int drop_copy, int timeout_us, sc_stream_t stream)
 {
     sc::LinearArgs a;
-    const int rc = take_linear(x, w, nullptr, nullptr, y, rows, Cin, Cout, SC_ACT_NONE, dtype, nullptr, a);
+    const int rc = take_linear(x, w, nullptr, residual, y, rows, Cin, Cout, SC_ACT_NONE, dtype, nullptr, a);
     if (rc != SC_OK) return rc;
     if (drop_copy < 0 || timeout_us < 1) return SC_ERR_SHAPE;
     sc::LinearTest test;

@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
     uint32_t issued = 0;   // stages asked for
+    uint32_t loads = 0;    // of the residual, by this warp
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_OTHER));
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t stg = base + STAGES * STAGE + warp * STG, stg_row = stg + lane * 128;
         const int col_part = COLS == BN ? 0 : part * COLS;
         const bool active = COLS < BN || part == 0;   // tiles of 64 columns: the first four warps
-        uint32_t use = 0, loads = 0;
+        uint32_t use = 0;
         for (int i = first; i < g.items; i += stride) {
             const Item it = item(i);
             const int row0 = (it.m * CG + rank) * TILE + quad * 32, row = row0 + lane;
@@ -516,7 +517,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int e = 0; e < BOX / 32; ++e) finish(v[e], d + 32 * e);
                         if (lane == 0 && !g.residual_tma) bulk_wait_read<0>();
                         __syncwarp();
-                        if (g.residual_tma) (void)wait(sh.residual[warp], loads++ & 1);
+                        // (no further copy behind one that has not come)
+                        if (g.residual_tma && !__all_sync(0xffffffffu, wait(sh.residual[warp], loads++ & 1))) break;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {   // 16-byte chunks of the row
                             const uint32_t at = stg_row + ((j ^ (lane & 7)) << 4);
@@ -603,6 +605,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 8 && lane == 0 && rank == 0)
             for (uint32_t e = issued > (uint32_t)STAGES ? issued - STAGES : 0; e < issued; ++e)
                 (void)mbar_wait_bounded(smem_u32(&sh.full[e % STAGES]), (e / STAGES) & 1, limit);
+        if (warp < EPI_WARPS && loads > 0) (void)mbar_wait_bounded(smem_u32(&sh.residual[warp]), (loads - 1) & 1, limit);
         if (warp == 9 && rank == 0) {
             commit<CG>(elect_one(), smem_u32(&sh.drain));
             (void)mbar_wait_bounded(smem_u32(&sh.drain), 0, limit);

@@ -261,6 +261,24 @@ def test_waits_that_expire_anywhere(sc, shape, dtype):
     check(torch, run(torch, sc, x, w, None, None, 0, dtype), x, w, None, None, 0, dtype)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(40, 256, 320), (1030, 512, 704), (5000, 512, 2112)])
+def test_waits_that_expire_beside_copies_of_the_residual(sc, shape, dtype):
+    """Waits that run out while parts of the residual are on their way to the epilogue's staging: every call ends, the
+    residual stays as it is, and the next ordinary call is right."""
+    import torch
+    x, w, _, r = tensors(torch, dtype, *shape, seed=10, bias=False)
+    keep, y, seen = r.clone(), torch.empty_like(r), set()
+    for drop_copy, limit in [(1 << 30, t) for t in (1, 2, 3, 5, 8, 13, 20, 30) for _ in range(8)] + [(2, 100)]:
+        sc.check(sc.sc_test_linear_wait_expiry(x, w, y, *shape, dtype, drop_copy, limit, residual=r), "sc_test_linear_wait_expiry")
+        torch.cuda.synchronize()
+        seen.add(sc.sc_last_device_status())
+    assert seen <= {sc.SC_OK, sc.SC_ERR_DEVICE_TIMEOUT} and sc.SC_ERR_DEVICE_TIMEOUT in seen
+    assert torch.equal(r, keep)
+    check(torch, run(torch, sc, x, w, None, r, 0, dtype), x, w, None, r, 0, dtype)
+
+
 def test_wait_expiry_hook_refusals():
     assert scl.sc_test_linear_wait_expiry(None, B, C, 5, 64, 32, BF16, 0, 10, stream=0) == scl.SC_ERR_NULL
     assert scl.sc_test_linear_wait_expiry(A, B, C, 5, 64, 32, BF16, -1, 10, stream=0) == scl.SC_ERR_SHAPE
