@@ -688,6 +688,16 @@ int sc_test_attn_q8_wait_expiry(const void *q, const void *k, const float *k_sca
                                 int drop_copy, int timeout_us, sc_stream_t stream);
 
 /*
+ * sc_test_attn_q8_rows_wait_expiry: the same for its kernel of few rows, with the
+ * copies of step `drop_copy` (0-based, of each warp) never issued.  A warp whose wait
+ * expires stops there.  With a drop_copy that no warp reaches the waits that
+ * happen to take longer than timeout_us expire, if any.
+ */
+int sc_test_attn_q8_rows_wait_expiry(const void *q, const void *k, const float *k_scale, const void *v, const float *v_scale,
+                                     void *out, int N, int Tq, int Tk, int Hq, int Hkv, int D, int block, int code, int dtype,
+                                     int drop_copy, int timeout_us, sc_stream_t stream);
+
+/*
  * sc_test_linear_wait_expiry: test hook for the device-status path, not part
  * of the operation.  Runs linear_fwd's tensor-core kernel (packed, no bias or
  * activation, residual or NULL, whatever the number of rows) with the copies of

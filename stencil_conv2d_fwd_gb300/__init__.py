@@ -89,6 +89,7 @@ SIGNATURES = {
     "residual_norm_fwd": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _I, _F, _I, _P, _P]),
     "kv_quantize_fwd": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "sc_test_attn_q8_wait_expiry": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "sc_test_attn_q8_rows_wait_expiry": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "cross_attention_q8_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P, _P]),
 }
 SC_CHAIN_MAX_LAYERS = 64
@@ -443,6 +444,13 @@ def sc_test_attn_q8_wait_expiry(q, k, k_scale, v, v_scale, out, N, Tq, Tk, Hq, H
     """Test hook: cross_attention_q8_fwd's tensor-core kernel with one copy never issued (see the header)."""
     return load().sc_test_attn_q8_wait_expiry(_ptr(q), _ptr(k), _ptr(k_scale), _ptr(v), _ptr(v_scale), _ptr(out), N, Tq, Tk, Hq,
                                               Hkv, D, block, code, dtype, drop_copy, timeout_us, _stream(stream))
+
+
+def sc_test_attn_q8_rows_wait_expiry(q, k, k_scale, v, v_scale, out, N, Tq, Tk, Hq, Hkv, D, block, code, dtype, drop_copy,
+                                     timeout_us, stream=None) -> int:
+    """Test hook: cross_attention_q8_fwd's kernel of few rows with one copy never issued (see the header)."""
+    return load().sc_test_attn_q8_rows_wait_expiry(_ptr(q), _ptr(k), _ptr(k_scale), _ptr(v), _ptr(v_scale), _ptr(out), N, Tq, Tk,
+                                                   Hq, Hkv, D, block, code, dtype, drop_copy, timeout_us, _stream(stream))
 
 
 def sc_test_linear_wait_expiry(x, w, y, rows, Cin, Cout, dtype, drop_copy, timeout_us, residual=None, stream=None) -> int:

@@ -112,8 +112,6 @@ __device__ __forceinline__ void load_states(uint32_t dst, const CUtensorMap *m, 
     tma_load_4d(dst, m, 0, t, h, n, bar);
 }
 
-constexpr unsigned long long kWaitNs = 1000000000ull;
-
 // A warp's ring: STAGES steps of KP keys and as many values, rows of DP bytes
 // swizzled by the copy: 16-byte chunk c of row r lies at c XOR (r / 2 mod 4) of a
 // 64-byte row, at c XOR (r mod 8) of a 128-byte one.
@@ -131,7 +129,8 @@ struct Q8Ring {
     const unsigned char *mb;
     uint64_t *bars;
     unsigned char *ring;
-    int len, key0, steps, lane, log2_block, byte, kn, kh, vn, vh;
+    int len, key0, steps, lane, log2_block, byte, kn, kh, vn, vh, drop_copy;
+    unsigned long long timeout_ns;
     float scales[2 * GROUPS];   // of the step after the current one
 
     __device__ __forceinline__ int mask_byte(int step) const
@@ -145,6 +144,7 @@ struct Q8Ring {
         if (step >= steps || lane != 0) return;
         const int slot = step % STAGES, t = key0 + step * STEP;
         const uint32_t bar = smem_u32(bars + slot), at = smem_u32(ring + slot * 2 * TILE);
+        if (step == drop_copy) return;
         mbar_arrive_expect_tx(bar, 2 * TILE);
         load_states(at, &m.k, t, kh, kn, bar);
         load_states(at + TILE, &m.v, t, vh, vn, bar);
@@ -161,8 +161,10 @@ struct Q8Ring {
         }
     }
     __device__ __forceinline__ void begin(unsigned char *memory, uint64_t *barriers, const AttnQ8Args &a, const Q8Maps &m,
-                                          const Q8Axes &ax, int n, int h, int split, int splits, int warp)
+                                          const Q8Axes &ax, const TcTest &test, int n, int h, int split, int splits, int warp)
     {
+        drop_copy = test.drop_copy;
+        timeout_ns = test.timeout_ns;
         ring = memory;
         bars = barriers;
         lane = threadIdx.x & 31;
@@ -190,8 +192,9 @@ struct Q8Ring {
         next_scales(0);
         byte = mb ? mask_byte(0) : 0;
     }
-    // Waits for a step's stage; valid: its states' bits, sc: its scales.
-    __device__ __forceinline__ const unsigned char *next(int step, uint32_t &valid, float (&sc)[2 * GROUPS], int *status)
+    // Waits for a step's stage; valid: its states' bits, sc: its scales, late: it did not
+    // come in time.
+    __device__ __forceinline__ unsigned char *next(int step, uint32_t &valid, float (&sc)[2 * GROUPS], bool &late)
     {
 #pragma unroll
         for (int i = 0; i < 2 * GROUPS; ++i) sc[i] = scales[i];
@@ -204,8 +207,17 @@ struct Q8Ring {
             valid = left >= KP ? FULL : (1u << left) - 1u;
         }
         const int slot = step % STAGES;
-        if (!mbar_wait_bounded(smem_u32(bars + slot), (step / STAGES) & 1, kWaitNs)) atomicExch(status, kDeviceTimeout);
+        late = !mbar_wait_bounded(smem_u32(bars + slot), (step / STAGES) & 1, timeout_ns);
         return ring + slot * 2 * TILE;
+    }
+    // Behind a step that was late: the copies that are on their way get their time, a
+    // thousand times what they take at least.
+    __device__ __forceinline__ void drain(int step)
+    {
+        const unsigned long long limit = timeout_ns > 1000000ull ? timeout_ns : 1000000ull;
+        for (int s = step; s < min(step + STAGES, steps); ++s)
+            (void)mbar_wait_bounded(smem_u32(bars + s % STAGES), (s / STAGES) & 1, limit);
+        __syncwarp();
     }
 };
 
@@ -226,7 +238,8 @@ constexpr float kWeightLog2 = 14.f;   // weights are 2^14 P
 // T: float or bf16 queries; R: 8 rows, or with bf16 16.
 template <class T, int DP, bool E4M3, int R>
 __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
-    attn_q8_kernel(const AttnQ8Args a, const RowsGeom g, const AttnPartials part, const __grid_constant__ Q8Maps maps, const Q8Axes axes)
+    attn_q8_kernel(const AttnQ8Args a, const RowsGeom g, const AttnPartials part, const __grid_constant__ Q8Maps maps, const Q8Axes axes,
+                   const TcTest test)
 {
     using Ring = Q8Ring<DP>;
     constexpr bool F32 = sizeof(T) == 4;
@@ -252,7 +265,7 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
     const int rows = a.Tq * a.G;
 
     Ring ring;
-    ring.begin(sm.ring[warp], sm.bars[warp], a, maps, axes, n, h, split, g.splits, warp);
+    ring.begin(sm.ring[warp], sm.bars[warp], a, maps, axes, test, n, h, split, g.splits, warp);
 
     // the rows' queries times a power of two that puts a row's largest element in
     // [2^12, 2^13); back[] undoes it and carries scale log2 e
@@ -341,7 +354,8 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
     for (int step = 0; step < ring.steps; ++step) {
         uint32_t ok;
         float sc[2 * Ring::GROUPS];
-        unsigned char *tile = const_cast<unsigned char *>(ring.next(step, ok, sc, axes.status));
+        bool late;
+        unsigned char *tile = ring.next(step, ok, sc, late);
         const uint4 *kt = reinterpret_cast<const uint4 *>(tile), *vt = reinterpret_cast<const uint4 *>(tile + Ring::TILE);
         const bool full = ok == Ring::FULL;
         if (E4M3 && !full) {
@@ -398,7 +412,12 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
             }
             if (joint) top[0][r] = top[Ring::GROUPS - 1][r] = fmaxf(top[0][r], top[Ring::GROUPS - 1][r]);
         }
-        if (__any_sync(0xffffffffu, grow)) {
+        if (__any_sync(0xffffffffu, grow || late)) {
+            if (__any_sync(0xffffffffu, late)) {   // the scores are of whatever was there: the warp's sums end here
+                if (lane == 0) atomicExch(axes.status, kDeviceTimeout);
+                ring.drain(step);
+                break;
+            }
 #pragma unroll
             for (int r = 0; r < RH; ++r) {
                 const float mm = fmaxf(m[r], fmaxf(top[0][r], top[Ring::GROUPS - 1][r]));
@@ -540,7 +559,7 @@ bool encode_map(CUtensorMap *m, const void *p, const HeadStrides &s, const AttnQ
 }
 
 template <class T, int DP, bool E4M3, int R>
-cudaError_t launch_q8(const AttnQ8Args &a, cudaStream_t st)
+cudaError_t launch_q8(const AttnQ8Args &a, cudaStream_t st, const TcTest &test)
 {
     static KernelCache cache;
     Q8Axes ax{a.ks.n != 0, a.ks.h != 0, a.vs.n != 0, a.vs.h != 0, device_status_ptr()};
@@ -548,25 +567,26 @@ cudaError_t launch_q8(const AttnQ8Args &a, cudaStream_t st)
     Q8Maps m;
     std::memset(&m, 0, sizeof(m));
     if (!encode_map<DP>(&m.k, a.k, a.ks, a) || !encode_map<DP>(&m.v, a.v, a.vs, a)) return cudaErrorInvalidValue;
-    return launch_rows_kernel(attn_q8_kernel<T, DP, E4M3, R>, cache, a, sizeof(T) == 2, R, (int)sizeof(Q8Shared<DP, R>), st, true, m, ax);
+    return launch_rows_kernel(attn_q8_kernel<T, DP, E4M3, R>, cache, a, sizeof(T) == 2, R, (int)sizeof(Q8Shared<DP, R>), st, true, m, ax,
+                              test);
 }
 
 template <class T, bool E4M3>
-cudaError_t dispatch(const AttnQ8Args &a, cudaStream_t st)
+cudaError_t dispatch(const AttnQ8Args &a, cudaStream_t st, const TcTest &test)
 {
     if constexpr (sizeof(T) == 2) {
-        if ((long long)a.Tq * a.G > 8) return a.D <= 64 ? launch_q8<T, 64, E4M3, 16>(a, st) : launch_q8<T, 128, E4M3, 16>(a, st);
+        if ((long long)a.Tq * a.G > 8) return a.D <= 64 ? launch_q8<T, 64, E4M3, 16>(a, st, test) : launch_q8<T, 128, E4M3, 16>(a, st, test);
     }
-    return a.D <= 64 ? launch_q8<T, 64, E4M3, 8>(a, st) : launch_q8<T, 128, E4M3, 8>(a, st);
+    return a.D <= 64 ? launch_q8<T, 64, E4M3, 8>(a, st, test) : launch_q8<T, 128, E4M3, 8>(a, st, test);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st)
+cudaError_t launch_attn_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st, const TcTest &test)
 {
     if (!encoder()) return cudaErrorNotSupported;
-    if (bf16) return e4m3 ? dispatch<__nv_bfloat16, true>(a, st) : dispatch<__nv_bfloat16, false>(a, st);
-    return e4m3 ? dispatch<float, true>(a, st) : dispatch<float, false>(a, st);
+    if (bf16) return e4m3 ? dispatch<__nv_bfloat16, true>(a, st, test) : dispatch<__nv_bfloat16, false>(a, st, test);
+    return e4m3 ? dispatch<float, true>(a, st, test) : dispatch<float, false>(a, st, test);
 }
 
 }  // namespace sc

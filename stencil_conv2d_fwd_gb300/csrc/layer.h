@@ -69,8 +69,8 @@ struct AttnQ8Args : AttnArgs {
     int block, log2_block, blocks;
 };
 // Rows in blocks of up to 16, each of which streams the codes through warp-wide
-// MMAs (attn_q8.cu).
-cudaError_t launch_attn_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st);
+// MMAs (attn_q8.cu).  test.drop_copy: that step of every warp.
+cudaError_t launch_attn_q8(const AttnQ8Args &a, bool bf16, bool e4m3, cudaStream_t st, const TcTest &test = TcTest());
 
 // Many rows per key head: the codes as bf16 in a workspace, and the tensor cores
 // (attn_split.cu, attn_tc.cu).

@@ -131,6 +131,23 @@ int take_q8(const void *q, const void *k, const float *k_scale, const void *v, c
     return SC_OK;
 }
 
+// The hooks of cross_attention_q8_fwd's bounded waits: its kernel of few rows, or of many.
+int q8_wait_expiry(bool few, const void *q, const void *k, const float *k_scale, const void *v, const float *v_scale, void *out,
+                   int N, int Tq, int Tk, int Hq, int Hkv, int D, int block, int code, int dtype, int drop_copy, int timeout_us,
+                   cudaStream_t st)
+{
+    sc::AttnQ8Args a;
+    const int rc = take_q8(q, k, k_scale, v, v_scale, out, nullptr, nullptr, nullptr, N, Tq, Tk, Hq, Hkv, D, 1.f, block, code, dtype,
+                           nullptr, a);
+    if (rc != SC_OK) return rc;
+    if (drop_copy < 0 || timeout_us < 1) return SC_ERR_SHAPE;
+    sc::TcTest test;
+    test.drop_copy = drop_copy;
+    test.timeout_ns = 1000ull * (unsigned long long)timeout_us;
+    const bool bf16 = dtype == SC_BF16, e4m3 = code == SC_CODE_E4M3;
+    return sc::from_cuda(few ? sc::launch_attn_q8(a, bf16, e4m3, st, test) : sc::launch_attn_tc_q8(a, bf16, e4m3, st, test));
+}
+
 }  // namespace
 
 extern "C" {
@@ -280,15 +297,16 @@ int sc_test_attn_q8_wait_expiry(const void *q, const void *k, const float *k_sca
                                 void *out, int N, int Tq, int Tk, int Hq, int Hkv, int D, int block, int code, int dtype,
                                 int drop_copy, int timeout_us, sc_stream_t stream)
 {
-    sc::AttnQ8Args a;
-    const int rc = take_q8(q, k, k_scale, v, v_scale, out, nullptr, nullptr, nullptr, N, Tq, Tk, Hq, Hkv, D, 1.f, block, code, dtype,
-                           nullptr, a);
-    if (rc != SC_OK) return rc;
-    if (drop_copy < 0 || timeout_us < 1) return SC_ERR_SHAPE;
-    sc::TcTest test;
-    test.drop_copy = drop_copy;
-    test.timeout_ns = 1000ull * (unsigned long long)timeout_us;
-    return sc::from_cuda(sc::launch_attn_tc_q8(a, dtype == SC_BF16, code == SC_CODE_E4M3, reinterpret_cast<cudaStream_t>(stream), test));
+    return q8_wait_expiry(false, q, k, k_scale, v, v_scale, out, N, Tq, Tk, Hq, Hkv, D, block, code, dtype, drop_copy, timeout_us,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+int sc_test_attn_q8_rows_wait_expiry(const void *q, const void *k, const float *k_scale, const void *v, const float *v_scale,
+                                     void *out, int N, int Tq, int Tk, int Hq, int Hkv, int D, int block, int code, int dtype,
+                                     int drop_copy, int timeout_us, sc_stream_t stream)
+{
+    return q8_wait_expiry(true, q, k, k_scale, v, v_scale, out, N, Tq, Tk, Hq, Hkv, D, block, code, dtype, drop_copy, timeout_us,
+                          reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

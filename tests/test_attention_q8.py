@@ -397,6 +397,40 @@ def test_expired_wait_is_reported(sc, shape, drop_copy, code, dtype):
     run_and_check(torch, sc, data, dtype, code, shape[-1])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("code", [I8, E4M3])
+@pytest.mark.parametrize("shape", [(1, 1, 40, 1, 1, 16, 16), (3, 1, 3000, 8, 2, 64, 32), (2, 3, 5000, 4, 1, 128, 64),
+                                   (1, 1, 60000, 4, 1, 64, 128), (64, 2, 700, 16, 2, 64, 64)])
+def test_expired_wait_of_few_rows_is_reported(sc, shape, code, dtype):
+    """A step that never comes (the first, a later one), then waits as short as the copies, that run out where they happen
+    to: every call ends, the status says so, and the next call is right.  The rings' memory is the sums' at the end, so no
+    copy may be on its way there."""
+    import torch
+    data = make(torch, dtype, code, *shape, seed=15)
+    q, k, ks, v, vs = data
+    out, seen = torch.empty_like(q), set()
+    sc.check(sc.sc_last_device_status())
+    for drop_copy, limit in [(0, 300), (0, 1)] + [(1 << 30, t) for t in (1, 1, 2, 2, 4, 8) for _ in range(4)]:
+        sc.check(sc.sc_test_attn_q8_rows_wait_expiry(q, k, ks, v, vs, out, *shape, code, dtype, drop_copy, limit))
+        torch.cuda.synchronize()
+        seen.add(sc.sc_last_device_status())
+        assert drop_copy > 0 or sc.SC_OK not in seen
+    assert seen <= {scl.SC_OK, scl.SC_ERR_DEVICE_TIMEOUT}
+    if shape[2] >= 60000:   # warps with many steps
+        sc.check(sc.sc_test_attn_q8_rows_wait_expiry(q, k, ks, v, vs, out, *shape, code, dtype, 1, 300))
+        assert sc.sc_last_device_status() == scl.SC_ERR_DEVICE_TIMEOUT
+    assert sc.sc_last_device_status() == scl.SC_OK
+    run_and_check(torch, sc, data, dtype, code, shape[-1])
+
+
+def test_rows_wait_expiry_hook_refusals():
+    args = (A, B, C, D_, E, G, 2, 4, 40, 2, 2, 32)
+    assert scl.sc_test_attn_q8_rows_wait_expiry(None, *args[1:], 16, I8, F32, 0, 10, stream=0) == scl.SC_ERR_NULL
+    assert scl.sc_test_attn_q8_rows_wait_expiry(*args, 16, I8, F32, -1, 10, stream=0) == scl.SC_ERR_SHAPE
+    assert scl.sc_test_attn_q8_rows_wait_expiry(*args, 16, I8, F32, 0, 0, stream=0) == scl.SC_ERR_SHAPE
+
+
 def test_wait_expiry_hook_refusals():
     args = (A, B, C, D_, E, G, 2, 4, 40, 2, 2, 32)
     assert scl.sc_test_attn_q8_wait_expiry(None, *args[1:], 16, I8, F32, 0, 10, stream=0) == scl.SC_ERR_NULL
