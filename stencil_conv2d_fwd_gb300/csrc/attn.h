@@ -57,8 +57,9 @@ cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, cudaStream_t st, const 
 // Copies of q ([plane][N][Hkv][Tq][G][D]), k and v ([plane][N][Hkv][Tk][D]) for
 // it: fp32 tensors as three bf16 planes, bf16 ones as one (attn_split.cu).
 cudaError_t launch_attn_split(const AttnArgs &a, bool bf16, void *const (&planes)[3], cudaStream_t st);
-// Joins partial results into out and lse (attn_join.cu).
-cudaError_t launch_attn_join(const AttnArgs &a, bool bf16, const AttnPartials &p, cudaStream_t st);
+// Joins partial results into out and lse (attn_join.cu).  sized: their maxima hold the
+// sizes of the values' scales (rescale_sum).
+cudaError_t launch_attn_join(const AttnArgs &a, bool bf16, const AttnPartials &p, cudaStream_t st, bool sized = false);
 
 // Norm and rotation of heads (rotary.cu).
 struct NormHeads {

@@ -17,11 +17,12 @@ constexpr int kJoinThreads = 256;
 constexpr int kAhead = 8;
 
 // m, l, o <- joined with (m2, l2, o2)
+template <bool SIZED>
 __device__ __forceinline__ void join4(float &m, float &l, float4 &o, float m2, float l2, const float4 &o2)
 {
     const float mm = fmaxf(m, m2), ms = mm == -INFINITY ? 0.f : mm;
     const float f1 = ex2(m - ms), f2 = ex2(m2 - ms);
-    l = join_sums(l, f1, m - ms, l2, f2, m2 - ms);
+    l = SIZED ? join_sums(l, f1, m - ms, l2, f2, m2 - ms) : l * f1 + l2 * f2;
     m = mm;
     o.x = o.x * f1 + o2.x * f2;
     o.y = o.y * f1 + o2.y * f2;
@@ -35,7 +36,9 @@ struct JoinGeom {
     int rows;     // rows of a CTA: quads * groups * rows <= kJoinThreads
 };
 
-template <bool BF16>
+// SIZED: the maxima hold the sizes of the values' scales (rescale_sum).  (152 parts of
+// four rows take 0.5 us more so.)
+template <bool BF16, bool SIZED>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, const AttnPartials p, const JoinGeom g)
 {
     __shared__ float4 so[kJoinThreads];
@@ -64,13 +67,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) mm = fmaxf(mm, ml[k].x);
             const float ms = mm == -INFINITY ? 0.f : mm, f0 = ex2(m - ms);
-            l = rescale_sum(l, f0, m - ms);
+            l = SIZED ? rescale_sum(l, f0, m - ms) : l * f0;
             o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
             m = mm;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const float d = ml[k].x - ms, f = ex2(d);
-                l = d >= -126.f ? fmaf(ml[k].y, f, l) : l + rescale_sum(ml[k].y, f, d);
+                l = !SIZED || d >= -126.f ? fmaf(ml[k].y, f, l) : l + rescale_sum(ml[k].y, f, d);
                 o.x = fmaf(q[k].x, f, o.x);
                 o.y = fmaf(q[k].y, f, o.y);
                 o.z = fmaf(q[k].z, f, o.z);
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
         if (!act || grp != 0) return;
         for (int j = 1; j < g.groups; ++j) {
             const int e = threadIdx.x + j * g.quads;
-            join4(m, l, o, sml[e].x, sml[e].y, so[e]);
+            join4<SIZED>(m, l, o, sml[e].x, sml[e].y, so[e]);
         }
     }
     if (!act) return;
@@ -108,7 +111,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
 
 }  // namespace
 
-cudaError_t launch_attn_join(const AttnArgs &a, bool bf16, const AttnPartials &p, cudaStream_t st)
+cudaError_t launch_attn_join(const AttnArgs &a, bool bf16, const AttnPartials &p, cudaStream_t st, bool sized)
 {
     JoinGeom g;
     g.quads = a.D / 4;
@@ -127,8 +130,9 @@ cudaError_t launch_attn_join(const AttnArgs &a, bool bf16, const AttnPartials &p
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true>, a, p, g)
-                : cudaLaunchKernelEx(&cfg, attn_join_kernel<false>, a, p, g);
+    if (!bf16) return cudaLaunchKernelEx(&cfg, attn_join_kernel<false, false>, a, p, g);   // (sized with bf16 tensors only)
+    return sized ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true, true>, a, p, g)
+                 : cudaLaunchKernelEx(&cfg, attn_join_kernel<true, false>, a, p, g);
 }
 
 }  // namespace sc

@@ -1380,7 +1380,7 @@ static cudaError_t attn_tc(const AttnArgs &a, const AttnQ8Args *q8, bool e4m3, b
     }
     if (e == cudaSuccess)
         e = q8 ? at::dispatch<true>(a, g, m, part, bf16, pair, st, test) : at::dispatch<false>(a, g, m, part, bf16, pair, st, test);
-    if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st);
+    if (e == cudaSuccess && part.parts > 0) e = launch_attn_join(a, bf16, part, st, q8 && bf16);
     if (ws) {
         const cudaError_t ef = workspace_free(ws, st);
         if (e == cudaSuccess) e = ef;
