@@ -661,7 +661,8 @@ int sc_test_stencil_wait_expiry(const float *in, float *out, int H, int W, int d
  * microseconds.  The kernel then records SC_ERR_DEVICE_TIMEOUT (read and
  * cleared by sc_last_device_status), waits for its other copies and products
  * and returns; the context stays usable.  `out` is left with no defined
- * values.
+ * values.  With a drop_copy that no CTA reaches the waits that happen to take
+ * longer than timeout_us expire, if any.
  */
 int sc_test_attn_wait_expiry(const void *q, const void *k, const void *v, void *out, int N, int Tq, int Tk, int Hq,
                              int Hkv, int D, int drop_copy, int timeout_us, sc_stream_t stream);

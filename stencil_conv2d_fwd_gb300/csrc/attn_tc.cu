@@ -1136,22 +1136,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncthreads();
     if (sh.abort) {
-        // give the copies and products in flight their time to end before the
-        // shared and tensor memory are given back
+        // give the copies and products in flight their time to end before the shared
+        // and tensor memory are given back: a thousand times what they take, however short
+        // the limit of the waits is
+        const unsigned long long limit = test.timeout_ns > 1000000ull ? test.timeout_ns : 1000000ull;
         if (tid == 0) atomicExch(status, kDeviceTimeout);
         if (warp == 8 && lane == 0) {
-            if (q_tiles > 0) (void)mbar_wait_bounded(smem_u32(&sh.q_full), 0, test.timeout_ns);
+            if (q_tiles > 0) (void)mbar_wait_bounded(smem_u32(&sh.q_full), 0, limit);
             if constexpr (CODES) {
                 for (uint32_t e = issued > (uint32_t)CSLOTS ? issued - CSLOTS : 0; e < issued; ++e)
-                    (void)mbar_wait_bounded(smem_u32(&sh.code_full[e % CSLOTS]), (e / CSLOTS) & 1, test.timeout_ns);
+                    (void)mbar_wait_bounded(smem_u32(&sh.code_full[e % CSLOTS]), (e / CSLOTS) & 1, limit);
             } else {
                 for (uint32_t e = issued > (uint32_t)SLOTS ? issued - SLOTS : 0; e < issued; ++e)
-                    (void)mbar_wait_bounded(smem_u32(&sh.full[e % SLOTS]), (e / SLOTS) & 1, test.timeout_ns);
+                    (void)mbar_wait_bounded(smem_u32(&sh.full[e % SLOTS]), (e / SLOTS) & 1, limit);
             }
         }
         if (warp == 9) {
             mma_commit(elect_one(), smem_u32(&sh.drain));   // by the thread that issued the products
-            (void)mbar_wait_bounded(smem_u32(&sh.drain), 0, test.timeout_ns);
+            (void)mbar_wait_bounded(smem_u32(&sh.drain), 0, limit);
             __syncwarp();
         }
         __syncthreads();

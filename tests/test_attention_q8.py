@@ -399,6 +399,24 @@ def test_expired_wait_is_reported(sc, shape, drop_copy, code, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(1, 140, 1000, 2, 2, 64, 32), (11, 300, 700, 6, 6, 64, 64), (1, 40, 20000, 2, 2, 128, 128)])
+def test_waits_that_expire_anywhere(sc, shape, dtype):
+    """No copy is left out, but the waits' limit is as short as the waits themselves: each call ends, says so or not, and
+    the next ordinary one is right; then the first copy left out with so short a limit."""
+    import torch
+    data = make(torch, dtype, I8, *shape, seed=16)
+    q, k, ks, v, vs = data
+    out, seen = torch.empty_like(q), set()
+    for drop_copy, limit in [(1 << 30, t) for t in (1, 2, 3, 5, 8, 13, 20, 30) for _ in range(4)] + [(0, 1)]:
+        sc.check(sc.sc_test_attn_q8_wait_expiry(q, k, ks, v, vs, out, *shape, I8, dtype, drop_copy, limit))
+        torch.cuda.synchronize()
+        seen.add(sc.sc_last_device_status())
+    assert seen <= {scl.SC_OK, scl.SC_ERR_DEVICE_TIMEOUT} and scl.SC_ERR_DEVICE_TIMEOUT in seen
+    run_and_check(torch, sc, data, dtype, I8, shape[-1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("code", [I8, E4M3])
 @pytest.mark.parametrize("shape", [(1, 1, 40, 1, 1, 16, 16), (3, 1, 3000, 8, 2, 64, 32), (2, 3, 5000, 4, 1, 128, 64),
                                    (1, 1, 60000, 4, 1, 64, 128), (64, 2, 700, 16, 2, 64, 64)])
