@@ -122,9 +122,20 @@ __device__ __forceinline__ uint32_t pack_bf16_finite(float lo, float hi)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Programmatic dependent launch: let the next kernel on the stream start its
-// prologue / wait until the previous kernel's writes are visible.
+// prologue / wait until the previous kernel's writes are visible.  A kernel that
+// waits is resident while those writes are made, so it takes no read-only loads
+// (ld.global.nc, __ldg), which are for what nothing writes in a kernel's lifetime.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 ld16_once(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 #endif
 
 }  // namespace sc

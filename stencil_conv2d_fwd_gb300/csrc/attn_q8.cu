@@ -156,8 +156,8 @@ struct Q8Ring {
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i) {
             const int at = step < steps ? min(key0 + step * STEP + 16 * i, len - 1) >> log2_block : 0;
-            scales[i] = __ldg(ks + at);
-            scales[GROUPS + i] = __ldg(vs + at);
+            scales[i] = ks[at];
+            scales[GROUPS + i] = vs[at];
         }
     }
     __device__ __forceinline__ void begin(unsigned char *memory, uint64_t *barriers, const AttnQ8Args &a, const Q8Maps &m,
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kRowThreads, R == 8 ? 2 : 1)
                     const T *p = static_cast<const T *>(a.q) + n * a.qs.n + tok * a.qs.t + hq * a.qs.h + d;
 #pragma unroll
                     for (int i = 0; i < 16; i += 16 / (int)sizeof(T)) {
-                        const uint4 v = ldg16(p + i);
+                        const uint4 v = ld16_once(p + i);
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {

@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto factor = [&](int j) {
             if (j >= nt || row >= 3 * KG) return 0.f;
             const float *f = row < KG ? g.k_factor : g.v_factor;
-            const float x = __ldg(f + (long long)nh * g.groups + (min(tile_key(j) + 16 * (row % KG), len - 1) >> g.log2_group));
+            const float x = f[(long long)nh * g.groups + (min(tile_key(j) + 16 * (row % KG), len - 1) >> g.log2_group)];
             // (beyond 2^80 either way a size is taken as that: a sum of unscaled weights
             // stays within fp32's range)
             if (row >= 2 * KG) return fminf(fmaxf(__log2f(fabsf(x)), -80.f), 80.f);

@@ -29,23 +29,14 @@ template <class T>
 constexpr int E = 16 / (int)sizeof(T);           // elements of a 16-byte chunk
 
 // (a warp's access is 512 bytes in a row whatever the type)
-__device__ __forceinline__ uint4 ld16(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 __device__ __forceinline__ void load_chunk(const float *p, float (&v)[4])
 {
-    const uint4 a = ld16(p);
+    const uint4 a = ld16_once(p);
     v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
 }
 __device__ __forceinline__ void load_chunk(const __nv_bfloat16 *p, float (&v)[8])
 {
-    const uint4 a = ld16(p);
+    const uint4 a = ld16_once(p);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -29,15 +29,6 @@ namespace {
 
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ uint4 ld_once16(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
@@ -101,7 +92,7 @@ __device__ __forceinline__ void finish_tiles(const LinearArgs &a, const float *s
         } else {
             v = cta_sum(tile, e - tile * R * TO);
         }
-        v = activate<sizeof(T) == 2>(a.b ? v + __ldg(a.b + col) : v, a.act);
+        v = activate<sizeof(T) == 2>(a.b ? v + a.b[col] : v, a.act);
         if (a.residual) v += to_float(static_cast<const T *>(a.residual)[(row0 + row) * a.rs + col]);
         store_as(static_cast<T *>(a.y) + (row0 + row) * a.ys + col, v);
     }
@@ -141,10 +132,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2) linear_rows_mma_
         for (int u = 0; u < U; ++u) {
             const bool on = s + u < s1 && (s + u) * 32 + t * 8 < a.Cin;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) w[u][i] = on ? ld_once16(wp[i] + (s + u) * 32LL) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 2; ++i) w[u][i] = on ? ld16_once(wp[i] + (s + u) * 32LL) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                x[u][i] = on ? __ldg(reinterpret_cast<const uint4 *>(xp[i] + (s + u) * 32LL)) : make_uint4(0u, 0u, 0u, 0u);
+                x[u][i] = on ? *reinterpret_cast<const uint4 *>(xp[i] + (s + u) * 32LL) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -221,10 +212,10 @@ __global__ void __launch_bounds__(kWarps * 32) linear_rows_split_kernel(const Li
         for (int u = 0; u < U; ++u) {
             const bool on = s + u < s1 && (s + u) * 16 + t * 4 < a.Cin;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) w[u][i] = on ? ld_once16(wp[i] + (s + u) * 16LL) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 2; ++i) w[u][i] = on ? ld16_once(wp[i] + (s + u) * 16LL) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                x[u][i] = on ? __ldg(reinterpret_cast<const uint4 *>(xp[i] + (s + u) * 16LL)) : make_uint4(0u, 0u, 0u, 0u);
+                x[u][i] = on ? *reinterpret_cast<const uint4 *>(xp[i] + (s + u) * 16LL) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
     load(s0);
@@ -299,14 +290,14 @@ __global__ void __launch_bounds__(kWarps * 32, R <= 2 ? 4 : 3) linear_rows_fma_k
         for (int u = 0; u < U; ++u) {
             const bool on = s + u < s1 && (s + u) * 128 + lane * 4 < a.Cin;
 #pragma unroll
-            for (int i = 0; i < O; ++i) w[u][i] = on ? ld_once16(wp[i] + (s + u) * 128LL) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < O; ++i) w[u][i] = on ? ld16_once(wp[i] + (s + u) * 128LL) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool on = s + u < s1 && (s + u) * 128 + lane * 4 < a.Cin;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float4 x = on ? __ldg(reinterpret_cast<const float4 *>(xp + min(r, a.rows - 1) * a.xs + (s + u) * 128LL))
+                const float4 x = on ? *reinterpret_cast<const float4 *>(xp + min(r, a.rows - 1) * a.xs + (s + u) * 128LL)
                                     : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < O; ++i) {

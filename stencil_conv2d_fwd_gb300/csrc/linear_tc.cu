@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int j = 0; j < COLS / 32; ++j) {
                 const int col = col0 + j * 32 + lane;
-                bias[j] = a.b && col < a.Cout ? __ldg(a.b + col) : 0.f;
+                bias[j] = a.b && col < a.Cout ? a.b[col] : 0.f;
             }
             float acc[F32 ? COLS : 1];
             auto columns = [&](int at, float (&v)[32]) {   // this row's 32 columns from col0 + at
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const SplitPart p0, c
         const long long row = e / cols8;
         const int c = (int)(e - row * cols8);
         const float4 *src = reinterpret_cast<const float4 *>(p.x + row * p.stride + c * 8);
-        const float4 v0 = __ldg(src), v1 = __ldg(src + 1);
+        const float4 v0 = src[0], v1 = src[1];
         const float x[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
         float f[8];
 #pragma unroll

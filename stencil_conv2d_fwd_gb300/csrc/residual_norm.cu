@@ -28,15 +28,6 @@ constexpr int kMaxWarps = 16;   // of a row, and of a CTA
 template <class T>
 constexpr int E = 16 / (int)sizeof(T);
 
-// (not a read-only load: a row may be written where it was read)
-__device__ __forceinline__ uint4 ld_row16(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 template <class T>
 __device__ __forceinline__ float element(const uint4 &v, int i)
@@ -59,7 +50,7 @@ __device__ __forceinline__ void vec(const float *p, int at, float (&v)[N])
 {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p + at + i));
+        const float4 a = *reinterpret_cast<const float4 *>(p + at + i);
         v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
     }
 }
@@ -146,11 +137,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_kernel(const Res
     uint4 xr[NV], rr[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (first + i * step < a.C) xr[i] = ld_row16(xp + first + i * step);
+        if (first + i * step < a.C) xr[i] = ld16_once(xp + first + i * step);
     if (a.residual) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (first + i * step < a.C) rr[i] = ld_row16(rp + first + i * step);
+            if (first + i * step < a.C) rr[i] = ld16_once(rp + first + i * step);
     }
     float v[NV][N];
 #pragma unroll
@@ -173,7 +164,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps) residual_norm_kernel(const Res
 #pragma unroll
             for (int j = 0; j < N; ++j) v[i][j] = fmaf(a.scale, element<T>(rr[i], j), v[i][j]);
         }
-        if (a.sum) store_row16<T>(static_cast<T *>(a.sum) + row * a.ss + at, v[i]);
+    }
+    if (a.sum) {   // (after all of the gate's loads, which would wait for the stores)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (first + i * step < a.C) store_row16<T>(static_cast<T *>(a.sum) + row * a.ss + first + i * step, v[i]);
     }
     if (!a.y) return;
     norm_row<NV, N, ONE>(v, a.pre, a.C, step, first, ONE ? slots : slots + 2 * kMaxWarps, W, w, lane);
