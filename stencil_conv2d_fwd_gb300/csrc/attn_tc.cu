@@ -886,8 +886,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const bool grow = top - m > GROW;   // false where both are -infinity
                 float f = 1.f;
                 if (grow) {
-                    f = ex2(m - top);
-                    l = Q8 ? rescale_sum(l, f, m - top) : l * f;
+                    if constexpr (Q8) {   // (as rescale_sum; its branch took 0.6% of a large call)
+                        const float h = ex2(0.5f * (m - top));
+                        f = h * h;
+                        l = l * h * h;
+                    } else {
+                        f = ex2(m - top);
+                        l *= f;
+                    }
                     m = top;
                 }
                 if (use > 0 && __any_sync(0xffffffffu, grow)) {
