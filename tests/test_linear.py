@@ -67,6 +67,25 @@ def test_epilogues(sc, shape, bias, residual, act, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [3, 12, 300, 1100])
+def test_fp32_gelu_keeps_its_digits_on_the_negative_side(sc, rows):
+    """Products that are one element exactly, from -12.5 to 12.5, against v erfc(-v / sqrt 2) / 2.  The exponent v^2 / 2 log2 e
+    has three roundings (v^2, the constant, the product), each U of it, so exp(-v^2 / 2) is off by 1.5 v^2 U, and by 4 U of
+    the exponential's own 2 ulp; the reciprocal has 2 U; 1 + 0.28 v, nine fused steps of a polynomial without cancellation (the
+    last two count, the earlier ones less and less), the fit's 5.8e-8 and four products are 1 U each: 2 v^2 + 16 in all."""
+    import torch
+    Cin, Cout = 8, 40
+    x, w = torch.zeros(rows, Cin, device="cuda"), torch.zeros(Cout, Cin, device="cuda")
+    w[:, 0] = torch.linspace(-12.5, 12.5, Cout, device="cuda")
+    x[:, 0] = 1.0
+    y = run(torch, sc, x, w, None, None, sc.SC_ACT_GELU, F32)
+    v = w[:, 0].double()
+    want = 0.5 * v * torch.erfc(-v / 2.0 ** 0.5)   # (ndtr is 1 + erf, which cancels in 64 bits too)
+    err = (y.double() - want).abs()
+    assert (err <= ref.U * (2 * v * v + 16) * want.abs()).all(), (err / want.abs()).amax(dim=0)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("shape", [(3, 128, 50), (16, 256, 100), (200, 128, 131), (513, 512, 264), (1100, 256, 264)])
 @pytest.mark.parametrize("pad", [8, 40])
