@@ -215,6 +215,33 @@ def test_offsets_beyond_32_bits(sc, dtype, rows):
     check(torch, got, x, w, b, r, 0, dtype)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,rows", [(F32, 2), (F32, 8), (F32, 40), (F32, 1100), (BF16, 2), (BF16, 12), (BF16, 40), (BF16, 300)])
+@pytest.mark.parametrize("odd", [False, True])
+def test_every_operand_beyond_32_bits(sc, dtype, rows, odd):
+    """The last row of each of x, w, y and the residual lies more than 2^31 elements behind its first, y's and the
+    residual's pitches whole 16-byte units (TMA takes them to and from the tensor cores' epilogue) or odd, in every kernel:
+    FMA, MMAs of few rows, three planes, tensor cores."""
+    import torch
+    Cin, Cout = 64, 24
+
+    def far(t, unit):
+        n, cols = t.shape
+        pitch = (((1 << 31) + 4096) // (n - 1) // unit + 1) * unit | (unit == 1)
+        v = torch.empty(pitch * (n - 1) + cols + 16, dtype=t.dtype, device="cuda").as_strided((n, cols), (pitch, 1))
+        v.copy_(t)
+        return v, pitch
+
+    x, w, b, r = tensors(torch, dtype, rows, Cin, Cout, seed=11)
+    unit = 1 if odd else 16
+    (xf, xs), (wf, ws), (rf, rs) = far(x, 16), far(w, 16), far(r, unit)
+    yf, ys = far(torch.full_like(r, float("nan")), unit)
+    assert min(xs * (rows - 1), ws * (Cout - 1), rs * (rows - 1), ys * (rows - 1)) > 1 << 31
+    sc.check(sc.linear_fwd(xf, wf, b, yf, rows, Cin, Cout, 0, dtype, residual=rf, strides=(xs, ws, ys, rs)), "linear_fwd")
+    sc.check(sc.sc_last_device_status())
+    check(torch, yf.contiguous(), x, w, b, r, 0, dtype)
+
+
 A, B, C, D_ = 1 << 20, 1 << 24, 1 << 28, 1 << 32   # addresses, 16-byte aligned, never dereferenced
 
 
