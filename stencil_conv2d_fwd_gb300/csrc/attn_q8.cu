@@ -34,7 +34,9 @@
 // e4m3 states 30.6 us (118 MB; 9 us of launch, ring start and join, the rest at 5.6
 // TB/s); 32 tokens, 16 heads on 4, over up to 3136 int8 states 17.1.  A warp's chain of
 // products, maximum and weights is what a step waits for (issue slots 49% busy); two
-// CTAs an SM took as long on one sequence and a third longer on a batch.
+// CTAs an SM took as long on one sequence and a third longer on a batch.  Heads of 128,
+// whose registers spill (8 rows): 32 tokens, 16 heads on 4, over 3136 int8 states 46 us in
+// bf16 (heads of 64 20), 40 in fp32 (20); 4 heads on one over 921600 states 74 and 65.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

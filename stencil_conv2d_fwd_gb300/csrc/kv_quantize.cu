@@ -11,8 +11,9 @@
 // 2^13th or so of fp32 values, and many bf16 ones, which lie on borders), top x is
 // compared with border times a in exact arithmetic made of fp32 FMAs (in 64 bits,
 // whose rate is 1/64 here, bf16 states took 794 us where they now take 90).
-// 32 x 3136 states, 8 heads of 64, keys and values: fp32 89 us (5.8 TB/s), bf16 90 (3.4
-// TB/s: some 27 instructions an element of both, issued 82% of the time).
+// 32 x 3136 states, 8 heads of 64, keys and values: fp32 88 to 89 us (5.8 TB/s, either
+// code), bf16 92 (e4m3) and 96 (int8; 3.3 TB/s: some 27 instructions an element of both,
+// issued 82% of the time).  Lengths from 1600 to 3136: fp32 75 us (5.0 TB/s), bf16 76 to 78.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -19,9 +19,9 @@ struct LinearArgs {
     int rows, Cin, Cout, act;
     long long xs, ws, ys, rs;   // row strides in elements
 };
-// Up to 16 rows (linear_rows.cu).
+// Few rows, and in fp32 few products (linear_rows.cu; layer_api.cu has the rule).
 cudaError_t launch_linear_rows(const LinearArgs &a, bool bf16, cudaStream_t st);
-// More: tensor cores (linear_tc.cu).  drop_copy >= 0 leaves that stage's copies
+// Others: tensor cores (linear_tc.cu).  drop_copy >= 0 leaves that stage's copies
 // of every CTA un-issued so that the bounded wait for them expires (tests of the
 // device-status path); timeout_ns bounds each wait.
 struct LinearTest {

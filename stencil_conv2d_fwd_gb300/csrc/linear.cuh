@@ -11,9 +11,9 @@
 namespace sc {
 
 // 1 - Phi(z) of the normal distribution, z >= 0, to 13 units of 2^-24 and 1.5 z^2 more (of
-// z^2's rounding in the exponent): exp(-z^2 / 2) t P(t), t = 1 / (1 + 0.4 z / sqrt 2), with P
-// fitted to exp(y^2) erfc(y) / (2 t) by weighted least squares in relative error, 5.8e-8 at
-// most for y = z / sqrt 2 up to 9.6.  0 above z = 13.2, where it is below 2^-126.
+// z^2's rounding in the exponent): exp(-z^2 / 2) t P(t) / 2, t = 1 / (1 + 0.4 y), y = z / sqrt 2,
+// with P fitted to exp(y^2) erfc(y) / t by weighted least squares in relative error, 5.8e-8 at
+// most for y up to 9.6.  0 above z = 13.2, where it is below 2^-126.
 __device__ __forceinline__ float normal_tail(float z)
 {
     float t;
@@ -30,14 +30,15 @@ __device__ __forceinline__ float normal_tail(float z)
 }
 
 // act as sc_act; a NaN stays one.  fp32 gelu takes the tail that v is on, where 1 + erf
-// would cancel (nothing was left of it from v = -5.5 on), in no more time than erff: 14401 x
-// 1024 x 4096 @T@ us, with erff 437, with erfcf 580.  BF16: an output that is rounded to bf16 next.
-// gelu then takes the normal distribution from Hastings' approximation of erf
-// (Abramowitz and Stegun, "Handbook of Mathematical Functions", 7.1.26: off by up
-// to 1.5e-7, and small on the negative side where 1 + erf would cancel), one
-// reciprocal, one exponential and eight products; with erff the epilogue was what
-// large products waited for (65536 x 2048 x 8192: 1545 us, without activation 1258).
-// silu takes the hardware's exponential and division (some 2^-21).
+// would cancel (nothing is left of that from v = -5.5 on), in no more time: 14401 x 1024 x
+// 4096 425 to 432 us, with erff 434, with erfcf 580.
+// BF16: an output that is rounded to bf16 next.  gelu then takes the normal distribution
+// from Hastings' approximation of erf (Abramowitz and Stegun, "Handbook of Mathematical
+// Functions", 7.1.26: off by up to 1.5e-7 of 1, on the negative side by 0.4% of the tail at
+// v = -6 and 2% at -10, where that is 10^-9 and 10^-23), one reciprocal, one exponential and
+// eight products; with erff the epilogue was what large products waited for (65536 x 2048 x
+// 8192: 1545 us, without activation 1258).  silu takes the hardware's exponential and division,
+// 2^-16 of itself at most (-87 < v), and 0 below.
 template <bool BF16>
 __device__ __forceinline__ float activate(float v, int act)
 {
