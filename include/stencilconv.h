@@ -391,7 +391,7 @@ typedef struct {
  * Products and sums are fp32, and so is everything up to y, which is rounded
  * once (to nearest even).  With bf16 tensors GELU's normal distribution is good to
  * 2^-22 of 1 (not of a far negative v's small tail: 0.4% of it at v = -6, 2% at -10),
- * SiLU to 2^-16 of itself (0 for v < -87.3).  fp32 tensors of more than 4 rows are multiplied in
+ * SiLU to 2^-16 of itself (0 for v < -87.3; with fp32 ones for v < -88.7).  fp32 tensors of more than 4 rows are multiplied in
  * three bf16 planes of 24 bits in all: there an infinity times another, or times
  * an element above 256, may be NaN, and an element below 2^-110 keeps 2^-134.
  * Supported: rows, Cin and Cout up to 2^30, strides below 2^40 bytes.  A call may

@@ -132,6 +132,58 @@ def test_layer(sc, dtype, code):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [3, 40, 700])
+@pytest.mark.parametrize("dtype", [scl.SC_F32, scl.SC_BF16])
+def test_calls_back_to_back_equal_calls_one_at_a_time(sc, dtype, rows):
+    """Every operator reads what the call before has written, many times over and in place, with new inputs each time: the
+    launches overlap their starts, and their temporary buffers are the ones that the last call has given back.  The same
+    bits as with a wait behind every call."""
+    import torch
+    t = torch.bfloat16 if dtype == scl.SC_BF16 else torch.float32
+    g = torch.Generator().manual_seed(5)
+    Tk, C, TURNS = 416, HEADS * D, 25
+    w = [(torch.randn(a, b, generator=g) * b ** -0.5).to(t).cuda() for a, b in ((C, C), (2 * KEY_HEADS * D, C), (MLP, C), (C, MLP))]
+    bias, norm = torch.randn(MLP, generator=g).cuda(), (1 + 0.2 * torch.randn(C, generator=g)).cuda()
+    xs = [torch.randn(rows, C, generator=g).to(t).cuda() for _ in range(TURNS)]
+    states = [torch.randn(Tk, C, generator=g).to(t).cuda() for _ in range(TURNS)]
+
+    def turns(wait):
+        x, h, u, a = (torch.zeros(rows, n, dtype=t, device="cuda") for n in (C, C, MLP, C))
+        kv = torch.zeros(Tk, 2, KEY_HEADS, D, dtype=t, device="cuda")
+        codes = [torch.zeros(1, Tk, KEY_HEADS, D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.zeros(1, KEY_HEADS, Tk // BLOCK, device="cuda") for _ in range(2)]
+        st = ((0, 2 * KEY_HEADS * D, D), None)
+        outs = []
+
+        def call(rc):
+            sc.check(rc)
+            if wait:
+                torch.cuda.synchronize()
+
+        for i in range(TURNS):
+            x.add_(xs[i])
+            call(sc.residual_norm_fwd(x, None, None, h, rows, C, pre=(sc.SC_NORM_RMS, norm, None, 1e-6), dtype=dtype))
+            call(sc.linear_fwd(states[i], w[1], None, kv, Tk, C, 2 * KEY_HEADS * D, dtype=dtype))
+            call(sc.kv_quantize_fwd((kv, codes[0], scales[0], *st), (kv[0, 1], codes[1], scales[1], *st), 1, Tk, KEY_HEADS, D, BLOCK,
+                                    scl.SC_CODE_I8, dtype))
+            call(sc.linear_fwd(h, w[0], None, a, rows, C, C, dtype=dtype))
+            call(sc.cross_attention_q8_fwd(a, codes[0], scales[0], codes[1], scales[1], h, 1, rows, Tk, HEADS, KEY_HEADS, D, D ** -0.5,
+                                           BLOCK, scl.SC_CODE_I8, dtype))
+            call(sc.residual_norm_fwd(h, x, x, h, rows, C, pre=(sc.SC_NORM_RMS, norm, None, 1e-6), dtype=dtype))
+            call(sc.linear_fwd(h, w[2], bias, u, rows, C, MLP, sc.SC_ACT_GELU, dtype))
+            call(sc.linear_fwd(u, w[3], None, x, rows, MLP, C, dtype=dtype, residual=x))
+            outs.append(x.clone())
+        torch.cuda.synchronize()
+        return outs
+
+    want = turns(True)
+    assert all(torch.isfinite(y.float()).all() for y in want)
+    for _ in range(3):
+        for i, (y, z) in enumerate(zip(turns(False), want)):
+            assert torch.equal(y, z), f"turn {i}"
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("code,near", [(scl.SC_CODE_I8, 127.0), (scl.SC_CODE_E4M3, 16.0)])
 @pytest.mark.parametrize("dtype", [scl.SC_F32, scl.SC_BF16])
 def test_example_with_states_in_8_bits(sc, dtype, code, near):
