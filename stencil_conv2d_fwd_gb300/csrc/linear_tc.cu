@@ -11,8 +11,8 @@
 // may address and half of the columns, adds bias, activation and residual in
 // fp32, rounds once and hands 32 rows of 128 bytes at a time to a TMA store
 // (the residual comes the same way); y or a residual that TMA cannot address (odd
-// pitches) is written and read a row at a time by the warp.  Warp 8 issues
-// the copies, warp 9 the products.
+// pitches, rows that end inside a 16-byte unit) is written and read a row at a time
+// by the warp.  Warp 8 issues the copies, warp 9 the products.
 //
 // fp32 tensors: x and w are three bf16 planes each (linear_split below), a
 // product the six of planes i + j <= 2, the small ones first.  The tensor cores
@@ -848,7 +848,8 @@ cudaError_t launch_linear_tc(const LinearArgs &a, bool bf16, cudaStream_t st, co
     auto tma_rows = [&](const void *p, long long stride) {
         return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * es % 16 == 0 && stride > 0;
     };
-    const bool y_tma = tma_rows(a.y, a.ys) && (!a.residual || tma_rows(a.residual, a.rs));
+    // (a TMA store leaves out whole 16-byte units past the row's end, but not a part of one)
+    const bool y_tma = tma_rows(a.y, a.ys) && (long long)a.Cout * es % 16 == 0 && (!a.residual || tma_rows(a.residual, a.rs));
     g.box = y_tma ? (bf16 ? 64 : 32) : 0;
     g.residual_tma = y_tma && a.residual;
 

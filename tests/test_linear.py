@@ -111,6 +111,26 @@ def test_strides(sc, shape, pad, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,rows", [(F32, 3), (F32, 12), (F32, 1100), (BF16, 12), (BF16, 40), (BF16, 300)])
+@pytest.mark.parametrize("Cout", [1, 2, 3, 5, 6, 7, 9, 31, 33, 34, 63, 65, 127, 129, 130, 423, 1377])
+@pytest.mark.parametrize("residual", [False, True])
+def test_nothing_beside_y_is_written(sc, dtype, rows, Cout, residual):
+    """Any number of outputs in rows of whole 16-byte units, y and the residual a slice of something wider: the columns
+    behind y's last one stay as they are."""
+    import torch
+    Cin = 64
+    x, w, b, r = tensors(torch, dtype, rows, Cin, Cout, seed=12, residual=True)
+    pitch = (Cout + 16) // 8 * 8
+    wide, rwide = (torch.full((rows, pitch), 7.0, dtype=x.dtype, device="cuda") for _ in range(2))
+    rwide[:, :Cout] = r
+    sc.check(sc.linear_fwd(x, w, b, wide, rows, Cin, Cout, 0, dtype, residual=rwide if residual else None,
+                           strides=(Cin, Cin, pitch, pitch)), "linear_fwd")
+    sc.check(sc.sc_last_device_status())
+    check(torch, wide[:, :Cout], x, w, b, r if residual else None, 0, dtype)
+    assert (wide[:, Cout:] == 7.0).all(), f"columns {sorted(set((wide[:, Cout:] != 7.0).nonzero()[:, 1].tolist()))} behind y"
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("shape", [(4, 256, 512), (300, 256, 515), (1100, 256, 512), (2000, 1024, 2048)])
 def test_residual_in_place_and_shared(sc, shape, dtype):
